@@ -20,7 +20,7 @@ from typing import Optional, Sequence
 __all__ = [
     "EP_OK", "EP_ERR_INVALID_ARG", "EP_ERR_CUDA", "EP_ERR_UNSUPPORTED",
     "EP_DEVERR_BAD_EXPERT", "EP_DEVERR_RECV_OVERFLOW", "EP_DEVERR_SLOT_OVERFLOW",
-    "EP_DEVERR_TIMEOUT",
+    "EP_DEVERR_TIMEOUT", "EP_DEVERR_BAD_ADAPTER",
     "EP_BF16", "EP_FP8_E4M3", "EP_COMBINE_SUM", "EP_COMBINE_WEIGHTED",
     "EP_PHASE_SEND", "EP_PHASE_RECV", "EP_PHASE_BOTH", "EP_MAX_RANKS",
     "EP_FP8_SCALE_FP32", "EP_FP8_SCALE_POW2", "EP_FP8_SCALE_UE8M0", "EP_FP8_SCALE_TENSOR",
@@ -33,10 +33,14 @@ __all__ = [
     "ep_ll_dispatch", "ep_ll_combine", "ep_clean_ll_buffer", "ep_read_recv_counts_sync",
     "ep_read_error_flags_sync", "ep_selftest_wait_timeout", "ep_kernel_launch_count",
     "ep_abi_version", "EXPORTED_SYMBOLS",
+    "ep_sort", "ep_gemm_shape", "ep_adapter_shape", "ep_sort_workspace_size", "ep_sort_layout",
+    "ep_sort_rows", "ep_unsort_rows", "ep_unsort_rows_backward", "ep_expert_gemm",
+    "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad", "ep_adapter_workspace_size", "ep_adapter_gemm",
 ]
 
 EP_OK, EP_ERR_INVALID_ARG, EP_ERR_CUDA, EP_ERR_UNSUPPORTED = 0, 1, 2, 3
 EP_DEVERR_BAD_EXPERT, EP_DEVERR_RECV_OVERFLOW, EP_DEVERR_SLOT_OVERFLOW, EP_DEVERR_TIMEOUT = 1, 2, 4, 8
+EP_DEVERR_BAD_ADAPTER = 16
 EP_BF16, EP_FP8_E4M3 = 0, 1
 EP_COMBINE_SUM, EP_COMBINE_WEIGHTED = 0, 1
 EP_PHASE_SEND, EP_PHASE_RECV, EP_PHASE_BOTH = 1, 2, 3
@@ -45,6 +49,7 @@ EP_LL_LAYOUT_SLOTS, EP_LL_LAYOUT_PACKED = 0, 1
 EP_MAX_RANKS = 64
 EP_MAX_TOPK = 32
 EP_EXPERT_MAJOR_MAX_EXPERTS = 4096
+EP_ADAPTER_MAX_RANK = 256
 
 # Every function include/ep.h declares (checked by the ABI test).
 EXPORTED_SYMBOLS = (
@@ -54,6 +59,9 @@ EXPORTED_SYMBOLS = (
     "ep_ll_dispatch", "ep_ll_combine", "ep_clean_ll_buffer", "ep_read_recv_counts_sync",
     "ep_read_error_flags_sync", "ep_selftest_wait_timeout", "ep_status_string",
     "ep_last_cuda_error", "ep_kernel_launch_count", "ep_abi_version",
+    "ep_sort_workspace_size", "ep_sort_layout", "ep_sort_rows", "ep_unsort_rows",
+    "ep_unsort_rows_backward", "ep_expert_gemm", "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad",
+    "ep_adapter_workspace_size", "ep_adapter_gemm",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -118,6 +126,21 @@ class ep_size_hint(ctypes.Structure):
         "ll_layout_range_bytes", "layout_workspace_bytes")]
 
 
+class ep_sort(ctypes.Structure):
+    _fields_ = [("entry_rows", _P), ("row_entries", _P), ("expert_prefix", _P),
+                ("num_rows", ctypes.c_int64)]
+
+
+class ep_gemm_shape(ctypes.Structure):
+    _fields_ = [("num_rows", _I32), ("num_experts", _I32), ("in_features", _I32),
+                ("out_features", _I32)]
+
+
+class ep_adapter_shape(ctypes.Structure):
+    _fields_ = [("num_rows", _I32), ("in_features", _I32), ("out_features", _I32),
+                ("num_adapters", _I32), ("rank", _I32)]
+
+
 _lib = None
 
 
@@ -164,6 +187,24 @@ def lib():
         L.ep_kernel_launch_count.restype = ctypes.c_uint64
         L.ep_abi_version.argtypes = []
         L.ep_abi_version.restype = _I32
+        L.ep_sort_workspace_size.argtypes = [S(ep_shape)]
+        L.ep_sort_workspace_size.restype = ctypes.c_size_t
+        L.ep_sort_layout.argtypes = [S(ep_shape), _P, S(ep_sort), _P, ctypes.c_size_t, S(ep_launch)]
+        L.ep_sort_rows.argtypes = [S(ep_shape), _P, ctypes.c_int, _P, _I32, S(ep_sort), _P, _P,
+                                   S(ep_launch)]
+        L.ep_unsort_rows.argtypes = [S(ep_shape), _P, _P, S(ep_sort), _P, S(ep_launch)]
+        L.ep_unsort_rows_backward.argtypes = [S(ep_shape), _P, _P, _P, S(ep_sort), _P, _P,
+                                              S(ep_launch)]
+        for name in ("ep_expert_gemm", "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad"):
+            getattr(L, name).argtypes = [S(ep_gemm_shape), _P, _P, _P, _P, S(ep_launch)]
+        L.ep_adapter_workspace_size.argtypes = [S(ep_adapter_shape)]
+        L.ep_adapter_workspace_size.restype = ctypes.c_size_t
+        L.ep_adapter_gemm.argtypes = [S(ep_adapter_shape), _P, _P, _P, _P, _P, _P, _P, _P,
+                                      ctypes.c_size_t, S(ep_launch)]
+        for name in ("ep_sort_layout", "ep_sort_rows", "ep_unsort_rows", "ep_unsort_rows_backward",
+                     "ep_expert_gemm", "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad",
+                     "ep_adapter_gemm"):
+            getattr(L, name).restype = _I32
         for name in ("ep_get_layout", "ep_get_layout_static_scratch", "ep_dispatch", "ep_combine",
                      "ep_dispatch_expert_major", "ep_combine_expert_major", "ep_ll_dispatch",
                      "ep_ll_combine", "ep_clean_ll_buffer", "ep_read_recv_counts_sync",
@@ -333,6 +374,75 @@ def ep_ll_combine(shape: ep_shape, y, topk_idx, topk_weights, handle: ep_ll_buff
 def ep_clean_ll_buffer(shape: ep_shape, buf: ep_ll_buffer, launch: Optional[ep_launch] = None) -> None:
     _check("ep_clean_ll_buffer", lib().ep_clean_ll_buffer(ctypes.byref(shape), ctypes.byref(buf),
                                                           ctypes.byref(_launch(launch))))
+
+
+def ep_sort_workspace_size(shape: ep_shape) -> int:
+    return int(lib().ep_sort_workspace_size(ctypes.byref(shape)))
+
+
+def ep_sort_layout(shape: ep_shape, topk_idx, sort: ep_sort, workspace,
+                   launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_sort_layout(ctypes.byref(shape), _ptr(topk_idx), ctypes.byref(sort), _ptr(workspace),
+                              workspace.numel() * workspace.element_size(),
+                              ctypes.byref(_launch(launch)))
+    _check("ep_sort_layout", st)
+
+
+def ep_sort_rows(shape: ep_shape, x, x_dtype: int, x_scales, sort: ep_sort, out_x, out_scales,
+                 launch: Optional[ep_launch] = None, scale_format: int = EP_FP8_SCALE_FP32) -> None:
+    st = lib().ep_sort_rows(ctypes.byref(shape), _ptr(x), x_dtype, _ptr(x_scales), scale_format,
+                            ctypes.byref(sort), _ptr(out_x), _ptr(out_scales),
+                            ctypes.byref(_launch(launch)))
+    _check("ep_sort_rows", st)
+
+
+def ep_unsort_rows(shape: ep_shape, y, topk_weights, sort: ep_sort, out,
+                   launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_unsort_rows(ctypes.byref(shape), _ptr(y), _ptr(topk_weights), ctypes.byref(sort),
+                              _ptr(out), ctypes.byref(_launch(launch)))
+    _check("ep_unsort_rows", st)
+
+
+def ep_unsort_rows_backward(shape: ep_shape, dout, y, topk_weights, sort: ep_sort, dy, dweights,
+                            launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_unsort_rows_backward(ctypes.byref(shape), _ptr(dout), _ptr(y), _ptr(topk_weights),
+                                       ctypes.byref(sort), _ptr(dy), _ptr(dweights),
+                                       ctypes.byref(_launch(launch)))
+    _check("ep_unsort_rows_backward", st)
+
+
+def ep_expert_gemm(shape: ep_gemm_shape, x, w, expert_prefix, y,
+                   launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_expert_gemm(ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(expert_prefix), _ptr(y),
+                              ctypes.byref(_launch(launch)))
+    _check("ep_expert_gemm", st)
+
+
+def ep_expert_gemm_dgrad(shape: ep_gemm_shape, dy, w, expert_prefix, dx,
+                         launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_expert_gemm_dgrad(ctypes.byref(shape), _ptr(dy), _ptr(w), _ptr(expert_prefix),
+                                    _ptr(dx), ctypes.byref(_launch(launch)))
+    _check("ep_expert_gemm_dgrad", st)
+
+
+def ep_expert_gemm_wgrad(shape: ep_gemm_shape, dy, x, expert_prefix, dw,
+                         launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_expert_gemm_wgrad(ctypes.byref(shape), _ptr(dy), _ptr(x), _ptr(expert_prefix),
+                                    _ptr(dw), ctypes.byref(_launch(launch)))
+    _check("ep_expert_gemm_wgrad", st)
+
+
+def ep_adapter_workspace_size(shape: ep_adapter_shape) -> int:
+    return int(lib().ep_adapter_workspace_size(ctypes.byref(shape)))
+
+
+def ep_adapter_gemm(shape: ep_adapter_shape, x, w, a, b, scales, adapter_idx, y, workspace,
+                    launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_adapter_gemm(ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(a), _ptr(b), _ptr(scales),
+                               _ptr(adapter_idx), _ptr(y), _ptr(workspace),
+                               0 if workspace is None else workspace.numel() * workspace.element_size(),
+                               ctypes.byref(_launch(launch)))
+    _check("ep_adapter_gemm", st)
 
 
 def ep_read_recv_counts_sync(shape: ep_shape, handle: ep_handle, stream=None) -> list:

@@ -11,7 +11,8 @@ import torch
 
 from . import (EP_BF16, EP_FP8_SCALE_FP32, EP_FP8_SCALE_UE8M0, EP_LL_LAYOUT_PACKED,
                EP_LL_LAYOUT_SLOTS, ep_fp8_options,
-               ep_handle, ep_layout, ep_layout_workspace_size, ep_ll_buffer, ep_shape, _ptr)
+               ep_handle, ep_layout, ep_layout_workspace_size, ep_ll_buffer, ep_shape,
+               ep_sort, ep_sort_workspace_size, _ptr)
 
 
 def new_event(stream=None) -> torch.cuda.Event:
@@ -166,6 +167,27 @@ class LLBuffers:
         return ep_ll_buffer(_ptr(self.recv_x), _ptr(self.recv_x_scales), _ptr(self.src_info),
                             _ptr(self.slot), _ptr(self.send_count), _ptr(self.recv_expert_count),
                             _ptr(self.layout_range), self.fp8, self.layout)
+
+
+class SortBuffers:
+    """The placement of an expert sort (see ep_sort in ep.h) with room for `rows` sorted rows
+    (default: one per entry), and its workspace. `shape` has num_ranks = 1."""
+
+    def __init__(self, shape: ep_shape, rows: Optional[int] = None, device="cuda"):
+        N, k, E = shape.num_tokens, shape.num_topk, shape.num_experts
+        i32 = dict(dtype=torch.int32, device=device)
+        self.rows = N * k if rows is None else int(rows)
+        self.entry_rows = torch.empty((N, k), **i32)
+        self.row_entries = torch.empty((self.rows,), **i32)
+        self.expert_prefix = torch.empty((E + 1,), **i32)
+        self.workspace = torch.empty(max(ep_sort_workspace_size(shape), 16), dtype=torch.uint8, device=device)
+
+    def handle(self) -> ep_sort:
+        return ep_sort(_ptr(self.entry_rows), _ptr(self.row_entries), _ptr(self.expert_prefix), self.rows)
+
+    def tensors(self) -> list:
+        """Every device tensor this object owns."""
+        return [v for v in vars(self).values() if isinstance(v, torch.Tensor)]
 
 
 def compact_row_offsets(counts: Sequence[int]) -> list:

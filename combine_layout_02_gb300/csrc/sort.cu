@@ -1,0 +1,608 @@
+// sort.cu -- rows into expert order and back, with the gradients of both directions.
+//
+// Placement (ep_sort_layout): a stable counting sort of the N*k entries by expert. Entries
+// are cut into segments, one per warp, in order. A segment's rows of expert e start at
+//   sum over e' < e of all entries of e'  +  sum over earlier segments of their entries of e
+// and within a segment a warp takes 32 entries at a time: an entry's rank among them is the
+// number of lower lanes with the same expert (__match_any_sync), on top of the warp's running
+// count in shared memory. Counts only, no global atomics: the placement is the same in every
+// run. Few entries: one block does all of it (sort_small_kernel). More: count, scan (one warp
+// per expert over the segments' counts) and place, three kernels without any inter-block wait.
+//
+// Rows (ep_sort_rows, ep_unsort_rows, ep_unsort_rows_backward): one warp per row in row order,
+// its placed entries' sorted rows as destinations or sources, as in the expert-major dispatch
+// and combine. Everything is bound by memory: each row is read once and each sorted row written
+// (or read) once.
+#include "rowops.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kSortWarps = 8;                  // warps per block of the count / place kernels
+constexpr int kSmallEntries = 8192;            // up to here one block sorts everything
+constexpr int kSmallThreads = 1024;
+constexpr int kTableInts = 48 * 1024 / 4;      // per-warp counts of a block, in shared memory
+constexpr int kSortSmemMax = (kTableInts + EP_MAX_EXPERTS) * 4;
+constexpr int kSegment = 128;                  // entries per segment, at least
+constexpr int kMaxSegments = 152 * 16;
+
+struct SortArgs {
+    const int64_t* topk_idx;
+    int32_t* entry_rows;
+    int32_t* row_entries;     // nullable
+    int32_t* expert_prefix;
+    int32_t* ws;              // [E][S] segment counts, then [E] totals
+    int64_t num_rows;
+    int n, E, S, seg_len, warps;
+    uint32_t* err;
+};
+
+// Segments of a sort of n entries: seg_len entries each (a multiple of 32).
+inline int segment_length(int64_t n) {
+    int64_t len = (n + kMaxSegments - 1) / kMaxSegments;
+    len = (len + 31) / 32 * 32;
+    return (int)(len < kSegment ? kSegment : len);
+}
+
+// Warps a block's count table has room for.
+inline int table_warps(int E, int most) {
+    const int w = kTableInts / E;
+    return w < 1 ? 1 : w < most ? w : most;
+}
+
+// Entry i's expert, or -1 if masked, out of range (flagged) or past the end.
+__device__ __forceinline__ int entry_expert(const SortArgs& a, int i, int end, bool flag) {
+    if (i >= end) return -1;
+    const int64_t e = a.topk_idx[i];
+    if (e >= 0 && e < a.E) return (int)e;
+    if (flag && e != -1) raise_flag(a.err, EP_DEVERR_BAD_EXPERT);
+    return -1;
+}
+
+// One warp: counts its segment's entries per expert into its (zeroed) table.
+__device__ __forceinline__ void count_segment(const SortArgs& a, int seg, int* table, int lane) {
+    const int begin = seg * a.seg_len, end = min(a.n, begin + a.seg_len);
+    for (int i = begin + lane; i < end; i += 32) {
+        const int e = entry_expert(a, i, end, true);
+        if (e >= 0) atomicAdd(&table[e], 1);      // shared memory; a count, so order is immaterial
+    }
+}
+
+// One warp: places its segment's entries; table[e] holds the segment's first row of expert e.
+__device__ __forceinline__ void place_segment(const SortArgs& a, int seg, int* table, int lane) {
+    const int begin = seg * a.seg_len, end = min(a.n, begin + a.seg_len);
+    for (int i0 = begin; i0 < end; i0 += 32) {
+        const int i = i0 + lane;
+        const int e = entry_expert(a, i, end, false);
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
+        int row = -1;
+        if (e >= 0) row = table[e] + __popc(same & lanemask_lt());
+        __syncwarp();
+        if (e >= 0 && (same & lanemask_lt()) == 0) table[e] += __popc(same);
+        __syncwarp();
+        if (i < end) {
+            if (row >= a.num_rows) {
+                raise_flag(a.err, EP_DEVERR_RECV_OVERFLOW);
+                row = -1;
+            }
+            a.entry_rows[i] = row;
+            if (row >= 0 && a.row_entries != nullptr) a.row_entries[row] = i;
+        }
+    }
+}
+
+// Block-wide: v[0..E) counts -> exclusive prefix in place (shared memory); returns the sum.
+// Each thread scans a run of ceil(E / threads) values, then the runs' sums are scanned.
+__device__ __forceinline__ int block_exclusive_scan(int* v, int E) {
+    __shared__ int warp_sums[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+    const int per = (E + blockDim.x - 1) / blockDim.x;
+    const int lo = min(E, (int)threadIdx.x * per), hi = min(E, lo + per);
+    int sum = 0;
+    for (int e = lo; e < hi; ++e) sum += v[e];
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        int s = lane < nwarps ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s += up;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    int run = inc - sum + (warp > 0 ? warp_sums[warp - 1] : 0);
+    for (int e = lo; e < hi; ++e) {
+        const int c = v[e];
+        v[e] = run;
+        run += c;
+    }
+    const int total = warp_sums[nwarps - 1];
+    __syncthreads();
+    return total;
+}
+
+// Every entry in one block: a.warps warps with one segment each.
+__global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(SortArgs a) {
+    extern __shared__ int smem[];
+    int* first = smem;                 // [E]
+    int* tables = smem + a.E;          // [warps][E]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) tables[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    if (warp < a.warps) count_segment(a, warp, tables + warp * a.E, lane);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        int run = 0;
+        for (int w = 0; w < a.warps; ++w) {
+            const int c = tables[w * a.E + e];
+            tables[w * a.E + e] = run;
+            run += c;
+        }
+        first[e] = run;
+    }
+    __syncthreads();
+    const int total = block_exclusive_scan(first, a.E);
+    for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) tables[i] += first[i % a.E];
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.expert_prefix[e] = e < a.E ? first[e] : total;
+    __syncthreads();
+    if (warp < a.warps) place_segment(a, warp, tables + warp * a.E, lane);
+    pdl_trigger();
+}
+
+__global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(SortArgs a) {
+    extern __shared__ int tables[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) tables[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    const int seg0 = blockIdx.x * a.warps;
+    if (warp < a.warps && seg0 + warp < a.S) count_segment(a, seg0 + warp, tables + warp * a.E, lane);
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) {
+        const int e = i / a.warps, w = i - e * a.warps;
+        if (seg0 + w < a.S) a.ws[(int64_t)e * a.S + seg0 + w] = tables[w * a.E + e];
+    }
+    pdl_trigger();
+}
+
+// One warp per expert: its segments' counts -> exclusive prefix in place, and their total.
+__global__ void __launch_bounds__(kSortWarps * 32) sort_scan_kernel(SortArgs a) {
+    const int e = blockIdx.x * kSortWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    pdl_wait();
+    if (e < a.E) {
+        int32_t* v = a.ws + (int64_t)e * a.S;
+        int run = 0;
+        constexpr int B = 8;                     // loads in flight per lane
+        for (int s0 = 0; s0 < a.S; s0 += 32 * B) {
+            int c[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int s = s0 + b * 32 + lane;
+                c[b] = s < a.S ? v[s] : 0;
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                int inc = c[b];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                    if (lane >= o) inc += up;
+                }
+                const int s = s0 + b * 32 + lane;
+                if (s < a.S) v[s] = run + inc - c[b];
+                run += __shfl_sync(0xFFFFFFFFu, inc, 31);
+            }
+        }
+        if (lane == 0) a.ws[(int64_t)a.E * a.S + e] = run;
+    }
+    pdl_trigger();
+}
+
+__global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(SortArgs a) {
+    extern __shared__ int smem[];
+    int* first = smem;                 // [E]
+    int* tables = smem + a.E;          // [warps][E]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    const int seg0 = blockIdx.x * a.warps;
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) first[e] = a.ws[(int64_t)a.E * a.S + e];
+    for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) {
+        const int e = i / a.warps, w = i - e * a.warps;
+        tables[w * a.E + e] = seg0 + w < a.S ? a.ws[(int64_t)e * a.S + seg0 + w] : 0;
+    }
+    __syncthreads();
+    const int total = block_exclusive_scan(first, a.E);
+    for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) tables[i] += first[i % a.E];
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.expert_prefix[e] = e < a.E ? first[e] : total;
+    __syncthreads();
+    if (warp < a.warps && seg0 + warp < a.S) place_segment(a, seg0 + warp, tables + warp * a.E, lane);
+    pdl_trigger();
+}
+
+// ------------------------------------------------------------------ rows
+
+constexpr int kRowWarps = 4;
+
+struct RowArgs {
+    const char* x;
+    const char* x_scales;      // nullable
+    const float* topk_weights; // nullable: 1
+    const int32_t* entry_rows;
+    const char* y;
+    char* out;
+    char* out_scales;
+    const char* dout;
+    char* dy;                  // nullable
+    float* dweights;           // nullable
+    int64_t num_rows;
+    int N, H, k;
+    uint32_t row_bytes, scale_bytes;
+    uint32_t* err;
+};
+
+// Sorted rows (and coefficients, and entry indices) of row t's placed entries, ascending j.
+__device__ __forceinline__ int placed_rows(const RowArgs& a, int64_t t, int lane, int64_t* s_row, float* s_coef,
+                                           int* s_entry) {
+    int64_t row = -1;
+    float w = 1.0f;
+    if (lane < a.k) {
+        row = a.entry_rows[t * a.k + lane];
+        if (a.topk_weights != nullptr) w = a.topk_weights[t * a.k + lane];
+        if (row >= a.num_rows) {
+            raise_flag(a.err, EP_DEVERR_RECV_OVERFLOW);
+            row = -1;
+        }
+    }
+    const unsigned bal = __ballot_sync(0xFFFFFFFFu, row >= 0);
+    if (row >= 0) {
+        const int p = __popc(bal & lanemask_lt());
+        s_row[p] = row;
+        if (s_coef != nullptr) s_coef[p] = w;
+        if (s_entry != nullptr) s_entry[p] = lane;
+    }
+    return __popc(bal);
+}
+
+// The e4m3 row's scales to every destination.
+__device__ __forceinline__ void copy_scales(const RowArgs& a, int64_t t, const int64_t* rows, int nd, int lane) {
+    if (a.x_scales == nullptr) return;
+    const char* src = a.x_scales + t * a.scale_bytes;
+    if ((a.scale_bytes & 3) == 0 && (((uintptr_t)a.x_scales | (uintptr_t)a.out_scales) & 3) == 0) {
+        for (uint32_t i = lane * 4; i < a.scale_bytes; i += 128) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(src + i);
+            for (int p = 0; p < nd; ++p) *reinterpret_cast<uint32_t*>(a.out_scales + rows[p] * a.scale_bytes + i) = v;
+        }
+    } else {
+        for (uint32_t i = lane; i < a.scale_bytes; i += 32) {
+            const char v = src[i];
+            for (int p = 0; p < nd; ++p) a.out_scales[rows[p] * a.scale_bytes + i] = v;
+        }
+    }
+}
+
+// Bulk copies: one load of the row into shared memory, one store per placed entry.
+__global__ void __launch_bounds__(kTmaWarps * 32) sort_rows_tma_kernel(RowArgs a) {
+    extern __shared__ __align__(128) unsigned char rowbuf[];
+    __shared__ int64_t s_row[kTmaWarps][EP_MAX_TOPK];
+    __shared__ __align__(8) uint64_t s_bar[kTmaWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned char* buf = rowbuf + (size_t)warp * a.row_bytes;
+    const int64_t nw = (int64_t)gridDim.x * kTmaWarps;
+    if (lane == 0) mbar_init(&s_bar[warp], 1);
+    __syncwarp();
+    pdl_wait();
+    uint32_t parity = 0;
+    bool live = true;       // lane 0: false once a row load failed to land in time
+    for (int64_t t = (int64_t)blockIdx.x * kTmaWarps + warp; t < a.N; t += nw) {
+        if (lane == 0 && live) tma_row_load(buf, a.x + t * (int64_t)a.row_bytes, a.row_bytes, &s_bar[warp]);
+        const int nd = placed_rows(a, t, lane, s_row[warp], nullptr, nullptr);
+        __syncwarp();
+        copy_scales(a, t, s_row[warp], nd, lane);
+        if (lane == 0 && live)
+            live = tma_row_store(buf, a.out, s_row[warp], nd, a.row_bytes, &s_bar[warp], parity, a.err);
+        __syncwarp();
+    }
+    if (lane == 0) bulk_wait_all();
+    pdl_trigger();
+}
+
+// Rows too wide for the shared-memory buffers: 16-byte vector copies.
+__global__ void __launch_bounds__(kRowWarps * 32) sort_rows_wide_kernel(RowArgs a) {
+    __shared__ int64_t s_row[kRowWarps][EP_MAX_TOPK];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    const int64_t t = (int64_t)blockIdx.x * kRowWarps + warp;
+    if (t < a.N) {
+        const int nd = placed_rows(a, t, lane, s_row[warp], nullptr, nullptr);
+        __syncwarp();
+        copy_scales(a, t, s_row[warp], nd, lane);
+        scatter_copy_row<8>(a.x + t * (int64_t)a.row_bytes, a.out, s_row[warp], nd, a.row_bytes, lane, 32);
+    }
+    pdl_trigger();
+}
+
+// The batch shape (units per lane U, rows P) and the resident blocks follow the row length and
+// the entries per row, as in the expert-major combine (unsort_form).
+template <int U, int P, bool V32, int MIN_BLOCKS = 0>
+__global__ void __launch_bounds__(kRowWarps * 32, MIN_BLOCKS) unsort_kernel(RowArgs a) {
+    __shared__ int64_t s_row[kRowWarps][EP_MAX_TOPK];
+    __shared__ float s_coef[kRowWarps][EP_MAX_TOPK];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    const int64_t t = (int64_t)blockIdx.x * kRowWarps + warp;
+    if (t < a.N) {
+        const int nd = placed_rows(a, t, lane, s_row[warp], s_coef[warp], nullptr);
+        __syncwarp();
+        char* out = a.out + t * (int64_t)a.H * 2;
+        if (V32) gather_reduce_row32<U, P>(a.y, s_row[warp], s_coef[warp], nd, a.H, out, lane, 32);
+        else gather_reduce_row<U, P>(a.y, s_row[warp], s_coef[warp], nd, a.H, out, lane, 32);
+    }
+    pdl_trigger();
+}
+
+using UnsortKernel = void (*)(RowArgs);
+UnsortKernel unsort_form(int H, int k, bool y32) {
+    if (H <= 256) return unsort_kernel<1, 4, false, 10>;
+    if (!y32) return unsort_kernel<4, 4, false>;
+    if (H <= 1024) return unsort_kernel<1, 4, true, 8>;
+    if (k <= 2) return unsort_kernel<2, 2, true, 5>;
+    return unsort_kernel<2, 4, true>;
+}
+
+// One warp per row: its gradient dout[t] is read once per batch of P placed entries (from L1 / L2
+// after the first), each entry's row of y once, each entry's dy written once; the weights'
+// gradients are summed in fp32, per lane over the row's units and then over the lanes by a fixed
+// tree. dy may be y: a lane reads its unit of y before it writes the same unit of dy.
+template <int P>
+__global__ void __launch_bounds__(kRowWarps * 32) unsort_backward_kernel(RowArgs a) {
+    __shared__ int64_t s_row[kRowWarps][EP_MAX_TOPK];
+    __shared__ float s_coef[kRowWarps][EP_MAX_TOPK];
+    __shared__ int s_entry[kRowWarps][EP_MAX_TOPK];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    const int64_t t = (int64_t)blockIdx.x * kRowWarps + warp;
+    if (t < a.N) {
+        const int nd = placed_rows(a, t, lane, s_row[warp], s_coef[warp], s_entry[warp]);
+        __syncwarp();
+        const int64_t row_bytes = (int64_t)a.H * 2;
+        const char* g = a.dout + t * row_bytes;
+        float mine = 0.0f;                       // lane j: the gradient of entry j's weight
+        for (int p0 = 0; p0 < nd; p0 += P) {
+            float acc[P];
+#pragma unroll
+            for (int p = 0; p < P; ++p) acc[p] = 0.0f;
+            for (int u = lane; u < a.H >> 3; u += 32) {
+                const uint4 d4 = *reinterpret_cast<const uint4*>(g + (int64_t)u * 16);
+                const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w};
+                uint4 v[P];
+                if (a.dweights != nullptr) {
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        if (p0 + p < nd) v[p] = *reinterpret_cast<const uint4*>(a.y + s_row[warp][p0 + p] * row_bytes + (int64_t)u * 16);
+                }
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    if (p0 + p >= nd) break;
+                    if (a.dweights != nullptr) {
+                        const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            acc[p] = fmaf(bf16_lo(d[j]), bf16_lo(w[j]), acc[p]);
+                            acc[p] = fmaf(bf16_hi(d[j]), bf16_hi(w[j]), acc[p]);
+                        }
+                    }
+                    if (a.dy != nullptr) {
+                        const float c = s_coef[warp][p0 + p];
+                        const uint4 o = make_uint4(pack_bf16x2(c * bf16_lo(d[0]), c * bf16_hi(d[0])),
+                                                   pack_bf16x2(c * bf16_lo(d[1]), c * bf16_hi(d[1])),
+                                                   pack_bf16x2(c * bf16_lo(d[2]), c * bf16_hi(d[2])),
+                                                   pack_bf16x2(c * bf16_lo(d[3]), c * bf16_hi(d[3])));
+                        st_v4(a.dy + s_row[warp][p0 + p] * row_bytes + (int64_t)u * 16, o);
+                    }
+                }
+            }
+            if (a.dweights != nullptr) {
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    float s = acc[p];
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+                    if (p0 + p < nd && lane == s_entry[warp][p0 + p]) mine = s;
+                }
+            }
+        }
+        if (a.dweights != nullptr && lane < a.k) a.dweights[t * a.k + lane] = mine;
+    }
+    pdl_trigger();
+}
+
+// ------------------------------------------------------------------ host
+
+ep_status check_sort(const ep_shape* sh, const ep_sort* sort, const ep_launch* launch) {
+    ep_status st = check_shape(sh);
+    if (st != EP_OK) return st;
+    if (sh->num_ranks != 1 || sort == nullptr || launch == nullptr || sort->num_rows < 0) return EP_ERR_INVALID_ARG;
+    if ((int64_t)sh->num_tokens * sh->num_topk > (int64_t)1 << 30) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+RowArgs row_args(const ep_shape* sh, const ep_sort* sort, const ep_launch* launch) {
+    RowArgs a{};
+    a.entry_rows = sort->entry_rows;
+    a.num_rows = sort->num_rows;
+    a.N = sh->num_tokens;
+    a.H = sh->hidden;
+    a.k = sh->num_topk;
+    a.row_bytes = (uint32_t)sh->hidden * 2u;
+    a.err = launch->error_flags;
+    return a;
+}
+
+unsigned row_blocks(int N, int warps) { return (unsigned)((N + warps - 1) / warps); }
+
+}  // namespace
+}  // namespace ep
+
+extern "C" {
+
+size_t ep_sort_workspace_size(const ep_shape* sh) {
+    using namespace ep;
+    if (check_shape(sh) != EP_OK || sh->num_ranks != 1) return 0;
+    const int64_t n = (int64_t)sh->num_tokens * sh->num_topk;
+    if (n > (int64_t)1 << 30) return 0;
+    if (n <= kSmallEntries) return 16;
+    const int64_t len = segment_length(n), S = (n + len - 1) / len;
+    return (size_t)(S + 1) * (size_t)sh->num_experts * sizeof(int32_t);
+}
+
+ep_status ep_sort_layout(const ep_shape* sh, const int64_t* topk_idx, const ep_sort* sort, void* workspace,
+                         size_t workspace_bytes, const ep_launch* launch) {
+    using namespace ep;
+    ep_status st = check_sort(sh, sort, launch);
+    if (st != EP_OK) return st;
+    const int n = sh->num_tokens * sh->num_topk;
+    if (sort->expert_prefix == nullptr) return EP_ERR_INVALID_ARG;
+    if (n > 0 && (topk_idx == nullptr || sort->entry_rows == nullptr)) return EP_ERR_INVALID_ARG;
+    const bool small = n <= kSmallEntries;
+    if (!small && (workspace == nullptr || ((uintptr_t)workspace & 15) != 0 ||
+                   workspace_bytes < ep_sort_workspace_size(sh)))
+        return EP_ERR_INVALID_ARG;
+    SortArgs a{};
+    a.topk_idx = topk_idx;
+    a.entry_rows = sort->entry_rows;
+    a.row_entries = sort->row_entries;
+    a.expert_prefix = sort->expert_prefix;
+    a.ws = reinterpret_cast<int32_t*>(workspace);
+    a.num_rows = sort->num_rows;
+    a.n = n;
+    a.E = sh->num_experts;
+    a.err = launch->error_flags;
+    if ((st = begin_call(launch)) != EP_OK) return st;
+    cudaError_t e = cudaSuccess;
+    if (small) {
+        a.warps = table_warps(a.E, kSmallThreads / 32);
+        a.seg_len = ceil_div(ceil_div(n > 0 ? n : 1, a.warps), 32) * 32;
+        a.S = a.warps;
+        const size_t smem = (size_t)(a.warps + 1) * a.E * sizeof(int);
+        e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
+        if (e == cudaSuccess)
+            e = launch_pdl(sort_small_kernel, dim3(1), dim3(kSmallThreads), smem, launch->stream, a);
+    } else {
+        a.warps = table_warps(a.E, kSortWarps);
+        a.seg_len = segment_length(n);
+        a.S = ceil_div(n, a.seg_len);
+        const unsigned blocks = (unsigned)ceil_div(a.S, a.warps);
+        const size_t tables = (size_t)a.warps * a.E * sizeof(int), smem = tables + (size_t)a.E * sizeof(int);
+        e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
+        if (e == cudaSuccess)
+            e = launch_pdl(sort_count_kernel, dim3(blocks), dim3(kSortWarps * 32), tables, launch->stream, a);
+        if (e == cudaSuccess)
+            e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div(a.E, kSortWarps)), dim3(kSortWarps * 32), 0,
+                           launch->stream, a);
+        if (e == cudaSuccess)
+            e = launch_pdl(sort_place_kernel, dim3(blocks), dim3(kSortWarps * 32), smem, launch->stream, a);
+    }
+    if (e != cudaSuccess) return cuda_fail(e);
+    return end_call(launch);
+}
+
+ep_status ep_sort_rows(const ep_shape* sh, const void* x, ep_dtype x_dtype, const void* x_scales,
+                       int32_t scale_format, const ep_sort* sort, void* out_x, void* out_scales,
+                       const ep_launch* launch) {
+    using namespace ep;
+    ep_status st = check_sort(sh, sort, launch);
+    if (st != EP_OK) return st;
+    if (x_dtype != EP_BF16 && x_dtype != EP_FP8_E4M3) return EP_ERR_INVALID_ARG;
+    if (scale_format < EP_FP8_SCALE_FP32 || scale_format > EP_FP8_SCALE_TENSOR) return EP_ERR_INVALID_ARG;
+    const int N = sh->num_tokens;
+    const bool rows = N > 0 && sort->num_rows > 0;
+    if (N > 0 && sort->entry_rows == nullptr) return EP_ERR_INVALID_ARG;
+    if (rows && (x == nullptr || out_x == nullptr)) return EP_ERR_INVALID_ARG;
+    if (rows && (x_scales == nullptr) != (out_scales == nullptr)) return EP_ERR_INVALID_ARG;
+    if (x_dtype == EP_BF16 && (x_scales != nullptr || out_scales != nullptr)) return EP_ERR_INVALID_ARG;
+    if (((uintptr_t)x & 15) != 0 || ((uintptr_t)out_x & 15) != 0) return EP_ERR_INVALID_ARG;
+    if (scale_format != EP_FP8_SCALE_UE8M0 && (((uintptr_t)x_scales | (uintptr_t)out_scales) & 3) != 0)
+        return EP_ERR_INVALID_ARG;
+    RowArgs a = row_args(sh, sort, launch);
+    a.x = reinterpret_cast<const char*>(x);
+    a.x_scales = reinterpret_cast<const char*>(x_scales);
+    a.out = reinterpret_cast<char*>(out_x);
+    a.out_scales = reinterpret_cast<char*>(out_scales);
+    if (x_dtype == EP_FP8_E4M3) a.row_bytes = (uint32_t)sh->hidden;
+    a.scale_bytes = (uint32_t)(sh->hidden / EP_FP8_GROUP) * (scale_format == EP_FP8_SCALE_UE8M0 ? 1u : 4u);
+    if ((st = begin_call(launch)) != EP_OK) return st;
+    if (rows) {
+        const size_t smem = (size_t)kTmaWarps * a.row_bytes;
+        cudaError_t e = cudaSuccess;
+        if (smem <= (size_t)kTmaSmemMax) {
+            e = cudaFuncSetAttribute(sort_rows_tma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTmaSmemMax);
+            if (e == cudaSuccess)
+                e = launch_pdl(sort_rows_tma_kernel, dim3(row_blocks(N, kTmaWarps)), dim3(kTmaWarps * 32), smem,
+                               launch->stream, a);
+        } else {
+            e = launch_pdl(sort_rows_wide_kernel, dim3(row_blocks(N, kRowWarps)), dim3(kRowWarps * 32), 0,
+                           launch->stream, a);
+        }
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return end_call(launch);
+}
+
+ep_status ep_unsort_rows(const ep_shape* sh, const void* y, const float* topk_weights, const ep_sort* sort,
+                         void* out, const ep_launch* launch) {
+    using namespace ep;
+    ep_status st = check_sort(sh, sort, launch);
+    if (st != EP_OK) return st;
+    const int N = sh->num_tokens;
+    if (N > 0 && (sort->entry_rows == nullptr || out == nullptr || (sort->num_rows > 0 && y == nullptr)))
+        return EP_ERR_INVALID_ARG;
+    if (((uintptr_t)y & 15) != 0 || ((uintptr_t)out & 15) != 0) return EP_ERR_INVALID_ARG;
+    RowArgs a = row_args(sh, sort, launch);
+    a.y = reinterpret_cast<const char*>(y);
+    a.out = reinterpret_cast<char*>(out);
+    a.topk_weights = topk_weights;
+    if ((st = begin_call(launch)) != EP_OK) return st;
+    if (N > 0) {
+        cudaError_t e = launch_pdl(unsort_form(a.H, a.k, ((uintptr_t)y & 31) == 0), dim3(row_blocks(N, kRowWarps)),
+                                   dim3(kRowWarps * 32), 0, launch->stream, a);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return end_call(launch);
+}
+
+ep_status ep_unsort_rows_backward(const ep_shape* sh, const void* dout, const void* y, const float* topk_weights,
+                                  const ep_sort* sort, void* dy, float* dweights, const ep_launch* launch) {
+    using namespace ep;
+    ep_status st = check_sort(sh, sort, launch);
+    if (st != EP_OK) return st;
+    const int N = sh->num_tokens;
+    if (dy == nullptr && dweights == nullptr && N > 0 && sort->num_rows > 0) return EP_ERR_INVALID_ARG;
+    if (N > 0 && (sort->entry_rows == nullptr || dout == nullptr)) return EP_ERR_INVALID_ARG;
+    if (N > 0 && sort->num_rows > 0 && dweights != nullptr && y == nullptr) return EP_ERR_INVALID_ARG;
+    if ((((uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy) & 15) != 0) return EP_ERR_INVALID_ARG;
+    RowArgs a = row_args(sh, sort, launch);
+    a.dout = reinterpret_cast<const char*>(dout);
+    a.y = reinterpret_cast<const char*>(y);
+    a.dy = reinterpret_cast<char*>(dy);
+    a.dweights = dweights;
+    a.topk_weights = topk_weights;
+    if ((st = begin_call(launch)) != EP_OK) return st;
+    if (N > 0) {
+        cudaError_t e = launch_pdl(unsort_backward_kernel<4>, dim3(row_blocks(N, kRowWarps)), dim3(kRowWarps * 32), 0,
+                                   launch->stream, a);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return end_call(launch);
+}
+
+}  // extern "C"

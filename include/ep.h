@@ -76,6 +76,7 @@ typedef int32_t ep_status;
 #define EP_DEVERR_RECV_OVERFLOW 2u /* a row fell outside its receive region, skipped */
 #define EP_DEVERR_SLOT_OVERFLOW 4u /* a low-latency slot index reached Nmax, skipped */
 #define EP_DEVERR_TIMEOUT 8u       /* a bounded device wait gave up; the affected rows were skipped */
+#define EP_DEVERR_BAD_ADAPTER 16u  /* an adapter_idx entry outside [-1, L) was treated as -1 */
 
 typedef enum ep_dtype { EP_BF16 = 0, EP_FP8_E4M3 = 1 } ep_dtype;
 typedef enum ep_combine_mode { EP_COMBINE_SUM = 0, EP_COMBINE_WEIGHTED = 1 } ep_combine_mode;
@@ -416,6 +417,146 @@ EP_API ep_status ep_ll_combine(const ep_shape* shape, const void* y, const int64
  * recv_expert_count and layout_range. Optional here (the send phase rewrites every
  * signal), kept for API parity. */
 EP_API ep_status ep_clean_ll_buffer(const ep_shape* shape, ep_ll_buffer* buf, const ep_launch* launch);
+
+/* ---------------------------------------------------------------- expert sort */
+
+/* The pages stop at the received rows; what a rank does with them next -- its experts'
+ * products -- needs each local expert's rows side by side. These calls bring N rows (for
+ * example one destination's recv_x of ep_dispatch, with its recv_topk_idx of local expert
+ * ids) into expert order and back, and give the gradients of both. They take an ep_shape
+ * with num_ranks = 1, num_tokens = N rows, num_experts = E local experts, num_topk = k
+ * entries per row (num_channels only has to be >= 1); entry i = t*k + j is row t's j-th.
+ *
+ * The placement. All dev, caller-owned.
+ *   entry_rows    [N][k] int32: sorted row of each entry, -1 if masked (or skipped)
+ *   row_entries   [num_rows] int32: the entry behind each sorted row (nullable)
+ *   expert_prefix [E + 1] int32: first sorted row of each expert; [E] = rows in all
+ *   num_rows      sorted rows the caller's buffers hold. N*k always suffices. Entries
+ *                 placed beyond it are skipped (EP_DEVERR_RECV_OVERFLOW, entry_rows -1);
+ *                 expert_prefix still holds the full counts.
+ * Sorted rows are ordered by expert, then by entry (stable); repeated experts within a
+ * row take one sorted row per entry. */
+typedef struct ep_sort {
+    int32_t* entry_rows;
+    int32_t* row_entries;
+    int32_t* expert_prefix;
+    int64_t num_rows;
+} ep_sort;
+
+/* Bytes of dev scratch ep_sort_layout needs (0 for a bad shape). */
+EP_API size_t ep_sort_workspace_size(const ep_shape* shape);
+
+/* Fills the placement from topk_idx (dev [N][k] int64, -1 = masked; others outside
+ * [0, E): EP_DEVERR_BAD_EXPERT, treated as masked). workspace: dev, >=
+ * ep_sort_workspace_size bytes, 16-byte aligned, contents need no initialisation. N = 0
+ * writes an all-zero expert_prefix. One kernel for few entries, else three. */
+EP_API ep_status ep_sort_layout(const ep_shape* shape, const int64_t* topk_idx, const ep_sort* sort,
+                                void* workspace, size_t workspace_bytes, const ep_launch* launch);
+
+/* Rows into expert order: out_x[entry_rows[t][j]] = x[t] for every placed entry; rows of
+ * no entry are not written.
+ *   x, out_x  dev [N][H] / [num_rows][H], both bf16 (EP_BF16) or both e4m3
+ *             (EP_FP8_E4M3); 16-byte aligned; they must not overlap
+ *   x_scales, out_scales  dev [N][H/128] / [num_rows][H/128], copied along with e4m3 rows:
+ *             fp32, or uint8 with scale_format EP_FP8_SCALE_UE8M0; both given or both
+ *             NULL; NULL for bf16
+ * The gradient of bf16 rows is ep_unsort_rows with topk_weights NULL. */
+EP_API ep_status ep_sort_rows(const ep_shape* shape, const void* x, ep_dtype x_dtype,
+                              const void* x_scales, int32_t scale_format, const ep_sort* sort,
+                              void* out_x, void* out_scales, const ep_launch* launch);
+
+/* Back into row order: out[t] = sum over placed j (ascending) of c_j * y[entry_rows[t][j]],
+ * c_j = topk_weights[t][j], or 1 with topk_weights NULL; fp32 accumulation, one bf16
+ * store. A row without a placed entry gets +0; rows of y that belong to no entry are not
+ * read.
+ *   y    dev [num_rows][H] bf16, 16-byte aligned
+ *   topk_weights dev [N][k] fp32, nullable
+ *   out  dev [N][H] bf16, 16-byte aligned; must not overlap y */
+EP_API ep_status ep_unsort_rows(const ep_shape* shape, const void* y, const float* topk_weights,
+                                const ep_sort* sort, void* out, const ep_launch* launch);
+
+/* Gradient of ep_unsort_rows: for every placed entry
+ *   dy[entry_rows[t][j]] = c_j * dout[t]        (bf16, one rounding)
+ *   dweights[t][j] = sum over h of dout[t][h] * y[entry_rows[t][j]][h]   (fp32)
+ * and dweights[t][j] = 0 for the others.
+ *   dout dev [N][H] bf16; y, dy dev [num_rows][H] bf16; all 16-byte aligned. dy may be
+ *   NULL (only the weights' gradient) and may be y (in place). dweights dev [N][k] fp32,
+ *   NULL to skip (y is then not read and may be NULL). */
+EP_API ep_status ep_unsort_rows_backward(const ep_shape* shape, const void* dout, const void* y,
+                                         const float* topk_weights, const ep_sort* sort, void* dy,
+                                         float* dweights, const ep_launch* launch);
+
+/* ---------------------------------------------------------------- experts' products */
+
+/* Products of each expert's rows with the expert's matrix, on rows in expert order
+ * (ep_sort_rows, or one destination of ep_dispatch_expert_major).
+ *   num_rows      rows the row buffers hold (>= 0)
+ *   num_experts   E, 1 to EP_MAX_EXPERTS
+ *   in_features, out_features  multiples of 8, 8 to EP_GEMM_MAX_FEATURES
+ * expert_prefix is dev [E + 1] int32, non-decreasing: expert e's rows are
+ * [expert_prefix[e], expert_prefix[e+1]). Values outside [0, num_rows] are clipped and
+ * flagged (EP_DEVERR_RECV_OVERFLOW). Rows of no expert are neither read nor written.
+ * bf16 operands, fp32 accumulation, one bf16 rounding; every pointer 16-byte aligned;
+ * outputs must not overlap inputs. */
+typedef struct ep_gemm_shape {
+    int32_t num_rows;
+    int32_t num_experts;
+    int32_t in_features;
+    int32_t out_features;
+} ep_gemm_shape;
+
+#define EP_GEMM_MAX_FEATURES (1 << 20)
+
+/* y[i] = W_e x[i] for each row i of expert e.
+ *   x dev [num_rows][in_features], w dev [E][out_features][in_features],
+ *   y dev [num_rows][out_features] */
+EP_API ep_status ep_expert_gemm(const ep_gemm_shape* shape, const void* x, const void* w,
+                                const int32_t* expert_prefix, void* y, const ep_launch* launch);
+
+/* Gradient to the rows: dx[i] = W_e^T dy[i]. */
+EP_API ep_status ep_expert_gemm_dgrad(const ep_gemm_shape* shape, const void* dy, const void* w,
+                                      const int32_t* expert_prefix, void* dx,
+                                      const ep_launch* launch);
+
+/* Gradient to the matrices: dw[e] = sum over expert e's rows of dy[i] x[i]^T (all zero for
+ * an expert without rows). dw dev [E][out_features][in_features] */
+EP_API ep_status ep_expert_gemm_wgrad(const ep_gemm_shape* shape, const void* dy, const void* x,
+                                      const int32_t* expert_prefix, void* dw,
+                                      const ep_launch* launch);
+
+/* ---------------------------------------------------------------- adapters */
+
+/* A projection that all rows share with, beside it, a low-rank adapter of each row's own
+ * (requests of many adapters served together):
+ *   y[t] = W x[t] + scales[i] * B_i (A_i x[t]),  i = adapter_idx[t];  y[t] = W x[t] if i = -1
+ *   num_rows      T >= 0
+ *   in_features, out_features  multiples of 8, 8 to EP_GEMM_MAX_FEATURES
+ *   num_adapters  L >= 0
+ *   rank          r, a multiple of 8, 8 to EP_ADAPTER_MAX_RANK (pad with zero rows of A) */
+typedef struct ep_adapter_shape {
+    int32_t num_rows;
+    int32_t in_features;
+    int32_t out_features;
+    int32_t num_adapters;
+    int32_t rank;
+} ep_adapter_shape;
+
+#define EP_ADAPTER_MAX_RANK 256
+
+/* Bytes of dev scratch ep_adapter_gemm needs (0 for a bad shape). */
+EP_API size_t ep_adapter_workspace_size(const ep_adapter_shape* shape);
+
+/*   x dev [T][in_features], w dev [out_features][in_features], a dev [L][r][in_features],
+ *   b dev [L][out_features][r], y dev [T][out_features]: bf16, 16-byte aligned
+ *   scales dev [L] fp32; adapter_idx dev [T] int64 (any order; -1 = none; others outside
+ *   [0, L): EP_DEVERR_BAD_ADAPTER, treated as none). a, b, scales may be NULL with L = 0.
+ *   workspace dev, >= ep_adapter_workspace_size bytes, 16-byte aligned
+ * fp32 accumulation, A_i x[t] is kept in fp32, one bf16 rounding of the sum. Values of one
+ * adapter never reach another adapter's rows. */
+EP_API ep_status ep_adapter_gemm(const ep_adapter_shape* shape, const void* x, const void* w,
+                                 const void* a, const void* b, const float* scales,
+                                 const int64_t* adapter_idx, void* y, void* workspace,
+                                 size_t workspace_bytes, const ep_launch* launch);
 
 /* ---------------------------------------------------------------- helpers */
 
