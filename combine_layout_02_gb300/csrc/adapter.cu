@@ -8,8 +8,6 @@
 namespace ep {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
-
 struct AdapterArgs {
     const __nv_bfloat16 *x, *w, *a, *b;
     const float* scales;
@@ -48,40 +46,53 @@ __global__ void __launch_bounds__(256) adapter_low_simple_kernel(AdapterArgs a) 
     pdl_trigger();
 }
 
-__global__ void __launch_bounds__(256) adapter_gemm_simple_kernel(AdapterArgs a) {
-    __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
-    pdl_wait();
-    const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
-    float acc[4][4] = {};
-    const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4;
-    for (int k0 = 0; k0 < a.K; k0 += kDepth) {
-        for (int q = threadIdx.x; q < kDepth * kTile; q += 256) {
-            const int k = k0 + q / kTile, i = i0 + q % kTile, j = j0 + q % kTile;
-            sa[q / kTile][q % kTile] = k < a.K && i < a.T ? __bfloat162float(a.x[(int64_t)i * a.K + k]) : 0.0f;
-            sb[q / kTile][q % kTile] = k < a.K && j < a.F ? __bfloat162float(a.w[(int64_t)j * a.K + k]) : 0.0f;
+// The epilogue's part: 32 rows (columns of the tile) of one output feature per lane. A row's adapter
+// is the same for the whole warp; B_i's row of the feature is loaded when the adapter changes.
+struct AdapterExtra {
+    const __nv_bfloat16* b;
+    const float* low;
+    const int64_t* idx;
+    int T, F, L, r;
+    __device__ __forceinline__ void operator()(float (&v)[32], const Tile& t, int c, int m, int) const {
+        const int row0 = t.n0 + c;
+        for (int q0 = 0; q0 < r; q0 += 32) {
+            int cur = -1;
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                if (row0 + j >= T) break;
+                const int64_t id = idx[row0 + j];
+                if (id < 0 || id >= L) continue;
+                if (id != cur) {
+                    cur = (int)id;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (m < F && q0 + g * 8 < r)
+                            u = *reinterpret_cast<const uint4*>(b + ((int64_t)cur * F + m) * r + q0 + g * 8);
+                        w[4 * g] = u.x, w[4 * g + 1] = u.y, w[4 * g + 2] = u.z, w[4 * g + 3] = u.w;
+                    }
+                }
+                const float4* l = reinterpret_cast<const float4*>(low + (int64_t)(row0 + j) * r + q0);
+                float acc = v[j];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (q0 + g * 8 >= r) break;
+                    const float4 lo = l[2 * g], hi = l[2 * g + 1];
+                    acc = fmaf(lo.x, bf16_lo(w[4 * g]), acc);
+                    acc = fmaf(lo.y, bf16_hi(w[4 * g]), acc);
+                    acc = fmaf(lo.z, bf16_lo(w[4 * g + 1]), acc);
+                    acc = fmaf(lo.w, bf16_hi(w[4 * g + 1]), acc);
+                    acc = fmaf(hi.x, bf16_lo(w[4 * g + 2]), acc);
+                    acc = fmaf(hi.y, bf16_hi(w[4 * g + 2]), acc);
+                    acc = fmaf(hi.z, bf16_lo(w[4 * g + 3]), acc);
+                    acc = fmaf(hi.w, bf16_hi(w[4 * g + 3]), acc);
+                }
+                v[j] = acc;
+            }
         }
-        __syncthreads();
-        for (int k = 0; k < kDepth; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ti + i], sb[k][tj + j], acc[i][j]);
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i) {
-        const int t = i0 + ti + i;
-        if (t >= a.T) break;
-        const int id = adapter_of(a, t, false);
-        for (int j = 0; j < 4; ++j) {
-            const int f = j0 + tj + j;
-            if (f >= a.F) break;
-            float v = acc[i][j];
-            if (id >= 0)
-                for (int q = 0; q < a.r; ++q)
-                    v = fmaf(a.low[(int64_t)t * a.r + q], __bfloat162float(a.b[((int64_t)id * a.F + f) * a.r + q]), v);
-            a.y[(int64_t)t * a.F + f] = __float2bfloat16_rn(v);
-        }
-    }
-    pdl_trigger();
-}
+};
 
 ep_status check_adapter(const ep_adapter_shape* sh) {
     if (sh == nullptr) return EP_ERR_INVALID_ARG;
@@ -118,6 +129,22 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
     if ((((uintptr_t)x | (uintptr_t)w | (uintptr_t)a | (uintptr_t)b | (uintptr_t)y | (uintptr_t)workspace) & 15) != 0)
         return EP_ERR_INVALID_ARG;
     if (((uintptr_t)scales & 3) != 0 || ((uintptr_t)adapter_idx & 7) != 0) return EP_ERR_INVALID_ARG;
+    GemmArgs m{};
+    GemmMaps maps{};
+    if (rows) {
+        m.out = reinterpret_cast<__nv_bfloat16*>(y);
+        m.num_rows = sh->num_rows;
+        m.E = 1;
+        m.M = sh->out_features;
+        m.N = m.C = sh->in_features;
+        m.err = launch->error_flags;
+        gemm_tiles(&m, false);
+        const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, T = (uint64_t)sh->num_rows;
+        const uint64_t da[3] = {K, F, 1}, db[2] = {K, T};
+        const uint32_t ba[3] = {64, (uint32_t)kBM, 1}, bb[2] = {64, (uint32_t)m.box};
+        if ((st = encode_map(&maps.a, w, 3, da, ba)) != EP_OK) return st;
+        if ((st = encode_map(&maps.b, x, 2, db, bb)) != EP_OK) return st;
+    }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
         AdapterArgs g{reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(w),
@@ -128,8 +155,11 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         cudaError_t e = launch_pdl(adapter_low_simple_kernel, dim3((unsigned)((items + 7) / 8)), dim3(256), 0,
                                    launch->stream, g);
         if (e == cudaSuccess)
-            e = launch_pdl(adapter_gemm_simple_kernel, dim3((unsigned)ceil_div(g.F, kTile), (unsigned)ceil_div(g.T, kTile)),
-                           dim3(256), 0, launch->stream, g);
+            e = cudaFuncSetAttribute(gemm_kernel<kForward, AdapterExtra>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kGemmSmemMax);
+        if (e == cudaSuccess)
+            e = launch_pdl(gemm_kernel<kForward, AdapterExtra>, dim3(gemm_blocks(m, false)), dim3(kGemmThreads),
+                           gemm_smem(m), launch->stream, maps, m, AdapterExtra{g.b, g.low, g.idx, g.T, g.F, g.L, g.r});
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return end_call(launch);

@@ -2,95 +2,53 @@
 //   forward  y[i]  = W_e x[i]            rows i of expert e
 //   dgrad    dx[i] = W_e^T dy[i]
 //   wgrad    dW_e  = sum_i dy[i] x[i]^T
-#include "ep_internal.cuh"
+// All three are gemm_kernel (gemm.cuh) with other operands:
+//            M side (K-major / MN-major)     N side                       contracted
+//   forward  W_e, out_features, K-major      x, rows, K-major             in_features
+//   dgrad    W_e, in_features, MN-major      dy, rows, K-major            out_features
+//   wgrad    dy, out_features, MN-major      x, in_features, MN-major     the expert's rows
 #include "gemm.cuh"
 
 namespace ep {
+
 namespace {
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// C[i][j] = sum_k A(i, k) B(k, j) in 64 x 64 tiles, 4 x 4 values a thread, fp32.
-constexpr int kTile = 64, kDepth = 16;
-
-enum Direction { kForward, kDgrad, kWgrad };
-
-struct GemmArgs {
-    const __nv_bfloat16* rows_a;    // x, dy, dy
-    const __nv_bfloat16* other;     // w, w, x
-    __nv_bfloat16* out;
-    const int32_t* prefix;
-    int num_rows, E, K, F;
-    uint32_t* err;
-};
-
-template <Direction D>
-__global__ void __launch_bounds__(256) expert_gemm_simple_kernel(GemmArgs a) {
-    __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
-    __shared__ int s_e, s_begin, s_end;
-    pdl_wait();
-    if (threadIdx.x == 0) {
-        int tile = blockIdx.y;
-        s_e = -1;
-        if (D == kWgrad) {
-            const int per = (a.F + kTile - 1) / kTile;
-            s_e = tile / per;
-            s_begin = expert_begin(a.prefix, s_e, a.num_rows);
-            s_end = expert_end(a.prefix, s_e, a.num_rows);
-        } else {
-            for (int e = 0; e < a.E; ++e) {
-                const int b = expert_begin(a.prefix, e, a.num_rows), n = expert_end(a.prefix, e, a.num_rows) - b;
-                const int tiles = n > 0 ? (n + kTile - 1) / kTile : 0;
-                if (tile < tiles) {
-                    s_e = e;
-                    s_begin = b + tile * kTile;
-                    s_end = b + n;
-                    break;
-                }
-                tile -= tiles;
-            }
-        }
-    }
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_prefix(a.prefix, a.E, a.num_rows, a.err);
-    __syncthreads();
-    if (s_e < 0) return;
-    const int e = s_e;
-    const int ni = D == kWgrad ? a.F : s_end - s_begin;                  // rows of C in this group
-    const int nj = D == kForward ? a.F : a.K;
-    const int nk = D == kForward ? a.K : D == kDgrad ? a.F : max(0, s_end - s_begin);
-    const int i0 = D == kWgrad ? (blockIdx.y % ((a.F + kTile - 1) / kTile)) * kTile : 0;
-    const int j0 = blockIdx.x * kTile;
-    const __nv_bfloat16* w = a.other + (int64_t)e * a.F * a.K;
-    float acc[4][4] = {};
-    const int ti = threadIdx.x / 16 * 4, tj = threadIdx.x % 16 * 4;
-    for (int k0 = 0; k0 < nk; k0 += kDepth) {
-        for (int q = threadIdx.x; q < kDepth * kTile; q += 256) {
-            const int k = k0 + q / kTile, i = i0 + q % kTile, j = j0 + q % kTile;
-            float va = 0.0f, vb = 0.0f;
-            if (k < nk && i < ni) {
-                if (D == kForward) va = __bfloat162float(a.rows_a[(int64_t)(s_begin + i) * a.K + k]);
-                if (D == kDgrad) va = __bfloat162float(a.rows_a[(int64_t)(s_begin + i) * a.F + k]);
-                if (D == kWgrad) va = __bfloat162float(a.rows_a[(int64_t)(s_begin + k) * a.F + i]);
-            }
-            if (k < nk && j < nj) {
-                if (D == kForward) vb = __bfloat162float(w[(int64_t)j * a.K + k]);
-                if (D == kDgrad) vb = __bfloat162float(w[(int64_t)k * a.K + j]);
-                if (D == kWgrad) vb = __bfloat162float(a.other[(int64_t)(s_begin + k) * a.K + j]);
-            }
-            sa[q / kTile][q % kTile] = va;
-            sb[q / kTile][q % kTile] = vb;
-        }
-        __syncthreads();
-        for (int k = 0; k < kDepth; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ti + i], sb[k][tj + j], acc[i][j]);
-        __syncthreads();
-    }
-    __nv_bfloat16* out = D == kWgrad ? a.out + (int64_t)e * a.F * a.K : a.out + (int64_t)s_begin * nj;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j)
-            if (i0 + ti + i < ni && j0 + tj + j < nj)
-                out[(int64_t)(i0 + ti + i) * nj + j0 + tj + j] = __float2bfloat16_rn(acc[i][j]);
-    pdl_trigger();
+// The driver's encoder, looked up once (the library does not link the driver library).
+EncodeFn encoder() {
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
 }
+}  // namespace
+
+ep_status encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint32_t* box) {
+    const EncodeFn fn = encoder();
+    if (fn == nullptr) return cuda_fail(cudaErrorNotSupported);
+    cuuint64_t d[3], strides[2];
+    cuuint32_t b[3], ones[3] = {1, 1, 1};
+    uint64_t stride = 2;
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        stride *= dims[i];
+        if (i + 1 < rank) strides[i] = stride;
+    }
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, strides, b,
+                          ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? EP_OK : EP_ERR_UNSUPPORTED;
+}
+
+namespace {
 
 ep_status check_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* other, bool other_rows,
                      const int32_t* prefix, const void* out, bool out_rows, const ep_launch* launch) {
@@ -114,16 +72,44 @@ ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* othe
                    const ep_launch* launch) {
     ep_status st = check_gemm(sh, rows_a, other, D == kWgrad, prefix, out, D != kWgrad, launch);
     if (st != EP_OK) return st;
+    const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, E = (uint64_t)sh->num_experts,
+                   rows = (uint64_t)sh->num_rows;
+    if (D == kWgrad && rows == 0) {
+        if ((st = begin_call(launch)) != EP_OK) return st;
+        cudaError_t e = cudaMemsetAsync(out, 0, E * F * K * 2, launch->stream);
+        if (e != cudaSuccess) return cuda_fail(e);
+        return end_call(launch);
+    }
+    GemmArgs a{};
+    a.prefix = prefix;
+    a.out = reinterpret_cast<__nv_bfloat16*>(out);
+    a.num_rows = sh->num_rows;
+    a.E = sh->num_experts;
+    a.M = D == kDgrad ? sh->in_features : sh->out_features;
+    a.N = sh->in_features;
+    a.C = D == kForward ? sh->in_features : sh->out_features;
+    a.err = launch->error_flags;
+    gemm_tiles(&a, D == kWgrad);
+    GemmMaps maps{};
+    if (rows > 0) {
+        if (D == kWgrad) {
+            const uint64_t da[2] = {F, rows}, db[2] = {K, rows};
+            const uint32_t box[2] = {64, 64};
+            if ((st = encode_map(&maps.a, rows_a, 2, da, box)) != EP_OK) return st;
+            if ((st = encode_map(&maps.b, other, 2, db, box)) != EP_OK) return st;
+        } else {
+            const uint64_t da[3] = {K, F, E}, db[2] = {(uint64_t)a.C, rows};
+            const uint32_t ba[3] = {64, D == kForward ? (uint32_t)kBM : 64u, 1}, bb[2] = {64, (uint32_t)a.box};
+            if ((st = encode_map(&maps.a, other, 3, da, ba)) != EP_OK) return st;
+            if ((st = encode_map(&maps.b, rows_a, 2, db, bb)) != EP_OK) return st;
+        }
+    }
     if ((st = begin_call(launch)) != EP_OK) return st;
-    GemmArgs a{reinterpret_cast<const __nv_bfloat16*>(rows_a), reinterpret_cast<const __nv_bfloat16*>(other),
-               reinterpret_cast<__nv_bfloat16*>(out), prefix, sh->num_rows, sh->num_experts, sh->in_features,
-               sh->out_features, launch->error_flags};
-    if (sh->num_rows > 0 || D == kWgrad) {
-        const int nj = D == kForward ? a.F : a.K;
-        const unsigned gy = D == kWgrad ? (unsigned)(a.E * ceil_div(a.F, kTile))
-                                        : (unsigned)(a.num_rows / kTile + (a.E < a.num_rows ? a.E : a.num_rows));
-        cudaError_t e = launch_pdl(expert_gemm_simple_kernel<D>, dim3((unsigned)ceil_div(nj, kTile), gy), dim3(256), 0,
-                                   launch->stream, a);
+    if (rows > 0) {
+        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<D, NoExtra>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemMax);
+        if (e == cudaSuccess)
+            e = launch_pdl(gemm_kernel<D, NoExtra>, dim3(gemm_blocks(a, D == kWgrad)), dim3(kGemmThreads), gemm_smem(a),
+                           launch->stream, maps, a, NoExtra{});
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return end_call(launch);

@@ -1,28 +1,463 @@
-// gemm.cuh -- what the experts' products and the adapters' projection share.
+// gemm.cuh -- the tensor-core product behind the experts' products and the adapters' projection.
 #pragma once
+
+#include <cuda.h>
 
 #include "ep_internal.cuh"
 
 namespace ep {
 
+enum Direction { kForward, kDgrad, kWgrad };
+
+struct GemmArgs {
+    const int32_t* prefix;     // [E + 1]; NULL: one group of all rows
+    __nv_bfloat16* out;
+    int num_rows, E;
+    int M;                     // forward: out_features, dgrad: in_features, wgrad: out_features
+    int N;                     // wgrad: in_features (forward / dgrad: the rows)
+    int C;                     // contracted features (wgrad: the rows)
+    int bn, box, stages;       // columns of the widest tile, rows of one load box of B, stages
+    uint32_t* err;
+};
+
+struct GemmMaps {
+    CUtensorMap a, b;
+};
+
 inline bool features_ok(int f) { return f >= 8 && f % 8 == 0; }
 
+// Encodes a tiled bf16 map of up to three dimensions (innermost first), 128-byte swizzle.
+ep_status encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint32_t* box);
+
+// ------------------------------------------------------------------ expert rows
+
 // Rows of expert e, clipped to the row buffers; end <= begin where there are none.
-__device__ __forceinline__ int expert_begin(const int32_t* prefix, int e, int num_rows) {
-    return min(max(prefix[e], 0), num_rows);
+__device__ __forceinline__ int expert_begin(const GemmArgs& a, int e) {
+    return a.prefix == nullptr ? 0 : min(max(a.prefix[e], 0), a.num_rows);
 }
-__device__ __forceinline__ int expert_end(const int32_t* prefix, int e, int num_rows) {
-    return min(max(prefix[e + 1], 0), num_rows);
+__device__ __forceinline__ int expert_end(const GemmArgs& a, int e) {
+    return a.prefix == nullptr ? a.num_rows : min(max(a.prefix[e + 1], 0), a.num_rows);
 }
 
-// Flags a prefix that leaves [0, num_rows] or decreases. One block calls it.
-__device__ __forceinline__ void check_prefix(const int32_t* prefix, int E, int num_rows, uint32_t* err) {
+// One warp: flags a prefix that leaves [0, num_rows] or decreases.
+__device__ __forceinline__ void check_prefix(const GemmArgs& a, int lane) {
+    if (a.prefix == nullptr) return;
     bool bad = false;
-    for (int e = threadIdx.x; e <= E; e += blockDim.x) {
-        const int v = prefix[e];
-        bad |= v < 0 || v > num_rows || (e < E && prefix[e + 1] < v);
+    for (int e = lane; e <= a.E; e += 32) {
+        const int v = a.prefix[e];
+        bad |= v < 0 || v > a.num_rows || (e < a.E && a.prefix[e + 1] < v);
     }
-    if (bad) raise_flag(err, EP_DEVERR_RECV_OVERFLOW);
+    if (bad) raise_flag(a.err, EP_DEVERR_RECV_OVERFLOW);
 }
+
+// ------------------------------------------------------------------ tensor memory, barriers
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+}
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// 32 consecutive columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+constexpr uint64_t kGemmWaitNs = 2000000000ull;   // bound on one barrier wait: 2 s
+
+// Waits for a phase. Gives up when another role has (*dead), or after kGemmWaitNs (then flags
+// EP_DEVERR_TIMEOUT and sets *dead): every role then leaves its loop.
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* err) {
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try(bar, parity)) return true;
+        if (*dead) return false;
+        if (global_ns() - t0 > kGemmWaitNs) {
+            raise_flag(err, EP_DEVERR_TIMEOUT);
+            *dead = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* err) {
+    if (mbar_try(bar, parity)) return true;
+    return mbar_wait_slow(bar, parity, dead, err);
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle (rows of 128 bytes, 8 rows a pattern).
+//   K-major:  rows are M / N indices, 64 contracted values a row; 8-row groups 1024 bytes apart
+//   MN-major: rows are contracted indices, 64 M / N values a row; 8-row groups 1024 bytes apart,
+//             the next 64 M / N values kMnChunk bytes on
+constexpr uint32_t kMnChunk = 64 * 128;
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn_major) {
+    const uint64_t lbo = mn_major ? kMnChunk >> 4 : 1, sbo = 1024 >> 4;
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (lbo << 16) | (sbo << 32) | (1ull << 46) | (2ull << 61);
+}
+// bf16 x bf16 -> fp32, M x n.
+__device__ __forceinline__ uint32_t instr_desc(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ tiles
+
+constexpr int kBM = 128, kBK = 64;
+constexpr uint32_t kABytes = kBM * kBK * 2;
+constexpr int kMaxStages = 8;
+constexpr int kGemmThreads = 256;
+
+struct Tile {
+    int e, m0, n0, n;          // expert, first M index, first column (row index or N index), columns
+    int begin, end;            // the expert's rows
+};
+
+// Walks the tiles of all experts in order: expert by expert, M tiles innermost.
+//   forward / dgrad: an expert's rows are cut into ceil(rows / bn) nearly even column tiles
+//   wgrad:           N is cut into tiles of bn
+template <Direction D>
+struct TileWalk {
+    const GemmArgs& a;
+    int e = -1, first = 0, count = 0, begin = 0, end = 0, mt, per = 0, nt = 0;
+    __device__ TileWalk(const GemmArgs& args) : a(args), mt((args.M + kBM - 1) / kBM) {}
+    // Tile number t (non-decreasing from call to call); false past the last one.
+    __device__ bool at(int t, Tile& out) {
+        while (t >= first + count) {
+            if (++e >= a.E) return false;
+            first += count;
+            begin = expert_begin(a, e);
+            end = expert_end(a, e);
+            const int rows = max(0, end - begin);
+            if (D == kWgrad) {
+                per = a.bn;
+                nt = (a.N + a.bn - 1) / a.bn;
+            } else {
+                nt = (rows + a.bn - 1) / a.bn;
+                per = nt > 0 ? ((rows + nt - 1) / nt + 15) & ~15 : 16;
+                if (nt > 0) nt = (rows + per - 1) / per;
+            }
+            count = nt * mt;
+        }
+        const int q = t - first, c = q / mt;
+        out.e = e;
+        out.m0 = (q - c * mt) * kBM;
+        out.begin = begin;
+        out.end = end;
+        if (D == kWgrad) {
+            out.n0 = c * per;
+            out.n = (min(per, a.N - out.n0) + 15) & ~15;
+        } else {
+            out.n0 = begin + c * per;
+            out.n = (min(per, end - out.n0) + 15) & ~15;
+        }
+        return true;
+    }
+};
+
+// Epilogue of one tile chunk of 32 columns: forward / dgrad. A lane holds one feature of 32 rows;
+// lanes exchange in pairs, so that a store covers 32 features of two rows (64 bytes each).
+__device__ __forceinline__ void store_features(const float (&v)[32], __nv_bfloat16* out, int ld, int64_t row0, int rows,
+                                               int feature, int M, int lane) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        if (j >= rows) break;
+        const bool odd = lane & 1;
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
+        const uint32_t p = odd ? pack_bf16x2(other, v[j + 1]) : pack_bf16x2(v[j], other);
+        const int jj = odd ? j + 1 : j;
+        if (jj < rows && feature < M)
+            *reinterpret_cast<uint32_t*>(out + (row0 + jj) * ld + (feature & ~1)) = p;
+    }
+}
+
+// wgrad: a lane holds 32 consecutive columns of one row of dW.
+__device__ __forceinline__ void store_columns(const float (&v)[32], __nv_bfloat16* out, int cols) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+        if (j < cols)
+            st_v4(out + j, make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
+                                      pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7])));
+    }
+}
+
+struct NoExtra {
+    __device__ __forceinline__ void operator()(float (&)[32], const Tile&, int, int, int) const {}
+};
+
+// D[m][n] over tiles of 128 x up to 256, one CTA per SM walking over tiles. The weights are the M side
+// and the rows the N side, so that a tile has as many columns (a multiple of 16) as its expert has
+// rows left: no padding of the experts. Warp 0 loads (TMA), warp 1 multiplies (tcgen05.mma, fp32
+// sums in tensor memory, two accumulators of 256 columns in turn), warp 2 clears the rows of a
+// wgrad tail that belong to the next expert, warps 4 to 7 write the previous tile meanwhile.
+template <Direction D, class Extra>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int dead;
+    constexpr bool kAMn = D != kForward, kBMn = D == kWgrad;
+    unsigned char* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const uint32_t stage_bytes = kABytes + (uint32_t)a.bn * 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&maps.a);
+        tma_prefetch_map(&maps.b);
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], D == kWgrad ? 2 : 1);     // the product, and the warp that clears tails
+            mbar_init(&tail[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);
+        }
+        mbar_init(&drain, 1);
+        dead = 0;
+    }
+    if (warp == 1) tmem_alloc(&s_tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_wait();
+
+    if (warp == 0 && lane == 0) {
+        TileWalk<D> walk(a);
+        Tile t;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; ok && walk.at(i, t); i += gridDim.x) {
+            const int depth = D == kWgrad ? t.end - t.begin : a.C;
+            const int boxes = kBMn ? (t.n + 63) / 64 : (t.n + a.box - 1) / a.box;
+            const uint32_t bytes = kABytes + (uint32_t)boxes * (kBMn ? 64 : a.box) * 128;
+            for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
+                const uint32_t s = it % a.stages;
+                if (!mbar_wait(&empty[s], ((it / a.stages) & 1) ^ 1, &dead, a.err)) {
+                    ok = false;
+                    break;
+                }
+                unsigned char* sa = smem + s * stage_bytes;
+                unsigned char* sb = sa + kABytes;
+                mbar_expect_bytes(&full[s], bytes);
+                if (D == kForward) {
+                    tma_load_3d(sa, &maps.a, k0, t.m0, t.e, &full[s]);
+                } else if (D == kDgrad) {
+                    tma_load_3d(sa, &maps.a, t.m0, k0, t.e, &full[s]);
+                    tma_load_3d(sa + kMnChunk, &maps.a, t.m0 + 64, k0, t.e, &full[s]);
+                } else {
+                    tma_load_2d(sa, &maps.a, t.m0, t.begin + k0, &full[s]);
+                    tma_load_2d(sa + kMnChunk, &maps.a, t.m0 + 64, t.begin + k0, &full[s]);
+                }
+                for (int b = 0; b < boxes; ++b) {
+                    if (kBMn) tma_load_2d(sb + b * kMnChunk, &maps.b, t.n0 + b * 64, t.begin + k0, &full[s]);
+                    else tma_load_2d(sb + b * a.box * 128, &maps.b, k0, t.n0 + b * a.box, &full[s]);
+                }
+            }
+        }
+        if (!ok) {     // wait, with a limit, for the copies still in flight
+            for (uint32_t q = it > (uint32_t)a.stages ? it - a.stages : 0; q < it; ++q)
+                mbar_wait_bounded(&full[q % a.stages], (q / a.stages) & 1, kGemmWaitNs / 8);
+        }
+    } else if (warp == 1 && lane == 0) {
+        TileWalk<D> walk(a);
+        Tile t;
+        uint32_t it = 0, used = 0, tails = 0;      // tails: a phase bit per stage
+        bool ok = true;
+        for (int i = blockIdx.x; ok && walk.at(i, t); i += gridDim.x) {
+            const int depth = D == kWgrad ? t.end - t.begin : a.C;
+            if (depth <= 0) continue;
+            const uint32_t acc = used & 1;
+            if (!(ok = mbar_wait(&acc_empty[acc], ((used >> 1) & 1) ^ 1, &dead, a.err))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + acc * 256, idesc = instr_desc(kBM, t.n, kAMn, kBMn);
+            for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
+                const uint32_t s = it % a.stages;
+                if (!(ok = mbar_wait(&full[s], (it / a.stages) & 1, &dead, a.err))) break;
+                const int left = depth - k0;
+                if (D == kWgrad && left < kBK && (left & 15) != 0) {
+                    if (!(ok = mbar_wait(&tail[s], (tails >> s) & 1, &dead, a.err))) break;
+                    tails ^= 1u << s;
+                }
+                tc_fence_after();
+                const uint32_t sa = smem_addr(smem + s * stage_bytes), sb = sa + kABytes;
+                const uint64_t da = smem_desc(sa, kAMn), db = smem_desc(sb, kBMn);
+#pragma unroll
+                for (int k = 0; k < kBK; k += 16) {
+                    if (k >= left) break;      // 16 contracted values: 32 bytes of a row, or 16 rows
+                    tc_mma(d, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, (k0 | k) != 0);
+                }
+                tc_commit(&empty[s]);
+            }
+            tc_commit(&acc_full[acc]);
+            ++used;
+        }
+        if (!ok) {
+            tc_commit(&drain);
+            mbar_wait_bounded(&drain, 0, kGemmWaitNs / 8);
+        }
+    } else if (D == kWgrad && warp == 2) {
+        // The last load of an expert's rows may hold rows of the next expert (whose values may be
+        // infinite): those up to the next multiple of 16 take part in a product, so both operands'
+        // are cleared. A row is a 128-byte line of each 64-column chunk, whatever the swizzle.
+        TileWalk<D> walk(a);
+        Tile t;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; ok && walk.at(i, t); i += gridDim.x) {
+            const int depth = t.end - t.begin;
+            for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
+                const uint32_t s = it % a.stages;
+                if (!(ok = mbar_wait(&full[s], (it / a.stages) & 1, &dead, a.err))) break;
+                const int left = depth - k0;
+                if (left < kBK && (left & 15) != 0) {
+                    const int rows = 16 - (left & 15), chunks = 2 + (t.n + 63) / 64;
+                    for (int p = lane; p < chunks * rows * 8; p += 32) {
+                        const int c = p / (rows * 8), r = (p / 8) % rows;
+                        *reinterpret_cast<uint4*>(smem + s * stage_bytes + c * kMnChunk + (left + r) * 128 + (p & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tail[s]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
+            }
+        }
+    } else if (warp == 3) {
+        if (blockIdx.x == 0) check_prefix(a, lane);
+    } else if (warp >= 4) {
+        TileWalk<D> walk(a);
+        Tile t;
+        uint32_t used = 0;
+        const int quarter = warp & 3;
+        for (int i = blockIdx.x; walk.at(i, t); i += gridDim.x) {
+            const bool some = D != kWgrad || t.end > t.begin;
+            const uint32_t acc = used & 1;
+            if (some) {
+                if (!mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err)) break;
+                tc_fence_after();
+            }
+            const int m = t.m0 + quarter * 32 + lane;
+            for (int c = 0; c < t.n; c += 32) {
+                float v[32];
+                if (some) {
+                    tmem_load32(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                }
+                if (D == kWgrad) {
+                    if (m < a.M)
+                        store_columns(v, a.out + ((int64_t)t.e * a.M + m) * a.N + t.n0 + c, a.N - t.n0 - c);
+                } else {
+                    extra(v, t, c, m, lane);
+                    store_features(v, a.out, a.M, t.n0 + c, t.end - t.n0 - c < t.n - c ? t.end - t.n0 - c : t.n - c, m, a.M, lane);
+                }
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[acc]);
+                ++used;
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_free(tmem, 512);
+    pdl_trigger();
+}
+
+// ------------------------------------------------------------------ host
+
+// Column tile width and stages. wgrad: 256. Else twice the average rows of an expert, so that most
+// experts are one tile, within [32, 256].
+inline void gemm_tiles(GemmArgs* a, bool wgrad) {
+    int bn = 256;
+    if (!wgrad) {
+        const int64_t want = 2 * (int64_t)((a->num_rows + a->E - 1) / a->E);
+        for (bn = 32; bn < 256 && bn < want; bn *= 2) {}
+    }
+    a->bn = bn;
+    a->box = bn < 64 ? bn : 64;
+    const int stage = (int)kABytes + bn * 128;
+    a->stages = 200 * 1024 / stage < kMaxStages ? 200 * 1024 / stage : kMaxStages;
+}
+
+// One CTA per SM, at most as many as there can be tiles.
+inline unsigned gemm_blocks(const GemmArgs& a, bool wgrad) {
+    const int64_t mt = ceil_div(a.M, kBM);
+    const int64_t nt = wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn)
+                             : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows);
+    const int64_t sms = sm_count();
+    return (unsigned)(mt * nt < sms ? mt * nt : sms);
+}
+
+inline size_t gemm_smem(const GemmArgs& a) { return (size_t)a.stages * (kABytes + a.bn * 128) + 1024; }
+constexpr int kGemmSmemMax = 200 * 1024 + 1024;
 
 }  // namespace ep
