@@ -25,25 +25,107 @@ __device__ __forceinline__ int adapter_of(const AdapterArgs& a, int t, bool flag
     return -1;
 }
 
-// One warp per (row, rank).
-__global__ void __launch_bounds__(256) adapter_low_simple_kernel(AdapterArgs a) {
-    const int lane = threadIdx.x & 31;
+// One 16 x 8 product of 16 contracted bf16 values, fp32 sums.
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+constexpr int kLowRows = 32, kLowWarps = 8;
+
+// low[t][q] = scales[i] * sum_k x[t][k] A_i[q][k] for 32 rows and the d-th of their distinct adapters,
+// d = blockIdx.y, + gridDim.y, ...; NT * 8 ranks at a time. The warps share the contraction and
+// join in shared memory in warp order. Operands come straight from memory: a lane of quad position
+// c loads the 8 values c*8 .. c*8+7 of a 32-deep step with one 16-byte load, for a row of x and for a
+// rank of A alike; which of them a product calls its k-th is immaterial as long as both agree, so
+// the lane's first four words feed two products. Rows of other adapters are not read (zero), and
+// each row is written by its own adapter's block alone.
+template <int NT>
+__global__ void __launch_bounds__(kLowWarps * 32) adapter_low_kernel(AdapterArgs a) {
+    extern __shared__ float parts[];                    // [warps][32][NT * 8]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();
-    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (item < (int64_t)a.T * a.r) {
-        const int t = (int)(item / a.r), q = (int)(item % a.r);
-        const int i = adapter_of(a, t, lane == 0 && q == 0);
-        float acc = 0.0f;
-        if (i >= 0) {
-            const __nv_bfloat16* row = a.a + ((int64_t)i * a.r + q) * a.K;
-            for (int k = lane; k < a.K; k += 32)
-                acc = fmaf(__bfloat162float(a.x[(int64_t)t * a.K + k]), __bfloat162float(row[k]), acc);
-            for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
-            acc *= a.scales[i];
+    pdl_trigger();       // the projection may start; it reads low after this kernel's end only
+    const int64_t t0 = (int64_t)blockIdx.x * kLowRows;
+    int id = -1;
+    if (t0 + lane < a.T) id = adapter_of(a, (int)(t0 + lane), warp == 0 && blockIdx.y == 0);
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+    unsigned firsts = __ballot_sync(0xFFFFFFFFu, id >= 0 && (same & lanemask_lt()) == 0);
+    const int steps = (a.K + 31) / 32;
+    const int s0 = (int)((int64_t)steps * warp / kLowWarps), s1 = (int)((int64_t)steps * (warp + 1) / kLowWarps);
+    for (int d = 0; firsts != 0; ++d, firsts &= firsts - 1) {
+        if (d % gridDim.y != blockIdx.y) continue;
+        const int i = __shfl_sync(0xFFFFFFFFu, id, __ffs(firsts) - 1);
+        const unsigned mine = __ballot_sync(0xFFFFFFFFu, id == i);
+        for (int q0 = 0; q0 < a.r; q0 += NT * 8) {
+            float acc[2][NT][4] = {};
+            const __nv_bfloat16* xr[4];
+            bool take[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                take[h] = (mine >> (h * 8 + g)) & 1;
+                xr[h] = a.x + (t0 + h * 8 + g) * a.K;
+            }
+            const __nv_bfloat16* ar = a.a + ((int64_t)i * a.r + q0 + g) * a.K;
+            const int ranks = a.r - q0;
+#pragma unroll 2
+            for (int s = s0; s < s1; ++s) {
+                const int k = s * 32 + c * 8;
+                const bool in = k < a.K;
+                uint4 xv[4], av[NT];
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    xv[h] = in && take[h] ? *reinterpret_cast<const uint4*>(xr[h] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    av[n] = in && n * 8 < ranks ? ld_stream_v4(ar + (int64_t)n * 8 * a.K + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mma_16816(acc[h][n], xv[2 * h].x, xv[2 * h + 1].x, xv[2 * h].y, xv[2 * h + 1].y, av[n].x, av[n].y);
+                        mma_16816(acc[h][n], xv[2 * h].z, xv[2 * h + 1].z, xv[2 * h].w, xv[2 * h + 1].w, av[n].z, av[n].w);
+                    }
+            }
+            float* part = parts + warp * kLowRows * NT * 8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    *reinterpret_cast<float2*>(part + (h * 16 + g) * NT * 8 + n * 8 + c * 2) = make_float2(acc[h][n][0], acc[h][n][1]);
+                    *reinterpret_cast<float2*>(part + (h * 16 + 8 + g) * NT * 8 + n * 8 + c * 2) = make_float2(acc[h][n][2], acc[h][n][3]);
+                }
+            __syncthreads();
+            const float scale = a.scales[i];
+            for (int p = threadIdx.x; p < kLowRows * NT * 8; p += blockDim.x) {
+                const int row = p / (NT * 8), q = p % (NT * 8);
+                if (((mine >> row) & 1) && q < ranks) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kLowWarps; ++w) sum += parts[w * kLowRows * NT * 8 + p];
+                    a.low[(t0 + row) * a.r + q0 + q] = scale * sum;
+                }
+            }
+            __syncthreads();
         }
-        if (lane == 0) a.low[item] = acc;
     }
-    pdl_trigger();
+}
+
+template <int NT>
+cudaError_t launch_low(const AdapterArgs& g, cudaStream_t stream) {
+    const int tiles = ceil_div(g.T, kLowRows);
+    // Few tiles: a block for each of a tile's adapters; many: each block takes them in turn.
+    int slots = 4 * sm_count() / tiles;
+    slots = slots < 1 ? 1 : slots > kLowRows ? kLowRows : slots;
+    const size_t smem = (size_t)kLowWarps * kLowRows * NT * 8 * sizeof(float);
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(adapter_low_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(adapter_low_kernel<NT>, dim3((unsigned)tiles, (unsigned)slots), dim3(kLowWarps * 32), smem, stream, g);
 }
 
 // The epilogue's part: 32 rows (columns of the tile) of one output feature per lane. A row's adapter
@@ -52,15 +134,15 @@ struct AdapterExtra {
     const __nv_bfloat16* b;
     const float* low;
     const int64_t* idx;
-    int T, F, L, r;
-    __device__ __forceinline__ void operator()(float (&v)[32], const Tile& t, int c, int m, int) const {
-        const int row0 = t.n0 + c;
+    int F, L, r;
+    static constexpr bool kFollows = true;
+    __device__ __forceinline__ void operator()(float (&v)[32], int64_t row0, int rows, int m) const {
         for (int q0 = 0; q0 < r; q0 += 32) {
             int cur = -1;
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-                if (row0 + j >= T) break;
+                if (j >= rows) break;
                 const int64_t id = idx[row0 + j];
                 if (id < 0 || id >= L) continue;
                 if (id != cur) {
@@ -151,15 +233,12 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
                       reinterpret_cast<const __nv_bfloat16*>(a), reinterpret_cast<const __nv_bfloat16*>(b), scales,
                       adapter_idx, reinterpret_cast<__nv_bfloat16*>(y), reinterpret_cast<float*>(workspace),
                       sh->num_rows, sh->in_features, sh->out_features, sh->num_adapters, sh->rank, launch->error_flags};
-        const int64_t items = (int64_t)g.T * g.r;
-        cudaError_t e = launch_pdl(adapter_low_simple_kernel, dim3((unsigned)((items + 7) / 8)), dim3(256), 0,
-                                   launch->stream, g);
+        cudaError_t e = g.r <= 8    ? launch_low<1>(g, launch->stream)
+                        : g.r <= 16 ? launch_low<2>(g, launch->stream)
+                        : g.r <= 32 ? launch_low<4>(g, launch->stream)
+                                    : launch_low<8>(g, launch->stream);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(gemm_kernel<kForward, AdapterExtra>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kGemmSmemMax);
-        if (e == cudaSuccess)
-            e = launch_pdl(gemm_kernel<kForward, AdapterExtra>, dim3(gemm_blocks(m, false)), dim3(kGemmThreads),
-                           gemm_smem(m), launch->stream, maps, m, AdapterExtra{g.b, g.low, g.idx, g.T, g.F, g.L, g.r});
+            e = launch_gemm<kForward>(maps, m, AdapterExtra{g.b, g.low, g.idx, g.F, g.L, g.r}, launch->stream);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return end_call(launch);

@@ -106,10 +106,7 @@ ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* othe
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows > 0) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<D, NoExtra>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemMax);
-        if (e == cudaSuccess)
-            e = launch_pdl(gemm_kernel<D, NoExtra>, dim3(gemm_blocks(a, D == kWgrad)), dim3(kGemmThreads), gemm_smem(a),
-                           launch->stream, maps, a, NoExtra{});
+        cudaError_t e = launch_gemm<D>(maps, a, NoExtra{}, launch->stream);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return end_call(launch);

@@ -17,6 +17,7 @@ struct GemmArgs {
     int N;                     // wgrad: in_features (forward / dgrad: the rows)
     int C;                     // contracted features (wgrad: the rows)
     int bn, box, stages;       // columns of the widest tile, rows of one load box of B, stages
+    int split;                 // CTAs that share a tile's contraction
     uint32_t* err;
 };
 
@@ -240,8 +241,13 @@ __device__ __forceinline__ void store_columns(const float (&v)[32], __nv_bfloat1
     }
 }
 
+// What an epilogue adds to the sums before they are rounded: v[j] is output feature m of row
+// row0 + j, j < rows (<= 32). kFollows: the kernel directly follows one of this library that has
+// returned from pdl_wait() before its trigger, so the call's inputs are complete when it starts;
+// only the epilogue waits.
 struct NoExtra {
-    __device__ __forceinline__ void operator()(float (&)[32], const Tile&, int, int, int) const {}
+    static constexpr bool kFollows = false;
+    __device__ __forceinline__ void operator()(float (&)[32], int64_t, int, int) const {}
 };
 
 // D[m][n] over tiles of 128 x up to 256, one CTA per SM walking over tiles. The weights are the M side
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    pdl_wait();
+    if (!Extra::kFollows || warp >= 4) pdl_wait();
 
     if (warp == 0 && lane == 0) {
         TileWalk<D> walk(a);
@@ -413,8 +419,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (m < a.M)
                         store_columns(v, a.out + ((int64_t)t.e * a.M + m) * a.N + t.n0 + c, a.N - t.n0 - c);
                 } else {
-                    extra(v, t, c, m, lane);
-                    store_features(v, a.out, a.M, t.n0 + c, t.end - t.n0 - c < t.n - c ? t.end - t.n0 - c : t.n - c, m, a.M, lane);
+                    const int rows = min(t.n, t.end - t.n0) - c;
+                    extra(v, t.n0 + c, min(rows, 32), m);
+                    store_features(v, a.out, a.M, t.n0 + c, rows, m, a.M, lane);
                 }
             }
             if (some) {
@@ -432,32 +439,294 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     pdl_trigger();
 }
 
+// ------------------------------------------------------------------ few rows: split contraction
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// fp32 value at the same shared-memory address of CTA `rank` of the cluster.
+__device__ __forceinline__ float peer_value(uint32_t addr, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// One warp: tile number i of all experts (forward / dgrad, as TileWalk counts them), 32 experts at a
+// time; false past the last one.
+__device__ __forceinline__ bool find_tile(const GemmArgs& a, int i, int lane, Tile& out) {
+    const int mt = (a.M + kBM - 1) / kBM;
+    int first = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane;
+        int begin = 0, end = 0;
+        if (e < a.E) {
+            begin = expert_begin(a, e);
+            end = expert_end(a, e);
+        }
+        const int rows = max(0, end - begin), cut = (rows + a.bn - 1) / a.bn;
+        const int per = cut > 0 ? ((rows + cut - 1) / cut + 15) & ~15 : 16;
+        const int count = (rows + per - 1) / per * mt;
+        int upto = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += up;
+        }
+        const int start = first + upto - count;
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, i >= start && i < start + count);
+        if (hit != 0) {
+            const int src = __ffs(hit) - 1, q = i - start, c = q / mt;
+            Tile t{e, (q - c * mt) * kBM, begin + c * per, 0, begin, end};
+            t.n = (min(per, end - t.n0) + 15) & ~15;
+            out.e = __shfl_sync(0xFFFFFFFFu, t.e, src);
+            out.m0 = __shfl_sync(0xFFFFFFFFu, t.m0, src);
+            out.n0 = __shfl_sync(0xFFFFFFFFu, t.n0, src);
+            out.n = __shfl_sync(0xFFFFFFFFu, t.n, src);
+            out.begin = __shfl_sync(0xFFFFFFFFu, t.begin, src);
+            out.end = __shfl_sync(0xFFFFFFFFu, t.end, src);
+            return true;
+        }
+        first += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    return false;
+}
+
+constexpr int kSplitThreads = 192;
+
+// forward / dgrad where rows are few and the weights are what is read: a cluster of `split` CTAs per
+// tile, each over its part of the contraction, so that enough CTAs stream weights at the same time
+// (and two fit an SM, one filling its pipeline while the other runs). Each CTA leaves its fp32 part
+// in its own shared memory; after a cluster barrier each adds up, in rank order, the parts of
+// its share of the rows. Warp 0 loads, warp 1 multiplies, warps 2 to 5 read tensor memory.
+template <Direction D, class Extra>
+__global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_constant__ GemmMaps maps,
+                                                                   const GemmArgs a, const Extra extra) {
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int dead;
+    __shared__ Tile s_tile;
+    __shared__ int s_has;
+    constexpr bool kAMn = D != kForward;
+    unsigned char* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const uint32_t stage_bytes = kABytes + (uint32_t)a.bn * 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = a.split > 1 ? (int)cluster_rank() : 0;
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_map(&maps.a);
+        tma_prefetch_map(&maps.b);
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&done, 1);
+        dead = 0;
+    }
+    if (warp == 1) tmem_alloc(&s_tmem, (uint32_t)a.bn);
+    if (!Extra::kFollows) pdl_wait();
+    if (warp == 2) {
+        Tile t{};
+        const bool has = find_tile(a, blockIdx.x / a.split, lane, t);
+        if (lane == 0) {
+            s_tile = t;
+            s_has = has;
+        }
+    }
+    if (warp == 3 && blockIdx.x == 0) check_prefix(a, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const Tile t = s_tile;
+    const bool has = s_has;            // the same in all CTAs of a cluster
+    const int blocks = (a.C + kBK - 1) / kBK;
+    const int kb0 = (int)((int64_t)blocks * rank / a.split), kb1 = (int)((int64_t)blocks * (rank + 1) / a.split);
+
+    if (has && warp == 0 && lane == 0) {
+        const int boxes = (t.n + a.box - 1) / a.box;
+        const uint32_t bytes = kABytes + (uint32_t)boxes * a.box * 128;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            const uint32_t s = it % a.stages;
+            if (!(ok = mbar_wait(&empty[s], ((it / a.stages) & 1) ^ 1, &dead, a.err))) break;
+            unsigned char* sa = smem + s * stage_bytes;
+            unsigned char* sb = sa + kABytes;
+            const int k0 = kb * kBK;
+            mbar_expect_bytes(&full[s], bytes);
+            if (D == kForward) {
+                tma_load_3d(sa, &maps.a, k0, t.m0, t.e, &full[s]);
+            } else {
+                tma_load_3d(sa, &maps.a, t.m0, k0, t.e, &full[s]);
+                tma_load_3d(sa + kMnChunk, &maps.a, t.m0 + 64, k0, t.e, &full[s]);
+            }
+            for (int b = 0; b < boxes; ++b) tma_load_2d(sb + b * a.box * 128, &maps.b, k0, t.n0 + b * a.box, &full[s]);
+        }
+        if (!ok) {     // wait, with a limit, for the copies still in flight
+            for (uint32_t q = it > (uint32_t)a.stages ? it - a.stages : 0; q < it; ++q)
+                mbar_wait_bounded(&full[q % a.stages], (q / a.stages) & 1, kGemmWaitNs / 8);
+        }
+    } else if (has && warp == 1 && lane == 0) {
+        const uint32_t idesc = instr_desc(kBM, t.n, kAMn, false);
+        uint32_t it = 0;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+            const uint32_t s = it % a.stages;
+            if (!mbar_wait(&full[s], (it / a.stages) & 1, &dead, a.err)) break;
+            tc_fence_after();
+            const uint32_t sa = smem_addr(smem + s * stage_bytes), sb = sa + kABytes;
+            const uint64_t da = smem_desc(sa, kAMn), db = smem_desc(sb, false);
+#pragma unroll
+            for (int k = 0; k < kBK; k += 16)
+                tc_mma(tmem, da + (kAMn ? k * 128 : k * 2) / 16, db + k * 2 / 16, idesc, (it | k) != 0);
+            tc_commit(&empty[s]);
+        }
+        tc_commit(&done);
+    }
+    __syncwarp();
+    const int quarter = warp & 3, m_local = quarter * 32 + lane, m = t.m0 + m_local;
+    const int rows = min(t.n, t.end - t.n0);
+    bool ok = has;
+    if (has && warp >= 2) {
+        ok = mbar_wait(&done, 0, &dead, a.err);
+        tc_fence_after();
+    }
+    ok = ok && !dead;
+    if (Extra::kFollows && warp >= 2) pdl_wait();
+    if (a.split == 1) {
+        if (ok && warp >= 2) {
+            for (int c = 0; c < rows; c += 32) {
+                float v[32];
+                tmem_load32(tmem + c + ((uint32_t)quarter << 21), v);
+                extra(v, t.n0 + c, min(rows - c, 32), m);
+                store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
+            }
+        }
+    } else {
+        float* part = reinterpret_cast<float*>(smem);      // [columns][128]; every product has read its stage
+        const bool some = kb1 > kb0;
+        if (ok && warp >= 2) {
+            for (int c = 0; c < rows; c += 32) {
+                float v[32];
+                if (some) {
+                    tmem_load32(tmem + c + ((uint32_t)quarter << 21), v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c + j < rows) part[(c + j) * kBM + m_local] = v[j];
+            }
+        }
+        __syncwarp();
+        cluster_barrier();
+        const int share = (rows + a.split - 1) / a.split, lo = rank * share, hi = min(rows, lo + share);
+        if (ok && warp >= 2) {
+            const uint32_t at = smem_addr(part);
+            for (int c = lo; c < hi; c += 32) {
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    v[j] = 0.0f;
+                    if (c + j < hi)
+                        for (int r = 0; r < a.split; ++r) v[j] += peer_value(at + ((c + j) * kBM + m_local) * 4, r);
+                }
+                extra(v, t.n0 + c, min(hi - c, 32), m);
+                store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
+            }
+        }
+        __syncwarp();
+        cluster_barrier();          // until here the peers read this CTA's shared memory
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_free(tmem, (uint32_t)a.bn);
+    pdl_trigger();
+}
+
 // ------------------------------------------------------------------ host
 
-// Column tile width and stages. wgrad: 256. Else twice the average rows of an expert, so that most
-// experts are one tile, within [32, 256].
+// Whether gemm_split_kernel runs (else gemm_kernel, one CTA per SM).
+inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1; }
+
+// Column tile width, stages and split.
+//   wgrad: tiles of 256 columns, one CTA per SM.
+//   else:  tiles of twice the average rows of an expert, within [32, 256], so that most experts
+//          are one tile. Up to 64 columns the weights' loads are what counts: two CTAs per SM, and
+//          the contraction split until about four CTAs per SM have work; wider tiles are split only
+//          where there are fewer of them than SMs. A part keeps at least eight 64-deep steps.
 inline void gemm_tiles(GemmArgs* a, bool wgrad) {
     int bn = 256;
-    if (!wgrad) {
-        const int64_t want = 2 * (int64_t)((a->num_rows + a->E - 1) / a->E);
-        for (bn = 32; bn < 256 && bn < want; bn *= 2) {}
-    }
+    const int avg = (a->num_rows + a->E - 1) / a->E;
+    if (!wgrad)
+        for (bn = 32; bn < 256 && bn < 2 * avg; bn *= 2) {}
     a->bn = bn;
     a->box = bn < 64 ? bn : 64;
-    const int stage = (int)kABytes + bn * 128;
-    a->stages = 200 * 1024 / stage < kMaxStages ? 200 * 1024 / stage : kMaxStages;
+    a->split = 1;
+    const int sms = sm_count();
+    if (!wgrad) {
+        const int64_t tiles = (int64_t)ceil_div(a->M, kBM) * (a->E < a->num_rows ? a->E : a->num_rows) * ceil_div(avg, bn);
+        const int64_t want = bn <= 64 ? 4 * sms : sms;
+        const int steps = ceil_div(a->C, kBK);
+        while (a->split < 8 && tiles * a->split * 2 <= want && steps >= a->split * 16) a->split *= 2;
+    }
+    const int stage = (int)kABytes + bn * 128, room = (gemm_by_split(*a) && bn <= 64 ? 96 : 200) * 1024;
+    a->stages = room / stage < kMaxStages ? room / stage : kMaxStages;
 }
 
 // One CTA per SM, at most as many as there can be tiles.
-inline unsigned gemm_blocks(const GemmArgs& a, bool wgrad) {
+inline int64_t gemm_most_tiles(const GemmArgs& a, bool wgrad) {
     const int64_t mt = ceil_div(a.M, kBM);
-    const int64_t nt = wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn)
-                             : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows);
-    const int64_t sms = sm_count();
-    return (unsigned)(mt * nt < sms ? mt * nt : sms);
+    return mt * (wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn) : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows));
 }
 
 inline size_t gemm_smem(const GemmArgs& a) { return (size_t)a.stages * (kABytes + a.bn * 128) + 1024; }
 constexpr int kGemmSmemMax = 200 * 1024 + 1024;
+
+template <class Kernel, class Extra>
+cudaError_t launch_gemm_as(Kernel kernel, unsigned blocks, unsigned threads, unsigned cluster, cudaStream_t stream,
+                           const GemmMaps& maps, const GemmArgs& a, const Extra& extra) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemMax);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = gemm_smem(a);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, maps, a, extra);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+// Launches the product (a.num_rows > 0) as gemm_tiles has laid it out.
+template <Direction D, class Extra>
+cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Extra& extra, cudaStream_t stream) {
+    const int64_t tiles = gemm_most_tiles(a, D == kWgrad), sms = sm_count();
+    if constexpr (D != kWgrad) {
+        if (gemm_by_split(a)) {
+            if (tiles * a.split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+            return launch_gemm_as(gemm_split_kernel<D, Extra>, (unsigned)(tiles * a.split), kSplitThreads,
+                                  (unsigned)a.split, stream, maps, a, extra);
+        }
+    }
+    return launch_gemm_as(gemm_kernel<D, Extra>, (unsigned)(tiles < sms ? tiles : sms), kGemmThreads, 1, stream, maps, a,
+                          extra);
+}
 
 }  // namespace ep
