@@ -1,7 +1,8 @@
 // adapter.cu -- a projection that all rows share plus each row's own low-rank adapter:
 //   y[t] = W x[t] + scales[i] * B_i (A_i x[t]),  i = adapter_idx[t]
-// Two kernels: low[t] = scales[i] * A_i x[t] in fp32, then the projection with B_i low[t] added
-// to its fp32 sums before the one rounding.
+// low[t] = scales[i] * A_i x[t] in fp32 (more than 32 rows: by adapter, after a sort of the rows),
+// then the projection with B_i low[t] added to its fp32 sums before the one rounding. The
+// projection starts while low is still computed; its epilogue waits for it.
 #include "ep_internal.cuh"
 #include "gemm.cuh"
 
@@ -9,16 +10,17 @@ namespace ep {
 namespace {
 
 struct AdapterArgs {
-    const __nv_bfloat16 *x, *w, *a, *b;
+    const __nv_bfloat16 *x, *a;
     const float* scales;
     const int64_t* idx;
-    __nv_bfloat16* y;
-    float* low;        // [T][r]
-    int T, K, F, L, r;
+    const int32_t* order;      // rows by adapter, and [L + 1] where each adapter's begin (many rows)
+    const int32_t* prefix;
+    float* low;                // [parts][T][r]
+    int T, K, L, r, parts;
     uint32_t* err;
 };
 
-__device__ __forceinline__ int adapter_of(const AdapterArgs& a, int t, bool flag) {
+__device__ __forceinline__ int adapter_of(const AdapterArgs& a, int64_t t, bool flag) {
     const int64_t i = a.idx[t];
     if (i >= 0 && i < a.L) return (int)i;
     if (flag && i != -1) raise_flag(a.err, EP_DEVERR_BAD_ADAPTER);
@@ -34,143 +36,295 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int kLowRows = 32, kLowWarps = 8;
+constexpr int kLowRows = 32, kLowWarps = 8, kLowPartsMost = 16, kLowBlocks = 304;
 
-// low[t][q] = scales[i] * sum_k x[t][k] A_i[q][k] for 32 rows and the d-th of their distinct adapters,
-// d = blockIdx.y, + gridDim.y, ...; NT * 8 ranks at a time. The warps share the contraction and
-// join in shared memory in warp order. Operands come straight from memory: a lane of quad position
-// c loads the 8 values c*8 .. c*8+7 of a 32-deep step with one 16-byte load, for a row of x and for a
-// rank of A alike; which of them a product calls its k-th is immaterial as long as both agree, so
-// the lane's first four words feed two products. Rows of other adapters are not read (zero), and
-// each row is written by its own adapter's block alone.
-template <int NT>
-__global__ void __launch_bounds__(kLowWarps * 32) adapter_low_kernel(AdapterArgs a) {
+// Blocks of the low-rank kernel: up to 32 rows are looked through for their distinct adapters
+// (one block per adapter, by its position among them); more are sorted by adapter first, and each
+// adapter's rows are cut into 32 at a time.
+inline int64_t low_blocks(int T, int L) {
+    return T <= kLowRows ? (T < L ? T : L) : (int64_t)T / kLowRows + (T < L ? T : L);
+}
+// Parts of the contraction, for as many blocks as two per SM: every part is at least four steps of
+// 32 for each warp.
+inline int low_parts(int T, int L, int K) {
+    const int64_t blocks = low_blocks(T, L);
+    if (blocks == 0) return 1;
+    int most = ceil_div(K, 32 * kLowWarps * 4);
+    if (most > kLowPartsMost) most = kLowPartsMost;
+    const int64_t want = kLowBlocks / blocks;
+    return (int)(want < 1 ? 1 : want < most ? want : most);
+}
+
+// low[part][t][q] = scales[i] * sum over the part's k of x[t][k] A_i[q][k], for up to 32 rows of one
+// adapter; NT * 8 ranks at a time. The warps share the part and join in shared memory in warp order;
+// the parts are added up by the projection's epilogue. Operands come straight from memory: a
+// lane of quad position c loads the 8 values c*8 .. c*8+7 of a 32-deep step with one 16-byte load,
+// for a row of x and for a rank of A alike; which of them a product calls its k-th is immaterial as
+// long as both agree, so the lane's four words feed two products. Rows of other adapters are not
+// read (zero) and not written.
+template <int NT, bool SORTED>
+__global__ void __launch_bounds__(kLowWarps * 32, 2) adapter_low_kernel(AdapterArgs a) {
     extern __shared__ float parts[];                    // [warps][32][NT * 8]
+    __shared__ int s_row[kLowRows];
+    __shared__ int s_adapter;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    pdl_wait();
-    pdl_trigger();       // the projection may start; it reads low after this kernel's end only
-    const int64_t t0 = (int64_t)blockIdx.x * kLowRows;
-    int id = -1;
-    if (t0 + lane < a.T) id = adapter_of(a, (int)(t0 + lane), warp == 0 && blockIdx.y == 0);
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
-    unsigned firsts = __ballot_sync(0xFFFFFFFFu, id >= 0 && (same & lanemask_lt()) == 0);
-    const int steps = (a.K + 31) / 32;
-    const int s0 = (int)((int64_t)steps * warp / kLowWarps), s1 = (int)((int64_t)steps * (warp + 1) / kLowWarps);
-    for (int d = 0; firsts != 0; ++d, firsts &= firsts - 1) {
-        if (d % gridDim.y != blockIdx.y) continue;
-        const int i = __shfl_sync(0xFFFFFFFFu, id, __ffs(firsts) - 1);
-        const unsigned mine = __ballot_sync(0xFFFFFFFFu, id == i);
-        for (int q0 = 0; q0 < a.r; q0 += NT * 8) {
-            float acc[2][NT][4] = {};
-            const __nv_bfloat16* xr[4];
-            bool take[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                take[h] = (mine >> (h * 8 + g)) & 1;
-                xr[h] = a.x + (t0 + h * 8 + g) * a.K;
-            }
-            const __nv_bfloat16* ar = a.a + ((int64_t)i * a.r + q0 + g) * a.K;
-            const int ranks = a.r - q0;
-#pragma unroll 2
-            for (int s = s0; s < s1; ++s) {
-                const int k = s * 32 + c * 8;
-                const bool in = k < a.K;
-                uint4 xv[4], av[NT];
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    xv[h] = in && take[h] ? *reinterpret_cast<const uint4*>(xr[h] + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    av[n] = in && n * 8 < ranks ? ld_stream_v4(ar + (int64_t)n * 8 * a.K + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        mma_16816(acc[h][n], xv[2 * h].x, xv[2 * h + 1].x, xv[2 * h].y, xv[2 * h + 1].y, av[n].x, av[n].y);
-                        mma_16816(acc[h][n], xv[2 * h].z, xv[2 * h + 1].z, xv[2 * h].w, xv[2 * h + 1].w, av[n].z, av[n].w);
-                    }
-            }
-            float* part = parts + warp * kLowRows * NT * 8;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    *reinterpret_cast<float2*>(part + (h * 16 + g) * NT * 8 + n * 8 + c * 2) = make_float2(acc[h][n][0], acc[h][n][1]);
-                    *reinterpret_cast<float2*>(part + (h * 16 + 8 + g) * NT * 8 + n * 8 + c * 2) = make_float2(acc[h][n][2], acc[h][n][3]);
+    if (SORTED) {
+        // The sort before this kernel has waited for all earlier work before its own trigger, so the
+        // projection may start on the call's inputs now.
+        pdl_trigger();
+        pdl_wait();
+    } else {
+        pdl_wait();
+        pdl_trigger();
+    }
+    if (warp == 0) {
+        int adapter = -1, row = -1;
+        if (SORTED) {
+            // block number -> adapter and which of its 32 rows, 32 adapters at a time
+            int first = 0;
+            for (int i0 = 0; i0 < a.L && adapter < 0; i0 += 32) {
+                int begin = 0, count = 0;
+                if (i0 + lane < a.L) {
+                    begin = a.prefix[i0 + lane];
+                    count = a.prefix[i0 + lane + 1] - begin;
                 }
-            __syncthreads();
-            const float scale = a.scales[i];
-            for (int p = threadIdx.x; p < kLowRows * NT * 8; p += blockDim.x) {
-                const int row = p / (NT * 8), q = p % (NT * 8);
-                if (((mine >> row) & 1) && q < ranks) {
-                    float sum = 0.0f;
+                const int tiles = (count + kLowRows - 1) / kLowRows;
+                int upto = tiles;
 #pragma unroll
-                    for (int w = 0; w < kLowWarps; ++w) sum += parts[w * kLowRows * NT * 8 + p];
-                    a.low[(t0 + row) * a.r + q0 + q] = scale * sum;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                    if (lane >= o) upto += up;
                 }
+                const int start = first + upto - tiles, b = (int)blockIdx.x;
+                const unsigned hit = __ballot_sync(0xFFFFFFFFu, b >= start && b < start + tiles);
+                if (hit != 0) {
+                    const int src = __ffs(hit) - 1;
+                    adapter = i0 + src;
+                    const int at = __shfl_sync(0xFFFFFFFFu, begin + (b - start) * kLowRows, src) + lane;
+                    if (at < __shfl_sync(0xFFFFFFFFu, begin + count, src)) row = a.order[at];
+                }
+                first += __shfl_sync(0xFFFFFFFFu, upto, 31);
             }
-            __syncthreads();
+        } else {
+            if (blockIdx.x == 0 && blockIdx.y == 0)
+                for (int t = lane; t < a.T; t += 32) adapter_of(a, t, true);
+            const int id = lane < a.T ? adapter_of(a, lane, false) : -1;
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+            unsigned firsts = __ballot_sync(0xFFFFFFFFu, id >= 0 && (same & lanemask_lt()) == 0);
+            for (unsigned d = 0; d < blockIdx.x && firsts != 0; ++d) firsts &= firsts - 1;
+            if (firsts != 0) adapter = __shfl_sync(0xFFFFFFFFu, id, __ffs(firsts) - 1);
+            if (adapter >= 0 && id == adapter) row = lane;
         }
+        s_row[lane] = row;
+        if (lane == 0) s_adapter = adapter;
+    }
+    __syncthreads();
+    const int i = s_adapter;
+    if (i < 0) return;
+    const int steps = (a.K + 31) / 32, share = gridDim.y * kLowWarps, w = blockIdx.y * kLowWarps + warp;
+    const int s0 = (int)((int64_t)steps * w / share), s1 = (int)((int64_t)steps * (w + 1) / share);
+    const __nv_bfloat16* xr[4];
+    bool take[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const int row = s_row[h * 8 + g];
+        take[h] = row >= 0;
+        xr[h] = a.x + (int64_t)max(row, 0) * a.K;
+    }
+    const float scale = a.scales[i];
+    for (int q0 = 0; q0 < a.r; q0 += NT * 8) {
+        float acc[2][NT][4] = {};
+        const __nv_bfloat16* ar = a.a + ((int64_t)i * a.r + q0 + g) * a.K;
+        const int ranks = a.r - q0;
+#pragma unroll(NT <= 2 ? 4 : NT <= 4 ? 2 : 1)
+        for (int s = s0; s < s1; ++s) {
+            const int k = s * 32 + c * 8;
+            const bool in = k < a.K;
+            uint4 xv[4], av[NT];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                xv[h] = in && take[h] ? *reinterpret_cast<const uint4*>(xr[h] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                av[n] = in && n * 8 < ranks ? *reinterpret_cast<const uint4*>(ar + (int64_t)n * 8 * a.K + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mma_16816(acc[h][n], xv[2 * h].x, xv[2 * h + 1].x, xv[2 * h].y, xv[2 * h + 1].y, av[n].x, av[n].y);
+                    mma_16816(acc[h][n], xv[2 * h].z, xv[2 * h + 1].z, xv[2 * h].w, xv[2 * h + 1].w, av[n].z, av[n].w);
+                }
+        }
+        float* part = parts + warp * kLowRows * NT * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                *reinterpret_cast<float2*>(part + (h * 16 + g) * NT * 8 + n * 8 + c * 2) = make_float2(acc[h][n][0], acc[h][n][1]);
+                *reinterpret_cast<float2*>(part + (h * 16 + 8 + g) * NT * 8 + n * 8 + c * 2) = make_float2(acc[h][n][2], acc[h][n][3]);
+            }
+        __syncthreads();
+        for (int p = threadIdx.x; p < kLowRows * NT * 8; p += blockDim.x) {
+            const int row = s_row[p / (NT * 8)], q = p % (NT * 8);
+            if (row >= 0 && q < ranks) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int v = 0; v < kLowWarps; ++v) sum += parts[v * kLowRows * NT * 8 + p];
+                a.low[((int64_t)blockIdx.y * a.T + row) * a.r + q0 + q] = scale * sum;
+            }
+        }
+        __syncthreads();
     }
 }
 
-template <int NT>
+template <int NT, bool SORTED>
 cudaError_t launch_low(const AdapterArgs& g, cudaStream_t stream) {
-    const int tiles = ceil_div(g.T, kLowRows);
-    // Few tiles: a block for each of a tile's adapters; many: each block takes them in turn.
-    int slots = 4 * sm_count() / tiles;
-    slots = slots < 1 ? 1 : slots > kLowRows ? kLowRows : slots;
     const size_t smem = (size_t)kLowWarps * kLowRows * NT * 8 * sizeof(float);
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(adapter_low_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = cudaFuncSetAttribute(adapter_low_kernel<NT, SORTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(adapter_low_kernel<NT>, dim3((unsigned)tiles, (unsigned)slots), dim3(kLowWarps * 32), smem, stream, g);
+    const int64_t blocks = low_blocks(g.T, g.L);
+    return launch_pdl(adapter_low_kernel<NT, SORTED>, dim3((unsigned)(blocks > 0 ? blocks : 1), (unsigned)g.parts),
+                      dim3(kLowWarps * 32), smem, stream, g);
 }
 
-// The epilogue's part: 32 rows (columns of the tile) of one output feature per lane. A row's adapter
-// is the same for the whole warp; B_i's row of the feature is loaded when the adapter changes.
+template <bool SORTED>
+cudaError_t launch_low_of(const AdapterArgs& g, cudaStream_t stream) {
+    return g.r <= 8    ? launch_low<1, SORTED>(g, stream)
+           : g.r <= 16 ? launch_low<2, SORTED>(g, stream)
+           : g.r <= 32 ? launch_low<4, SORTED>(g, stream)
+                       : launch_low<8, SORTED>(g, stream);
+}
+
+// Workspace: low, then (more than 32 rows) the order, where each adapter's rows begin, and the
+// sort's scratch.
+struct AdapterWorkspace {
+    size_t order, prefix, scratch, bytes;
+    int parts;
+};
+AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
+    AdapterWorkspace w{};
+    const auto round = [](size_t n) { return (n + 255) / 256 * 256; };
+    w.parts = low_parts(sh->num_rows, sh->num_adapters, sh->in_features);
+    w.order = round((size_t)w.parts * sh->num_rows * sh->rank * sizeof(float));
+    w.prefix = w.scratch = w.bytes = w.order;
+    if (sh->num_rows > kLowRows && sh->num_adapters > 0) {
+        w.prefix = w.order + round((size_t)sh->num_rows * 4);
+        w.scratch = w.prefix + round((size_t)(sh->num_adapters + 1) * 4);
+        w.bytes = w.scratch + round(sort_ids_workspace(sh->num_rows, sh->num_adapters));
+    }
+    return w;
+}
+
+// The epilogue's part: y += B_i low, for one output feature per lane. Sixteen rows' low values (64
+// ranks at a time) are staged in shared memory by the four warps, the next sixteen's loaded
+// meanwhile; a row's adapter is the same for the whole warp, and B_i's values of the feature are
+// loaded when the adapter changes. fp32 throughout.
+constexpr int kStageRows = 16, kStageRanks = 64, kStageStride = kStageRanks + 4;
+
 struct AdapterExtra {
+    static constexpr bool kFollows = true;
+    static constexpr int kFloats = 2 * kStageRows * kStageStride;
     const __nv_bfloat16* b;
     const float* low;
     const int64_t* idx;
-    int F, L, r;
-    static constexpr bool kFollows = true;
-    __device__ __forceinline__ void operator()(float (&v)[32], int64_t row0, int rows, int m) const {
-        for (int q0 = 0; q0 < r; q0 += 32) {
-            int cur = -1;
-            uint32_t w[16];
+    int64_t part;          // floats from one part of low to the next
+    int parts, F, L, r;
+
+    struct State {
+        int64_t row0;
+        int rows, m, cur, buf;
+        uint32_t w[kStageRanks / 2];
+    };
+
+    // This thread's eight low values of the sixteen rows from row c on, ranks from q0 on.
+    __device__ __forceinline__ void load(const State& s, int c, int q0, float4 (&v)[2]) const {
+        const int tid = threadIdx.x & 127, row = c + (tid >> 3), q = q0 + (tid & 7) * 8;
+        v[0] = v[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (row < s.rows && q < r) {
+            const float* at = low + (s.row0 + row) * r + q;
+            for (int p = 0; p < parts; ++p, at += part) {
+                const float4 x = *reinterpret_cast<const float4*>(at), y = *reinterpret_cast<const float4*>(at + 4);
+                v[0].x += x.x, v[0].y += x.y, v[0].z += x.z, v[0].w += x.w;
+                v[1].x += y.x, v[1].y += y.y, v[1].z += y.z, v[1].w += y.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void put(float* shared, int buf, const float4 (&v)[2]) const {
+        const int tid = threadIdx.x & 127;
+        float4* at = reinterpret_cast<float4*>(shared + (buf * kStageRows + (tid >> 3)) * kStageStride + (tid & 7) * 8);
+        at[0] = v[0];
+        at[1] = v[1];
+    }
+    // B's lines of this tile towards L2, while the projection is computed.
+    __device__ __forceinline__ void ahead(int64_t row0, int rows, int m) const {
+        if (m >= F) return;
+        for (int j = 0; j < rows; ++j) {
+            const int64_t id = idx[row0 + j];
+            if (id < 0 || id >= L) continue;
+            const char* at = reinterpret_cast<const char*>(b + (id * F + m) * r);
+            for (int q = 0; q < r * 2; q += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + q));
+        }
+    }
+    __device__ __forceinline__ void begin(State& s, float* shared, int64_t row0, int rows, int m) const {
+        s.row0 = row0, s.rows = rows, s.m = m, s.cur = -1, s.buf = 0;
+        float4 v[2];
+        load(s, 0, 0, v);
+        epilogue_barrier();          // the tile before has been read
+        put(shared, 0, v);
+        epilogue_barrier();
+    }
+    __device__ __forceinline__ void apply(State& s, float* shared, float (&v)[32], int c) const {
+        const int lane = threadIdx.x & 31;
+        int id = -1;
+        if (c + lane < s.rows) {
+            const int64_t i = idx[s.row0 + c + lane];
+            id = i >= 0 && i < L ? (int)i : -1;
+        }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                if (j >= rows) break;
-                const int64_t id = idx[row0 + j];
-                if (id < 0 || id >= L) continue;
-                if (id != cur) {
-                    cur = (int)id;
+        for (int h = 0; h < 32; h += kStageRows) {
+            if (c + h >= s.rows) break;
+            for (int q0 = 0; q0 < r; q0 += kStageRanks) {
+                float4 next[2];
+                const bool last = q0 + kStageRanks >= r;
+                load(s, last ? c + h + kStageRows : c + h, last ? 0 : q0 + kStageRanks, next);
+                if (r > kStageRanks) s.cur = -1;
+                const float* stage = shared + s.buf * kStageRows * kStageStride;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (m < F && q0 + g * 8 < r)
-                            u = *reinterpret_cast<const uint4*>(b + ((int64_t)cur * F + m) * r + q0 + g * 8);
-                        w[4 * g] = u.x, w[4 * g + 1] = u.y, w[4 * g + 2] = u.z, w[4 * g + 3] = u.w;
+                for (int j = 0; j < kStageRows; ++j) {
+                    const int i = __shfl_sync(0xFFFFFFFFu, id, h + j);
+                    if (i < 0) continue;
+                    if (i != s.cur) {
+                        s.cur = i;
+                        const __nv_bfloat16* at = b + ((int64_t)i * F + s.m) * r + q0;
+#pragma unroll
+                        for (int g = 0; g < kStageRanks / 8; ++g) {
+                            uint4 u = make_uint4(0, 0, 0, 0);
+                            if (s.m < F && q0 + g * 8 < r) u = *reinterpret_cast<const uint4*>(at + g * 8);
+                            s.w[4 * g] = u.x, s.w[4 * g + 1] = u.y, s.w[4 * g + 2] = u.z, s.w[4 * g + 3] = u.w;
+                        }
                     }
-                }
-                const float4* l = reinterpret_cast<const float4*>(low + (int64_t)(row0 + j) * r + q0);
-                float acc = v[j];
+                    const float4* l = reinterpret_cast<const float4*>(stage + j * kStageStride);
+                    float acc = v[h + j];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    if (q0 + g * 8 >= r) break;
-                    const float4 lo = l[2 * g], hi = l[2 * g + 1];
-                    acc = fmaf(lo.x, bf16_lo(w[4 * g]), acc);
-                    acc = fmaf(lo.y, bf16_hi(w[4 * g]), acc);
-                    acc = fmaf(lo.z, bf16_lo(w[4 * g + 1]), acc);
-                    acc = fmaf(lo.w, bf16_hi(w[4 * g + 1]), acc);
-                    acc = fmaf(hi.x, bf16_lo(w[4 * g + 2]), acc);
-                    acc = fmaf(hi.y, bf16_hi(w[4 * g + 2]), acc);
-                    acc = fmaf(hi.z, bf16_lo(w[4 * g + 3]), acc);
-                    acc = fmaf(hi.w, bf16_hi(w[4 * g + 3]), acc);
+                    for (int g = 0; g < kStageRanks / 8; ++g) {
+                        if (q0 + g * 8 >= r) break;
+                        const float4 lo = l[2 * g], hi = l[2 * g + 1];
+                        acc = fmaf(lo.x, bf16_lo(s.w[4 * g]), acc);
+                        acc = fmaf(lo.y, bf16_hi(s.w[4 * g]), acc);
+                        acc = fmaf(lo.z, bf16_lo(s.w[4 * g + 1]), acc);
+                        acc = fmaf(lo.w, bf16_hi(s.w[4 * g + 1]), acc);
+                        acc = fmaf(hi.x, bf16_lo(s.w[4 * g + 2]), acc);
+                        acc = fmaf(hi.y, bf16_hi(s.w[4 * g + 2]), acc);
+                        acc = fmaf(hi.z, bf16_lo(s.w[4 * g + 3]), acc);
+                        acc = fmaf(hi.w, bf16_hi(s.w[4 * g + 3]), acc);
+                    }
+                    v[h + j] = acc;
                 }
-                v[j] = acc;
+                s.buf ^= 1;
+                put(shared, s.buf, next);
+                epilogue_barrier();
             }
         }
     }
@@ -182,7 +336,7 @@ ep_status check_adapter(const ep_adapter_shape* sh) {
         sh->rank < 8 || sh->rank % 8 != 0)
         return EP_ERR_INVALID_ARG;
     if (sh->num_rows > 1 << 30 || sh->in_features > EP_GEMM_MAX_FEATURES || sh->out_features > EP_GEMM_MAX_FEATURES ||
-        sh->rank > EP_ADAPTER_MAX_RANK)
+        sh->rank > EP_ADAPTER_MAX_RANK || sh->num_adapters > EP_MAX_EXPERTS)
         return EP_ERR_UNSUPPORTED;
     return EP_OK;
 }
@@ -194,7 +348,7 @@ extern "C" {
 
 size_t ep_adapter_workspace_size(const ep_adapter_shape* sh) {
     if (ep::check_adapter(sh) != EP_OK) return 0;
-    return (size_t)sh->num_rows * sh->rank * sizeof(float);
+    return ep::adapter_workspace(sh).bytes;
 }
 
 ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void* w, const void* a, const void* b,
@@ -229,16 +383,26 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
-        AdapterArgs g{reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(w),
-                      reinterpret_cast<const __nv_bfloat16*>(a), reinterpret_cast<const __nv_bfloat16*>(b), scales,
-                      adapter_idx, reinterpret_cast<__nv_bfloat16*>(y), reinterpret_cast<float*>(workspace),
-                      sh->num_rows, sh->in_features, sh->out_features, sh->num_adapters, sh->rank, launch->error_flags};
-        cudaError_t e = g.r <= 8    ? launch_low<1>(g, launch->stream)
-                        : g.r <= 16 ? launch_low<2>(g, launch->stream)
-                        : g.r <= 32 ? launch_low<4>(g, launch->stream)
-                                    : launch_low<8>(g, launch->stream);
+        const AdapterWorkspace ws = adapter_workspace(sh);
+        char* base = reinterpret_cast<char*>(workspace);
+        int32_t* order = reinterpret_cast<int32_t*>(base + ws.order);
+        int32_t* prefix = reinterpret_cast<int32_t*>(base + ws.prefix);
+        const AdapterArgs g{reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(a), scales,
+                            adapter_idx, order, prefix, reinterpret_cast<float*>(workspace), sh->num_rows,
+                            sh->in_features, sh->num_adapters, sh->rank, ws.parts, launch->error_flags};
+        cudaError_t e = cudaSuccess;
+        if (g.T <= kLowRows || g.L == 0) {
+            e = launch_low_of<false>(g, launch->stream);
+        } else {
+            e = launch_sort_ids(adapter_idx, g.T, g.L, g.T, nullptr, order, prefix, base + ws.scratch,
+                                EP_DEVERR_BAD_ADAPTER, launch->error_flags, launch->stream);
+            if (e == cudaSuccess) e = launch_low_of<true>(g, launch->stream);
+        }
         if (e == cudaSuccess)
-            e = launch_gemm<kForward>(maps, m, AdapterExtra{g.b, g.low, g.idx, g.F, g.L, g.r}, launch->stream);
+            e = launch_gemm<kForward>(maps, m,
+                                      AdapterExtra{reinterpret_cast<const __nv_bfloat16*>(b), g.low, adapter_idx,
+                                                   (int64_t)g.T * g.r, g.parts, sh->out_features, g.L, g.r},
+                                      launch->stream);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return end_call(launch);

@@ -241,14 +241,32 @@ __device__ __forceinline__ void store_columns(const float (&v)[32], __nv_bfloat1
     }
 }
 
-// What an epilogue adds to the sums before they are rounded: v[j] is output feature m of row
-// row0 + j, j < rows (<= 32). kFollows: the kernel directly follows one of this library that has
-// returned from pdl_wait() before its trigger, so the call's inputs are complete when it starts;
-// only the epilogue waits.
+// What an epilogue adds to the sums before they are rounded. All 128 epilogue threads call begin for
+// the rows row0 .. row0 + rows - 1 of a tile and then apply for each 32 of them in order: v[j] is
+// output feature m of row row0 + c + j. `shared`: kFloats floats of the block. kFollows: the kernel
+// directly follows one of this library after which the call's inputs are complete; only the epilogue
+// waits for that kernel itself. ahead: called while the products run, before that wait.
 struct NoExtra {
     static constexpr bool kFollows = false;
-    __device__ __forceinline__ void operator()(float (&)[32], int64_t, int, int) const {}
+    static constexpr int kFloats = 1;
+    struct State {};
+    __device__ __forceinline__ void ahead(int64_t, int, int) const {}
+    __device__ __forceinline__ void begin(State&, float*, int64_t, int, int) const {}
+    __device__ __forceinline__ void apply(State&, float*, float (&)[32], int) const {}
 };
+
+// The four epilogue warps: a barrier, and whether all of them have `mine` (the same answer to all,
+// so that none waits at a later barrier that another has left out).
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool epilogue_all(bool mine) {
+    uint32_t all;
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.and.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+        : "=r"(all)
+        : "r"((uint32_t)mine)
+        : "memory");
+    return all != 0;
+}
 
 // D[m][n] over tiles of 128 x up to 256, one CTA per SM walking over tiles. The weights are the M side
 // and the rows the N side, so that a tile has as many columns (a multiple of 16) as its expert has
@@ -262,6 +280,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int dead;
+    __shared__ __align__(16) float s_extra[Extra::kFloats];
     constexpr bool kAMn = D != kForward, kBMn = D == kWgrad;
     unsigned char* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const uint32_t stage_bytes = kABytes + (uint32_t)a.bn * 128;
@@ -403,11 +422,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const bool some = D != kWgrad || t.end > t.begin;
             const uint32_t acc = used & 1;
             if (some) {
-                if (!mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err)) break;
+                if (!epilogue_all(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err))) break;
                 tc_fence_after();
             }
             const int m = t.m0 + quarter * 32 + lane;
-            for (int c = 0; c < t.n; c += 32) {
+            const int rows = min(t.n, t.end - t.n0);
+            typename Extra::State state;
+            if (D != kWgrad) extra.begin(state, s_extra, t.n0, rows, m);
+            for (int c = 0; c < (D == kWgrad ? t.n : rows); c += 32) {
                 float v[32];
                 if (some) {
                     tmem_load32(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
@@ -419,9 +441,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (m < a.M)
                         store_columns(v, a.out + ((int64_t)t.e * a.M + m) * a.N + t.n0 + c, a.N - t.n0 - c);
                 } else {
-                    const int rows = min(t.n, t.end - t.n0) - c;
-                    extra(v, t.n0 + c, min(rows, 32), m);
-                    store_features(v, a.out, a.M, t.n0 + c, rows, m, a.M, lane);
+                    extra.apply(state, s_extra, v, c);
+                    store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
                 }
             }
             if (some) {
@@ -512,6 +533,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int dead;
+    __shared__ __align__(16) float s_extra[Extra::kFloats];
     __shared__ Tile s_tile;
     __shared__ int s_has;
     constexpr bool kAMn = D != kForward;
@@ -593,19 +615,22 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     __syncwarp();
     const int quarter = warp & 3, m_local = quarter * 32 + lane, m = t.m0 + m_local;
     const int rows = min(t.n, t.end - t.n0);
+    const int share = (rows + a.split - 1) / a.split, lo = rank * share, hi = min(rows, lo + share);   // of the rows
     bool ok = has;
     if (has && warp >= 2) {
-        ok = mbar_wait(&done, 0, &dead, a.err);
+        extra.ahead(t.n0 + lo, hi - lo, m);
+        ok = epilogue_all(mbar_wait(&done, 0, &dead, a.err));
         tc_fence_after();
     }
-    ok = ok && !dead;
     if (Extra::kFollows && warp >= 2) pdl_wait();
     if (a.split == 1) {
         if (ok && warp >= 2) {
+            typename Extra::State state;
+            extra.begin(state, s_extra, t.n0, rows, m);
             for (int c = 0; c < rows; c += 32) {
                 float v[32];
                 tmem_load32(tmem + c + ((uint32_t)quarter << 21), v);
-                extra(v, t.n0 + c, min(rows - c, 32), m);
+                extra.apply(state, s_extra, v, c);
                 store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
             }
         }
@@ -628,9 +653,10 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         }
         __syncwarp();
         cluster_barrier();
-        const int share = (rows + a.split - 1) / a.split, lo = rank * share, hi = min(rows, lo + share);
-        if (ok && warp >= 2) {
+        if (ok && warp >= 2 && lo < hi) {
             const uint32_t at = smem_addr(part);
+            typename Extra::State state;
+            extra.begin(state, s_extra, t.n0 + lo, hi - lo, m);
             for (int c = lo; c < hi; c += 32) {
                 float v[32];
 #pragma unroll
@@ -639,7 +665,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
                     if (c + j < hi)
                         for (int r = 0; r < a.split; ++r) v[j] += peer_value(at + ((c + j) * kBM + m_local) * 4, r);
                 }
-                extra(v, t.n0 + c, min(hi - c, 32), m);
+                extra.apply(state, s_extra, v, c - lo);
                 store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
             }
         }
@@ -659,15 +685,15 @@ inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1;
 
 // Column tile width, stages and split.
 //   wgrad: tiles of 256 columns, one CTA per SM.
-//   else:  tiles of twice the average rows of an expert, within [32, 256], so that most experts
-//          are one tile. Up to 64 columns the weights' loads are what counts: two CTAs per SM, and
+//   else:  tiles of twice the average rows of an expert (one group: of its rows), within [32, 256],
+//          so that most experts are one tile. Up to 64 columns the weights' loads are what counts: two CTAs per SM, and
 //          the contraction split until about four CTAs per SM have work; wider tiles are split only
 //          where there are fewer of them than SMs. A part keeps at least eight 64-deep steps.
 inline void gemm_tiles(GemmArgs* a, bool wgrad) {
     int bn = 256;
-    const int avg = (a->num_rows + a->E - 1) / a->E;
+    const int avg = (a->num_rows + a->E - 1) / a->E, wide = a->E > 1 ? 2 * (avg < 256 ? avg : 256) : avg;
     if (!wgrad)
-        for (bn = 32; bn < 256 && bn < 2 * avg; bn *= 2) {}
+        for (bn = 32; bn < 256 && bn < wide; bn *= 2) {}
     a->bn = bn;
     a->box = bn < 64 ? bn : 64;
     a->split = 1;

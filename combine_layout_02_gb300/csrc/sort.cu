@@ -28,12 +28,13 @@ constexpr int kMaxSegments = 152 * 16;
 
 struct SortArgs {
     const int64_t* topk_idx;
-    int32_t* entry_rows;
+    int32_t* entry_rows;      // nullable
     int32_t* row_entries;     // nullable
     int32_t* expert_prefix;
     int32_t* ws;              // [E][S] segment counts, then [E] totals
     int64_t num_rows;
     int n, E, S, seg_len, warps;
+    uint32_t bad_bit;
     uint32_t* err;
 };
 
@@ -55,7 +56,7 @@ __device__ __forceinline__ int entry_expert(const SortArgs& a, int i, int end, b
     if (i >= end) return -1;
     const int64_t e = a.topk_idx[i];
     if (e >= 0 && e < a.E) return (int)e;
-    if (flag && e != -1) raise_flag(a.err, EP_DEVERR_BAD_EXPERT);
+    if (flag && e != -1) raise_flag(a.err, a.bad_bit);
     return -1;
 }
 
@@ -85,7 +86,7 @@ __device__ __forceinline__ void place_segment(const SortArgs& a, int seg, int* t
                 raise_flag(a.err, EP_DEVERR_RECV_OVERFLOW);
                 row = -1;
             }
-            a.entry_rows[i] = row;
+            if (a.entry_rows != nullptr) a.entry_rows[i] = row;
             if (row >= 0 && a.row_entries != nullptr) a.row_entries[row] = i;
         }
     }
@@ -451,6 +452,50 @@ RowArgs row_args(const ep_shape* sh, const ep_sort* sort, const ep_launch* launc
 unsigned row_blocks(int N, int warps) { return (unsigned)((N + warps - 1) / warps); }
 
 }  // namespace
+
+size_t sort_ids_workspace(int64_t n, int E) {
+    if (n <= kSmallEntries) return 16;
+    const int64_t len = segment_length(n), S = (n + len - 1) / len;
+    return (size_t)(S + 1) * (size_t)E * sizeof(int32_t);
+}
+
+cudaError_t launch_sort_ids(const int64_t* ids, int n, int E, int64_t num_rows, int32_t* entry_rows,
+                            int32_t* row_entries, int32_t* prefix, void* ws, uint32_t bad_bit, uint32_t* err,
+                            cudaStream_t stream) {
+    SortArgs a{};
+    a.topk_idx = ids;
+    a.entry_rows = entry_rows;
+    a.row_entries = row_entries;
+    a.expert_prefix = prefix;
+    a.ws = reinterpret_cast<int32_t*>(ws);
+    a.num_rows = num_rows;
+    a.n = n;
+    a.E = E;
+    a.bad_bit = bad_bit;
+    a.err = err;
+    cudaError_t e = cudaSuccess;
+    if (n <= kSmallEntries) {
+        a.warps = table_warps(E, kSmallThreads / 32);
+        a.seg_len = ceil_div(ceil_div(n > 0 ? n : 1, a.warps), 32) * 32;
+        a.S = a.warps;
+        const size_t smem = (size_t)(a.warps + 1) * E * sizeof(int);
+        e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
+        if (e == cudaSuccess) e = launch_pdl(sort_small_kernel, dim3(1), dim3(kSmallThreads), smem, stream, a);
+    } else {
+        a.warps = table_warps(E, kSortWarps);
+        a.seg_len = segment_length(n);
+        a.S = ceil_div(n, a.seg_len);
+        const unsigned blocks = (unsigned)ceil_div(a.S, a.warps);
+        const size_t tables = (size_t)a.warps * E * sizeof(int), smem = tables + (size_t)E * sizeof(int);
+        e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
+        if (e == cudaSuccess) e = launch_pdl(sort_count_kernel, dim3(blocks), dim3(kSortWarps * 32), tables, stream, a);
+        if (e == cudaSuccess)
+            e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div(E, kSortWarps)), dim3(kSortWarps * 32), 0, stream, a);
+        if (e == cudaSuccess) e = launch_pdl(sort_place_kernel, dim3(blocks), dim3(kSortWarps * 32), smem, stream, a);
+    }
+    return e;
+}
+
 }  // namespace ep
 
 extern "C" {
@@ -460,9 +505,7 @@ size_t ep_sort_workspace_size(const ep_shape* sh) {
     if (check_shape(sh) != EP_OK || sh->num_ranks != 1) return 0;
     const int64_t n = (int64_t)sh->num_tokens * sh->num_topk;
     if (n > (int64_t)1 << 30) return 0;
-    if (n <= kSmallEntries) return 16;
-    const int64_t len = segment_length(n), S = (n + len - 1) / len;
-    return (size_t)(S + 1) * (size_t)sh->num_experts * sizeof(int32_t);
+    return sort_ids_workspace(n, sh->num_experts);
 }
 
 ep_status ep_sort_layout(const ep_shape* sh, const int64_t* topk_idx, const ep_sort* sort, void* workspace,
@@ -473,45 +516,13 @@ ep_status ep_sort_layout(const ep_shape* sh, const int64_t* topk_idx, const ep_s
     const int n = sh->num_tokens * sh->num_topk;
     if (sort->expert_prefix == nullptr) return EP_ERR_INVALID_ARG;
     if (n > 0 && (topk_idx == nullptr || sort->entry_rows == nullptr)) return EP_ERR_INVALID_ARG;
-    const bool small = n <= kSmallEntries;
-    if (!small && (workspace == nullptr || ((uintptr_t)workspace & 15) != 0 ||
+    if (n > kSmallEntries && (workspace == nullptr || ((uintptr_t)workspace & 15) != 0 ||
                    workspace_bytes < ep_sort_workspace_size(sh)))
         return EP_ERR_INVALID_ARG;
-    SortArgs a{};
-    a.topk_idx = topk_idx;
-    a.entry_rows = sort->entry_rows;
-    a.row_entries = sort->row_entries;
-    a.expert_prefix = sort->expert_prefix;
-    a.ws = reinterpret_cast<int32_t*>(workspace);
-    a.num_rows = sort->num_rows;
-    a.n = n;
-    a.E = sh->num_experts;
-    a.err = launch->error_flags;
     if ((st = begin_call(launch)) != EP_OK) return st;
-    cudaError_t e = cudaSuccess;
-    if (small) {
-        a.warps = table_warps(a.E, kSmallThreads / 32);
-        a.seg_len = ceil_div(ceil_div(n > 0 ? n : 1, a.warps), 32) * 32;
-        a.S = a.warps;
-        const size_t smem = (size_t)(a.warps + 1) * a.E * sizeof(int);
-        e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
-        if (e == cudaSuccess)
-            e = launch_pdl(sort_small_kernel, dim3(1), dim3(kSmallThreads), smem, launch->stream, a);
-    } else {
-        a.warps = table_warps(a.E, kSortWarps);
-        a.seg_len = segment_length(n);
-        a.S = ceil_div(n, a.seg_len);
-        const unsigned blocks = (unsigned)ceil_div(a.S, a.warps);
-        const size_t tables = (size_t)a.warps * a.E * sizeof(int), smem = tables + (size_t)a.E * sizeof(int);
-        e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
-        if (e == cudaSuccess)
-            e = launch_pdl(sort_count_kernel, dim3(blocks), dim3(kSortWarps * 32), tables, launch->stream, a);
-        if (e == cudaSuccess)
-            e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div(a.E, kSortWarps)), dim3(kSortWarps * 32), 0,
-                           launch->stream, a);
-        if (e == cudaSuccess)
-            e = launch_pdl(sort_place_kernel, dim3(blocks), dim3(kSortWarps * 32), smem, launch->stream, a);
-    }
+    const cudaError_t e = launch_sort_ids(topk_idx, n, sh->num_experts, sort->num_rows, sort->entry_rows,
+                                          sort->row_entries, sort->expert_prefix, workspace, EP_DEVERR_BAD_EXPERT,
+                                          launch->error_flags, launch->stream);
     if (e != cudaSuccess) return cuda_fail(e);
     return end_call(launch);
 }

@@ -531,7 +531,7 @@ EP_API ep_status ep_expert_gemm_wgrad(const ep_gemm_shape* shape, const void* dy
  *   y[t] = W x[t] + scales[i] * B_i (A_i x[t]),  i = adapter_idx[t];  y[t] = W x[t] if i = -1
  *   num_rows      T >= 0
  *   in_features, out_features  multiples of 8, 8 to EP_GEMM_MAX_FEATURES
- *   num_adapters  L >= 0
+ *   num_adapters  L, 0 to EP_MAX_EXPERTS
  *   rank          r, a multiple of 8, 8 to EP_ADAPTER_MAX_RANK (pad with zero rows of A) */
 typedef struct ep_adapter_shape {
     int32_t num_rows;

@@ -97,7 +97,7 @@ def test_adapter_refusals(ep):
     for s in (S(-1, 64, 64, 3, 16), S(10, 60, 64, 3, 16), S(10, 64, 0, 3, 16), S(10, 64, 64, -1, 16), S(10, 64, 64, 3, 12),
               S(10, 64, 64, 3, 0)):
         assert call(shape=s) == bad and ep.ep_adapter_workspace_size(s) == 0
-    for s in (S(10, 64, 64, 3, 264), S(10, (1 << 20) + 8, 64, 3, 16), S((1 << 30) + 1, 64, 64, 3, 16)):
+    for s in (S(10, 64, 64, 3, 264), S(10, 64, 64, 8193, 16), S(10, (1 << 20) + 8, 64, 3, 16), S((1 << 30) + 1, 64, 64, 3, 16)):
         assert call(shape=s) == unsup and ep.ep_adapter_workspace_size(s) == 0
     for name in ("x", "w", "a", "b", "s", "ids", "y", "ws"):
         assert call(**{name: None}) == bad, name
