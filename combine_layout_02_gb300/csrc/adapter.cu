@@ -217,116 +217,228 @@ AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
     return w;
 }
 
-// The epilogue's part: y += B_i low, for one output feature per lane. Sixteen rows' low values (64
-// ranks at a time) are staged in shared memory by the four warps, the next sixteen's loaded
-// meanwhile; a row's adapter is the same for the whole warp, and B_i's values of the feature are
-// loaded when the adapter changes. fp32 throughout.
-constexpr int kStageRows = 16, kStageRanks = 64, kStageStride = kStageRanks + 4;
+// d += a * b on a pair of fp32 values, each rounded as fmaf rounds.
+__device__ __forceinline__ void fma_pair(float2& d, const float2& a, const float2& b) {
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mov.b64 z, {%4, %5}; fma.rn.f32x2 x, y, z, x; "
+        "mov.b64 {%0, %1}, x; }"
+        : "+f"(d.x), "+f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+}
 
-struct AdapterExtra {
-    static constexpr bool kFollows = true;
-    static constexpr int kFloats = 2 * kStageRows * kStageStride;
+// The epilogue's part: y += B_i low, one output feature per lane, fp32. A row only ever meets its own
+// adapter's values.
+struct AdapterSide {
     const __nv_bfloat16* b;
     const float* low;
     const int64_t* idx;
     int64_t part;          // floats from one part of low to the next
     int parts, F, L, r;
 
+    // Row t's adapter, -1 without one.
+    __device__ __forceinline__ int adapter(int64_t t) const {
+        const int64_t i = idx[t];
+        return i >= 0 && i < L ? (int)i : -1;
+    }
+    // Four low values of row t, ranks from q on: the sum of the parts.
+    __device__ __forceinline__ float4 low4(int64_t t, int q) const {
+        const float* at = low + t * r + q;
+        float4 v = *reinterpret_cast<const float4*>(at);
+        for (int p = 1; p < parts; ++p) {
+            const float4 x = *reinterpret_cast<const float4*>(at + p * part);
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        return v;
+    }
+};
+
+// gemm_split_kernel, few rows, each usually with another adapter: four rows at a time. Their B values
+// are requested before their low values are staged, and towards L2 while the projection is
+// computed. Loops, not unrolled code: a launch meets each instruction once, out of L2.
+struct AdapterFew : AdapterSide {
+    static constexpr bool kFollows = true;
+    static constexpr int kGroup = 4, kRows = 256;
+    static constexpr int kFloats = kGroup * EP_ADAPTER_MAX_RANK + kRows;     // low, the rows' adapters
+    struct State {};
+
+    __device__ __forceinline__ void ahead(float* shared, int64_t row0, int rows, int m) const {
+        int* ids = reinterpret_cast<int*>(shared + kGroup * EP_ADAPTER_MAX_RANK);
+        const int tid = threadIdx.x & 127;
+        for (int j = tid; j < rows; j += 128) ids[j] = adapter(row0 + j);
+        epilogue_barrier();
+        if (m >= F) return;
+        for (int j = 0; j < rows; ++j) {
+            if (ids[j] < 0) continue;
+            const char* at = reinterpret_cast<const char*>(b + ((int64_t)ids[j] * F + m) * r);
+            for (int q = 0; q < r * 2; q += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + q));
+        }
+    }
+    __device__ __forceinline__ void apply(State&, float* shared, float (&v)[kGroup], int64_t row0, int rows, int c,
+                                          int m) const {
+        const int* ids = reinterpret_cast<const int*>(shared + kGroup * EP_ADAPTER_MAX_RANK) + c;
+        const int tid = threadIdx.x & 127;
+        uint4 u[kGroup][2];
+        const auto load_b = [&](int q0) {
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                const int i = c + j < rows && m < F ? ids[j] : -1;
+                const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q0;
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    u[j][g] = i >= 0 && q0 + g * 8 < r ? *reinterpret_cast<const uint4*>(at + g * 8) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        load_b(0);
+        epilogue_barrier();          // the four rows before have been read
+        for (int e = tid; e < r; e += 128) {          // four rows of r / 4 float4
+            const int j = e / (r / 4), q = (e % (r / 4)) * 4;
+            const float4 x = c + j < rows && ids[j] >= 0 ? low4(row0 + c + j, q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            *reinterpret_cast<float4*>(shared + j * r + q) = x;
+        }
+        epilogue_barrier();
+#pragma unroll 1
+        for (int q0 = 0; q0 < r; q0 += 16) {
+            if (q0 > 0) load_b(q0);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (q0 + g * 8 >= r) break;
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) {
+                    if (c + j >= rows || ids[j] < 0) continue;
+                    const float4* l = reinterpret_cast<const float4*>(shared + j * r + q0 + g * 8);
+                    const float4 x = l[0], y = l[1];
+                    v[j] = fmaf(x.x, bf16_lo(u[j][g].x), v[j]);
+                    v[j] = fmaf(x.y, bf16_hi(u[j][g].x), v[j]);
+                    v[j] = fmaf(x.z, bf16_lo(u[j][g].y), v[j]);
+                    v[j] = fmaf(x.w, bf16_hi(u[j][g].y), v[j]);
+                    v[j] = fmaf(y.x, bf16_lo(u[j][g].z), v[j]);
+                    v[j] = fmaf(y.y, bf16_hi(u[j][g].z), v[j]);
+                    v[j] = fmaf(y.z, bf16_lo(u[j][g].w), v[j]);
+                    v[j] = fmaf(y.w, bf16_hi(u[j][g].w), v[j]);
+                }
+            }
+        }
+    }
+};
+
+// gemm_kernel, many rows: eight rows at a time. Their low values are staged in shared memory by the
+// four warps, the next eight's loaded meanwhile. Eight rows of one adapter (prompts) keep B_i's
+// values of the feature in registers, as long as the adapter stays; of several, each row's are
+// loaded while the row before is worked on.
+constexpr int kStageRanks = 128, kStageStride = kStageRanks + 4, kHeld = 64;
+
+struct AdapterWide : AdapterSide {
+    static constexpr bool kFollows = true;
+    static constexpr int kGroup = 8;
+    static constexpr int kFloats = 2 * kGroup * kStageStride;
+
     struct State {
         int64_t row0;
-        int rows, m, cur, buf;
-        uint32_t w[kStageRanks / 2];
+        int rows, m, held, buf;
+        float2 w[kHeld / 2];
     };
 
-    // This thread's eight low values of the sixteen rows from row c on, ranks from q0 on.
+    // This thread's eight low values of the eight rows from row c on, ranks from q0 on.
     __device__ __forceinline__ void load(const State& s, int c, int q0, float4 (&v)[2]) const {
-        const int tid = threadIdx.x & 127, row = c + (tid >> 3), q = q0 + (tid & 7) * 8;
+        const int tid = threadIdx.x & 127, row = c + (tid >> 4), q = q0 + (tid & 15) * 8;
         v[0] = v[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (row < s.rows && q < r) {
-            const float* at = low + (s.row0 + row) * r + q;
-            for (int p = 0; p < parts; ++p, at += part) {
-                const float4 x = *reinterpret_cast<const float4*>(at), y = *reinterpret_cast<const float4*>(at + 4);
-                v[0].x += x.x, v[0].y += x.y, v[0].z += x.z, v[0].w += x.w;
-                v[1].x += y.x, v[1].y += y.y, v[1].z += y.z, v[1].w += y.w;
-            }
+            v[0] = low4(s.row0 + row, q);
+            v[1] = low4(s.row0 + row, q + 4);
         }
     }
     __device__ __forceinline__ void put(float* shared, int buf, const float4 (&v)[2]) const {
         const int tid = threadIdx.x & 127;
-        float4* at = reinterpret_cast<float4*>(shared + (buf * kStageRows + (tid >> 3)) * kStageStride + (tid & 7) * 8);
+        float4* at = reinterpret_cast<float4*>(shared + (buf * kGroup + (tid >> 4)) * kStageStride + (tid & 15) * 8);
         at[0] = v[0];
         at[1] = v[1];
     }
-    // B's lines of this tile towards L2, while the projection is computed.
-    __device__ __forceinline__ void ahead(int64_t row0, int rows, int m) const {
-        if (m >= F) return;
-        for (int j = 0; j < rows; ++j) {
-            const int64_t id = idx[row0 + j];
-            if (id < 0 || id >= L) continue;
-            const char* at = reinterpret_cast<const char*>(b + (id * F + m) * r);
-            for (int q = 0; q < r * 2; q += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + q));
-        }
-    }
     __device__ __forceinline__ void begin(State& s, float* shared, int64_t row0, int rows, int m) const {
-        s.row0 = row0, s.rows = rows, s.m = m, s.cur = -1, s.buf = 0;
+        s.row0 = row0, s.rows = rows, s.m = m, s.held = -1, s.buf = 0;
         float4 v[2];
         load(s, 0, 0, v);
         epilogue_barrier();          // the tile before has been read
         put(shared, 0, v);
         epilogue_barrier();
     }
-    __device__ __forceinline__ void apply(State& s, float* shared, float (&v)[32], int c) const {
+    // B_i's values of this feature, kHeld ranks from q0 on.
+    __device__ __forceinline__ void load_b(const State& s, int i, int q0, uint4 (&u)[kHeld / 8]) const {
+        const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + s.m) * r + q0;
+#pragma unroll
+        for (int g = 0; g < kHeld / 8; ++g)
+            u[g] = i >= 0 && s.m < F && q0 + g * 8 < r ? *reinterpret_cast<const uint4*>(at + g * 8) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void apply(State& s, float* shared, float (&v)[kGroup], int64_t, int, int c, int) const {
         const int lane = threadIdx.x & 31;
-        int id = -1;
-        if (c + lane < s.rows) {
-            const int64_t i = idx[s.row0 + c + lane];
-            id = i >= 0 && i < L ? (int)i : -1;
-        }
+        const int id = lane < kGroup && c + lane < s.rows ? adapter(s.row0 + c + lane) : -1;
+        const int first = __shfl_sync(0xFFFFFFFFu, id, 0);
+        const bool one = __all_sync(0xFFFFFFFFu, id == first || lane >= kGroup || c + lane >= s.rows);
+        float2 acc[kGroup];
 #pragma unroll
-        for (int h = 0; h < 32; h += kStageRows) {
-            if (c + h >= s.rows) break;
-            for (int q0 = 0; q0 < r; q0 += kStageRanks) {
-                float4 next[2];
-                const bool last = q0 + kStageRanks >= r;
-                load(s, last ? c + h + kStageRows : c + h, last ? 0 : q0 + kStageRanks, next);
-                if (r > kStageRanks) s.cur = -1;
-                const float* stage = shared + s.buf * kStageRows * kStageStride;
+        for (int j = 0; j < kGroup; ++j) acc[j] = make_float2(v[j], 0.0f);
+        for (int s0 = 0; s0 < r; s0 += kStageRanks) {
+            float4 next[2];
+            const bool last = s0 + kStageRanks >= r;
+            load(s, last ? c + kGroup : c, last ? 0 : s0 + kStageRanks, next);
+            const float* stage = shared + s.buf * kGroup * kStageStride;
+            for (int q0 = s0; q0 < min(r, s0 + kStageRanks); q0 += kHeld) {
+                const float4* l = reinterpret_cast<const float4*>(stage + q0 - s0);
+                if (one) {
+                    if (first >= 0) {
+                        if (s.held != first || r > kHeld) {
+                            uint4 u[kHeld / 8];
+                            load_b(s, first, q0, u);
 #pragma unroll
-                for (int j = 0; j < kStageRows; ++j) {
-                    const int i = __shfl_sync(0xFFFFFFFFu, id, h + j);
-                    if (i < 0) continue;
-                    if (i != s.cur) {
-                        s.cur = i;
-                        const __nv_bfloat16* at = b + ((int64_t)i * F + s.m) * r + q0;
+                            for (int g = 0; g < kHeld / 8; ++g) {
+                                s.w[4 * g] = make_float2(bf16_lo(u[g].x), bf16_hi(u[g].x));
+                                s.w[4 * g + 1] = make_float2(bf16_lo(u[g].y), bf16_hi(u[g].y));
+                                s.w[4 * g + 2] = make_float2(bf16_lo(u[g].z), bf16_hi(u[g].z));
+                                s.w[4 * g + 3] = make_float2(bf16_lo(u[g].w), bf16_hi(u[g].w));
+                            }
+                            s.held = first;
+                        }
 #pragma unroll
-                        for (int g = 0; g < kStageRanks / 8; ++g) {
-                            uint4 u = make_uint4(0, 0, 0, 0);
-                            if (s.m < F && q0 + g * 8 < r) u = *reinterpret_cast<const uint4*>(at + g * 8);
-                            s.w[4 * g] = u.x, s.w[4 * g + 1] = u.y, s.w[4 * g + 2] = u.z, s.w[4 * g + 3] = u.w;
+                        for (int g = 0; g < kHeld / 8; ++g) {
+                            if (q0 + g * 8 >= r) break;
+#pragma unroll
+                            for (int j = 0; j < kGroup; ++j) {
+                                const float4 x = l[j * (kStageStride / 4) + 2 * g], y = l[j * (kStageStride / 4) + 2 * g + 1];
+                                fma_pair(acc[j], make_float2(x.x, x.y), s.w[4 * g]);
+                                fma_pair(acc[j], make_float2(x.z, x.w), s.w[4 * g + 1]);
+                                fma_pair(acc[j], make_float2(y.x, y.y), s.w[4 * g + 2]);
+                                fma_pair(acc[j], make_float2(y.z, y.w), s.w[4 * g + 3]);
+                            }
                         }
                     }
-                    const float4* l = reinterpret_cast<const float4*>(stage + j * kStageStride);
-                    float acc = v[h + j];
+                } else {
+                    uint4 u[2][kHeld / 8];
+                    load_b(s, first, q0, u[0]);
 #pragma unroll
-                    for (int g = 0; g < kStageRanks / 8; ++g) {
-                        if (q0 + g * 8 >= r) break;
-                        const float4 lo = l[2 * g], hi = l[2 * g + 1];
-                        acc = fmaf(lo.x, bf16_lo(s.w[4 * g]), acc);
-                        acc = fmaf(lo.y, bf16_hi(s.w[4 * g]), acc);
-                        acc = fmaf(lo.z, bf16_lo(s.w[4 * g + 1]), acc);
-                        acc = fmaf(lo.w, bf16_hi(s.w[4 * g + 1]), acc);
-                        acc = fmaf(hi.x, bf16_lo(s.w[4 * g + 2]), acc);
-                        acc = fmaf(hi.y, bf16_hi(s.w[4 * g + 2]), acc);
-                        acc = fmaf(hi.z, bf16_lo(s.w[4 * g + 3]), acc);
-                        acc = fmaf(hi.w, bf16_hi(s.w[4 * g + 3]), acc);
+                    for (int j = 0; j < kGroup; ++j) {
+                        const int i = __shfl_sync(0xFFFFFFFFu, id, j);
+                        if (j + 1 < kGroup) load_b(s, __shfl_sync(0xFFFFFFFFu, id, j + 1), q0, u[(j + 1) & 1]);
+                        if (i < 0) continue;
+                        float2 even = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int g = 0; g < kHeld / 8; ++g) {
+                            if (q0 + g * 8 >= r) break;
+                            const float4 x = l[j * (kStageStride / 4) + 2 * g], y = l[j * (kStageStride / 4) + 2 * g + 1];
+                            const uint4 w = u[j & 1][g];
+                            fma_pair(acc[j], make_float2(x.x, x.y), make_float2(bf16_lo(w.x), bf16_hi(w.x)));
+                            fma_pair(even, make_float2(x.z, x.w), make_float2(bf16_lo(w.y), bf16_hi(w.y)));
+                            fma_pair(acc[j], make_float2(y.x, y.y), make_float2(bf16_lo(w.z), bf16_hi(w.z)));
+                            fma_pair(even, make_float2(y.z, y.w), make_float2(bf16_lo(w.w), bf16_hi(w.w)));
+                        }
+                        acc[j].x += even.x;
+                        acc[j].y += even.y;
                     }
-                    v[h + j] = acc;
                 }
-                s.buf ^= 1;
-                put(shared, s.buf, next);
-                epilogue_barrier();
             }
+            s.buf ^= 1;
+            put(shared, s.buf, next);
+            epilogue_barrier();
         }
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) v[j] = acc[j].x + acc[j].y;
     }
 };
 
@@ -390,6 +502,8 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         const AdapterArgs g{reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(a), scales,
                             adapter_idx, order, prefix, reinterpret_cast<float*>(workspace), sh->num_rows,
                             sh->in_features, sh->num_adapters, sh->rank, ws.parts, launch->error_flags};
+        const AdapterSide side{reinterpret_cast<const __nv_bfloat16*>(b), g.low, adapter_idx, (int64_t)g.T * g.r, g.parts,
+                               sh->out_features, g.L, g.r};
         cudaError_t e = cudaSuccess;
         if (g.T <= kLowRows || g.L == 0) {
             e = launch_low_of<false>(g, launch->stream);
@@ -399,10 +513,7 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
             if (e == cudaSuccess) e = launch_low_of<true>(g, launch->stream);
         }
         if (e == cudaSuccess)
-            e = launch_gemm<kForward>(maps, m,
-                                      AdapterExtra{reinterpret_cast<const __nv_bfloat16*>(b), g.low, adapter_idx,
-                                                   (int64_t)g.T * g.r, g.parts, sh->out_features, g.L, g.r},
-                                      launch->stream);
+            e = launch_gemm<kForward>(maps, m, AdapterWide{side}, AdapterFew{side}, launch->stream);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return end_call(launch);

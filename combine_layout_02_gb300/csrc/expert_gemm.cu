@@ -106,7 +106,7 @@ ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* othe
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows > 0) {
-        cudaError_t e = launch_gemm<D>(maps, a, NoExtra{}, launch->stream);
+        cudaError_t e = launch_gemm<D>(maps, a, NoExtra{}, NoExtra{}, launch->stream);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return end_call(launch);

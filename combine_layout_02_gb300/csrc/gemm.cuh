@@ -77,7 +77,7 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 
 // 32 consecutive columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
     uint32_t r[32];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -90,6 +90,26 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 4, 8 consecutive columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[4]) {
+    uint32_t r[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -215,12 +235,13 @@ struct TileWalk {
     }
 };
 
-// Epilogue of one tile chunk of 32 columns: forward / dgrad. A lane holds one feature of 32 rows;
+// Epilogue of one tile chunk of G columns: forward / dgrad. A lane holds one feature of G rows;
 // lanes exchange in pairs, so that a store covers 32 features of two rows (64 bytes each).
-__device__ __forceinline__ void store_features(const float (&v)[32], __nv_bfloat16* out, int ld, int64_t row0, int rows,
+template <int G>
+__device__ __forceinline__ void store_features(const float (&v)[G], __nv_bfloat16* out, int ld, int64_t row0, int rows,
                                                int feature, int M, int lane) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
+    for (int j = 0; j < G; j += 2) {
         if (j >= rows) break;
         const bool odd = lane & 1;
         const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
@@ -241,18 +262,20 @@ __device__ __forceinline__ void store_columns(const float (&v)[32], __nv_bfloat1
     }
 }
 
-// What an epilogue adds to the sums before they are rounded. All 128 epilogue threads call begin for
-// the rows row0 .. row0 + rows - 1 of a tile and then apply for each 32 of them in order: v[j] is
-// output feature m of row row0 + c + j. `shared`: kFloats floats of the block. kFollows: the kernel
-// directly follows one of this library after which the call's inputs are complete; only the epilogue
-// waits for that kernel itself. ahead: called while the products run, before that wait.
+// What an epilogue adds to the sums before they are rounded; all 128 epilogue threads make the calls
+// together, each for output feature m. `shared`: kFloats floats of the block. kFollows: the kernel
+// directly follows one of this library after which the call's inputs are complete; only the
+// epilogue waits for that kernel itself.
+//   gemm_kernel:        begin for rows row0 .. row0 + rows - 1 of a tile, then apply for each kGroup of
+//                       them in order: v[j] belongs to row row0 + c + j
+//   gemm_split_kernel:  ahead for the CTA's rows while the products run (before that wait), then apply
 struct NoExtra {
     static constexpr bool kFollows = false;
-    static constexpr int kFloats = 1;
+    static constexpr int kFloats = 4, kGroup = 32;
     struct State {};
-    __device__ __forceinline__ void ahead(int64_t, int, int) const {}
+    __device__ __forceinline__ void ahead(float*, int64_t, int, int) const {}
     __device__ __forceinline__ void begin(State&, float*, int64_t, int, int) const {}
-    __device__ __forceinline__ void apply(State&, float*, float (&)[32], int) const {}
+    __device__ __forceinline__ void apply(State&, float*, float (&)[32], int64_t, int, int, int) const {}
 };
 
 // The four epilogue warps: a barrier, and whether all of them have `mine` (the same answer to all,
@@ -429,19 +452,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int rows = min(t.n, t.end - t.n0);
             typename Extra::State state;
             if (D != kWgrad) extra.begin(state, s_extra, t.n0, rows, m);
-            for (int c = 0; c < (D == kWgrad ? t.n : rows); c += 32) {
-                float v[32];
+            constexpr int G = Extra::kGroup;
+            for (int c = 0; c < (D == kWgrad ? t.n : rows); c += G) {
+                float v[G];
                 if (some) {
-                    tmem_load32(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
+                    tmem_load(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    for (int j = 0; j < G; ++j) v[j] = 0.0f;
                 }
-                if (D == kWgrad) {
+                if constexpr (D == kWgrad) {
                     if (m < a.M)
                         store_columns(v, a.out + ((int64_t)t.e * a.M + m) * a.N + t.n0 + c, a.N - t.n0 - c);
                 } else {
-                    extra.apply(state, s_extra, v, c);
+                    extra.apply(state, s_extra, v, t.n0, rows, c, m);
                     store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
                 }
             }
@@ -470,11 +494,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// fp32 value at the same shared-memory address of CTA `rank` of the cluster.
-__device__ __forceinline__ float peer_value(uint32_t addr, uint32_t rank) {
+// The same shared-memory address in CTA `rank` of the cluster, and a value there.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
     uint32_t at;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ float peer_value(uint32_t at) {
+    float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
 }
@@ -618,19 +645,19 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     const int share = (rows + a.split - 1) / a.split, lo = rank * share, hi = min(rows, lo + share);   // of the rows
     bool ok = has;
     if (has && warp >= 2) {
-        extra.ahead(t.n0 + lo, hi - lo, m);
+        extra.ahead(s_extra, t.n0 + lo, hi - lo, m);
         ok = epilogue_all(mbar_wait(&done, 0, &dead, a.err));
         tc_fence_after();
     }
     if (Extra::kFollows && warp >= 2) pdl_wait();
+    constexpr int G = Extra::kGroup;
     if (a.split == 1) {
         if (ok && warp >= 2) {
             typename Extra::State state;
-            extra.begin(state, s_extra, t.n0, rows, m);
-            for (int c = 0; c < rows; c += 32) {
-                float v[32];
-                tmem_load32(tmem + c + ((uint32_t)quarter << 21), v);
-                extra.apply(state, s_extra, v, c);
+            for (int c = 0; c < rows; c += G) {
+                float v[G];
+                tmem_load(tmem + c + ((uint32_t)quarter << 21), v);
+                extra.apply(state, s_extra, v, t.n0, rows, c, m);
                 store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
             }
         }
@@ -638,17 +665,16 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         float* part = reinterpret_cast<float*>(smem);      // [columns][128]; every product has read its stage
         const bool some = kb1 > kb0;
         if (ok && warp >= 2) {
-            for (int c = 0; c < rows; c += 32) {
-                float v[32];
+            for (int c = 0; c < rows; c += 8) {
+                float v[8];
                 if (some) {
-                    tmem_load32(tmem + c + ((uint32_t)quarter << 21), v);
+                    tmem_load(tmem + c + ((uint32_t)quarter << 21), v);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
                 }
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (c + j < rows) part[(c + j) * kBM + m_local] = v[j];
+                for (int j = 0; j < 8; ++j) part[(c + j) * kBM + m_local] = v[j];     // up to bn columns
             }
         }
         __syncwarp();
@@ -656,16 +682,17 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         if (ok && warp >= 2 && lo < hi) {
             const uint32_t at = smem_addr(part);
             typename Extra::State state;
-            extra.begin(state, s_extra, t.n0 + lo, hi - lo, m);
-            for (int c = lo; c < hi; c += 32) {
-                float v[32];
+            for (int c = lo; c < hi; c += G) {
+                float v[G];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    v[j] = 0.0f;
-                    if (c + j < hi)
-                        for (int r = 0; r < a.split; ++r) v[j] += peer_value(at + ((c + j) * kBM + m_local) * 4, r);
+                for (int j = 0; j < G; ++j) v[j] = 0.0f;
+                for (int r = 0; r < a.split; ++r) {
+                    const uint32_t peer = peer_addr(at, r);
+#pragma unroll
+                    for (int j = 0; j < G; ++j)
+                        if (c + j < hi) v[j] += peer_value(peer + ((c + j) * kBM + m_local) * 4);
                 }
-                extra.apply(state, s_extra, v, c - lo);
+                extra.apply(state, s_extra, v, t.n0 + lo, hi - lo, c - lo, m);
                 store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
             }
         }
@@ -741,18 +768,18 @@ cudaError_t launch_gemm_as(Kernel kernel, unsigned blocks, unsigned threads, uns
 }
 
 // Launches the product (a.num_rows > 0) as gemm_tiles has laid it out.
-template <Direction D, class Extra>
-cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Extra& extra, cudaStream_t stream) {
+template <Direction D, class Wide, class Few>
+cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Wide& wide, const Few& few, cudaStream_t stream) {
     const int64_t tiles = gemm_most_tiles(a, D == kWgrad), sms = sm_count();
     if constexpr (D != kWgrad) {
         if (gemm_by_split(a)) {
             if (tiles * a.split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-            return launch_gemm_as(gemm_split_kernel<D, Extra>, (unsigned)(tiles * a.split), kSplitThreads,
-                                  (unsigned)a.split, stream, maps, a, extra);
+            return launch_gemm_as(gemm_split_kernel<D, Few>, (unsigned)(tiles * a.split), kSplitThreads,
+                                  (unsigned)a.split, stream, maps, a, few);
         }
     }
-    return launch_gemm_as(gemm_kernel<D, Extra>, (unsigned)(tiles < sms ? tiles : sms), kGemmThreads, 1, stream, maps, a,
-                          extra);
+    return launch_gemm_as(gemm_kernel<D, Wide>, (unsigned)(tiles < sms ? tiles : sms), kGemmThreads, 1, stream, maps, a,
+                          wide);
 }
 
 }  // namespace ep
