@@ -18,6 +18,7 @@ struct GemmArgs {
     int C;                     // contracted features (wgrad: the rows)
     int bn, box, stages;       // columns of the widest tile, rows of one load box of B, stages
     int split;                 // CTAs that share a tile's contraction
+    int smem;                  // bytes of dynamic shared memory
     uint32_t* err;
 };
 
@@ -67,6 +68,30 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
+}
+
+// Pair forms (cta_group::2): one thread of the leader CTA multiplies for both.
+__device__ __forceinline__ void tmem_alloc2(uint32_t* slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free2(uint32_t at, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+}
+// Arrives at the barrier at this offset in both CTAs.
+__device__ __forceinline__ void tc_commit2(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
 }
 
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
@@ -148,6 +173,51 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     return mbar_wait_slow(bar, parity, dead, err);
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same shared-memory address in CTA `rank` of the cluster, and a value there.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ float peer_value(uint32_t at) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t at) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+}
+// Orders shared-memory writes of one CTA of a pair before the other's products, around an arrival.
+__device__ __forceinline__ void cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ void mbar_expect_peer(uint32_t at, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(at), "r"(bytes)
+                 : "memory");
+}
+// Pair loads: into this CTA's shared memory, completing on a barrier of either CTA (cluster address).
+__device__ __forceinline__ void tma_load2_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load2_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -193,14 +263,15 @@ struct Tile {
     int begin, end;            // the expert's rows
 };
 
-// Walks the tiles of all experts in order: expert by expert, M tiles innermost.
+// Walks the tiles of all experts in order: expert by expert, M tiles (of a pair's 256) innermost.
 //   forward / dgrad: an expert's rows are cut into ceil(rows / bn) nearly even column tiles
 //   wgrad:           N is cut into tiles of bn
+// A tile's columns are a multiple of 32 (16 for each CTA).
 template <Direction D>
 struct TileWalk {
     const GemmArgs& a;
     int e = -1, first = 0, count = 0, begin = 0, end = 0, mt, per = 0, nt = 0;
-    __device__ TileWalk(const GemmArgs& args) : a(args), mt((args.M + kBM - 1) / kBM) {}
+    __device__ TileWalk(const GemmArgs& args) : a(args), mt((args.M + 2 * kBM - 1) / (2 * kBM)) {}
     // Tile number t (non-decreasing from call to call); false past the last one.
     __device__ bool at(int t, Tile& out) {
         while (t >= first + count) {
@@ -214,22 +285,22 @@ struct TileWalk {
                 nt = (a.N + a.bn - 1) / a.bn;
             } else {
                 nt = (rows + a.bn - 1) / a.bn;
-                per = nt > 0 ? ((rows + nt - 1) / nt + 15) & ~15 : 16;
+                per = nt > 0 ? ((rows + nt - 1) / nt + 31) & ~31 : 32;
                 if (nt > 0) nt = (rows + per - 1) / per;
             }
             count = nt * mt;
         }
         const int q = t - first, c = q / mt;
         out.e = e;
-        out.m0 = (q - c * mt) * kBM;
+        out.m0 = (q - c * mt) * 2 * kBM;
         out.begin = begin;
         out.end = end;
         if (D == kWgrad) {
             out.n0 = c * per;
-            out.n = (min(per, a.N - out.n0) + 15) & ~15;
+            out.n = (min(per, a.N - out.n0) + 31) & ~31;
         } else {
             out.n0 = begin + c * per;
-            out.n = (min(per, end - out.n0) + 15) & ~15;
+            out.n = (min(per, end - out.n0) + 31) & ~31;
         }
         return true;
     }
@@ -291,11 +362,18 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
     return all != 0;
 }
 
-// D[m][n] over tiles of 128 x up to 256, one CTA per SM walking over tiles. The weights are the M side
-// and the rows the N side, so that a tile has as many columns (a multiple of 16) as its expert has
-// rows left: no padding of the experts. Warp 0 loads (TMA), warp 1 multiplies (tcgen05.mma, fp32
-// sums in tensor memory, two accumulators of 256 columns in turn), warp 2 clears the rows of a
-// wgrad tail that belong to the next expert, warps 4 to 7 write the previous tile meanwhile.
+// D[m][n] over tiles of 256 x up to 256, a pair of CTAs per tile (cta_group::2), each pair walking over
+// tiles. The weights are the M side and the rows the N side, so that a tile has as many columns as
+// its expert has rows left (to a multiple of 32): no padding of the experts. Each CTA loads its 128 of
+// the M side and half of the columns; the tensor cores of both read both halves, which halves the
+// shared memory traffic of the columns (one CTA per tile, 128 x 256, was bound by it: 1.13
+// PFLOP/s). Warp 0 loads (TMA), warp 1 of the leader multiplies (tcgen05.mma, fp32 sums in tensor
+// memory, two accumulators of 256 columns in turn), warp 2 clears the rows of a wgrad tail that belong
+// to the next expert, warps 4 to 7 write the tile before meanwhile.
+//   full[s]   leader's: both CTAs' loads (an arrival of each, and the bytes)
+//   empty[s]  each CTA's: the products that read stage s are done
+//   tail[s]   each CTA's: its loads of a stage that has rows to clear; the clearing warp then
+//             arrives at full[s] in the producer's place
 template <Direction D, class Extra>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
@@ -306,27 +384,31 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __shared__ __align__(16) float s_extra[Extra::kFloats];
     constexpr bool kAMn = D != kForward, kBMn = D == kWgrad;
     unsigned char* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    const uint32_t stage_bytes = kABytes + (uint32_t)a.bn * 128;
+    const uint32_t stage_bytes = kABytes + (uint32_t)a.bn * 64;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&maps.a);
         tma_prefetch_map(&maps.b);
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], D == kWgrad ? 2 : 1);     // the product, and the warp that clears tails
+            mbar_init(&full[s], 2);
+            mbar_init(&empty[s], 1);
             mbar_init(&tail[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4);
+            mbar_init(&acc_empty[i], 8);
         }
         mbar_init(&drain, 1);
         dead = 0;
     }
-    if (warp == 1) tmem_alloc(&s_tmem, 512);
+    __syncwarp();
+    if (warp == 1) tmem_alloc2(&s_tmem, 512);
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    cluster_barrier();          // the barriers and the tensor memory of both CTAs are there
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     if (!Extra::kFollows || warp >= 4) pdl_wait();
@@ -336,10 +418,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         Tile t;
         uint32_t it = 0;
         bool ok = true;
-        for (int i = blockIdx.x; ok && walk.at(i, t); i += gridDim.x) {
+        for (int i = first; ok && walk.at(i, t); i += step) {
             const int depth = D == kWgrad ? t.end - t.begin : a.C;
-            const int boxes = kBMn ? (t.n + 63) / 64 : (t.n + a.box - 1) / a.box;
-            const uint32_t bytes = kABytes + (uint32_t)boxes * (kBMn ? 64 : a.box) * 128;
+            const int half = t.n / 2, m0 = t.m0 + (int)rank * kBM, n0 = t.n0 + (int)rank * half;
+            const int box = kBMn ? 64 : a.box, boxes = (half + box - 1) / box;
+            const uint32_t bytes = kABytes + (uint32_t)(boxes * box) * 128;
             for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
                 const uint32_t s = it % a.stages;
                 if (!mbar_wait(&empty[s], ((it / a.stages) & 1) ^ 1, &dead, a.err)) {
@@ -348,45 +431,53 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 unsigned char* sa = smem + s * stage_bytes;
                 unsigned char* sb = sa + kABytes;
-                mbar_expect_bytes(&full[s], bytes);
-                if (D == kForward) {
-                    tma_load_3d(sa, &maps.a, k0, t.m0, t.e, &full[s]);
-                } else if (D == kDgrad) {
-                    tma_load_3d(sa, &maps.a, t.m0, k0, t.e, &full[s]);
-                    tma_load_3d(sa + kMnChunk, &maps.a, t.m0 + 64, k0, t.e, &full[s]);
+                const bool clear = D == kWgrad && depth - k0 < kBK && ((depth - k0) & 15) != 0;
+                const uint32_t own = smem_addr(&tail[s]), shared = peer_addr(smem_addr(&full[s]), 0);
+                uint32_t bar = shared;
+                if (clear) {
+                    bar = peer_addr(own, rank);
+                    mbar_expect_bytes(&tail[s], bytes);
                 } else {
-                    tma_load_2d(sa, &maps.a, t.m0, t.begin + k0, &full[s]);
-                    tma_load_2d(sa + kMnChunk, &maps.a, t.m0 + 64, t.begin + k0, &full[s]);
+                    mbar_expect_peer(shared, bytes);
+                }
+                if (D == kForward) {
+                    tma_load2_3d(sa, &maps.a, k0, m0, t.e, bar);
+                } else if (D == kDgrad) {
+                    tma_load2_3d(sa, &maps.a, m0, k0, t.e, bar);
+                    tma_load2_3d(sa + kMnChunk, &maps.a, m0 + 64, k0, t.e, bar);
+                } else {
+                    tma_load2_2d(sa, &maps.a, m0, t.begin + k0, bar);
+                    tma_load2_2d(sa + kMnChunk, &maps.a, m0 + 64, t.begin + k0, bar);
                 }
                 for (int b = 0; b < boxes; ++b) {
-                    if (kBMn) tma_load_2d(sb + b * kMnChunk, &maps.b, t.n0 + b * 64, t.begin + k0, &full[s]);
-                    else tma_load_2d(sb + b * a.box * 128, &maps.b, k0, t.n0 + b * a.box, &full[s]);
+                    if (kBMn) tma_load2_2d(sb + b * kMnChunk, &maps.b, n0 + b * 64, t.begin + k0, bar);
+                    else tma_load2_2d(sb + b * box * 128, &maps.b, k0, n0 + b * box, bar);
                 }
             }
         }
-        if (!ok) {     // wait, with a limit, for the copies still in flight
-            for (uint32_t q = it > (uint32_t)a.stages ? it - a.stages : 0; q < it; ++q)
-                mbar_wait_bounded(&full[q % a.stages], (q / a.stages) & 1, kGemmWaitNs / 8);
-        }
-    } else if (warp == 1 && lane == 0) {
+        // The last loads' stages are free: nothing more arrives at this CTA's barriers. (Where a role has
+        // given up, that is waited for as long as copies in flight may take.)
+        for (uint32_t q = it; q < it + a.stages; ++q)
+            mbar_wait_bounded(&empty[q % a.stages], ((q / a.stages) & 1) ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
         TileWalk<D> walk(a);
         Tile t;
-        uint32_t it = 0, used = 0, tails = 0;      // tails: a phase bit per stage
+        uint32_t it = 0, used = 0;
         bool ok = true;
-        for (int i = blockIdx.x; ok && walk.at(i, t); i += gridDim.x) {
+        for (int i = first; ok && walk.at(i, t); i += step) {
             const int depth = D == kWgrad ? t.end - t.begin : a.C;
             if (depth <= 0) continue;
             const uint32_t acc = used & 1;
             if (!(ok = mbar_wait(&acc_empty[acc], ((used >> 1) & 1) ^ 1, &dead, a.err))) break;
             tc_fence_after();
-            const uint32_t d = tmem + acc * 256, idesc = instr_desc(kBM, t.n, kAMn, kBMn);
+            const uint32_t d = tmem + acc * 256, idesc = instr_desc(2 * kBM, t.n, kAMn, kBMn);
             for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
                 const uint32_t s = it % a.stages;
                 if (!(ok = mbar_wait(&full[s], (it / a.stages) & 1, &dead, a.err))) break;
                 const int left = depth - k0;
                 if (D == kWgrad && left < kBK && (left & 15) != 0) {
-                    if (!(ok = mbar_wait(&tail[s], (tails >> s) & 1, &dead, a.err))) break;
-                    tails ^= 1u << s;
+                    cluster_fence();
+                    fence_async_smem();
                 }
                 tc_fence_after();
                 const uint32_t sa = smem_addr(smem + s * stage_bytes), sb = sa + kABytes;
@@ -394,15 +485,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kBK; k += 16) {
                     if (k >= left) break;      // 16 contracted values: 32 bytes of a row, or 16 rows
-                    tc_mma(d, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, (k0 | k) != 0);
+                    tc_mma2(d, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, (k0 | k) != 0);
                 }
-                tc_commit(&empty[s]);
+                tc_commit2(&empty[s]);
             }
-            tc_commit(&acc_full[acc]);
+            tc_commit2(&acc_full[acc]);
             ++used;
         }
         if (!ok) {
-            tc_commit(&drain);
+            tc_commit2(&drain);
             mbar_wait_bounded(&drain, 0, kGemmWaitNs / 8);
         }
     } else if (D == kWgrad && warp == 2) {
@@ -411,28 +502,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // are cleared. A row is a 128-byte line of each 64-column chunk, whatever the swizzle.
         TileWalk<D> walk(a);
         Tile t;
-        uint32_t it = 0;
-        bool ok = true;
-        for (int i = blockIdx.x; ok && walk.at(i, t); i += gridDim.x) {
+        uint32_t it = 0, phases = 0;
+        for (int i = first; walk.at(i, t); i += step) {
             const int depth = t.end - t.begin;
-            for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
-                const uint32_t s = it % a.stages;
-                if (!(ok = mbar_wait(&full[s], (it / a.stages) & 1, &dead, a.err))) break;
-                const int left = depth - k0;
-                if (left < kBK && (left & 15) != 0) {
-                    const int rows = 16 - (left & 15), chunks = 2 + (t.n + 63) / 64;
-                    for (int p = lane; p < chunks * rows * 8; p += 32) {
-                        const int c = p / (rows * 8), r = (p / 8) % rows;
-                        *reinterpret_cast<uint4*>(smem + s * stage_bytes + c * kMnChunk + (left + r) * 128 + (p & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tail[s]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
+            if (depth <= 0) continue;
+            const int blocks = (depth + kBK - 1) / kBK, left = depth - (blocks - 1) * kBK;
+            it += blocks;
+            if ((left & 15) == 0) continue;
+            const uint32_t s = (it - 1) % a.stages;
+            if (!mbar_wait(&tail[s], (phases >> s) & 1, &dead, a.err)) break;
+            phases ^= 1u << s;
+            const int rows = 16 - (left & 15), chunks = 2 + (t.n / 2 + 63) / 64;
+            for (int p = lane; p < chunks * rows * 8; p += 32) {
+                const int c = p / (rows * 8), r = (p / 8) % rows;
+                *reinterpret_cast<uint4*>(smem + s * stage_bytes + c * kMnChunk + (left + r) * 128 + (p & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
             }
+            fence_async_smem();
+            cluster_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(peer_addr(smem_addr(&full[s]), 0));
         }
     } else if (warp == 3) {
         if (blockIdx.x == 0) check_prefix(a, lane);
@@ -441,14 +530,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         Tile t;
         uint32_t used = 0;
         const int quarter = warp & 3;
-        for (int i = blockIdx.x; walk.at(i, t); i += gridDim.x) {
+        for (int i = first; walk.at(i, t); i += step) {
             const bool some = D != kWgrad || t.end > t.begin;
             const uint32_t acc = used & 1;
             if (some) {
                 if (!epilogue_all(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err))) break;
                 tc_fence_after();
             }
-            const int m = t.m0 + quarter * 32 + lane;
+            const int m = t.m0 + (int)rank * kBM + quarter * 32 + lane;
             const int rows = min(t.n, t.end - t.n0);
             typename Extra::State state;
             if (D != kWgrad) extra.begin(state, s_extra, t.n0, rows, m);
@@ -472,39 +561,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (some) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[acc]);
+                if (lane == 0) mbar_arrive_peer(peer_addr(smem_addr(&acc_empty[acc]), 0));
                 ++used;
             }
         }
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
-    if (warp == 1) tmem_free(tmem, 512);
+    cluster_barrier();          // both are done with each other's barriers and tensor memory
+    if (warp == 1) tmem_free2(tmem, 512);
     pdl_trigger();
 }
 
 // ------------------------------------------------------------------ few rows: split contraction
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The same shared-memory address in CTA `rank` of the cluster, and a value there.
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    return at;
-}
-__device__ __forceinline__ float peer_value(uint32_t at) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
-}
 
 // One warp: tile number i of all experts (forward / dgrad, as TileWalk counts them), 32 experts at a
 // time; false past the last one.
@@ -707,11 +776,11 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
 
 // ------------------------------------------------------------------ host
 
-// Whether gemm_split_kernel runs (else gemm_kernel, one CTA per SM).
+// Whether gemm_split_kernel runs (else gemm_kernel).
 inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1; }
 
 // Column tile width, stages and split.
-//   wgrad: tiles of 256 columns, one CTA per SM.
+//   wgrad: tiles of 256 columns, a pair of CTAs each.
 //   else:  tiles of twice the average rows of an expert (one group: of its rows), within [32, 256],
 //          so that most experts are one tile. Up to 64 columns the weights' loads are what counts: two CTAs per SM, and
 //          the contraction split until about four CTAs per SM have work; wider tiles are split only
@@ -731,17 +800,18 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad) {
         const int steps = ceil_div(a->C, kBK);
         while (a->split < 8 && tiles * a->split * 2 <= want && steps >= a->split * 16) a->split *= 2;
     }
-    const int stage = (int)kABytes + bn * 128, room = (gemm_by_split(*a) && bn <= 64 ? 96 : 200) * 1024;
+    const bool split = gemm_by_split(*a) && !wgrad;
+    const int stage = (int)kABytes + (split ? bn * 128 : bn * 64), room = (split && bn <= 64 ? 96 : 200) * 1024;
     a->stages = room / stage < kMaxStages ? room / stage : kMaxStages;
+    a->smem = a->stages * stage + 1024;
 }
 
-// One CTA per SM, at most as many as there can be tiles.
-inline int64_t gemm_most_tiles(const GemmArgs& a, bool wgrad) {
-    const int64_t mt = ceil_div(a.M, kBM);
+// How many tiles of `wide` M indices there can be at most.
+inline int64_t gemm_most_tiles(const GemmArgs& a, bool wgrad, int wide) {
+    const int64_t mt = ceil_div(a.M, wide);
     return mt * (wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn) : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows));
 }
 
-inline size_t gemm_smem(const GemmArgs& a) { return (size_t)a.stages * (kABytes + a.bn * 128) + 1024; }
 constexpr int kGemmSmemMax = 200 * 1024 + 1024;
 
 template <class Kernel, class Extra>
@@ -752,7 +822,7 @@ cudaError_t launch_gemm_as(Kernel kernel, unsigned blocks, unsigned threads, uns
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = gemm_smem(a);
+    cfg.dynamicSmemBytes = (size_t)a.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -770,16 +840,17 @@ cudaError_t launch_gemm_as(Kernel kernel, unsigned blocks, unsigned threads, uns
 // Launches the product (a.num_rows > 0) as gemm_tiles has laid it out.
 template <Direction D, class Wide, class Few>
 cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Wide& wide, const Few& few, cudaStream_t stream) {
-    const int64_t tiles = gemm_most_tiles(a, D == kWgrad), sms = sm_count();
     if constexpr (D != kWgrad) {
         if (gemm_by_split(a)) {
+            const int64_t tiles = gemm_most_tiles(a, false, kBM);
             if (tiles * a.split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
             return launch_gemm_as(gemm_split_kernel<D, Few>, (unsigned)(tiles * a.split), kSplitThreads,
                                   (unsigned)a.split, stream, maps, a, few);
         }
     }
-    return launch_gemm_as(gemm_kernel<D, Wide>, (unsigned)(tiles < sms ? tiles : sms), kGemmThreads, 1, stream, maps, a,
-                          wide);
+    const int64_t tiles = gemm_most_tiles(a, D == kWgrad, 2 * kBM), pairs = sm_count() / 2;
+    return launch_gemm_as(gemm_kernel<D, Wide>, 2u * (unsigned)(tiles < pairs ? tiles : pairs), kGemmThreads, 2, stream,
+                          maps, a, wide);
 }
 
 }  // namespace ep
