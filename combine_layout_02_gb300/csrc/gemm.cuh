@@ -80,10 +80,10 @@ __device__ __forceinline__ void tmem_free2(uint32_t at, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
 }
 // Arrives at the barrier at this offset in both CTAs.
-__device__ __forceinline__ void tc_commit2(uint64_t* bar) {
+__device__ __forceinline__ void tc_commit2(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_addr(bar)),
+            bar),
         "h"((uint16_t)3)
         : "memory");
 }
@@ -141,12 +141,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try_at(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
         "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
         : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
     return done != 0;
 }
@@ -154,13 +154,16 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
 constexpr uint64_t kGemmWaitNs = 2000000000ull;   // bound on one barrier wait: 2 s
 
 // Waits for a phase. Gives up when another role has (*dead), or after kGemmWaitNs (then flags
-// EP_DEVERR_TIMEOUT and sets *dead): every role then leaves its loop.
-static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* err) {
-    const uint64_t t0 = global_ns();
-    for (;;) {
+// EP_DEVERR_TIMEOUT and sets *dead): every role then leaves its loop. The global timer is first read
+// after many tries.
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead, uint32_t* err) {
+    uint64_t t0 = 0;
+    for (uint32_t n = 0;; ++n) {
         for (int i = 0; i < 64; ++i)
-            if (mbar_try(bar, parity)) return true;
+            if (mbar_try_at(bar, parity)) return true;
         if (*dead) return false;
+        if ((n & 255) != 255) continue;
+        if (t0 == 0) t0 = global_ns();
         if (global_ns() - t0 > kGemmWaitNs) {
             raise_flag(err, EP_DEVERR_TIMEOUT);
             *dead = 1;
@@ -168,10 +171,27 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
         }
     }
 }
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* err) {
-    if (mbar_try(bar, parity)) return true;
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, volatile int* dead, uint32_t* err) {
+    if (mbar_try_at(bar, parity)) return true;
     return mbar_wait_slow(bar, parity, dead, err);
 }
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* err) {
+    return mbar_wait_at(smem_addr(bar), parity, dead, err);
+}
+
+// Position in the ring of stages: the loops that issue loads and products are one thread each, whose
+// own instructions a step must not take longer than the step's product (no division by the
+// number of stages: that alone held the rate at 1.38 of 1.9 PFLOP/s).
+struct Ring {
+    uint32_t stages, s = 0, phase = 0;
+    __device__ explicit Ring(uint32_t n) : stages(n) {}
+    __device__ __forceinline__ void next() {
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -202,18 +222,21 @@ __device__ __forceinline__ void mbar_expect_peer(uint32_t at, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(at), "r"(bytes)
                  : "memory");
 }
+__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 // Pair loads: into this CTA's shared memory, completing on a barrier of either CTA (cluster address).
-__device__ __forceinline__ void tma_load2_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void tma_load2_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_addr(dst)),
+            dst),
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_load2_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_load2_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_addr(dst)),
+            dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
@@ -416,29 +439,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp == 0 && lane == 0) {
         TileWalk<D> walk(a);
         Tile t;
-        uint32_t it = 0;
+        Ring ring(a.stages);
         bool ok = true;
+        const uint32_t full0 = peer_addr(smem_addr(full), 0), tail0 = smem_addr(tail), tail0_here = peer_addr(tail0, rank);
+        const uint32_t empty0 = smem_addr(empty), smem0 = smem_addr(smem);
         for (int i = first; ok && walk.at(i, t); i += step) {
             const int depth = D == kWgrad ? t.end - t.begin : a.C;
             const int half = t.n / 2, m0 = t.m0 + (int)rank * kBM, n0 = t.n0 + (int)rank * half;
             const int box = kBMn ? 64 : a.box, boxes = (half + box - 1) / box;
             const uint32_t bytes = kABytes + (uint32_t)(boxes * box) * 128;
-            for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
-                const uint32_t s = it % a.stages;
-                if (!mbar_wait(&empty[s], ((it / a.stages) & 1) ^ 1, &dead, a.err)) {
-                    ok = false;
-                    break;
-                }
-                unsigned char* sa = smem + s * stage_bytes;
-                unsigned char* sb = sa + kABytes;
-                const bool clear = D == kWgrad && depth - k0 < kBK && ((depth - k0) & 15) != 0;
-                const uint32_t own = smem_addr(&tail[s]), shared = peer_addr(smem_addr(&full[s]), 0);
-                uint32_t bar = shared;
-                if (clear) {
-                    bar = peer_addr(own, rank);
-                    mbar_expect_bytes(&tail[s], bytes);
+            for (int k0 = 0; k0 < depth; k0 += kBK, ring.next()) {
+                if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a.err))) break;
+                const uint32_t sa = smem0 + ring.s * stage_bytes, sb = sa + kABytes;
+                uint32_t bar = full0 + ring.s * 8;
+                if (D == kWgrad && depth - k0 < kBK && ((depth - k0) & 15) != 0) {
+                    bar = tail0_here + ring.s * 8;
+                    mbar_expect_at(tail0 + ring.s * 8, bytes);
                 } else {
-                    mbar_expect_peer(shared, bytes);
+                    mbar_expect_peer(bar, bytes);
                 }
                 if (D == kForward) {
                     tma_load2_3d(sa, &maps.a, k0, m0, t.e, bar);
@@ -457,13 +475,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         // The last loads' stages are free: nothing more arrives at this CTA's barriers. (Where a role has
         // given up, that is waited for as long as copies in flight may take.)
-        for (uint32_t q = it; q < it + a.stages; ++q)
-            mbar_wait_bounded(&empty[q % a.stages], ((q / a.stages) & 1) ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
+        for (int q = 0; q < a.stages; ++q, ring.next())
+            mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
     } else if (warp == 1 && lane == 0 && rank == 0) {
         TileWalk<D> walk(a);
         Tile t;
-        uint32_t it = 0, used = 0;
+        Ring ring(a.stages);
+        uint32_t used = 0;
         bool ok = true;
+        const uint32_t full0 = smem_addr(full), empty0 = smem_addr(empty);
+        const uint64_t da0 = smem_desc(smem_addr(smem), kAMn), db0 = smem_desc(smem_addr(smem) + kABytes, kBMn);
         for (int i = first; ok && walk.at(i, t); i += step) {
             const int depth = D == kWgrad ? t.end - t.begin : a.C;
             if (depth <= 0) continue;
@@ -471,29 +492,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (!(ok = mbar_wait(&acc_empty[acc], ((used >> 1) & 1) ^ 1, &dead, a.err))) break;
             tc_fence_after();
             const uint32_t d = tmem + acc * 256, idesc = instr_desc(2 * kBM, t.n, kAMn, kBMn);
-            for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
-                const uint32_t s = it % a.stages;
-                if (!(ok = mbar_wait(&full[s], (it / a.stages) & 1, &dead, a.err))) break;
+            for (int k0 = 0; k0 < depth; k0 += kBK, ring.next()) {
+                if (!(ok = mbar_wait_at(full0 + ring.s * 8, ring.phase, &dead, a.err))) break;
                 const int left = depth - k0;
                 if (D == kWgrad && left < kBK && (left & 15) != 0) {
                     cluster_fence();
                     fence_async_smem();
                 }
                 tc_fence_after();
-                const uint32_t sa = smem_addr(smem + s * stage_bytes), sb = sa + kABytes;
-                const uint64_t da = smem_desc(sa, kAMn), db = smem_desc(sb, kBMn);
+                const uint64_t at = (uint64_t)((ring.s * stage_bytes) >> 4), da = da0 + at, db = db0 + at;
 #pragma unroll
                 for (int k = 0; k < kBK; k += 16) {
                     if (k >= left) break;      // 16 contracted values: 32 bytes of a row, or 16 rows
                     tc_mma2(d, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, (k0 | k) != 0);
                 }
-                tc_commit2(&empty[s]);
+                tc_commit2(empty0 + ring.s * 8);
             }
-            tc_commit2(&acc_full[acc]);
+            tc_commit2(smem_addr(&acc_full[acc]));
             ++used;
         }
         if (!ok) {
-            tc_commit2(&drain);
+            tc_commit2(smem_addr(&drain));
             mbar_wait_bounded(&drain, 0, kGemmWaitNs / 8);
         }
     } else if (D == kWgrad && warp == 2) {
