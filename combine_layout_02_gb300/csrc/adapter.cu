@@ -489,9 +489,12 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         gemm_tiles(&m, false);
         const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, T = (uint64_t)sh->num_rows;
         const uint64_t da[3] = {K, F, 1}, db[2] = {K, T};
-        const uint32_t ba[3] = {64, (uint32_t)kBM, 1}, bb[2] = {64, (uint32_t)m.box};
+        const uint32_t ba[3] = {64, (uint32_t)kBM, 1};
+        uint32_t bb[2] = {64, (uint32_t)m.box};
         if ((st = encode_map(&maps.a, w, 3, da, ba)) != EP_OK) return st;
         if ((st = encode_map(&maps.b, x, 2, db, bb)) != EP_OK) return st;
+        bb[1] *= 2;
+        if ((st = encode_map(&maps.b2, x, 2, db, bb)) != EP_OK) return st;
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {

@@ -99,9 +99,12 @@ ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* othe
             if ((st = encode_map(&maps.b, other, 2, db, box)) != EP_OK) return st;
         } else {
             const uint64_t da[3] = {K, F, E}, db[2] = {(uint64_t)a.C, rows};
-            const uint32_t ba[3] = {64, D == kForward ? (uint32_t)kBM : 64u, 1}, bb[2] = {64, (uint32_t)a.box};
+            const uint32_t ba[3] = {64, D == kForward ? (uint32_t)kBM : 64u, 1};
+            uint32_t bb[2] = {64, (uint32_t)a.box};
             if ((st = encode_map(&maps.a, other, 3, da, ba)) != EP_OK) return st;
             if ((st = encode_map(&maps.b, rows_a, 2, db, bb)) != EP_OK) return st;
+            bb[1] *= 2;
+            if ((st = encode_map(&maps.b2, rows_a, 2, db, bb)) != EP_OK) return st;
         }
     }
     if ((st = begin_call(launch)) != EP_OK) return st;

@@ -23,7 +23,7 @@ struct GemmArgs {
 };
 
 struct GemmMaps {
-    CUtensorMap a, b;
+    CUtensorMap a, b, b2;      // b2: b with boxes of twice the rows
 };
 
 inline bool features_ok(int f) { return f >= 8 && f % 8 == 0; }
@@ -179,9 +179,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     return mbar_wait_at(smem_addr(bar), parity, dead, err);
 }
 
-// Position in the ring of stages: the loops that issue loads and products are one thread each, whose
-// own instructions a step must not take longer than the step's product (no division by the
-// number of stages: that alone held the rate at 1.38 of 1.9 PFLOP/s).
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one != 0;
+}
+
+// Position in the ring of stages. The warps that issue loads and products must not take longer for a
+// step than the step's product, so their loops hold no division by the number of stages (that
+// alone kept the rate at 1.38 of 1.9 PFLOP/s), and the whole warp runs them, one elected lane
+// issuing, so that addresses and descriptors stay in uniform registers.
 struct Ring {
     uint32_t stages, s = 0, phase = 0;
     __device__ explicit Ring(uint32_t n) : stages(n) {}
@@ -389,14 +397,13 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
 // tiles. The weights are the M side and the rows the N side, so that a tile has as many columns as
 // its expert has rows left (to a multiple of 32): no padding of the experts. Each CTA loads its 128 of
 // the M side and half of the columns; the tensor cores of both read both halves, which halves the
-// shared memory traffic of the columns (one CTA per tile, 128 x 256, was bound by it: 1.13
-// PFLOP/s). Warp 0 loads (TMA), warp 1 of the leader multiplies (tcgen05.mma, fp32 sums in tensor
-// memory, two accumulators of 256 columns in turn), warp 2 clears the rows of a wgrad tail that belong
+// shared memory traffic of the columns. Warp 0 loads the M side (TMA), warp 1 of the leader multiplies (tcgen05.mma, fp32 sums in tensor
+// memory, two accumulators of 256 columns in turn), warp 3 loads the columns, warp 2 clears the rows of a wgrad tail that belong
 // to the next expert, warps 4 to 7 write the tile before meanwhile.
-//   full[s]   leader's: both CTAs' loads (an arrival of each, and the bytes)
+//   full[s]   leader's: both CTAs' loads (an arrival of each loading warp, and the bytes)
 //   empty[s]  each CTA's: the products that read stage s are done
 //   tail[s]   each CTA's: its loads of a stage that has rows to clear; the clearing warp then
-//             arrives at full[s] in the producer's place
+//             arrives at full[s] in the loading warps' place
 template <Direction D, class Extra>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
@@ -416,9 +423,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tma_prefetch_map(&maps.a);
         tma_prefetch_map(&maps.b);
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(&full[s], 2);
+            mbar_init(&full[s], 4);
             mbar_init(&empty[s], 1);
-            mbar_init(&tail[s], 1);
+            mbar_init(&tail[s], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -436,48 +443,54 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t tmem = s_tmem;
     if (!Extra::kFollows || warp >= 4) pdl_wait();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 || warp == 3) {
+        // Warp 0 loads the M side, warp 3 the columns.
+        if (warp == 3 && blockIdx.x == 0) check_prefix(a, lane);
         TileWalk<D> walk(a);
         Tile t;
         Ring ring(a.stages);
         bool ok = true;
         const uint32_t full0 = peer_addr(smem_addr(full), 0), tail0 = smem_addr(tail), tail0_here = peer_addr(tail0, rank);
-        const uint32_t empty0 = smem_addr(empty), smem0 = smem_addr(smem);
+        const uint32_t empty0 = smem_addr(empty), smem0 = smem_addr(smem) + (warp == 0 ? 0 : kABytes);
+        const CUtensorMap* map = warp == 0 ? &maps.a : &maps.b;
         for (int i = first; ok && walk.at(i, t); i += step) {
             const int depth = D == kWgrad ? t.end - t.begin : a.C;
             const int half = t.n / 2, m0 = t.m0 + (int)rank * kBM, n0 = t.n0 + (int)rank * half;
-            const int box = kBMn ? 64 : a.box, boxes = (half + box - 1) / box;
-            const uint32_t bytes = kABytes + (uint32_t)(boxes * box) * 128;
+            const int box = kBMn ? 64 : half > 64 ? 2 * a.box : a.box, boxes = (half + box - 1) / box;
+            const uint32_t bytes = warp == 0 ? kABytes : (uint32_t)(boxes * box) * 128;
             for (int k0 = 0; k0 < depth; k0 += kBK, ring.next()) {
                 if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a.err))) break;
-                const uint32_t sa = smem0 + ring.s * stage_bytes, sb = sa + kABytes;
-                uint32_t bar = full0 + ring.s * 8;
-                if (D == kWgrad && depth - k0 < kBK && ((depth - k0) & 15) != 0) {
-                    bar = tail0_here + ring.s * 8;
-                    mbar_expect_at(tail0 + ring.s * 8, bytes);
-                } else {
-                    mbar_expect_peer(bar, bytes);
+                const uint32_t at = smem0 + ring.s * stage_bytes;
+                const bool clear = D == kWgrad && depth - k0 < kBK && ((depth - k0) & 15) != 0;
+                const uint32_t bar = (clear ? tail0_here : full0) + ring.s * 8;
+                if (elect_one()) {
+                    if (clear) mbar_expect_at(tail0 + ring.s * 8, bytes);
+                    else mbar_expect_peer(bar, bytes);
+                    if (warp == 0) {
+                        if (D == kForward) {
+                            tma_load2_3d(at, map, k0, m0, t.e, bar);
+                        } else if (D == kDgrad) {
+                            tma_load2_3d(at, map, m0, k0, t.e, bar);
+                            tma_load2_3d(at + kMnChunk, map, m0 + 64, k0, t.e, bar);
+                        } else {
+                            tma_load2_2d(at, map, m0, t.begin + k0, bar);
+                            tma_load2_2d(at + kMnChunk, map, m0 + 64, t.begin + k0, bar);
+                        }
+                    } else if (kBMn) {
+                        for (int b = 0; b < boxes; ++b) tma_load2_2d(at + b * kMnChunk, map, n0 + b * 64, t.begin + k0, bar);
+                    } else {
+                        tma_load2_2d(at, half > 64 ? &maps.b2 : map, k0, n0, bar);
+                    }
                 }
-                if (D == kForward) {
-                    tma_load2_3d(sa, &maps.a, k0, m0, t.e, bar);
-                } else if (D == kDgrad) {
-                    tma_load2_3d(sa, &maps.a, m0, k0, t.e, bar);
-                    tma_load2_3d(sa + kMnChunk, &maps.a, m0 + 64, k0, t.e, bar);
-                } else {
-                    tma_load2_2d(sa, &maps.a, m0, t.begin + k0, bar);
-                    tma_load2_2d(sa + kMnChunk, &maps.a, m0 + 64, t.begin + k0, bar);
-                }
-                for (int b = 0; b < boxes; ++b) {
-                    if (kBMn) tma_load2_2d(sb + b * kMnChunk, &maps.b, n0 + b * 64, t.begin + k0, bar);
-                    else tma_load2_2d(sb + b * box * 128, &maps.b, k0, n0 + b * box, bar);
-                }
+                __syncwarp();
             }
         }
         // The last loads' stages are free: nothing more arrives at this CTA's barriers. (Where a role has
         // given up, that is waited for as long as copies in flight may take.)
-        for (int q = 0; q < a.stages; ++q, ring.next())
-            mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+        if (warp == 0)
+            for (int q = 0; q < a.stages; ++q, ring.next())
+                mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
+    } else if (warp == 1 && rank == 0) {
         TileWalk<D> walk(a);
         Tile t;
         Ring ring(a.stages);
@@ -501,18 +514,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 tc_fence_after();
                 const uint64_t at = (uint64_t)((ring.s * stage_bytes) >> 4), da = da0 + at, db = db0 + at;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kBK; k += 16) {
-                    if (k >= left) break;      // 16 contracted values: 32 bytes of a row, or 16 rows
-                    tc_mma2(d, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, (k0 | k) != 0);
+                    for (int k = 0; k < kBK; k += 16) {
+                        if (k >= left) break;      // 16 contracted values: 32 bytes of a row, or 16 rows
+                        tc_mma2(d, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, (k0 | k) != 0);
+                    }
+                    tc_commit2(empty0 + ring.s * 8);
                 }
-                tc_commit2(empty0 + ring.s * 8);
+                __syncwarp();
             }
-            tc_commit2(smem_addr(&acc_full[acc]));
+            if (elect_one()) tc_commit2(smem_addr(&acc_full[acc]));
+            __syncwarp();
             ++used;
         }
         if (!ok) {
-            tc_commit2(smem_addr(&drain));
+            if (elect_one()) tc_commit2(smem_addr(&drain));
             mbar_wait_bounded(&drain, 0, kGemmWaitNs / 8);
         }
     } else if (D == kWgrad && warp == 2) {
@@ -540,10 +557,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             fence_async_smem();
             cluster_fence();
             __syncwarp();
-            if (lane == 0) mbar_arrive_peer(peer_addr(smem_addr(&full[s]), 0));
+            if (lane < 2) mbar_arrive_peer(peer_addr(smem_addr(&full[s]), 0));
         }
-    } else if (warp == 3) {
-        if (blockIdx.x == 0) check_prefix(a, lane);
     } else if (warp >= 4) {
         TileWalk<D> walk(a);
         Tile t;
