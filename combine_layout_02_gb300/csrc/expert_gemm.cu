@@ -97,6 +97,9 @@ ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* othe
             const uint32_t box[2] = {64, 64};
             if ((st = encode_map(&maps.a, rows_a, 2, da, box)) != EP_OK) return st;
             if ((st = encode_map(&maps.b, other, 2, db, box)) != EP_OK) return st;
+            const uint64_t dout[3] = {K, F, E};
+            const uint32_t bout[3] = {64, 32, 1};
+            if ((st = encode_map(&maps.out, out, 3, dout, bout)) != EP_OK) return st;
         } else {
             const uint64_t da[3] = {K, F, E}, db[2] = {(uint64_t)a.C, rows};
             const uint32_t ba[3] = {64, D == kForward ? (uint32_t)kBM : 64u, 1};

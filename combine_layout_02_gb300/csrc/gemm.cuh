@@ -23,7 +23,7 @@ struct GemmArgs {
 };
 
 struct GemmMaps {
-    CUtensorMap a, b, b2;      // b2: b with boxes of twice the rows
+    CUtensorMap a, b, b2, out;      // b2: b with boxes of twice the rows; out: wgrad's
 };
 
 inline bool features_ok(int f) { return f >= 8 && f % 8 == 0; }
@@ -294,10 +294,13 @@ struct Tile {
     int begin, end;            // the expert's rows
 };
 
-// Walks the tiles of all experts in order: expert by expert, M tiles (of a pair's 256) innermost.
+// Walks the tiles of all experts in order: expert by expert, in bands of four M tiles (of a pair's
+// 256), column by column within a band: the tiles in work at a time then share their operands in
+// L2 (8192^3: 662 -> 606 us; bands of 8 and 16: 647, 596; 32 experts of 512 rows: 350, 364, 366 us).
 //   forward / dgrad: an expert's rows are cut into ceil(rows / bn) nearly even column tiles
 //   wgrad:           N is cut into tiles of bn
 // A tile's columns are a multiple of 32 (16 for each CTA).
+constexpr int kBand = 4;
 template <Direction D>
 struct TileWalk {
     const GemmArgs& a;
@@ -321,9 +324,10 @@ struct TileWalk {
             }
             count = nt * mt;
         }
-        const int q = t - first, c = q / mt;
+        const int q = t - first, band = q / (nt * kBand), width = min(kBand, mt - band * kBand);
+        const int in = q - band * nt * kBand, c = in / width;
         out.e = e;
-        out.m0 = (q - c * mt) * 2 * kBM;
+        out.m0 = (band * kBand + in - c * width) * 2 * kBM;
         out.begin = begin;
         out.end = end;
         if (D == kWgrad) {
@@ -354,14 +358,24 @@ __device__ __forceinline__ void store_features(const float (&v)[G], __nv_bfloat1
     }
 }
 
-// wgrad: a lane holds 32 consecutive columns of one row of dW.
-__device__ __forceinline__ void store_columns(const float (&v)[32], __nv_bfloat16* out, int cols) {
+// wgrad: a lane holds 64 consecutive columns of one row of dW; a warp stages its 32 rows x 64 columns
+// in shared memory (16-byte pieces swizzled within 128-byte rows) and stores them with one bulk
+// tensor copy, which leaves out what lies beyond dW's edges. Two buffers a warp.
+constexpr uint32_t kOutBytes = 32 * 128;
+__device__ __forceinline__ void stage_columns(const float (&v)[32], uint32_t buf, int lane, int piece0) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-        if (j < cols)
-            st_v4(out + j, make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
-                                      pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7])));
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t at = buf + lane * 128 + (((piece0 + j) ^ (lane & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack_bf16x2(v[8 * j], v[8 * j + 1])),
+                     "r"(pack_bf16x2(v[8 * j + 2], v[8 * j + 3])), "r"(pack_bf16x2(v[8 * j + 4], v[8 * j + 5])),
+                     "r"(pack_bf16x2(v[8 * j + 6], v[8 * j + 7]))
+                     : "memory");
     }
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
 // What an epilogue adds to the sums before they are rounded; all 128 epilogue threads make the calls
@@ -564,6 +578,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         Tile t;
         uint32_t used = 0;
         const int quarter = warp & 3;
+        const uint32_t out0 = smem_addr(smem) + a.stages * stage_bytes + quarter * 2 * kOutBytes;     // wgrad
+        uint32_t turn = 0;
         for (int i = first; walk.at(i, t); i += step) {
             const bool some = D != kWgrad || t.end > t.begin;
             const uint32_t acc = used & 1;
@@ -575,19 +591,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int rows = min(t.n, t.end - t.n0);
             typename Extra::State state;
             if (D != kWgrad) extra.begin(state, s_extra, t.n0, rows, m);
-            constexpr int G = Extra::kGroup;
-            for (int c = 0; c < (D == kWgrad ? t.n : rows); c += G) {
-                float v[G];
-                if (some) {
-                    tmem_load(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
-                } else {
+            if constexpr (D == kWgrad) {
+                const int m_warp = t.m0 + (int)rank * kBM + quarter * 32;
+                for (int c = 0; m_warp < a.M && c < t.n; c += 64, turn ^= 1) {
+                    const uint32_t buf = out0 + turn * kOutBytes;
+                    if (lane == 0) bulk_wait_smem_read_but_one();      // this buffer's last store has read it
+                    __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < G; ++j) v[j] = 0.0f;
+                    for (int h = 0; h < 2; ++h) {
+                        float v[32];
+                        if (some) {
+                            tmem_load(tmem + acc * 256 + c + h * 32 + ((uint32_t)quarter << 21), v);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                        }
+                        stage_columns(v, buf, lane, h * 4);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&maps.out, buf, t.n0 + c, m_warp, t.e);
+                        bulk_commit();
+                    }
                 }
-                if constexpr (D == kWgrad) {
-                    if (m < a.M)
-                        store_columns(v, a.out + ((int64_t)t.e * a.M + m) * a.N + t.n0 + c, a.N - t.n0 - c);
-                } else {
+            } else {
+                constexpr int G = Extra::kGroup;
+                for (int c = 0; c < rows; c += G) {
+                    float v[G];
+                    tmem_load(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
                     extra.apply(state, s_extra, v, t.n0, rows, c, m);
                     store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
                 }
@@ -599,6 +631,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 ++used;
             }
         }
+        if (D == kWgrad && lane == 0) bulk_wait_all();
     }
     __syncwarp();
     tc_fence_before();
@@ -837,7 +870,7 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad) {
     const bool split = gemm_by_split(*a) && !wgrad;
     const int stage = (int)kABytes + (split ? bn * 128 : bn * 64), room = (split && bn <= 64 ? 96 : 200) * 1024;
     a->stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-    a->smem = a->stages * stage + 1024;
+    a->smem = a->stages * stage + 1024 + (wgrad ? 8 * (int)kOutBytes : 0);
 }
 
 // How many tiles of `wide` M indices there can be at most.
@@ -846,12 +879,12 @@ inline int64_t gemm_most_tiles(const GemmArgs& a, bool wgrad, int wide) {
     return mt * (wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn) : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows));
 }
 
-constexpr int kGemmSmemMax = 200 * 1024 + 1024;
+constexpr int kGemmSmemMax = 201 * 1024, kWgradSmemMax = 225 * 1024;
 
 template <class Kernel, class Extra>
-cudaError_t launch_gemm_as(Kernel kernel, unsigned blocks, unsigned threads, unsigned cluster, cudaStream_t stream,
+cudaError_t launch_gemm_as(Kernel kernel, int smem_most, unsigned blocks, unsigned threads, unsigned cluster, cudaStream_t stream,
                            const GemmMaps& maps, const GemmArgs& a, const Extra& extra) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemMax);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
@@ -878,12 +911,12 @@ cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Wide& wid
         if (gemm_by_split(a)) {
             const int64_t tiles = gemm_most_tiles(a, false, kBM);
             if (tiles * a.split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-            return launch_gemm_as(gemm_split_kernel<D, Few>, (unsigned)(tiles * a.split), kSplitThreads,
+            return launch_gemm_as(gemm_split_kernel<D, Few>, kGemmSmemMax, (unsigned)(tiles * a.split), kSplitThreads,
                                   (unsigned)a.split, stream, maps, a, few);
         }
     }
     const int64_t tiles = gemm_most_tiles(a, D == kWgrad, 2 * kBM), pairs = sm_count() / 2;
-    return launch_gemm_as(gemm_kernel<D, Wide>, 2u * (unsigned)(tiles < pairs ? tiles : pairs), kGemmThreads, 2, stream,
+    return launch_gemm_as(gemm_kernel<D, Wide>, D == kWgrad ? kWgradSmemMax : kGemmSmemMax, 2u * (unsigned)(tiles < pairs ? tiles : pairs), kGemmThreads, 2, stream,
                           maps, a, wide);
 }
 
