@@ -217,13 +217,22 @@ AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
     return w;
 }
 
-// d += a * b on a pair of fp32 values, each rounded as fmaf rounds.
-__device__ __forceinline__ void fma_pair(float2& d, const float2& a, const float2& b) {
-    asm("{ .reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mov.b64 z, {%4, %5}; fma.rn.f32x2 x, y, z, x; "
-        "mov.b64 {%0, %1}, x; }"
-        : "+f"(d.x), "+f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+// Pairs of fp32 values in 64 bits: d += a * b, each half rounded as fmaf rounds.
+using f32pair = unsigned long long;
+__device__ __forceinline__ void fma_pair(f32pair& d, f32pair a, f32pair b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
+__device__ __forceinline__ f32pair make_pair(float lo, float hi) {
+    f32pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float pair_sum(f32pair p) {
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+    return lo + hi;
+}
+__device__ __forceinline__ f32pair pair_of_bf16(uint32_t w) { return make_pair(bf16_lo(w), bf16_hi(w)); }
 
 // The epilogue's part: y += B_i low, one output feature per lane, fp32. A row only ever meets its own
 // adapter's values.
@@ -243,9 +252,13 @@ struct AdapterSide {
     __device__ __forceinline__ float4 low4(int64_t t, int q) const {
         const float* at = low + t * r + q;
         float4 v = *reinterpret_cast<const float4*>(at);
-        for (int p = 1; p < parts; ++p) {
-            const float4 x = *reinterpret_cast<const float4*>(at + p * part);
-            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        for (int p0 = 1; p0 < parts; p0 += 4) {
+            float4 x[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                x[p] = p0 + p < parts ? *reinterpret_cast<const float4*>(at + (p0 + p) * part) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) v.x += x[p].x, v.y += x[p].y, v.z += x[p].z, v.w += x[p].w;
         }
         return v;
     }
@@ -328,22 +341,24 @@ constexpr int kStageRanks = 128, kStageStride = kStageRanks + 4, kHeld = 64;
 
 struct AdapterWide : AdapterSide {
     static constexpr bool kFollows = true;
-    static constexpr int kGroup = 8;
-    static constexpr int kFloats = 2 * kGroup * kStageStride;
+    static constexpr int kGroup = 8, kRows = 256;
+    static constexpr int kFloats = 2 * kGroup * kStageStride + kRows;      // low twice, the rows' adapters
 
     struct State {
-        int64_t row0;
-        int rows, m, held, buf;
-        float2 w[kHeld / 2];
+        int held, buf;
+        f32pair w[kHeld / 2];
     };
 
+    __device__ __forceinline__ int* ids(float* shared) const {
+        return reinterpret_cast<int*>(shared + 2 * kGroup * kStageStride);
+    }
     // This thread's eight low values of the eight rows from row c on, ranks from q0 on.
-    __device__ __forceinline__ void load(const State& s, int c, int q0, float4 (&v)[2]) const {
+    __device__ __forceinline__ void load(int64_t row0, int rows, int c, int q0, float4 (&v)[2]) const {
         const int tid = threadIdx.x & 127, row = c + (tid >> 4), q = q0 + (tid & 15) * 8;
         v[0] = v[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (row < s.rows && q < r) {
-            v[0] = low4(s.row0 + row, q);
-            v[1] = low4(s.row0 + row, q + 4);
+        if (row < rows && q < r) {
+            v[0] = low4(row0 + row, q);
+            v[1] = low4(row0 + row, q + 4);
         }
     }
     __device__ __forceinline__ void put(float* shared, int buf, const float4 (&v)[2]) const {
@@ -352,84 +367,90 @@ struct AdapterWide : AdapterSide {
         at[0] = v[0];
         at[1] = v[1];
     }
-    __device__ __forceinline__ void begin(State& s, float* shared, int64_t row0, int rows, int m) const {
-        s.row0 = row0, s.rows = rows, s.m = m, s.held = -1, s.buf = 0;
+    __device__ __forceinline__ void begin(State& s, float* shared, int64_t row0, int rows, int) const {
+        s.held = -1, s.buf = 0;
+        const int tid = threadIdx.x & 127;
         float4 v[2];
-        load(s, 0, 0, v);
+        load(row0, rows, 0, 0, v);
+        int id[kRows / 128];
+#pragma unroll
+        for (int h = 0; h < kRows / 128; ++h) id[h] = tid + h * 128 < rows ? adapter(row0 + tid + h * 128) : -1;
         epilogue_barrier();          // the tile before has been read
         put(shared, 0, v);
+#pragma unroll
+        for (int h = 0; h < kRows / 128; ++h) ids(shared)[tid + h * 128] = id[h];
         epilogue_barrier();
     }
     // B_i's values of this feature, kHeld ranks from q0 on.
-    __device__ __forceinline__ void load_b(const State& s, int i, int q0, uint4 (&u)[kHeld / 8]) const {
-        const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + s.m) * r + q0;
+    __device__ __forceinline__ void load_b(int i, int m, int q0, uint4 (&u)[kHeld / 8]) const {
+        const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q0;
 #pragma unroll
         for (int g = 0; g < kHeld / 8; ++g)
-            u[g] = i >= 0 && s.m < F && q0 + g * 8 < r ? *reinterpret_cast<const uint4*>(at + g * 8) : make_uint4(0, 0, 0, 0);
+            u[g] = i >= 0 && m < F && q0 + g * 8 < r ? *reinterpret_cast<const uint4*>(at + g * 8) : make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void apply(State& s, float* shared, float (&v)[kGroup], int64_t, int, int c, int) const {
-        const int lane = threadIdx.x & 31;
-        const int id = lane < kGroup && c + lane < s.rows ? adapter(s.row0 + c + lane) : -1;
-        const int first = __shfl_sync(0xFFFFFFFFu, id, 0);
-        const bool one = __all_sync(0xFFFFFFFFu, id == first || lane >= kGroup || c + lane >= s.rows);
-        float2 acc[kGroup];
+    __device__ __forceinline__ void apply(State& s, float* shared, float (&v)[kGroup], int64_t row0, int rows, int c,
+                                          int m) const {
+        const int4 ia = *reinterpret_cast<const int4*>(ids(shared) + c), ib = *reinterpret_cast<const int4*>(ids(shared) + c + 4);
+        const int id[kGroup] = {ia.x, ia.y, ia.z, ia.w, ib.x, ib.y, ib.z, ib.w};      // -1 past the last row
+        bool one = true;
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) acc[j] = make_float2(v[j], 0.0f);
+        for (int j = 1; j < kGroup; ++j) one = one && (id[j] == id[0] || c + j >= rows);
+        f32pair acc[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) acc[j] = make_pair(v[j], 0.0f);
         for (int s0 = 0; s0 < r; s0 += kStageRanks) {
             float4 next[2];
             const bool last = s0 + kStageRanks >= r;
-            load(s, last ? c + kGroup : c, last ? 0 : s0 + kStageRanks, next);
+            load(row0, rows, last ? c + kGroup : c, last ? 0 : s0 + kStageRanks, next);
             const float* stage = shared + s.buf * kGroup * kStageStride;
             for (int q0 = s0; q0 < min(r, s0 + kStageRanks); q0 += kHeld) {
-                const float4* l = reinterpret_cast<const float4*>(stage + q0 - s0);
+                const ulonglong2* l = reinterpret_cast<const ulonglong2*>(stage + q0 - s0);
                 if (one) {
-                    if (first >= 0) {
-                        if (s.held != first || r > kHeld) {
+                    if (id[0] >= 0) {
+                        if (s.held != id[0] || r > kHeld) {
                             uint4 u[kHeld / 8];
-                            load_b(s, first, q0, u);
+                            load_b(id[0], m, q0, u);
 #pragma unroll
                             for (int g = 0; g < kHeld / 8; ++g) {
-                                s.w[4 * g] = make_float2(bf16_lo(u[g].x), bf16_hi(u[g].x));
-                                s.w[4 * g + 1] = make_float2(bf16_lo(u[g].y), bf16_hi(u[g].y));
-                                s.w[4 * g + 2] = make_float2(bf16_lo(u[g].z), bf16_hi(u[g].z));
-                                s.w[4 * g + 3] = make_float2(bf16_lo(u[g].w), bf16_hi(u[g].w));
+                                s.w[4 * g] = pair_of_bf16(u[g].x);
+                                s.w[4 * g + 1] = pair_of_bf16(u[g].y);
+                                s.w[4 * g + 2] = pair_of_bf16(u[g].z);
+                                s.w[4 * g + 3] = pair_of_bf16(u[g].w);
                             }
-                            s.held = first;
+                            s.held = id[0];
                         }
 #pragma unroll
                         for (int g = 0; g < kHeld / 8; ++g) {
                             if (q0 + g * 8 >= r) break;
 #pragma unroll
                             for (int j = 0; j < kGroup; ++j) {
-                                const float4 x = l[j * (kStageStride / 4) + 2 * g], y = l[j * (kStageStride / 4) + 2 * g + 1];
-                                fma_pair(acc[j], make_float2(x.x, x.y), s.w[4 * g]);
-                                fma_pair(acc[j], make_float2(x.z, x.w), s.w[4 * g + 1]);
-                                fma_pair(acc[j], make_float2(y.x, y.y), s.w[4 * g + 2]);
-                                fma_pair(acc[j], make_float2(y.z, y.w), s.w[4 * g + 3]);
+                                const ulonglong2 x = l[j * (kStageStride / 4) + 2 * g], y = l[j * (kStageStride / 4) + 2 * g + 1];
+                                fma_pair(acc[j], x.x, s.w[4 * g]);
+                                fma_pair(acc[j], x.y, s.w[4 * g + 1]);
+                                fma_pair(acc[j], y.x, s.w[4 * g + 2]);
+                                fma_pair(acc[j], y.y, s.w[4 * g + 3]);
                             }
                         }
                     }
                 } else {
                     uint4 u[2][kHeld / 8];
-                    load_b(s, first, q0, u[0]);
+                    load_b(id[0], m, q0, u[0]);
 #pragma unroll
                     for (int j = 0; j < kGroup; ++j) {
-                        const int i = __shfl_sync(0xFFFFFFFFu, id, j);
-                        if (j + 1 < kGroup) load_b(s, __shfl_sync(0xFFFFFFFFu, id, j + 1), q0, u[(j + 1) & 1]);
-                        if (i < 0) continue;
-                        float2 even = make_float2(0.0f, 0.0f);
+                        if (j + 1 < kGroup) load_b(id[j + 1], m, q0, u[(j + 1) & 1]);
+                        if (id[j] < 0) continue;
+                        f32pair even = make_pair(0.0f, 0.0f);
 #pragma unroll
                         for (int g = 0; g < kHeld / 8; ++g) {
                             if (q0 + g * 8 >= r) break;
-                            const float4 x = l[j * (kStageStride / 4) + 2 * g], y = l[j * (kStageStride / 4) + 2 * g + 1];
+                            const ulonglong2 x = l[j * (kStageStride / 4) + 2 * g], y = l[j * (kStageStride / 4) + 2 * g + 1];
                             const uint4 w = u[j & 1][g];
-                            fma_pair(acc[j], make_float2(x.x, x.y), make_float2(bf16_lo(w.x), bf16_hi(w.x)));
-                            fma_pair(even, make_float2(x.z, x.w), make_float2(bf16_lo(w.y), bf16_hi(w.y)));
-                            fma_pair(acc[j], make_float2(y.x, y.y), make_float2(bf16_lo(w.z), bf16_hi(w.z)));
-                            fma_pair(even, make_float2(y.z, y.w), make_float2(bf16_lo(w.w), bf16_hi(w.w)));
+                            fma_pair(acc[j], x.x, pair_of_bf16(w.x));
+                            fma_pair(even, x.y, pair_of_bf16(w.y));
+                            fma_pair(acc[j], y.x, pair_of_bf16(w.z));
+                            fma_pair(even, y.y, pair_of_bf16(w.w));
                         }
-                        acc[j].x += even.x;
-                        acc[j].y += even.y;
+                        acc[j] = make_pair(pair_sum(acc[j]), pair_sum(even));
                     }
                 }
             }
@@ -438,7 +459,7 @@ struct AdapterWide : AdapterSide {
             epilogue_barrier();
         }
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) v[j] = acc[j].x + acc[j].y;
+        for (int j = 0; j < kGroup; ++j) v[j] = pair_sum(acc[j]);
     }
 };
 

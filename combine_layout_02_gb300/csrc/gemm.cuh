@@ -562,12 +562,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t s = (it - 1) % a.stages;
             if (!mbar_wait(&tail[s], (phases >> s) & 1, &dead, a.err)) break;
             phases ^= 1u << s;
-            const int rows = 16 - (left & 15), chunks = 2 + (t.n / 2 + 63) / 64;
-            for (int p = lane; p < chunks * rows * 8; p += 32) {
-                const int c = p / (rows * 8), r = (p / 8) % rows;
-                *reinterpret_cast<uint4*>(smem + s * stage_bytes + c * kMnChunk + (left + r) * 128 + (p & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
+            // Four chunks of 64 columns (two of A, up to two of B) of eight 16-byte pieces: a row a step.
+            if (lane >> 3 < 2 + (t.n / 2 + 63) / 64)
+                for (int row = left; row < ((left + 15) & ~15); ++row)
+                    *reinterpret_cast<uint4*>(smem + s * stage_bytes + (lane >> 3) * kMnChunk + row * 128 + (lane & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
             fence_async_smem();
             cluster_fence();
             __syncwarp();
