@@ -217,25 +217,7 @@ AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
     return w;
 }
 
-// Pairs of fp32 values in 64 bits: d += a * b, each half rounded as fmaf rounds.
-using f32pair = unsigned long long;
-__device__ __forceinline__ void fma_pair(f32pair& d, f32pair a, f32pair b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ f32pair make_pair(float lo, float hi) {
-    f32pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
-    return p;
-}
-__device__ __forceinline__ float pair_sum(f32pair p) {
-    float lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
-    return lo + hi;
-}
-__device__ __forceinline__ f32pair pair_of_bf16(uint32_t w) { return make_pair(bf16_lo(w), bf16_hi(w)); }
-
-// The epilogue's part: y += B_i low, one output feature per lane, fp32. A row only ever meets its own
-// adapter's values.
+// The epilogue's part: y += B_i low. A row only ever meets its own adapter's values.
 struct AdapterSide {
     const __nv_bfloat16* b;
     const float* low;
@@ -264,14 +246,14 @@ struct AdapterSide {
     }
 };
 
-// gemm_split_kernel, few rows, each usually with another adapter: four rows at a time. Their B values
+// gemm_split_kernel, few rows, each usually with another adapter: one output feature per lane, four
+// rows at a time, fp32. Their B values
 // are requested before their low values are staged, and towards L2 while the projection is
 // computed. Loops, not unrolled code: a launch meets each instruction once, out of L2.
 struct AdapterFew : AdapterSide {
     static constexpr bool kFollows = true;
     static constexpr int kGroup = 4, kRows = 256;
     static constexpr int kFloats = kGroup * EP_ADAPTER_MAX_RANK + kRows;     // low, the rows' adapters
-    struct State {};
 
     __device__ __forceinline__ void ahead(float* shared, int64_t row0, int rows, int m) const {
         int* ids = reinterpret_cast<int*>(shared + kGroup * EP_ADAPTER_MAX_RANK);
@@ -285,7 +267,7 @@ struct AdapterFew : AdapterSide {
             for (int q = 0; q < r * 2; q += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + q));
         }
     }
-    __device__ __forceinline__ void apply(State&, float* shared, float (&v)[kGroup], int64_t row0, int rows, int c,
+    __device__ __forceinline__ void apply(float* shared, float (&v)[kGroup], int64_t row0, int rows, int c,
                                           int m) const {
         const int* ids = reinterpret_cast<const int*>(shared + kGroup * EP_ADAPTER_MAX_RANK) + c;
         const int tid = threadIdx.x & 127;
@@ -333,133 +315,148 @@ struct AdapterFew : AdapterSide {
     }
 };
 
-// gemm_kernel, many rows: eight rows at a time. Their low values are staged in shared memory by the
-// four warps, the next eight's loaded meanwhile. Eight rows of one adapter (prompts) keep B_i's
-// values of the feature in registers, as long as the adapter stays; of several, each row's are
-// loaded while the row before is worked on.
-constexpr int kStageRanks = 128, kStageStride = kStageRanks + 4, kHeld = 64;
+// gemm_kernel, many rows. A warp has 32 output features; eight rows at a time it takes their sums out of
+// tensor memory in the layout of warp-level products, so that B_i (32 features x 64 ranks, held in
+// registers as long as the adapter stays) times low comes from those too. (One feature per lane
+// with low broadcast out of shared memory was bound by that broadcast: 500 us where this is
+// 330.) low is fp32: it enters as two bf16 terms, hi + lo, which leave 2^-17 of it; the sums are
+// fp32. A product is taken of one adapter for all eight rows and added to its own rows alone.
+// The sums then go through two transpositions, within 8 x 8 blocks and within quads of lanes, so
+// that a lane stores 16 bytes of a row.
+constexpr int kHeld = 64;
+
+// hi and lo terms of two fp32 values (an infinite one is its hi term).
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(a, b);
+    const float x = a - bf16_lo(hi), y = b - bf16_hi(hi);
+    lo = pack_bf16x2(isinf(a) ? 0.0f : x, isinf(b) ? 0.0f : y);
+}
+
+// Transposes an 8 x 8 block of 16-bit values: lane 4g + c has columns 2c, 2c+1 of row g.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t t;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
+    return t;
+}
 
 struct AdapterWide : AdapterSide {
-    static constexpr bool kFollows = true;
-    static constexpr int kGroup = 8, kRows = 256;
-    static constexpr int kFloats = 2 * kGroup * kStageStride + kRows;      // low twice, the rows' adapters
+    static constexpr bool kFollows = true, kOwnTile = true;
+    static constexpr int kRows = 256, kFloats = kRows;      // the rows' adapters
 
-    struct State {
-        int held, buf;
-        f32pair w[kHeld / 2];
-    };
-
-    __device__ __forceinline__ int* ids(float* shared) const {
-        return reinterpret_cast<int*>(shared + 2 * kGroup * kStageStride);
-    }
-    // This thread's eight low values of the eight rows from row c on, ranks from q0 on.
-    __device__ __forceinline__ void load(int64_t row0, int rows, int c, int q0, float4 (&v)[2]) const {
-        const int tid = threadIdx.x & 127, row = c + (tid >> 4), q = q0 + (tid & 15) * 8;
-        v[0] = v[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (row < rows && q < r) {
-            v[0] = low4(row0 + row, q);
-            v[1] = low4(row0 + row, q + 4);
+    // B_i's values of the warp's 32 features (from m0 on), 64 ranks from q0 on: of features 8h + g, the
+    // 8 ranks c*8 .. of each 32. Zero past the edges.
+    __device__ __forceinline__ void load_b(int i, int m0, int q0, int g, int c, uint4 (&w)[2][4]) const {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const int m = m0 + h * 8 + g;
+            const __nv_bfloat16* at = b + ((int64_t)i * F + m) * r + q0 + c * 8;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                w[s][h] = m < F && q0 + s * 32 + c * 8 < r ? *reinterpret_cast<const uint4*>(at + s * 32) : make_uint4(0, 0, 0, 0);
         }
     }
-    __device__ __forceinline__ void put(float* shared, int buf, const float4 (&v)[2]) const {
-        const int tid = threadIdx.x & 127;
-        float4* at = reinterpret_cast<float4*>(shared + (buf * kGroup + (tid >> 4)) * kStageStride + (tid & 15) * 8);
-        at[0] = v[0];
-        at[1] = v[1];
-    }
-    __device__ __forceinline__ void begin(State& s, float* shared, int64_t row0, int rows, int) const {
-        s.held = -1, s.buf = 0;
-        const int tid = threadIdx.x & 127;
-        float4 v[2];
-        load(row0, rows, 0, 0, v);
-        int id[kRows / 128];
+    // Row row0 + j's low values, ranks q0 + s*32 + c*8 .. + 8.
+    __device__ __forceinline__ void load_low(int64_t row0, int j, int rows, int q0, int c, float4 (&v)[2][2]) const {
 #pragma unroll
-        for (int h = 0; h < kRows / 128; ++h) id[h] = tid + h * 128 < rows ? adapter(row0 + tid + h * 128) : -1;
+        for (int s = 0; s < 2; ++s) {
+            const int q = q0 + s * 32 + c * 8;
+            const bool in = j < rows && q < r;
+            v[s][0] = in ? low4(row0 + j, q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[s][1] = in ? low4(row0 + j, q + 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+    }
+
+    __device__ __forceinline__ void tile(uint32_t tmem, float* shared, __nv_bfloat16* out, int64_t row0, int rows, int m0,
+                                         int M, int lane) const {
+        const int g = lane >> 2, c = lane & 3, tid = threadIdx.x & 127;
+        int* ids = reinterpret_cast<int*>(shared);
+        int mine[kRows / 128];
+#pragma unroll
+        for (int h = 0; h < kRows / 128; ++h) mine[h] = tid + h * 128 < rows ? adapter(row0 + tid + h * 128) : -1;
         epilogue_barrier();          // the tile before has been read
-        put(shared, 0, v);
 #pragma unroll
-        for (int h = 0; h < kRows / 128; ++h) ids(shared)[tid + h * 128] = id[h];
+        for (int h = 0; h < kRows / 128; ++h) ids[tid + h * 128] = mine[h];
         epilogue_barrier();
-    }
-    // B_i's values of this feature, kHeld ranks from q0 on.
-    __device__ __forceinline__ void load_b(int i, int m, int q0, uint4 (&u)[kHeld / 8]) const {
-        const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q0;
+        int held = -1;
+        uint4 w[2][4];
+        float4 next[2][2];
+        load_low(row0, g, rows, 0, c, next);
+#pragma unroll 1
+        for (int n = 0; n < rows; n += 8) {
+            uint32_t raw[2][4];
+            tmem_load_16x8(tmem + n, raw[0]);
+            tmem_load_16x8(tmem + n + (16u << 16), raw[1]);
+            const int4 ia = *reinterpret_cast<const int4*>(ids + n), ib = *reinterpret_cast<const int4*>(ids + n + 4);
+            const int id[8] = {ia.x, ia.y, ia.z, ia.w, ib.x, ib.y, ib.z, ib.w};      // -1 past the last row
+            const int id0 = ids[n + 2 * c], id1 = ids[n + 2 * c + 1];               // of this lane's columns
+            float delta[2][4] = {};
+#pragma unroll 1
+            for (int q0 = 0; q0 < r; q0 += kHeld) {
+                uint32_t hi[2][4], lo[2][4];
 #pragma unroll
-        for (int g = 0; g < kHeld / 8; ++g)
-            u[g] = i >= 0 && m < F && q0 + g * 8 < r ? *reinterpret_cast<const uint4*>(at + g * 8) : make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void apply(State& s, float* shared, float (&v)[kGroup], int64_t row0, int rows, int c,
-                                          int m) const {
-        const int4 ia = *reinterpret_cast<const int4*>(ids(shared) + c), ib = *reinterpret_cast<const int4*>(ids(shared) + c + 4);
-        const int id[kGroup] = {ia.x, ia.y, ia.z, ia.w, ib.x, ib.y, ib.z, ib.w};      // -1 past the last row
-        bool one = true;
+                for (int s = 0; s < 2; ++s) {
+                    split_pair(next[s][0].x, next[s][0].y, hi[s][0], lo[s][0]);
+                    split_pair(next[s][0].z, next[s][0].w, hi[s][1], lo[s][1]);
+                    split_pair(next[s][1].x, next[s][1].y, hi[s][2], lo[s][2]);
+                    split_pair(next[s][1].z, next[s][1].w, hi[s][3], lo[s][3]);
+                }
+                const bool last = q0 + kHeld >= r;
+                load_low(row0, (last ? n + 8 : n) + g, rows, last ? 0 : q0 + kHeld, c, next);
+#pragma unroll 1
+                for (int j = 0; j < 8; ++j) {
+                    const int i = ids[n + j];
+                    bool seen = i < 0;
 #pragma unroll
-        for (int j = 1; j < kGroup; ++j) one = one && (id[j] == id[0] || c + j >= rows);
-        f32pair acc[kGroup];
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) acc[j] = make_pair(v[j], 0.0f);
-        for (int s0 = 0; s0 < r; s0 += kStageRanks) {
-            float4 next[2];
-            const bool last = s0 + kStageRanks >= r;
-            load(row0, rows, last ? c + kGroup : c, last ? 0 : s0 + kStageRanks, next);
-            const float* stage = shared + s.buf * kGroup * kStageStride;
-            for (int q0 = s0; q0 < min(r, s0 + kStageRanks); q0 += kHeld) {
-                const ulonglong2* l = reinterpret_cast<const ulonglong2*>(stage + q0 - s0);
-                if (one) {
-                    if (id[0] >= 0) {
-                        if (s.held != id[0] || r > kHeld) {
-                            uint4 u[kHeld / 8];
-                            load_b(id[0], m, q0, u);
-#pragma unroll
-                            for (int g = 0; g < kHeld / 8; ++g) {
-                                s.w[4 * g] = pair_of_bf16(u[g].x);
-                                s.w[4 * g + 1] = pair_of_bf16(u[g].y);
-                                s.w[4 * g + 2] = pair_of_bf16(u[g].z);
-                                s.w[4 * g + 3] = pair_of_bf16(u[g].w);
-                            }
-                            s.held = id[0];
-                        }
-#pragma unroll
-                        for (int g = 0; g < kHeld / 8; ++g) {
-                            if (q0 + g * 8 >= r) break;
-#pragma unroll
-                            for (int j = 0; j < kGroup; ++j) {
-                                const ulonglong2 x = l[j * (kStageStride / 4) + 2 * g], y = l[j * (kStageStride / 4) + 2 * g + 1];
-                                fma_pair(acc[j], x.x, s.w[4 * g]);
-                                fma_pair(acc[j], x.y, s.w[4 * g + 1]);
-                                fma_pair(acc[j], y.x, s.w[4 * g + 2]);
-                                fma_pair(acc[j], y.y, s.w[4 * g + 3]);
-                            }
-                        }
+                    for (int k = 0; k < 7; ++k) seen = seen || (k < j && id[k] == i);
+                    if (seen) continue;
+                    if (held != i || r > kHeld) {
+                        load_b(i, m0, q0, g, c, w);
+                        held = i;
                     }
-                } else {
-                    uint4 u[2][kHeld / 8];
-                    load_b(id[0], m, q0, u[0]);
+                    float d[2][4] = {};
 #pragma unroll
-                    for (int j = 0; j < kGroup; ++j) {
-                        if (j + 1 < kGroup) load_b(id[j + 1], m, q0, u[(j + 1) & 1]);
-                        if (id[j] < 0) continue;
-                        f32pair even = make_pair(0.0f, 0.0f);
+                    for (int s = 0; s < 2; ++s) {
+                        if (q0 + s * 32 >= r) break;
 #pragma unroll
-                        for (int g = 0; g < kHeld / 8; ++g) {
-                            if (q0 + g * 8 >= r) break;
-                            const ulonglong2 x = l[j * (kStageStride / 4) + 2 * g], y = l[j * (kStageStride / 4) + 2 * g + 1];
-                            const uint4 w = u[j & 1][g];
-                            fma_pair(acc[j], x.x, pair_of_bf16(w.x));
-                            fma_pair(even, x.y, pair_of_bf16(w.y));
-                            fma_pair(acc[j], y.x, pair_of_bf16(w.z));
-                            fma_pair(even, y.y, pair_of_bf16(w.w));
-                        }
-                        acc[j] = make_pair(pair_sum(acc[j]), pair_sum(even));
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                const uint4 x = w[s][2 * t], y = w[s][2 * t + 1];
+                                const uint32_t a0 = k ? x.z : x.x, a1 = k ? y.z : y.x, a2 = k ? x.w : x.y, a3 = k ? y.w : y.y;
+                                mma_16816(d[t], a0, a1, a2, a3, hi[s][2 * k], hi[s][2 * k + 1]);
+                                mma_16816(d[t], a0, a1, a2, a3, lo[s][2 * k], lo[s][2 * k + 1]);
+                            }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (id0 == i) delta[t][0] += d[t][0], delta[t][2] += d[t][2];
+                        if (id1 == i) delta[t][1] += d[t][1], delta[t][3] += d[t][3];
                     }
                 }
             }
-            s.buf ^= 1;
-            put(shared, s.buf, next);
-            epilogue_barrier();
-        }
+            tmem_wait(raw);
+            uint32_t p[4];          // block h: features 8h + g of rows 2c, 2c+1 -> of row g, features 8h + 2c, +1
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) v[j] = pair_sum(acc[j]);
+            for (int t = 0; t < 2; ++t) {
+                p[2 * t] = pack_bf16x2(__uint_as_float(raw[t][0]) + delta[t][0], __uint_as_float(raw[t][1]) + delta[t][1]);
+                p[2 * t + 1] = pack_bf16x2(__uint_as_float(raw[t][2]) + delta[t][2], __uint_as_float(raw[t][3]) + delta[t][3]);
+            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) p[h] = transpose_8x8(p[h]);
+            // 4 x 4 transposition within the quad: lane c then has all of block c.
+#pragma unroll
+            for (int bit = 1; bit <= 2; bit *= 2)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    if (h & bit) continue;
+                    const bool up = c & bit;
+                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? p[h] : p[h | bit], bit);
+                    if (up) p[h] = got;
+                    else p[h | bit] = got;
+                }
+            if (n + g < rows && m0 + c * 8 < M)
+                st_v4(out + (row0 + n + g) * M + m0 + c * 8, make_uint4(p[0], p[1], p[2], p[3]));
+        }
     }
 };
 

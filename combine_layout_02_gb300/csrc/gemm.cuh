@@ -137,6 +137,20 @@ __device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 16 lanes (from the address's lane on) x 8 columns in the layout of a 16 x 8 product's sums: lane
+// 4g + c has columns 2c, 2c+1 of lanes g (v[0], v[1]) and g + 8 (v[2], v[3]). The caller waits
+// (tmem_wait) before it uses v.
+__device__ __forceinline__ void tmem_load_16x8(uint32_t at, uint32_t (&v)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[2][4]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0][0]), "+r"(v[0][1]), "+r"(v[0][2]), "+r"(v[0][3]), "+r"(v[1][0]), "+r"(v[1][1]),
+                   "+r"(v[1][2]), "+r"(v[1][3])::"memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -224,8 +238,20 @@ __device__ __forceinline__ float peer_value(uint32_t at) {
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t at) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
 }
-// Orders shared-memory writes of one CTA of a pair before the other's products, around an arrival.
-__device__ __forceinline__ void cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// An arrival that publishes this CTA's shared-memory writes to the pair's other CTA, and the wait there.
+__device__ __forceinline__ void mbar_arrive_peer_release(uint32_t at) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_peer(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* err) {
+    if (!mbar_wait(bar, parity, dead, err)) return false;
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ void mbar_expect_peer(uint32_t at, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(at), "r"(bytes)
                  : "memory");
@@ -382,16 +408,16 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 // together, each for output feature m. `shared`: kFloats floats of the block. kFollows: the kernel
 // directly follows one of this library after which the call's inputs are complete; only the
 // epilogue waits for that kernel itself.
-//   gemm_kernel:        begin for rows row0 .. row0 + rows - 1 of a tile, then apply for each kGroup of
-//                       them in order: v[j] belongs to row row0 + c + j
+//   gemm_kernel:        tile writes rows row0 .. row0 + rows - 1 of a tile out of tensor memory itself
+//                       (kOwnTile)
 //   gemm_split_kernel:  ahead for the CTA's rows while the products run (before that wait), then apply
+//                       for each kGroup of them in order: v[j] belongs to row row0 + c + j
 struct NoExtra {
     static constexpr bool kFollows = false;
+    static constexpr bool kOwnTile = false;
     static constexpr int kFloats = 4, kGroup = 32;
-    struct State {};
     __device__ __forceinline__ void ahead(float*, int64_t, int, int) const {}
-    __device__ __forceinline__ void begin(State&, float*, int64_t, int, int) const {}
-    __device__ __forceinline__ void apply(State&, float*, float (&)[32], int64_t, int, int, int) const {}
+    __device__ __forceinline__ void apply(float*, float (&)[32], int64_t, int, int, int) const {}
 };
 
 // The four epilogue warps: a barrier, and whether all of them have `mine` (the same answer to all,
@@ -416,13 +442,16 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
 // to the next expert, warps 4 to 7 write the tile before meanwhile.
 //   full[s]   leader's: both CTAs' loads (an arrival of each loading warp, and the bytes)
 //   empty[s]  each CTA's: the products that read stage s are done
-//   tail[s]   each CTA's: its loads of a stage that has rows to clear; the clearing warp then
-//             arrives at full[s] in the loading warps' place
+//   tail[s]   each CTA's: its loads of a stage that has rows to clear. The other CTA's clearing warp
+//             then arrives at the leader's peer_tail[s], the leader's waits for that and arrives at
+//             full[s] in all loading warps' place: the order between the CTAs is made here, since a fence
+//             at cluster scope in the multiplying warp waits for its products (492 -> 373 us)
 template <Direction D, class Extra>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], drain;
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], peer_tail[kMaxStages];
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int dead;
     __shared__ __align__(16) float s_extra[Extra::kFloats];
@@ -440,6 +469,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             mbar_init(&full[s], 4);
             mbar_init(&empty[s], 1);
             mbar_init(&tail[s], 2);
+            mbar_init(&peer_tail[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -522,10 +552,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             for (int k0 = 0; k0 < depth; k0 += kBK, ring.next()) {
                 if (!(ok = mbar_wait_at(full0 + ring.s * 8, ring.phase, &dead, a.err))) break;
                 const int left = depth - k0;
-                if (D == kWgrad && left < kBK && (left & 15) != 0) {
-                    cluster_fence();
-                    fence_async_smem();
-                }
                 tc_fence_after();
                 const uint64_t at = (uint64_t)((ring.s * stage_bytes) >> 4), da = da0 + at, db = db0 + at;
                 if (elect_one()) {
@@ -561,16 +587,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if ((left & 15) == 0) continue;
             const uint32_t s = (it - 1) % a.stages;
             if (!mbar_wait(&tail[s], (phases >> s) & 1, &dead, a.err)) break;
-            phases ^= 1u << s;
             // Four chunks of 64 columns (two of A, up to two of B) of eight 16-byte pieces: a row a step.
             if (lane >> 3 < 2 + (t.n / 2 + 63) / 64)
                 for (int row = left; row < ((left + 15) & ~15); ++row)
                     *reinterpret_cast<uint4*>(smem + s * stage_bytes + (lane >> 3) * kMnChunk + row * 128 + (lane & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
             fence_async_smem();
-            cluster_fence();
             __syncwarp();
-            if (lane < 2) mbar_arrive_peer(peer_addr(smem_addr(&full[s]), 0));
+            if (rank != 0) {
+                if (lane == 0) mbar_arrive_peer_release(peer_addr(smem_addr(&peer_tail[s]), 0));
+            } else {
+                if (!mbar_wait_peer(&peer_tail[s], (phases >> s) & 1, &dead, a.err)) break;
+                fence_async_smem();
+                __syncwarp();
+                if (lane < 4) mbar_arrive(&full[s]);
+            }
+            phases ^= 1u << s;
         }
     } else if (warp >= 4) {
         TileWalk<D> walk(a);
@@ -588,8 +620,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
             const int m = t.m0 + (int)rank * kBM + quarter * 32 + lane;
             const int rows = min(t.n, t.end - t.n0);
-            typename Extra::State state;
-            if (D != kWgrad) extra.begin(state, s_extra, t.n0, rows, m);
             if constexpr (D == kWgrad) {
                 const int m_warp = t.m0 + (int)rank * kBM + quarter * 32;
                 for (int c = 0; m_warp < a.M && c < t.n; c += 64, turn ^= 1) {
@@ -614,12 +644,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         bulk_commit();
                     }
                 }
+            } else if constexpr (Extra::kOwnTile) {
+                extra.tile(tmem + acc * 256 + ((uint32_t)quarter << 21), s_extra, a.out, t.n0, rows, m - lane, a.M, lane);
             } else {
-                constexpr int G = Extra::kGroup;
-                for (int c = 0; c < rows; c += G) {
-                    float v[G];
+                for (int c = 0; c < rows; c += 32) {
+                    float v[32];
                     tmem_load(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
-                    extra.apply(state, s_extra, v, t.n0, rows, c, m);
                     store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
                 }
             }
@@ -788,11 +818,10 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     constexpr int G = Extra::kGroup;
     if (a.split == 1) {
         if (ok && warp >= 2) {
-            typename Extra::State state;
             for (int c = 0; c < rows; c += G) {
                 float v[G];
                 tmem_load(tmem + c + ((uint32_t)quarter << 21), v);
-                extra.apply(state, s_extra, v, t.n0, rows, c, m);
+                extra.apply(s_extra, v, t.n0, rows, c, m);
                 store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
             }
         }
@@ -816,7 +845,6 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         cluster_barrier();
         if (ok && warp >= 2 && lo < hi) {
             const uint32_t at = smem_addr(part);
-            typename Extra::State state;
             for (int c = lo; c < hi; c += G) {
                 float v[G];
 #pragma unroll
@@ -827,7 +855,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
                     for (int j = 0; j < G; ++j)
                         if (c + j < hi) v[j] += peer_value(peer + ((c + j) * kBM + m_local) * 4);
                 }
-                extra.apply(state, s_extra, v, t.n0 + lo, hi - lo, c - lo, m);
+                extra.apply(s_extra, v, t.n0 + lo, hi - lo, c - lo, m);
                 store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
             }
         }
