@@ -342,6 +342,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
 struct AdapterWide : AdapterSide {
     static constexpr bool kFollows = true, kOwnTile = true;
     static constexpr int kRows = 256, kFloats = kRows;      // the rows' adapters
+    static constexpr int kTileWarps = 8;                    // two per quarter of the features, half the rows each
 
     // B_i's values of the warp's 32 features (from m0 on), 64 ranks from q0 on: of features 8h + g, the
     // 8 ranks c*8 .. of each 32. Zero past the edges.
@@ -367,28 +368,29 @@ struct AdapterWide : AdapterSide {
     }
 
     __device__ __forceinline__ void tile(uint32_t tmem, float* shared, __nv_bfloat16* out, int64_t row0, int rows, int m0,
-                                         int M, int lane) const {
-        const int g = lane >> 2, c = lane & 3, tid = threadIdx.x & 127;
+                                         int M, int half, int lane) const {
+        const int g = lane >> 2, c = lane & 3, tid = threadIdx.x - 128;
         int* ids = reinterpret_cast<int*>(shared);
-        int mine[kRows / 128];
-#pragma unroll
-        for (int h = 0; h < kRows / 128; ++h) mine[h] = tid + h * 128 < rows ? adapter(row0 + tid + h * 128) : -1;
-        epilogue_barrier();          // the tile before has been read
-#pragma unroll
-        for (int h = 0; h < kRows / 128; ++h) ids[tid + h * 128] = mine[h];
-        epilogue_barrier();
+        const int mine = tid < rows ? adapter(row0 + tid) : -1;
+        epilogue_barrier<256>();          // the tile before has been read
+        ids[tid] = mine;
+        epilogue_barrier<256>();
+        const int split = ((rows + 15) / 16) * 8, begin = half * split, end = half ? rows : min(rows, split);
         int held = -1;
         uint4 w[2][4];
         float4 next[2][2];
-        load_low(row0, g, rows, 0, c, next);
+        load_low(row0, begin + g, rows, 0, c, next);
 #pragma unroll 1
-        for (int n = 0; n < rows; n += 8) {
+        for (int n = begin; n < end; n += 8) {
             uint32_t raw[2][4];
             tmem_load_16x8(tmem + n, raw[0]);
             tmem_load_16x8(tmem + n + (16u << 16), raw[1]);
             const int4 ia = *reinterpret_cast<const int4*>(ids + n), ib = *reinterpret_cast<const int4*>(ids + n + 4);
             const int id[8] = {ia.x, ia.y, ia.z, ia.w, ib.x, ib.y, ib.z, ib.w};      // -1 past the last row
             const int id0 = ids[n + 2 * c], id1 = ids[n + 2 * c + 1];               // of this lane's columns
+            bool one = true;
+#pragma unroll
+            for (int k = 1; k < 8; ++k) one = one && (id[k] == id[0] || n + k >= rows);
             float delta[2][4] = {};
 #pragma unroll 1
             for (int q0 = 0; q0 < r; q0 += kHeld) {
@@ -402,18 +404,11 @@ struct AdapterWide : AdapterSide {
                 }
                 const bool last = q0 + kHeld >= r;
                 load_low(row0, (last ? n + 8 : n) + g, rows, last ? 0 : q0 + kHeld, c, next);
-#pragma unroll 1
-                for (int j = 0; j < 8; ++j) {
-                    const int i = ids[n + j];
-                    bool seen = i < 0;
-#pragma unroll
-                    for (int k = 0; k < 7; ++k) seen = seen || (k < j && id[k] == i);
-                    if (seen) continue;
+                const auto product = [&](int i, float (&d)[2][4]) {
                     if (held != i || r > kHeld) {
                         load_b(i, m0, q0, g, c, w);
                         held = i;
                     }
-                    float d[2][4] = {};
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         if (q0 + s * 32 >= r) break;
@@ -427,10 +422,24 @@ struct AdapterWide : AdapterSide {
                                 mma_16816(d[t], a0, a1, a2, a3, lo[s][2 * k], lo[s][2 * k + 1]);
                             }
                     }
+                };
+                if (one) {
+                    if (id[0] >= 0) product(id[0], delta);
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < 8; ++j) {
+                        const int i = ids[n + j];
+                        bool seen = i < 0;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (id0 == i) delta[t][0] += d[t][0], delta[t][2] += d[t][2];
-                        if (id1 == i) delta[t][1] += d[t][1], delta[t][3] += d[t][3];
+                        for (int k = 0; k < 7; ++k) seen = seen || (k < j && id[k] == i);
+                        if (seen) continue;
+                        float d[2][4] = {};
+                        product(i, d);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (id0 == i) delta[t][0] += d[t][0], delta[t][2] += d[t][2];
+                            if (id1 == i) delta[t][1] += d[t][1], delta[t][3] += d[t][3];
+                        }
                     }
                 }
             }

@@ -313,7 +313,6 @@ __device__ __forceinline__ uint32_t instr_desc(int m, int n, bool a_mn, bool b_m
 constexpr int kBM = 128, kBK = 64;
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr int kMaxStages = 8;
-constexpr int kGemmThreads = 256;
 
 struct Tile {
     int e, m0, n0, n;          // expert, first M index, first column (row index or N index), columns
@@ -415,20 +414,24 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 struct NoExtra {
     static constexpr bool kFollows = false;
     static constexpr bool kOwnTile = false;
-    static constexpr int kFloats = 4, kGroup = 32;
+    static constexpr int kFloats = 4, kGroup = 32, kTileWarps = 4;
     __device__ __forceinline__ void ahead(float*, int64_t, int, int) const {}
     __device__ __forceinline__ void apply(float*, float (&)[32], int64_t, int, int, int) const {}
 };
 
-// The four epilogue warps: a barrier, and whether all of them have `mine` (the same answer to all,
-// so that none waits at a later barrier that another has left out).
-__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The epilogue's THREADS: a barrier, and whether all of them have `mine` (the same answer to all, so
+// that none waits at a later barrier that another has left out).
+template <int THREADS = 128>
+__device__ __forceinline__ void epilogue_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+template <int THREADS = 128>
 __device__ __forceinline__ bool epilogue_all(bool mine) {
     uint32_t all;
     asm volatile(
-        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.and.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.and.pred q, 1, %2, p; selp.u32 %0, 1, 0, q; }"
         : "=r"(all)
-        : "r"((uint32_t)mine)
+        : "r"((uint32_t)mine), "n"(THREADS)
         : "memory");
     return all != 0;
 }
@@ -439,7 +442,7 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
 // the M side and half of the columns; the tensor cores of both read both halves, which halves the
 // shared memory traffic of the columns. Warp 0 loads the M side (TMA), warp 1 of the leader multiplies (tcgen05.mma, fp32 sums in tensor
 // memory, two accumulators of 256 columns in turn), warp 3 loads the columns, warp 2 clears the rows of a wgrad tail that belong
-// to the next expert, warps 4 to 7 write the tile before meanwhile.
+// to the next expert, warps 4 on write the tile before meanwhile.
 //   full[s]   leader's: both CTAs' loads (an arrival of each loading warp, and the bytes)
 //   empty[s]  each CTA's: the products that read stage s are done
 //   tail[s]   each CTA's: its loads of a stage that has rows to clear. The other CTA's clearing warp
@@ -447,7 +450,7 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
 //             full[s] in all loading warps' place: the order between the CTAs is made here, since a fence
 //             at cluster scope in the multiplying warp waits for its products (492 -> 373 us)
 template <Direction D, class Extra>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(128 + 32 * Extra::kTileWarps, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], peer_tail[kMaxStages];
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 8);
+            mbar_init(&acc_empty[i], 2 * Extra::kTileWarps);
         }
         mbar_init(&drain, 1);
         dead = 0;
@@ -615,7 +618,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const bool some = D != kWgrad || t.end > t.begin;
             const uint32_t acc = used & 1;
             if (some) {
-                if (!epilogue_all(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err))) break;
+                if (!epilogue_all<32 * Extra::kTileWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err))) break;
                 tc_fence_after();
             }
             const int m = t.m0 + (int)rank * kBM + quarter * 32 + lane;
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                 }
             } else if constexpr (Extra::kOwnTile) {
-                extra.tile(tmem + acc * 256 + ((uint32_t)quarter << 21), s_extra, a.out, t.n0, rows, m - lane, a.M, lane);
+                extra.tile(tmem + acc * 256 + ((uint32_t)quarter << 21), s_extra, a.out, t.n0, rows, m - lane, a.M, (warp - 4) >> 2, lane);
             } else {
                 for (int c = 0; c < rows; c += 32) {
                     float v[32];
@@ -943,7 +946,8 @@ cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Wide& wid
         }
     }
     const int64_t tiles = gemm_most_tiles(a, D == kWgrad, 2 * kBM), pairs = sm_count() / 2;
-    return launch_gemm_as(gemm_kernel<D, Wide>, D == kWgrad ? kWgradSmemMax : kGemmSmemMax, 2u * (unsigned)(tiles < pairs ? tiles : pairs), kGemmThreads, 2, stream,
+    return launch_gemm_as(gemm_kernel<D, Wide>, D == kWgrad ? kWgradSmemMax : kGemmSmemMax, 2u * (unsigned)(tiles < pairs ? tiles : pairs),
+                          128 + 32 * Wide::kTileWarps, 2, stream,
                           maps, a, wide);
 }
 
