@@ -253,24 +253,26 @@ struct AdapterSide {
 struct AdapterFew : AdapterSide {
     static constexpr bool kFollows = true;
     static constexpr int kGroup = 4, kRows = 256;
-    static constexpr int kFloats = kGroup * EP_ADAPTER_MAX_RANK + kRows;     // low, the rows' adapters
+    // shared: low of each half, then the rows' adapters
+    static constexpr int kLow = kGroup * EP_ADAPTER_MAX_RANK, kIds = 2 * kLow, kFloats = kIds + kRows;
 
-    __device__ __forceinline__ void ahead(float* shared, int64_t row0, int rows, int m) const {
-        int* ids = reinterpret_cast<int*>(shared + kGroup * EP_ADAPTER_MAX_RANK);
-        const int tid = threadIdx.x & 127;
-        for (int j = tid; j < rows; j += 128) ids[j] = adapter(row0 + j);
-        epilogue_barrier();
+    __device__ __forceinline__ void ahead(float* shared, int64_t row0, int rows, int m, int half) const {
+        int* ids = reinterpret_cast<int*>(shared + kIds);
+        const int tid = threadIdx.x - 64;
+        if (tid < rows) ids[tid] = adapter(row0 + tid);
+        epilogue_barrier<256>();
         if (m >= F) return;
-        for (int j = 0; j < rows; ++j) {
+        for (int j = half; j < rows; j += 2) {
             if (ids[j] < 0) continue;
             const char* at = reinterpret_cast<const char*>(b + ((int64_t)ids[j] * F + m) * r);
             for (int q = 0; q < r * 2; q += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + q));
         }
     }
-    __device__ __forceinline__ void apply(float* shared, float (&v)[kGroup], int64_t row0, int rows, int c,
-                                          int m) const {
-        const int* ids = reinterpret_cast<const int*>(shared + kGroup * EP_ADAPTER_MAX_RANK) + c;
-        const int tid = threadIdx.x & 127;
+    __device__ __forceinline__ void apply(float* shared, float (&v)[kGroup], int64_t row0, int rows, int c, int m,
+                                          int half) const {
+        const int* ids = reinterpret_cast<const int*>(shared + kIds) + c;
+        const int tid = (threadIdx.x - 64) & 127;
+        shared += half * kLow;
         uint4 u[kGroup][2];
         const auto load_b = [&](int q0) {
 #pragma unroll
@@ -283,13 +285,13 @@ struct AdapterFew : AdapterSide {
             }
         };
         load_b(0);
-        epilogue_barrier();          // the four rows before have been read
+        epilogue_barrier<128>(2 + half);          // the four rows before have been read
         for (int e = tid; e < r; e += 128) {          // four rows of r / 4 float4
             const int j = e / (r / 4), q = (e % (r / 4)) * 4;
             const float4 x = c + j < rows && ids[j] >= 0 ? low4(row0 + c + j, q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             *reinterpret_cast<float4*>(shared + j * r + q) = x;
         }
-        epilogue_barrier();
+        epilogue_barrier<128>(2 + half);
 #pragma unroll 1
         for (int q0 = 0; q0 < r; q0 += 16) {
             if (q0 > 0) load_b(q0);

@@ -410,22 +410,23 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 //   gemm_kernel:        tile writes rows row0 .. row0 + rows - 1 of a tile out of tensor memory itself
 //                       (kOwnTile)
 //   gemm_split_kernel:  ahead for the CTA's rows while the products run (before that wait), then apply
-//                       for each kGroup of them in order: v[j] belongs to row row0 + c + j
+//                       for each kGroup of them: v[j] belongs to row row0 + c + j. Two halves of 128
+//                       threads take groups in turn
 struct NoExtra {
     static constexpr bool kFollows = false;
     static constexpr bool kOwnTile = false;
     static constexpr int kFloats = 4, kGroup = 32, kTileWarps = 4;
-    __device__ __forceinline__ void ahead(float*, int64_t, int, int) const {}
-    __device__ __forceinline__ void apply(float*, float (&)[32], int64_t, int, int, int) const {}
+    __device__ __forceinline__ void ahead(float*, int64_t, int, int, int) const {}
+    __device__ __forceinline__ void apply(float*, float (&)[32], int64_t, int, int, int, int) const {}
 };
 
 // The epilogue's THREADS: a barrier, and whether all of them have `mine` (the same answer to all, so
 // that none waits at a later barrier that another has left out).
-template <int THREADS = 128>
-__device__ __forceinline__ void epilogue_barrier() {
-    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+template <int THREADS>
+__device__ __forceinline__ void epilogue_barrier(int id = 1) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
 }
-template <int THREADS = 128>
+template <int THREADS>
 __device__ __forceinline__ bool epilogue_all(bool mine) {
     uint32_t all;
     asm volatile(
@@ -714,13 +715,13 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& a, int i, int lane, Ti
     return false;
 }
 
-constexpr int kSplitThreads = 192;
+constexpr int kSplitThreads = 320;
 
 // forward / dgrad where rows are few and the weights are what is read: a cluster of `split` CTAs per
 // tile, each over its part of the contraction, so that enough CTAs stream weights at the same time
 // (and two fit an SM, one filling its pipeline while the other runs). Each CTA leaves its fp32 part
 // in its own shared memory; after a cluster barrier each adds up, in rank order, the parts of
-// its share of the rows. Warp 0 loads, warp 1 multiplies, warps 2 to 5 read tensor memory.
+// its share of the rows. Warp 0 loads, warp 1 multiplies, warps 2 to 9 write.
 template <Direction D, class Extra>
 __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_constant__ GemmMaps maps,
                                                                    const GemmArgs a, const Extra extra) {
@@ -808,23 +809,23 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         tc_commit(&done);
     }
     __syncwarp();
-    const int quarter = warp & 3, m_local = quarter * 32 + lane, m = t.m0 + m_local;
+    const int quarter = warp & 3, half = (warp - 2) >> 2, m_local = quarter * 32 + lane, m = t.m0 + m_local;
     const int rows = min(t.n, t.end - t.n0);
     const int share = (rows + a.split - 1) / a.split, lo = rank * share, hi = min(rows, lo + share);   // of the rows
     bool ok = has;
     if (has && warp >= 2) {
-        extra.ahead(s_extra, t.n0 + lo, hi - lo, m);
-        ok = epilogue_all(mbar_wait(&done, 0, &dead, a.err));
+        extra.ahead(s_extra, t.n0 + lo, hi - lo, m, half);
+        ok = epilogue_all<256>(mbar_wait(&done, 0, &dead, a.err));
         tc_fence_after();
     }
     if (Extra::kFollows && warp >= 2) pdl_wait();
     constexpr int G = Extra::kGroup;
     if (a.split == 1) {
         if (ok && warp >= 2) {
-            for (int c = 0; c < rows; c += G) {
+            for (int c = half * G; c < rows; c += 2 * G) {
                 float v[G];
                 tmem_load(tmem + c + ((uint32_t)quarter << 21), v);
-                extra.apply(s_extra, v, t.n0, rows, c, m);
+                extra.apply(s_extra, v, t.n0, rows, c, m, half);
                 store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
             }
         }
@@ -832,7 +833,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         float* part = reinterpret_cast<float*>(smem);      // [columns][128]; every product has read its stage
         const bool some = kb1 > kb0;
         if (ok && warp >= 2) {
-            for (int c = 0; c < rows; c += 8) {
+            for (int c = half * 8; c < rows; c += 16) {
                 float v[8];
                 if (some) {
                     tmem_load(tmem + c + ((uint32_t)quarter << 21), v);
@@ -848,7 +849,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         cluster_barrier();
         if (ok && warp >= 2 && lo < hi) {
             const uint32_t at = smem_addr(part);
-            for (int c = lo; c < hi; c += G) {
+            for (int c = lo + half * G; c < hi; c += 2 * G) {
                 float v[G];
 #pragma unroll
                 for (int j = 0; j < G; ++j) v[j] = 0.0f;
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
                     for (int j = 0; j < G; ++j)
                         if (c + j < hi) v[j] += peer_value(peer + ((c + j) * kBM + m_local) * 4);
                 }
-                extra.apply(s_extra, v, t.n0 + lo, hi - lo, c - lo, m);
+                extra.apply(s_extra, v, t.n0 + lo, hi - lo, c - lo, m, half);
                 store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
             }
         }
@@ -879,8 +880,9 @@ inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1;
 // Column tile width, stages and split.
 //   wgrad: tiles of 256 columns, a pair of CTAs each.
 //   else:  tiles of twice the average rows of an expert (one group: of its rows), within [32, 256],
-//          so that most experts are one tile. Up to 64 columns the weights' loads are what counts: two CTAs per SM, and
-//          the contraction split until about four CTAs per SM have work; wider tiles are split only
+//          so that most experts are one tile. Up to 64 columns the weights' loads are what counts:
+//          two CTAs per SM, and the contraction split as long as all CTAs fit at once (one row,
+//          7168 x 7168: 4 parts 21 us, 8 parts, more CTAs than fit, 35 us); wider tiles are split only
 //          where there are fewer of them than SMs. A part keeps at least eight 64-deep steps.
 inline void gemm_tiles(GemmArgs* a, bool wgrad) {
     int bn = 256;
@@ -893,7 +895,7 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad) {
     const int sms = sm_count();
     if (!wgrad) {
         const int64_t tiles = (int64_t)ceil_div(a->M, kBM) * (a->E < a->num_rows ? a->E : a->num_rows) * ceil_div(avg, bn);
-        const int64_t want = bn <= 64 ? 4 * sms : sms;
+        const int64_t want = bn <= 64 ? 2 * sms : sms;
         const int steps = ceil_div(a->C, kBK);
         while (a->split < 8 && tiles * a->split * 2 <= want && steps >= a->split * 16) a->split *= 2;
     }
