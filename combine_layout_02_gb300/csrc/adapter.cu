@@ -323,8 +323,6 @@ struct AdapterFew : AdapterSide {
 // with low broadcast out of shared memory was bound by that broadcast: 500 us where this is
 // 330.) low is fp32: it enters as two bf16 terms, hi + lo, which leave 2^-17 of it; the sums are
 // fp32. A product is taken of one adapter for all eight rows and added to its own rows alone.
-// The sums then go through two transpositions, within 8 x 8 blocks and within quads of lanes, so
-// that a lane stores 16 bytes of a row.
 constexpr int kHeld = 64;
 
 // hi and lo terms of two fp32 values (an infinite one is its hi term).
@@ -334,17 +332,9 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
     lo = pack_bf16x2(isinf(a) ? 0.0f : x, isinf(b) ? 0.0f : y);
 }
 
-// Transposes an 8 x 8 block of 16-bit values: lane 4g + c has columns 2c, 2c+1 of row g.
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
-    uint32_t t;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
-    return t;
-}
-
 struct AdapterWide : AdapterSide {
-    static constexpr bool kFollows = true, kOwnTile = true;
+    static constexpr bool kFollows = true;
     static constexpr int kRows = 256, kFloats = kRows;      // the rows' adapters
-    static constexpr int kTileWarps = 8;                    // two per quarter of the features, half the rows each
 
     // B_i's values of the warp's 32 features (from m0 on), 64 ranks from q0 on: of features 8h + g, the
     // 8 ranks c*8 .. of each 32. Zero past the edges.
@@ -380,13 +370,14 @@ struct AdapterWide : AdapterSide {
         const int split = ((rows + 15) / 16) * 8, begin = half * split, end = half ? rows : min(rows, split);
         int held = -1;
         uint4 w[2][4];
-        float4 next[2][2];
+        float4 next[2][2], after[2][2];        // low of the eight rows at work and of the eight to come
         load_low(row0, begin + g, rows, 0, c, next);
+        if (r <= kHeld) load_low(row0, begin + 8 + g, rows, 0, c, after);
 #pragma unroll 1
         for (int n = begin; n < end; n += 8) {
-            uint32_t raw[2][4];
-            tmem_load_16x8(tmem + n, raw[0]);
-            tmem_load_16x8(tmem + n + (16u << 16), raw[1]);
+            float v[2][4];
+            tmem_load_16x8(tmem + n, v[0]);
+            tmem_load_16x8(tmem + n + (16u << 16), v[1]);
             const int4 ia = *reinterpret_cast<const int4*>(ids + n), ib = *reinterpret_cast<const int4*>(ids + n + 4);
             const int id[8] = {ia.x, ia.y, ia.z, ia.w, ib.x, ib.y, ib.z, ib.w};      // -1 past the last row
             const int id0 = ids[n + 2 * c], id1 = ids[n + 2 * c + 1];               // of this lane's columns
@@ -404,8 +395,14 @@ struct AdapterWide : AdapterSide {
                     split_pair(next[s][1].x, next[s][1].y, hi[s][2], lo[s][2]);
                     split_pair(next[s][1].z, next[s][1].w, hi[s][3], lo[s][3]);
                 }
-                const bool last = q0 + kHeld >= r;
-                load_low(row0, (last ? n + 8 : n) + g, rows, last ? 0 : q0 + kHeld, c, next);
+                if (r <= kHeld) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) next[s][0] = after[s][0], next[s][1] = after[s][1];
+                    load_low(row0, n + 16 + g, rows, 0, c, after);
+                } else {
+                    const bool last = q0 + kHeld >= r;
+                    load_low(row0, (last ? n + 8 : n) + g, rows, last ? 0 : q0 + kHeld, c, next);
+                }
                 const auto product = [&](int i, float (&d)[2][4]) {
                     if (held != i || r > kHeld) {
                         load_b(i, m0, q0, g, c, w);
@@ -445,28 +442,13 @@ struct AdapterWide : AdapterSide {
                     }
                 }
             }
-            tmem_wait(raw);
-            uint32_t p[4];          // block h: features 8h + g of rows 2c, 2c+1 -> of row g, features 8h + 2c, +1
+            tmem_wait(v);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                p[2 * t] = pack_bf16x2(__uint_as_float(raw[t][0]) + delta[t][0], __uint_as_float(raw[t][1]) + delta[t][1]);
-                p[2 * t + 1] = pack_bf16x2(__uint_as_float(raw[t][2]) + delta[t][2], __uint_as_float(raw[t][3]) + delta[t][3]);
-            }
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int h = 0; h < 4; ++h) p[h] = transpose_8x8(p[h]);
-            // 4 x 4 transposition within the quad: lane c then has all of block c.
-#pragma unroll
-            for (int bit = 1; bit <= 2; bit *= 2)
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (h & bit) continue;
-                    const bool up = c & bit;
-                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? p[h] : p[h | bit], bit);
-                    if (up) p[h] = got;
-                    else p[h | bit] = got;
-                }
-            if (n + g < rows && m0 + c * 8 < M)
-                st_v4(out + (row0 + n + g) * M + m0 + c * 8, make_uint4(p[0], p[1], p[2], p[3]));
+                for (int k = 0; k < 4; ++k) v[t][k] += delta[t][k];
+            const uint4 p = rows_of_features(v, c);
+            if (n + g < rows && m0 + c * 8 < M) st_v4(out + (row0 + n + g) * M + m0 + c * 8, p);
         }
     }
 };

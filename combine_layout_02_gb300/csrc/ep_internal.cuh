@@ -178,10 +178,6 @@ __device__ __forceinline__ void bulk_commit() {
 __device__ __forceinline__ void bulk_wait_smem_read() {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
-// All of the issuing thread's committed stores but the last group have.
-__device__ __forceinline__ void bulk_wait_smem_read_but_one() {
-    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
 // The issuing thread's committed stores are complete (written to global memory).
 __device__ __forceinline__ void bulk_wait_all() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

@@ -140,15 +140,15 @@ __device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[8]) {
 // 16 lanes (from the address's lane on) x 8 columns in the layout of a 16 x 8 product's sums: lane
 // 4g + c has columns 2c, 2c+1 of lanes g (v[0], v[1]) and g + 8 (v[2], v[3]). The caller waits
 // (tmem_wait) before it uses v.
-__device__ __forceinline__ void tmem_load_16x8(uint32_t at, uint32_t (&v)[4]) {
+__device__ __forceinline__ void tmem_load_16x8(uint32_t at, float (&v)[4]) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                  : "r"(at));
 }
-__device__ __forceinline__ void tmem_wait(uint32_t (&v)[2][4]) {
+__device__ __forceinline__ void tmem_wait(float (&v)[2][4]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0][0]), "+r"(v[0][1]), "+r"(v[0][2]), "+r"(v[0][3]), "+r"(v[1][0]), "+r"(v[1][1]),
-                   "+r"(v[1][2]), "+r"(v[1][3])::"memory");
+                 : "+f"(v[0][0]), "+f"(v[0][1]), "+f"(v[0][2]), "+f"(v[0][3]), "+f"(v[1][0]), "+f"(v[1][1]),
+                   "+f"(v[1][2]), "+f"(v[1][3])::"memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -313,6 +313,7 @@ __device__ __forceinline__ uint32_t instr_desc(int m, int n, bool a_mn, bool b_m
 constexpr int kBM = 128, kBK = 64;
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr int kMaxStages = 8;
+constexpr int kTileWarps = 8;          // writing warps of gemm_kernel, two per quarter of the lanes
 
 struct Tile {
     int e, m0, n0, n;          // expert, first M index, first column (row index or N index), columns
@@ -366,8 +367,8 @@ struct TileWalk {
     }
 };
 
-// Epilogue of one tile chunk of G columns: forward / dgrad. A lane holds one feature of G rows;
-// lanes exchange in pairs, so that a store covers 32 features of two rows (64 bytes each).
+// Epilogue of G columns: forward / dgrad, few rows. A lane holds one feature of G rows; lanes exchange
+// in pairs, so that a store covers 32 features of two rows (64 bytes each).
 template <int G>
 __device__ __forceinline__ void store_features(const float (&v)[G], __nv_bfloat16* out, int ld, int64_t row0, int rows,
                                                int feature, int M, int lane) {
@@ -383,9 +384,39 @@ __device__ __forceinline__ void store_features(const float (&v)[G], __nv_bfloat1
     }
 }
 
+// Transposes an 8 x 8 block of 16-bit values: lane 4g + c has columns 2c, 2c+1 of row g.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t t;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
+    return t;
+}
+// Sums of 32 features x 8 rows in the layout of tmem_load_16x8 (lane 4g + c: rows 2c, 2c+1 of features
+// g, 8 + g in v[0], 16 + g, 24 + g in v[1]) -> bf16, lane 4g + c the eight features 8c .. 8c+7 of row
+// g: a transposition within 8 x 8 blocks and one within quads of lanes. A lane then stores 16
+// bytes, a warp 64 bytes of eight rows.
+__device__ __forceinline__ uint4 rows_of_features(const float (&v)[2][4], int c) {
+    uint32_t p[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        p[2 * t] = transpose_8x8(pack_bf16x2(v[t][0], v[t][1]));
+        p[2 * t + 1] = transpose_8x8(pack_bf16x2(v[t][2], v[t][3]));
+    }
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit *= 2)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            if (h & bit) continue;
+            const bool up = c & bit;
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? p[h] : p[h | bit], bit);
+            if (up) p[h] = got;
+            else p[h | bit] = got;
+        }
+    return make_uint4(p[0], p[1], p[2], p[3]);
+}
+
 // wgrad: a lane holds 64 consecutive columns of one row of dW; a warp stages its 32 rows x 64 columns
 // in shared memory (16-byte pieces swizzled within 128-byte rows) and stores them with one bulk
-// tensor copy, which leaves out what lies beyond dW's edges. Two buffers a warp.
+// tensor copy, which leaves out what lies beyond dW's edges.
 constexpr uint32_t kOutBytes = 32 * 128;
 __device__ __forceinline__ void stage_columns(const float (&v)[32], uint32_t buf, int lane, int piece0) {
 #pragma unroll
@@ -407,15 +438,36 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 // together, each for output feature m. `shared`: kFloats floats of the block. kFollows: the kernel
 // directly follows one of this library after which the call's inputs are complete; only the
 // epilogue waits for that kernel itself.
-//   gemm_kernel:        tile writes rows row0 .. row0 + rows - 1 of a tile out of tensor memory itself
-//                       (kOwnTile)
+//   gemm_kernel:        tile writes rows row0 .. row0 + rows - 1 of a tile, features m0 .. m0 + 31, out of
+//                       tensor memory; two warps do, `half` 0 and 1
 //   gemm_split_kernel:  ahead for the CTA's rows while the products run (before that wait), then apply
 //                       for each kGroup of them: v[j] belongs to row row0 + c + j. Two halves of 128
 //                       threads take groups in turn
 struct NoExtra {
     static constexpr bool kFollows = false;
-    static constexpr bool kOwnTile = false;
-    static constexpr int kFloats = 4, kGroup = 32, kTileWarps = 4;
+    static constexpr int kFloats = 4, kGroup = 32;
+    // Sixteen rows at a time, to have two blocks' steps in flight.
+    __device__ __forceinline__ void tile(uint32_t tmem, float*, __nv_bfloat16* out, int64_t row0, int rows, int m0, int M,
+                                         int half, int lane) const {
+        const int g = lane >> 2, c = lane & 3;
+        const bool in = m0 + c * 8 < M;
+        __nv_bfloat16* at = out + (row0 + g) * M + m0 + c * 8;
+        for (int n = half * 16; n < rows; n += 32) {
+            float v[2][2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                tmem_load_16x8(tmem + n + b * 8, v[b][0]);
+                tmem_load_16x8(tmem + n + b * 8 + (16u << 16), v[b][1]);
+            }
+            tmem_wait(v[0]);
+            tmem_wait(v[1]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint4 p = rows_of_features(v[b], c);
+                if (in && n + b * 8 + g < rows) st_v4(at + (int64_t)(n + b * 8) * M, p);
+            }
+        }
+    }
     __device__ __forceinline__ void ahead(float*, int64_t, int, int, int) const {}
     __device__ __forceinline__ void apply(float*, float (&)[32], int64_t, int, int, int, int) const {}
 };
@@ -451,7 +503,7 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
 //             full[s] in all loading warps' place: the order between the CTAs is made here, since a fence
 //             at cluster scope in the multiplying warp waits for its products (492 -> 373 us)
 template <Direction D, class Extra>
-__global__ void __launch_bounds__(128 + 32 * Extra::kTileWarps, 1)
+__global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], peer_tail[kMaxStages];
@@ -477,7 +529,7 @@ __global__ void __launch_bounds__(128 + 32 * Extra::kTileWarps, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 2 * Extra::kTileWarps);
+            mbar_init(&acc_empty[i], 2 * kTileWarps);
         }
         mbar_init(&drain, 1);
         dead = 0;
@@ -612,23 +664,22 @@ __global__ void __launch_bounds__(128 + 32 * Extra::kTileWarps, 1)
         TileWalk<D> walk(a);
         Tile t;
         uint32_t used = 0;
-        const int quarter = warp & 3;
-        const uint32_t out0 = smem_addr(smem) + a.stages * stage_bytes + quarter * 2 * kOutBytes;     // wgrad
-        uint32_t turn = 0;
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t out0 = smem_addr(smem) + a.stages * stage_bytes + (warp - 4) * kOutBytes;     // wgrad
         for (int i = first; walk.at(i, t); i += step) {
             const bool some = D != kWgrad || t.end > t.begin;
             const uint32_t acc = used & 1;
             if (some) {
-                if (!epilogue_all<32 * Extra::kTileWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err))) break;
+                if (!epilogue_all<32 * kTileWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err))) break;
                 tc_fence_after();
             }
             const int m = t.m0 + (int)rank * kBM + quarter * 32 + lane;
             const int rows = min(t.n, t.end - t.n0);
             if constexpr (D == kWgrad) {
                 const int m_warp = t.m0 + (int)rank * kBM + quarter * 32;
-                for (int c = 0; m_warp < a.M && c < t.n; c += 64, turn ^= 1) {
-                    const uint32_t buf = out0 + turn * kOutBytes;
-                    if (lane == 0) bulk_wait_smem_read_but_one();      // this buffer's last store has read it
+                for (int c = half * 64; m_warp < a.M && c < t.n; c += 128) {
+                    const uint32_t buf = out0;
+                    if (lane == 0) bulk_wait_smem_read();      // this buffer's last store has read it
                     __syncwarp();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -648,14 +699,8 @@ __global__ void __launch_bounds__(128 + 32 * Extra::kTileWarps, 1)
                         bulk_commit();
                     }
                 }
-            } else if constexpr (Extra::kOwnTile) {
-                extra.tile(tmem + acc * 256 + ((uint32_t)quarter << 21), s_extra, a.out, t.n0, rows, m - lane, a.M, (warp - 4) >> 2, lane);
             } else {
-                for (int c = 0; c < rows; c += 32) {
-                    float v[32];
-                    tmem_load(tmem + acc * 256 + c + ((uint32_t)quarter << 21), v);
-                    store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
-                }
+                extra.tile(tmem + acc * 256 + ((uint32_t)quarter << 21), s_extra, a.out, t.n0, rows, m - lane, a.M, half, lane);
             }
             if (some) {
                 tc_fence_before();
@@ -949,7 +994,7 @@ cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Wide& wid
     }
     const int64_t tiles = gemm_most_tiles(a, D == kWgrad, 2 * kBM), pairs = sm_count() / 2;
     return launch_gemm_as(gemm_kernel<D, Wide>, D == kWgrad ? kWgradSmemMax : kGemmSmemMax, 2u * (unsigned)(tiles < pairs ? tiles : pairs),
-                          128 + 32 * Wide::kTileWarps, 2, stream,
+                          128 + 32 * kTileWarps, 2, stream,
                           maps, a, wide);
 }
 
