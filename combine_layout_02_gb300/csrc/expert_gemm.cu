@@ -97,6 +97,11 @@ ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* othe
             const uint32_t box[2] = {64, 64};
             if ((st = encode_map(&maps.a, rows_a, 2, da, box)) != EP_OK) return st;
             if ((st = encode_map(&maps.b, other, 2, db, box)) != EP_OK) return st;
+            for (int i = 0; i < 6; ++i) {
+                const uint32_t some[2] = {64, 1u << i};
+                if ((st = encode_map(&maps.part_a[i], rows_a, 2, da, some)) != EP_OK) return st;
+                if ((st = encode_map(&maps.part_b[i], other, 2, db, some)) != EP_OK) return st;
+            }
             const uint64_t dout[3] = {K, F, E};
             const uint32_t bout[3] = {64, 32, 1};
             if ((st = encode_map(&maps.out, out, 3, dout, bout)) != EP_OK) return st;

@@ -24,6 +24,7 @@ struct GemmArgs {
 
 struct GemmMaps {
     CUtensorMap a, b, b2, out;      // b2: b with boxes of twice the rows; out: wgrad's
+    CUtensorMap part_a[6], part_b[6];      // wgrad: a and b with boxes of 1, 2, 4, 8, 16, 32 rows
 };
 
 inline bool features_ok(int f) { return f >= 8 && f % 8 == 0; }
@@ -238,26 +239,9 @@ __device__ __forceinline__ float peer_value(uint32_t at) {
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t at) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
 }
-// An arrival that publishes this CTA's shared-memory writes to the pair's other CTA, and the wait there.
-__device__ __forceinline__ void mbar_arrive_peer_release(uint32_t at) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
-}
-__device__ __forceinline__ bool mbar_wait_peer(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* err) {
-    if (!mbar_wait(bar, parity, dead, err)) return false;
-    uint32_t done;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
 __device__ __forceinline__ void mbar_expect_peer(uint32_t at, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(at), "r"(bytes)
                  : "memory");
-}
-__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 // Pair loads: into this CTA's shared memory, completing on a barrier of either CTA (cluster address).
 __device__ __forceinline__ void tma_load2_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -273,6 +257,26 @@ __device__ __forceinline__ void tma_load2_3d(uint32_t dst, const CUtensorMap* ma
             dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+
+// wgrad: the last `left` < 64 rows of an expert, 64 columns from x on. A product takes 16 rows at a time,
+// and the rows that follow are another expert's, whose values may be infinite: so exactly the
+// expert's rows are loaded, in boxes of powers of two, and the rest of the last 16 in boxes that lie beyond the tensor, which reads as zero. (Clearing them with stores and ordering
+// those between the two CTAs cost a third of the whole product's time.)
+__device__ __forceinline__ void load_tail_chunk(uint32_t at, const CUtensorMap* part, int x, int row, int left,
+                                                int num_rows, uint32_t bar) {
+    const int none = 16 - (left & 15);
+    for (int bit = 5; bit >= 0; --bit)
+        if (left >> bit & 1) {
+            tma_load2_2d(at, &part[bit], x, row, bar);
+            at += 128 << bit;
+            row += 1 << bit;
+        }
+    for (int bit = 3; bit >= 0; --bit)
+        if (none >> bit & 1) {
+            tma_load2_2d(at, &part[bit], x, num_rows, bar);
+            at += 128 << bit;
+        }
 }
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -494,20 +498,15 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
 // its expert has rows left (to a multiple of 32): no padding of the experts. Each CTA loads its 128 of
 // the M side and half of the columns; the tensor cores of both read both halves, which halves the
 // shared memory traffic of the columns. Warp 0 loads the M side (TMA), warp 1 of the leader multiplies (tcgen05.mma, fp32 sums in tensor
-// memory, two accumulators of 256 columns in turn), warp 3 loads the columns, warp 2 clears the rows of a wgrad tail that belong
-// to the next expert, warps 4 on write the tile before meanwhile.
+// memory, two accumulators of 256 columns in turn), warp 3 loads the columns, warps 4 on write the tile before
+// meanwhile.
 //   full[s]   leader's: both CTAs' loads (an arrival of each loading warp, and the bytes)
 //   empty[s]  each CTA's: the products that read stage s are done
-//   tail[s]   each CTA's: its loads of a stage that has rows to clear. The other CTA's clearing warp
-//             then arrives at the leader's peer_tail[s], the leader's waits for that and arrives at
-//             full[s] in all loading warps' place: the order between the CTAs is made here, since a fence
-//             at cluster scope in the multiplying warp waits for its products (492 -> 373 us)
 template <Direction D, class Extra>
 __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], peer_tail[kMaxStages];
-    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain;
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int dead;
     __shared__ __align__(16) float s_extra[Extra::kFloats];
@@ -524,8 +523,6 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&full[s], 4);
             mbar_init(&empty[s], 1);
-            mbar_init(&tail[s], 2);
-            mbar_init(&peer_tail[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -550,7 +547,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         Tile t;
         Ring ring(a.stages);
         bool ok = true;
-        const uint32_t full0 = peer_addr(smem_addr(full), 0), tail0 = smem_addr(tail), tail0_here = peer_addr(tail0, rank);
+        const uint32_t full0 = peer_addr(smem_addr(full), 0);
         const uint32_t empty0 = smem_addr(empty), smem0 = smem_addr(smem) + (warp == 0 ? 0 : kABytes);
         const CUtensorMap* map = warp == 0 ? &maps.a : &maps.b;
         for (int i = first; ok && walk.at(i, t); i += step) {
@@ -560,12 +557,20 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             const uint32_t bytes = warp == 0 ? kABytes : (uint32_t)(boxes * box) * 128;
             for (int k0 = 0; k0 < depth; k0 += kBK, ring.next()) {
                 if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a.err))) break;
-                const uint32_t at = smem0 + ring.s * stage_bytes;
-                const bool clear = D == kWgrad && depth - k0 < kBK && ((depth - k0) & 15) != 0;
-                const uint32_t bar = (clear ? tail0_here : full0) + ring.s * 8;
+                const uint32_t at = smem0 + ring.s * stage_bytes, bar = full0 + ring.s * 8;
+                if (D == kWgrad && depth - k0 < kBK && ((depth - k0) & 15) != 0) {
+                    if (elect_one()) {
+                        const int chunks = warp == 0 ? 2 : boxes;
+                        mbar_expect_peer(bar, (uint32_t)(chunks * ((depth - k0 + 15) & ~15)) * 128);
+                        for (int b = 0; b < chunks; ++b)
+                            load_tail_chunk(at + b * kMnChunk, warp == 0 ? maps.part_a : maps.part_b,
+                                            (warp == 0 ? m0 : n0) + b * 64, t.begin + k0, depth - k0, a.num_rows, bar);
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 if (elect_one()) {
-                    if (clear) mbar_expect_at(tail0 + ring.s * 8, bytes);
-                    else mbar_expect_peer(bar, bytes);
+                    mbar_expect_peer(bar, bytes);
                     if (warp == 0) {
                         if (D == kForward) {
                             tma_load2_3d(at, map, k0, m0, t.e, bar);
@@ -627,38 +632,6 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         if (!ok) {
             if (elect_one()) tc_commit2(smem_addr(&drain));
             mbar_wait_bounded(&drain, 0, kGemmWaitNs / 8);
-        }
-    } else if (D == kWgrad && warp == 2) {
-        // The last load of an expert's rows may hold rows of the next expert (whose values may be
-        // infinite): those up to the next multiple of 16 take part in a product, so both operands'
-        // are cleared. A row is a 128-byte line of each 64-column chunk, whatever the swizzle.
-        TileWalk<D> walk(a);
-        Tile t;
-        uint32_t it = 0, phases = 0;
-        for (int i = first; walk.at(i, t); i += step) {
-            const int depth = t.end - t.begin;
-            if (depth <= 0) continue;
-            const int blocks = (depth + kBK - 1) / kBK, left = depth - (blocks - 1) * kBK;
-            it += blocks;
-            if ((left & 15) == 0) continue;
-            const uint32_t s = (it - 1) % a.stages;
-            if (!mbar_wait(&tail[s], (phases >> s) & 1, &dead, a.err)) break;
-            // Four chunks of 64 columns (two of A, up to two of B) of eight 16-byte pieces: a row a step.
-            if (lane >> 3 < 2 + (t.n / 2 + 63) / 64)
-                for (int row = left; row < ((left + 15) & ~15); ++row)
-                    *reinterpret_cast<uint4*>(smem + s * stage_bytes + (lane >> 3) * kMnChunk + row * 128 + (lane & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-            fence_async_smem();
-            __syncwarp();
-            if (rank != 0) {
-                if (lane == 0) mbar_arrive_peer_release(peer_addr(smem_addr(&peer_tail[s]), 0));
-            } else {
-                if (!mbar_wait_peer(&peer_tail[s], (phases >> s) & 1, &dead, a.err)) break;
-                fence_async_smem();
-                __syncwarp();
-                if (lane < 4) mbar_arrive(&full[s]);
-            }
-            phases ^= 1u << s;
         }
     } else if (warp >= 4) {
         TileWalk<D> walk(a);
