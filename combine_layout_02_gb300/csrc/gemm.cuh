@@ -265,7 +265,7 @@ __device__ __forceinline__ void tma_load2_3d(uint32_t dst, const CUtensorMap* ma
 // those between the two CTAs cost a third of the whole product's time.)
 __device__ __forceinline__ void load_tail_chunk(uint32_t at, const CUtensorMap* part, int x, int row, int left,
                                                 int num_rows, uint32_t bar) {
-    const int none = 16 - (left & 15);
+    const int none = -left & 15;
     for (int bit = 5; bit >= 0; --bit)
         if (left >> bit & 1) {
             tma_load2_2d(at, &part[bit], x, row, bar);
@@ -516,6 +516,9 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    // wgrad keeps its last stage for the tails: their loads are issued early in a tile, since their many
+    // small boxes take longer than the ring is ahead (32 experts of 511 rows: 397 -> 330 us).
+    const uint32_t ring_stages = D == kWgrad ? a.stages - 1 : a.stages;
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&maps.a);
@@ -545,8 +548,9 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         if (warp == 3 && blockIdx.x == 0) check_prefix(a, lane);
         TileWalk<D> walk(a);
         Tile t;
-        Ring ring(a.stages);
+        Ring ring(ring_stages);
         bool ok = true;
+        uint32_t tails = 0;
         const uint32_t full0 = peer_addr(smem_addr(full), 0);
         const uint32_t empty0 = smem_addr(empty), smem0 = smem_addr(smem) + (warp == 0 ? 0 : kABytes);
         const CUtensorMap* map = warp == 0 ? &maps.a : &maps.b;
@@ -555,20 +559,26 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             const int half = t.n / 2, m0 = t.m0 + (int)rank * kBM, n0 = t.n0 + (int)rank * half;
             const int box = kBMn ? 64 : half > 64 ? 2 * a.box : a.box, boxes = (half + box - 1) / box;
             const uint32_t bytes = warp == 0 ? kABytes : (uint32_t)(boxes * box) * 128;
-            for (int k0 = 0; k0 < depth; k0 += kBK, ring.next()) {
-                if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a.err))) break;
-                const uint32_t at = smem0 + ring.s * stage_bytes, bar = full0 + ring.s * 8;
-                if (D == kWgrad && depth - k0 < kBK && ((depth - k0) & 15) != 0) {
+            const int whole = D == kWgrad ? depth & ~(kBK - 1) : depth;
+            const int tail_at = depth > whole ? min(whole, (int)ring_stages * kBK) : -1;
+            for (int k0 = 0; k0 < whole || k0 == tail_at; k0 += kBK, ring.next()) {
+                if (D == kWgrad && k0 == tail_at) {
+                    // By now the products of the tile before have freed the tail's stage.
+                    const uint32_t bar = full0 + ring_stages * 8, at = smem0 + ring_stages * stage_bytes;
+                    if (!(ok = mbar_wait_at(empty0 + ring_stages * 8, (tails & 1) ^ 1, &dead, a.err))) break;
+                    ++tails;
                     if (elect_one()) {
-                        const int chunks = warp == 0 ? 2 : boxes;
-                        mbar_expect_peer(bar, (uint32_t)(chunks * ((depth - k0 + 15) & ~15)) * 128);
+                        const int chunks = warp == 0 ? 2 : boxes, left = depth - whole;
+                        mbar_expect_peer(bar, (uint32_t)(chunks * ((left + 15) & ~15)) * 128);
                         for (int b = 0; b < chunks; ++b)
                             load_tail_chunk(at + b * kMnChunk, warp == 0 ? maps.part_a : maps.part_b,
-                                            (warp == 0 ? m0 : n0) + b * 64, t.begin + k0, depth - k0, a.num_rows, bar);
+                                            (warp == 0 ? m0 : n0) + b * 64, t.begin + whole, left, a.num_rows, bar);
                     }
                     __syncwarp();
-                    continue;
+                    if (k0 >= whole) break;
                 }
+                if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a.err))) break;
+                const uint32_t at = smem0 + ring.s * stage_bytes, bar = full0 + ring.s * 8;
                 if (elect_one()) {
                     mbar_expect_peer(bar, bytes);
                     if (warp == 0) {
@@ -592,14 +602,16 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         }
         // The last loads' stages are free: nothing more arrives at this CTA's barriers. (Where a role has
         // given up, that is waited for as long as copies in flight may take.)
-        if (warp == 0)
-            for (int q = 0; q < a.stages; ++q, ring.next())
+        if (warp == 0) {
+            for (uint32_t q = 0; q < ring_stages; ++q, ring.next())
                 mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
+            if (D == kWgrad) mbar_wait_bounded(&empty[ring_stages], (tails & 1) ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
+        }
     } else if (warp == 1 && rank == 0) {
         TileWalk<D> walk(a);
         Tile t;
-        Ring ring(a.stages);
-        uint32_t used = 0;
+        Ring ring(ring_stages);
+        uint32_t used = 0, tails = 0;
         bool ok = true;
         const uint32_t full0 = smem_addr(full), empty0 = smem_addr(empty);
         const uint64_t da0 = smem_desc(smem_addr(smem), kAMn), db0 = smem_desc(smem_addr(smem) + kABytes, kBMn);
@@ -610,18 +622,21 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             if (!(ok = mbar_wait(&acc_empty[acc], ((used >> 1) & 1) ^ 1, &dead, a.err))) break;
             tc_fence_after();
             const uint32_t d = tmem + acc * 256, idesc = instr_desc(2 * kBM, t.n, kAMn, kBMn);
-            for (int k0 = 0; k0 < depth; k0 += kBK, ring.next()) {
-                if (!(ok = mbar_wait_at(full0 + ring.s * 8, ring.phase, &dead, a.err))) break;
+            for (int k0 = 0; k0 < depth; k0 += kBK) {
                 const int left = depth - k0;
+                uint32_t s = ring.s, phase = ring.phase;
+                if (D == kWgrad && left < kBK) s = ring_stages, phase = tails++ & 1;
+                else ring.next();
+                if (!(ok = mbar_wait_at(full0 + s * 8, phase, &dead, a.err))) break;
                 tc_fence_after();
-                const uint64_t at = (uint64_t)((ring.s * stage_bytes) >> 4), da = da0 + at, db = db0 + at;
+                const uint64_t at = (uint64_t)((s * stage_bytes) >> 4), da = da0 + at, db = db0 + at;
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kBK; k += 16) {
                         if (k >= left) break;      // 16 contracted values: 32 bytes of a row, or 16 rows
                         tc_mma2(d, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, (k0 | k) != 0);
                     }
-                    tc_commit2(empty0 + ring.s * 8);
+                    tc_commit2(empty0 + s * 8);
                 }
                 __syncwarp();
             }
