@@ -24,6 +24,7 @@ struct GemmArgs {
 
 struct GemmMaps {
     CUtensorMap a, b, b2, out;      // b2: b with boxes of twice the rows; out: wgrad's
+    CUtensorMap other_b[2];         // b and b2 of the same rows in another order (Extra::reordered)
     CUtensorMap part_a[6], part_b[6];      // wgrad: a and b with boxes of 1, 2, 4, 8, 16, 32 rows
 };
 
@@ -443,13 +444,15 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 // directly follows one of this library after which the call's inputs are complete; only the
 // epilogue waits for that kernel itself.
 //   gemm_kernel:        tile writes rows row0 .. row0 + rows - 1 of a tile, features m0 .. m0 + 31, out of
-//                       tensor memory; two warps do, `half` 0 and 1
+//                       tensor memory; two warps do, `half` 0 and 1. reordered: the rows are loaded
+//                       through other_b
 //   gemm_split_kernel:  ahead for the CTA's rows while the products run (before that wait), then apply
 //                       for each kGroup of them: v[j] belongs to row row0 + c + j. Two halves of 128
 //                       threads take groups in turn
 struct NoExtra {
     static constexpr bool kFollows = false;
     static constexpr int kFloats = 4, kGroup = 32;
+    __device__ __forceinline__ bool reordered() const { return false; }
     // Sixteen rows at a time, to have two blocks' steps in flight.
     __device__ __forceinline__ void tile(uint32_t tmem, float*, __nv_bfloat16* out, int64_t row0, int rows, int m0, int M,
                                          int half, int lane) const {
@@ -553,7 +556,9 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         uint32_t tails = 0;
         const uint32_t full0 = peer_addr(smem_addr(full), 0);
         const uint32_t empty0 = smem_addr(empty), smem0 = smem_addr(smem) + (warp == 0 ? 0 : kABytes);
-        const CUtensorMap* map = warp == 0 ? &maps.a : &maps.b;
+        const bool reordered = extra.reordered();
+        const CUtensorMap* map = warp == 0 ? &maps.a : reordered ? &maps.other_b[0] : &maps.b;
+        const CUtensorMap* map2 = reordered ? &maps.other_b[1] : &maps.b2;
         for (int i = first; ok && walk.at(i, t); i += step) {
             const int depth = D == kWgrad ? t.end - t.begin : a.C;
             const int half = t.n / 2, m0 = t.m0 + (int)rank * kBM, n0 = t.n0 + (int)rank * half;
@@ -594,7 +599,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
                     } else if (kBMn) {
                         for (int b = 0; b < boxes; ++b) tma_load2_2d(at + b * kMnChunk, map, n0 + b * 64, t.begin + k0, bar);
                     } else {
-                        tma_load2_2d(at, half > 64 ? &maps.b2 : map, k0, n0, bar);
+                        tma_load2_2d(at, half > 64 ? map2 : map, k0, n0, bar);
                     }
                 }
                 __syncwarp();

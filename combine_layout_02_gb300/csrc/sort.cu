@@ -22,7 +22,7 @@ constexpr int kSortWarps = 8;                  // warps per block of the count /
 constexpr int kSmallEntries = 8192;            // up to here one block sorts everything
 constexpr int kSmallThreads = 1024;
 constexpr int kTableInts = 48 * 1024 / 4;      // per-warp counts of a block, in shared memory
-constexpr int kSortSmemMax = (kTableInts + EP_MAX_EXPERTS) * 4;
+constexpr int kSortSmemMax = (kTableInts + EP_MAX_EXPERTS + 8) * 4;
 constexpr int kSegment = 128;                  // entries per segment, at least
 constexpr int kMaxSegments = 152 * 16;
 
@@ -31,9 +31,11 @@ struct SortArgs {
     int32_t* entry_rows;      // nullable
     int32_t* row_entries;     // nullable
     int32_t* expert_prefix;
-    int32_t* ws;              // [E][S] segment counts, then [E] totals
+    int32_t* ws;              // [E][S] segment counts ([S] of changes), then [E] totals
     int64_t num_rows;
     int n, E, S, seg_len, warps;
+    int rest;                 // bucket of ids that are none of [0, E), or -1 to leave them out
+    int32_t* changes;         // nullable: how many entries differ from the one before
     uint32_t bad_bit;
     uint32_t* err;
 };
@@ -55,18 +57,22 @@ inline int table_warps(int E, int most) {
 __device__ __forceinline__ int entry_expert(const SortArgs& a, int i, int end, bool flag) {
     if (i >= end) return -1;
     const int64_t e = a.topk_idx[i];
-    if (e >= 0 && e < a.E) return (int)e;
+    if (e >= 0 && e < (a.rest < 0 ? a.E : a.rest)) return (int)e;
     if (flag && e != -1) raise_flag(a.err, a.bad_bit);
-    return -1;
+    return a.rest;
 }
 
-// One warp: counts its segment's entries per expert into its (zeroed) table.
-__device__ __forceinline__ void count_segment(const SortArgs& a, int seg, int* table, int lane) {
+// One warp: counts its segment's entries per expert into its (zeroed) table. Returns, if asked for,
+// this lane's share of the entries that differ from the one before.
+__device__ __forceinline__ int count_segment(const SortArgs& a, int seg, int* table, int lane) {
     const int begin = seg * a.seg_len, end = min(a.n, begin + a.seg_len);
+    int changes = 0;
     for (int i = begin + lane; i < end; i += 32) {
         const int e = entry_expert(a, i, end, true);
         if (e >= 0) atomicAdd(&table[e], 1);      // shared memory; a count, so order is immaterial
+        if (a.changes != nullptr && i > 0) changes += entry_expert(a, i - 1, end, false) != e;
     }
+    return changes;
 }
 
 // One warp: places its segment's entries; table[e] holds the segment's first row of expert e.
@@ -139,8 +145,13 @@ __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(SortArgs a) {
     for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) tables[i] = 0;
     __syncthreads();
     pdl_wait();
-    if (warp < a.warps) count_segment(a, warp, tables + warp * a.E, lane);
+    const int changes = warp < a.warps ? count_segment(a, warp, tables + warp * a.E, lane) : 0;
+    __shared__ int s_changes;
+    if (threadIdx.x == 0) s_changes = 0;
     __syncthreads();
+    if (a.changes != nullptr && changes > 0) atomicAdd(&s_changes, changes);
+    __syncthreads();
+    if (a.changes != nullptr && threadIdx.x == 0) *a.changes = s_changes;
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         int run = 0;
         for (int w = 0; w < a.warps; ++w) {
@@ -166,7 +177,10 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(SortArgs a)
     __syncthreads();
     pdl_wait();
     const int seg0 = blockIdx.x * a.warps;
-    if (warp < a.warps && seg0 + warp < a.S) count_segment(a, seg0 + warp, tables + warp * a.E, lane);
+    if (warp < a.warps && seg0 + warp < a.S) {
+        const int changes = warp_sum(count_segment(a, seg0 + warp, tables + warp * a.E, lane));
+        if (a.changes != nullptr && lane == 0) a.ws[(int64_t)a.E * a.S + seg0 + warp] = changes;
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) {
         const int e = i / a.warps, w = i - e * a.warps;
@@ -175,11 +189,13 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(SortArgs a)
     pdl_trigger();
 }
 
-// One warp per expert: its segments' counts -> exclusive prefix in place, and their total.
+// One warp per expert: its segments' counts -> exclusive prefix in place, and their total (one warp
+// more for the changes, which stand like an expert's after the last one's).
 __global__ void __launch_bounds__(kSortWarps * 32) sort_scan_kernel(SortArgs a) {
     const int e = blockIdx.x * kSortWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     pdl_wait();
-    if (e < a.E) {
+    const int columns = a.E + (a.changes != nullptr);
+    if (e < columns) {
         int32_t* v = a.ws + (int64_t)e * a.S;
         int run = 0;
         constexpr int B = 8;                     // loads in flight per lane
@@ -203,7 +219,8 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_scan_kernel(SortArgs a) 
                 run += __shfl_sync(0xFFFFFFFFu, inc, 31);
             }
         }
-        if (lane == 0) a.ws[(int64_t)a.E * a.S + e] = run;
+        if (lane == 0 && e < a.E) a.ws[(int64_t)columns * a.S + e] = run;
+        if (lane == 0 && e == a.E) *a.changes = run;
     }
     pdl_trigger();
 }
@@ -215,7 +232,8 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(SortArgs a)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const int seg0 = blockIdx.x * a.warps;
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) first[e] = a.ws[(int64_t)a.E * a.S + e];
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+        first[e] = a.ws[(int64_t)(a.E + (a.changes != nullptr)) * a.S + e];
     for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) {
         const int e = i / a.warps, w = i - e * a.warps;
         tables[w * a.E + e] = seg0 + w < a.S ? a.ws[(int64_t)e * a.S + seg0 + w] : 0;
@@ -458,11 +476,16 @@ size_t sort_ids_workspace(int64_t n, int E) {
     const int64_t len = segment_length(n), S = (n + len - 1) / len;
     return (size_t)(S + 1) * (size_t)E * sizeof(int32_t);
 }
+size_t sort_ids_workspace_changes(int64_t n, int E) {
+    return sort_ids_workspace(n, E) + (size_t)(kMaxSegments + 1) * sizeof(int32_t);
+}
 
 cudaError_t launch_sort_ids(const int64_t* ids, int n, int E, int64_t num_rows, int32_t* entry_rows,
                             int32_t* row_entries, int32_t* prefix, void* ws, uint32_t bad_bit, uint32_t* err,
-                            cudaStream_t stream) {
+                            cudaStream_t stream, int rest, int32_t* changes) {
     SortArgs a{};
+    a.rest = rest;
+    a.changes = changes;
     a.topk_idx = ids;
     a.entry_rows = entry_rows;
     a.row_entries = row_entries;
@@ -490,7 +513,8 @@ cudaError_t launch_sort_ids(const int64_t* ids, int n, int E, int64_t num_rows, 
         e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
         if (e == cudaSuccess) e = launch_pdl(sort_count_kernel, dim3(blocks), dim3(kSortWarps * 32), tables, stream, a);
         if (e == cudaSuccess)
-            e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div(E, kSortWarps)), dim3(kSortWarps * 32), 0, stream, a);
+            e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div(E + (changes != nullptr), kSortWarps)),
+                           dim3(kSortWarps * 32), 0, stream, a);
         if (e == cudaSuccess) e = launch_pdl(sort_place_kernel, dim3(blocks), dim3(kSortWarps * 32), smem, stream, a);
     }
     return e;
