@@ -335,12 +335,14 @@ struct AdapterFew : AdapterSide {
     }
 };
 
-// gemm_kernel, many rows. A warp has 32 output features; eight rows at a time it takes their sums out of
-// tensor memory in the layout of warp-level products, so that B_i (32 features x 64 ranks, held in
-// registers as long as the adapter stays) times low comes from those too. (One feature per lane
-// with low broadcast out of shared memory was bound by that broadcast: 500 us where this is
-// 330.) low is fp32: it enters as two bf16 terms, hi + lo, which leave 2^-17 of it; the sums are
-// fp32. A product is taken of one adapter for all eight rows and added to its own rows alone.
+// gemm_kernel, many rows. A warp has 32 output features; it takes the sums of sixteen rows at a time out of
+// tensor memory in the layout of warp-level products, and adds B_i (32 features x 64 ranks, held in
+// registers as long as the adapter stays) times low by such products. low is fp32: it enters as
+// two bf16 terms, hi + lo, which leave 2^-17 of it; the sums are fp32. The terms of the tile's rows
+// are staged in shared memory while the tile's own products run. Where sixteen rows have several
+// adapters, a product is taken of one adapter for eight rows and added to its own rows alone.
+// (One feature per lane with low broadcast out of shared memory was bound by that broadcast, and
+// low taken from memory row by row by its latency: 500 and 365 us where this is 290.)
 constexpr int kHeld = 64;
 
 // hi and lo terms of two fp32 values (an infinite one is its hi term).
@@ -352,12 +354,54 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
 
 struct AdapterWide : AdapterSide {
     static constexpr bool kFollows = false;
-    static constexpr int kRows = 256, kFloats = 2 * kRows;      // the rows' adapters, and which rows they are
+    // shared: the rows' adapters, which rows they are, and the one adapter of sixteen rows (-2: several)
+    static constexpr int kRows = 256, kFloats = 2 * kRows + kRows / 16;
     const int32_t* order;
     const int32_t* changes;
     int T;
 
     __device__ __forceinline__ bool reordered() const { return order != nullptr && scattered(*changes, T); }
+
+    // Staged ranks, and bytes from one row's terms to the next's (16 more than a multiple of 32: eight
+    // rows' pieces of one column lie in different banks).
+    __host__ __device__ static int staged(int r) { return r < kHeld ? (r + 31) / 32 * 32 : kHeld; }
+    __host__ __device__ static int stride(int r) { return 2 * staged(r) + 16; }
+    static int beside(int r) { return 2 * kRows * stride(r); }
+
+    // hi and lo terms of the tile's rows, ranks q0 .. q0 + staged, zero past the last rank.
+    __device__ __forceinline__ void stage(const int* which, unsigned char* terms, int rows, int q0) const {
+        const int pieces = staged(r) / 8, pitch = stride(r);
+        for (int e = threadIdx.x - 128; e < rows * pieces; e += 256) {
+            const int j = e / pieces, q = (e - j * pieces) * 8;
+            uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+            if (q0 + q < r) {
+                const float4 x = low4(which[j], q0 + q), y = low4(which[j], q0 + q + 4);
+                split_pair(x.x, x.y, hi.x, lo.x);
+                split_pair(x.z, x.w, hi.y, lo.y);
+                split_pair(y.x, y.y, hi.z, lo.z);
+                split_pair(y.z, y.w, hi.w, lo.w);
+            }
+            *reinterpret_cast<uint4*>(terms + j * pitch + q * 2) = hi;
+            *reinterpret_cast<uint4*>(terms + kRows * pitch + j * pitch + q * 2) = lo;
+        }
+    }
+    __device__ __forceinline__ void prepare(float* shared, unsigned char* terms, int64_t row0, int rows) const {
+        int* ids = reinterpret_cast<int*>(shared);
+        int* which = ids + kRows;
+        int* one = which + kRows;
+        const int tid = threadIdx.x - 128;
+        const int row = tid >= rows ? 0 : reordered() ? order[row0 + tid] : (int)row0 + tid;
+        const int mine = tid < rows ? adapter(row) : -1;
+        epilogue_barrier<256>();          // the tile before has been read
+        ids[tid] = mine;
+        which[tid] = row;
+        const int lead = __shfl_sync(0xFFFFFFFFu, mine, tid & 16);
+        const unsigned same = __ballot_sync(0xFFFFFFFFu, mine == lead || tid >= rows);
+        if ((tid & 15) == 0) one[tid >> 4] = ((same >> (tid & 16)) & 0xFFFFu) == 0xFFFFu ? mine : -2;
+        epilogue_barrier<256>();
+        stage(which, terms, rows, 0);
+        epilogue_barrier<256>();
+    }
 
     // B_i's values of the warp's 32 features (from m0 on), 64 ranks from q0 on: of features 8h + g, the
     // 8 ranks c*8 .. of each 32. Zero past the edges.
@@ -371,110 +415,95 @@ struct AdapterWide : AdapterSide {
                 w[s][h] = m < F && q0 + s * 32 + c * 8 < r ? *reinterpret_cast<const uint4*>(at + s * 32) : make_uint4(0, 0, 0, 0);
         }
     }
-    // Row j's low values, ranks q0 + s*32 + c*8 .. + 8. which: the tile's rows.
-    __device__ __forceinline__ void load_low(const int* which, int j, int rows, int q0, int c, float4 (&v)[2][2]) const {
+    // d += B_i times the terms of eight rows (`at`: this lane's piece of row g).
+    __device__ __forceinline__ void product(const uint4 (&w)[2][4], const unsigned char* at, float (&d)[2][4]) const {
+        const int pitch = stride(r);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int q = q0 + s * 32 + c * 8;
-            const bool in = j < rows && q < r;
-            v[s][0] = in ? low4(which[j], q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            v[s][1] = in ? low4(which[j], q + 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (s * 32 >= staged(r)) break;
+            const uint4 hi = *reinterpret_cast<const uint4*>(at + s * 64), lo = *reinterpret_cast<const uint4*>(at + kRows * pitch + s * 64);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint4 x = w[s][2 * t], y = w[s][2 * t + 1];
+                mma_16816(d[t], x.x, y.x, x.y, y.y, hi.x, hi.y);
+                mma_16816(d[t], x.z, y.z, x.w, y.w, hi.z, hi.w);
+                mma_16816(d[t], x.x, y.x, x.y, y.y, lo.x, lo.y);
+                mma_16816(d[t], x.z, y.z, x.w, y.w, lo.z, lo.w);
+            }
         }
     }
-
-    __device__ __forceinline__ void tile(uint32_t tmem, float* shared, __nv_bfloat16* out, int64_t row0, int rows, int m0,
-                                         int M, int half, int lane) const {
-        const int g = lane >> 2, c = lane & 3, tid = threadIdx.x - 128;
-        int* ids = reinterpret_cast<int*>(shared);
-        int* which = ids + kRows;
-        const int row = tid >= rows ? 0 : reordered() ? order[row0 + tid] : (int)row0 + tid;
-        const int mine = tid < rows ? adapter(row) : -1;
-        epilogue_barrier<256>();          // the tile before has been read
-        ids[tid] = mine;
-        which[tid] = row;
-        epilogue_barrier<256>();
-        const int split = ((rows + 15) / 16) * 8, begin = half * split, end = half ? rows : min(rows, split);
-        int held = -1;
-        uint4 w[2][4];
-        float4 next[2][2], after[2][2];        // low of the eight rows at work and of the eight to come
-        load_low(which, begin + g, rows, 0, c, next);
-        if (r <= kHeld) load_low(which, begin + 8 + g, rows, 0, c, after);
+    __device__ __forceinline__ void tile(uint32_t tmem, float* shared, unsigned char* terms, __nv_bfloat16* out, int64_t,
+                                         int rows, int m0, int M, int half, int lane) const {
+        const int g = lane >> 2, c = lane & 3, pitch = stride(r);
+        const int* ids = reinterpret_cast<const int*>(shared);
+        const int* which = ids + kRows;
+        const int* one = which + kRows;
+        const bool in = m0 + c * 8 < M;
+        out += m0 + c * 8;
+        for (int q0 = 0; q0 < r; q0 += kHeld) {
+            const bool last = q0 + kHeld >= r;
+            int held = -1;
+            uint4 w[2][4];
+            if (q0 > 0) {
+                epilogue_barrier<256>();
+                stage(which, terms, rows, q0);
+                epilogue_barrier<256>();
+            }
 #pragma unroll 1
-        for (int n = begin; n < end; n += 8) {
-            float v[2][4];
-            tmem_load_16x8(tmem + n, v[0]);
-            tmem_load_16x8(tmem + n + (16u << 16), v[1]);
-            const int4 ia = *reinterpret_cast<const int4*>(ids + n), ib = *reinterpret_cast<const int4*>(ids + n + 4);
-            const int id[8] = {ia.x, ia.y, ia.z, ia.w, ib.x, ib.y, ib.z, ib.w};      // -1 past the last row
-            const int id0 = ids[n + 2 * c], id1 = ids[n + 2 * c + 1];               // of this lane's columns
-            bool one = true;
+            for (int n = half * 16; n < rows; n += 32) {
+                float v[2][2][4];
 #pragma unroll
-            for (int k = 1; k < 8; ++k) one = one && (id[k] == id[0] || n + k >= rows);
-            float delta[2][4] = {};
+                for (int b = 0; b < 2; ++b) {
+                    tmem_load_16x8(tmem + n + b * 8, v[b][0]);
+                    tmem_load_16x8(tmem + n + b * 8 + (16u << 16), v[b][1]);
+                }
+                const int i = one[n >> 4];
+                const unsigned char* at = terms + (n + g) * pitch + c * 16;
+                if (i >= 0 && held != i) {
+                    load_b(i, m0, q0, g, c, w);
+                    held = i;
+                }
+                tmem_wait(v[0]);
+                tmem_wait(v[1]);
+                if (i >= 0) {
+                    product(w, at, v[0]);
+                    product(w, at + 8 * pitch, v[1]);
+                } else if (i == -2) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int id0 = ids[n + b * 8 + 2 * c], id1 = ids[n + b * 8 + 2 * c + 1];      // of this lane's columns
 #pragma unroll 1
-            for (int q0 = 0; q0 < r; q0 += kHeld) {
-                uint32_t hi[2][4], lo[2][4];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    split_pair(next[s][0].x, next[s][0].y, hi[s][0], lo[s][0]);
-                    split_pair(next[s][0].z, next[s][0].w, hi[s][1], lo[s][1]);
-                    split_pair(next[s][1].x, next[s][1].y, hi[s][2], lo[s][2]);
-                    split_pair(next[s][1].z, next[s][1].w, hi[s][3], lo[s][3]);
-                }
-                if (r <= kHeld) {
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) next[s][0] = after[s][0], next[s][1] = after[s][1];
-                    load_low(which, n + 16 + g, rows, 0, c, after);
-                } else {
-                    const bool last = q0 + kHeld >= r;
-                    load_low(which, (last ? n + 8 : n) + g, rows, last ? 0 : q0 + kHeld, c, next);
-                }
-                const auto product = [&](int i, float (&d)[2][4]) {
-                    if (held != i || r > kHeld) {
-                        load_b(i, m0, q0, g, c, w);
-                        held = i;
-                    }
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (q0 + s * 32 >= r) break;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
+                        for (int j = 0; j < 8; ++j) {
+                            const int k = ids[n + b * 8 + j];
+                            bool seen = k < 0;
+                            for (int e = 0; e < j; ++e) seen = seen || ids[n + b * 8 + e] == k;
+                            if (seen) continue;
+                            if (held != k) {
+                                load_b(k, m0, q0, g, c, w);
+                                held = k;
+                            }
+                            float d[2][4] = {};
+                            product(w, at + b * 8 * pitch, d);
 #pragma unroll
                             for (int t = 0; t < 2; ++t) {
-                                const uint4 x = w[s][2 * t], y = w[s][2 * t + 1];
-                                const uint32_t a0 = k ? x.z : x.x, a1 = k ? y.z : y.x, a2 = k ? x.w : x.y, a3 = k ? y.w : y.y;
-                                mma_16816(d[t], a0, a1, a2, a3, hi[s][2 * k], hi[s][2 * k + 1]);
-                                mma_16816(d[t], a0, a1, a2, a3, lo[s][2 * k], lo[s][2 * k + 1]);
+                                if (id0 == k) v[b][t][0] += d[t][0], v[b][t][2] += d[t][2];
+                                if (id1 == k) v[b][t][1] += d[t][1], v[b][t][3] += d[t][3];
                             }
-                    }
-                };
-                if (one) {
-                    if (id[0] >= 0) product(id[0], delta);
-                } else {
-#pragma unroll 1
-                    for (int j = 0; j < 8; ++j) {
-                        const int i = ids[n + j];
-                        bool seen = i < 0;
-#pragma unroll
-                        for (int k = 0; k < 7; ++k) seen = seen || (k < j && id[k] == i);
-                        if (seen) continue;
-                        float d[2][4] = {};
-                        product(i, d);
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (id0 == i) delta[t][0] += d[t][0], delta[t][2] += d[t][2];
-                            if (id1 == i) delta[t][1] += d[t][1], delta[t][3] += d[t][3];
                         }
                     }
                 }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if (!last) {
+                        tmem_store_16x8(tmem + n + b * 8, v[b][0]);
+                        tmem_store_16x8(tmem + n + b * 8 + (16u << 16), v[b][1]);
+                        continue;
+                    }
+                    const uint4 p = rows_of_features(v[b], c);
+                    if (in && n + b * 8 + g < rows) st_v4(out + (int64_t)which[n + b * 8 + g] * M, p);
+                }
             }
-            tmem_wait(v);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[t][k] += delta[t][k];
-            const uint4 p = rows_of_features(v, c);
-            if (n + g < rows && m0 + c * 8 < M) st_v4(out + (int64_t)which[n + g] * M + m0 + c * 8, p);
+            if (!last) tmem_store_wait();
         }
     }
 };
@@ -525,7 +554,7 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         m.M = sh->out_features;
         m.N = m.C = sh->in_features;
         m.err = launch->error_flags;
-        gemm_tiles(&m, false);
+        gemm_tiles(&m, false, AdapterWide::beside(sh->rank));
         const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, T = (uint64_t)sh->num_rows;
         const uint64_t da[3] = {K, F, 1}, db[2] = {K, T};
         const uint32_t ba[3] = {64, (uint32_t)kBM, 1};

@@ -19,6 +19,7 @@ struct GemmArgs {
     int bn, box, stages;       // columns of the widest tile, rows of one load box of B, stages
     int split;                 // CTAs that share a tile's contraction
     int smem;                  // bytes of dynamic shared memory
+    int beside;                // of them beside the stages, for gemm_kernel's epilogue
     uint32_t* err;
 };
 
@@ -118,6 +119,13 @@ __device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+
+__device__ __forceinline__ void tmem_store_16x8(uint32_t at, const float (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 4, 8 consecutive columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[4]) {
@@ -445,7 +453,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 // epilogue waits for that kernel itself.
 //   gemm_kernel:        tile writes rows row0 .. row0 + rows - 1 of a tile, features m0 .. m0 + 31, out of
 //                       tensor memory; two warps do, `half` 0 and 1. reordered: the rows are loaded
-//                       through other_b
+//                       through other_b. prepare is called by all 256 writing threads before, while
+//                       the products run. Both get a.beside bytes of shared memory
 //   gemm_split_kernel:  ahead for the CTA's rows while the products run (before that wait), then apply
 //                       for each kGroup of them: v[j] belongs to row row0 + c + j. Two halves of 128
 //                       threads take groups in turn
@@ -453,9 +462,10 @@ struct NoExtra {
     static constexpr bool kFollows = false;
     static constexpr int kFloats = 4, kGroup = 32;
     __device__ __forceinline__ bool reordered() const { return false; }
+    __device__ __forceinline__ void prepare(float*, unsigned char*, int64_t, int) const {}
     // Sixteen rows at a time, to have two blocks' steps in flight.
-    __device__ __forceinline__ void tile(uint32_t tmem, float*, __nv_bfloat16* out, int64_t row0, int rows, int m0, int M,
-                                         int half, int lane) const {
+    __device__ __forceinline__ void tile(uint32_t tmem, float*, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows,
+                                         int m0, int M, int half, int lane) const {
         const int g = lane >> 2, c = lane & 3;
         const bool in = m0 + c * 8 < M;
         __nv_bfloat16* at = out + (row0 + g) * M + m0 + c * 8;
@@ -662,12 +672,13 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         for (int i = first; walk.at(i, t); i += step) {
             const bool some = D != kWgrad || t.end > t.begin;
             const uint32_t acc = used & 1;
+            const int rows = min(t.n, t.end - t.n0);
+            if (D != kWgrad) extra.prepare(s_extra, smem + a.stages * stage_bytes, t.n0, rows);
             if (some) {
                 if (!epilogue_all<32 * kTileWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err))) break;
                 tc_fence_after();
             }
             const int m = t.m0 + (int)rank * kBM + quarter * 32 + lane;
-            const int rows = min(t.n, t.end - t.n0);
             if constexpr (D == kWgrad) {
                 const int m_warp = t.m0 + (int)rank * kBM + quarter * 32;
                 for (int c = half * 64; m_warp < a.M && c < t.n; c += 128) {
@@ -693,7 +704,8 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
                     }
                 }
             } else {
-                extra.tile(tmem + acc * 256 + ((uint32_t)quarter << 21), s_extra, a.out, t.n0, rows, m - lane, a.M, half, lane);
+                extra.tile(tmem + acc * 256 + ((uint32_t)quarter << 21), s_extra, smem + a.stages * stage_bytes, a.out, t.n0, rows,
+                           m - lane, a.M, half, lane);
             }
             if (some) {
                 tc_fence_before();
@@ -922,7 +934,7 @@ inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1;
 //          two CTAs per SM, and the contraction split as long as all CTAs fit at once (one row,
 //          7168 x 7168: 4 parts 21 us, 8 parts, more CTAs than fit, 35 us); wider tiles are split only
 //          where there are fewer of them than SMs. A part keeps at least eight 64-deep steps.
-inline void gemm_tiles(GemmArgs* a, bool wgrad) {
+inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0) {
     int bn = 256;
     const int avg = (a->num_rows + a->E - 1) / a->E, wide = a->E > 1 ? 2 * (avg < 256 ? avg : 256) : avg;
     if (!wgrad)
@@ -939,8 +951,10 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad) {
     }
     const bool split = gemm_by_split(*a) && !wgrad;
     const int stage = (int)kABytes + (split ? bn * 128 : bn * 64), room = (split && bn <= 64 ? 96 : 200) * 1024;
-    a->stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-    a->smem = a->stages * stage + 1024 + (wgrad ? 8 * (int)kOutBytes : 0);
+    a->beside = split ? 0 : wgrad ? 8 * (int)kOutBytes : beside;
+    const int left = (wgrad ? 224 : 222) * 1024 - a->beside, most = split || left > room ? room : left;
+    a->stages = most / stage < kMaxStages ? most / stage : kMaxStages;
+    a->smem = a->stages * stage + 1024 + a->beside;
 }
 
 // How many tiles of `wide` M indices there can be at most.
@@ -949,7 +963,7 @@ inline int64_t gemm_most_tiles(const GemmArgs& a, bool wgrad, int wide) {
     return mt * (wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn) : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows));
 }
 
-constexpr int kGemmSmemMax = 201 * 1024, kWgradSmemMax = 225 * 1024;
+constexpr int kSplitSmemMax = 201 * 1024, kGemmSmemMax = 224 * 1024, kWgradSmemMax = 225 * 1024;
 
 template <class Kernel, class Extra>
 cudaError_t launch_gemm_as(Kernel kernel, int smem_most, unsigned blocks, unsigned threads, unsigned cluster, cudaStream_t stream,
@@ -981,7 +995,7 @@ cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Wide& wid
         if (gemm_by_split(a)) {
             const int64_t tiles = gemm_most_tiles(a, false, kBM);
             if (tiles * a.split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-            return launch_gemm_as(gemm_split_kernel<D, Few>, kGemmSmemMax, (unsigned)(tiles * a.split), kSplitThreads,
+            return launch_gemm_as(gemm_split_kernel<D, Few>, kSplitSmemMax, (unsigned)(tiles * a.split), kSplitThreads,
                                   (unsigned)a.split, stream, maps, a, few);
         }
     }
