@@ -339,12 +339,12 @@ struct AdapterFew : AdapterSide {
 // tensor memory in the layout of warp-level products, and adds B_i (32 features x 64 ranks, held in
 // registers as long as the adapter stays) times low by such products. low is fp32: it enters as
 // two bf16 terms, hi + lo, which leave 2^-17 of it; the sums are fp32. The terms of the tile's rows
-// are staged in shared memory while the tile's own products run. Where sixteen rows have several
-// adapters, a product is taken of one adapter for eight rows and added to its own rows alone.
+// are staged in shared memory while the tile's own products run, and the tile is cut into runs of
+// rows of one adapter; the next run's part of B is on its way while a run is worked on. Where sixteen
+// rows hold several runs, a product is taken of one run's adapter for eight rows and added to the
+// run's rows alone.
 // (One feature per lane with low broadcast out of shared memory was bound by that broadcast, and
 // low taken from memory row by row by its latency: 500 and 365 us where this is 290.)
-constexpr int kHeld = 64;
-
 // hi and lo terms of two fp32 values (an infinite one is its hi term).
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = pack_bf16x2(a, b);
@@ -352,27 +352,28 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
     lo = pack_bf16x2(isinf(a) ? 0.0f : x, isinf(b) ? 0.0f : y);
 }
 
+// NS: 32 ranks at a time, or 64.
+template <int NS>
 struct AdapterWide : AdapterSide {
     static constexpr bool kFollows = false;
-    // shared: the rows' adapters, which rows they are, and the one adapter of sixteen rows (-2: several)
-    static constexpr int kRows = 256, kFloats = 2 * kRows + kRows / 16;
+    // shared: which rows the tile has, the run each is in, and each run's adapter (and one -1 after)
+    static constexpr int kRows = 256, kHeld = 32 * NS, kFloats = 3 * kRows + 4 + 8;
     const int32_t* order;
     const int32_t* changes;
     int T;
 
     __device__ __forceinline__ bool reordered() const { return order != nullptr && scattered(*changes, T); }
 
-    // Staged ranks, and bytes from one row's terms to the next's (16 more than a multiple of 32: eight
-    // rows' pieces of one column lie in different banks).
-    __host__ __device__ static int staged(int r) { return r < kHeld ? (r + 31) / 32 * 32 : kHeld; }
-    __host__ __device__ static int stride(int r) { return 2 * staged(r) + 16; }
-    static int beside(int r) { return 2 * kRows * stride(r); }
+    // Bytes from one row's terms to the next's (16 more than a multiple of 32: eight rows' pieces of one
+    // column lie in different banks).
+    static constexpr int kPitch = 2 * kHeld + 16, kBeside = 2 * kRows * kPitch;
 
-    // hi and lo terms of the tile's rows, ranks q0 .. q0 + staged, zero past the last rank.
+    // hi and lo terms of the tile's rows, kHeld ranks from q0 on, zero past the last rank.
     __device__ __forceinline__ void stage(const int* which, unsigned char* terms, int rows, int q0) const {
-        const int pieces = staged(r) / 8, pitch = stride(r);
-        for (int e = threadIdx.x - 128; e < rows * pieces; e += 256) {
-            const int j = e / pieces, q = (e - j * pieces) * 8;
+        constexpr int kPieces = kHeld / 8;
+#pragma unroll 2
+        for (int e = threadIdx.x - 128; e < rows * kPieces; e += 256) {
+            const int j = e / kPieces, q = e % kPieces * 8;
             uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
             if (q0 + q < r) {
                 const float4 x = low4(which[j], q0 + q), y = low4(which[j], q0 + q + 4);
@@ -381,47 +382,58 @@ struct AdapterWide : AdapterSide {
                 split_pair(y.x, y.y, hi.z, lo.z);
                 split_pair(y.z, y.w, hi.w, lo.w);
             }
-            *reinterpret_cast<uint4*>(terms + j * pitch + q * 2) = hi;
-            *reinterpret_cast<uint4*>(terms + kRows * pitch + j * pitch + q * 2) = lo;
+            *reinterpret_cast<uint4*>(terms + j * kPitch + q * 2) = hi;
+            *reinterpret_cast<uint4*>(terms + (kRows + j) * kPitch + q * 2) = lo;
         }
     }
     __device__ __forceinline__ void prepare(float* shared, unsigned char* terms, int64_t row0, int rows) const {
-        int* ids = reinterpret_cast<int*>(shared);
-        int* which = ids + kRows;
-        int* one = which + kRows;
-        const int tid = threadIdx.x - 128;
-        const int row = tid >= rows ? 0 : reordered() ? order[row0 + tid] : (int)row0 + tid;
+        int* which = reinterpret_cast<int*>(shared);
+        int* run_of = which + kRows;
+        int* runs = run_of + kRows;
+        int* counts = runs + kRows + 4;
+        const int tid = threadIdx.x - 128, lane = tid & 31, warp = tid >> 5;
+        const bool by_adapter = reordered();
+        const auto row_at = [&](int j) { return by_adapter ? order[row0 + j] : (int)row0 + j; };
+        const int row = tid < rows ? row_at(tid) : 0;
         const int mine = tid < rows ? adapter(row) : -1;
+        const int before = tid < rows && tid > 0 ? adapter(row_at(tid - 1)) : -2;
+        const bool starts = tid < rows && mine != before;
+        const unsigned mask = __ballot_sync(0xFFFFFFFFu, starts);
         epilogue_barrier<256>();          // the tile before has been read
-        ids[tid] = mine;
         which[tid] = row;
-        const int lead = __shfl_sync(0xFFFFFFFFu, mine, tid & 16);
-        const unsigned same = __ballot_sync(0xFFFFFFFFu, mine == lead || tid >= rows);
-        if ((tid & 15) == 0) one[tid >> 4] = ((same >> (tid & 16)) & 0xFFFFu) == 0xFFFFu ? mine : -2;
+        if (lane == 0) counts[warp] = __popc(mask);
         epilogue_barrier<256>();
+        int run = __popc(mask & (lanemask_lt() | 1u << lane)) - 1, all = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) run += counts[w];
+            all += counts[w];
+        }
+        run_of[tid] = tid < rows ? run : all;
+        if (starts) runs[run] = mine;
+        if (tid == 0) runs[all] = -1;
         stage(which, terms, rows, 0);
         epilogue_barrier<256>();
     }
 
-    // B_i's values of the warp's 32 features (from m0 on), 64 ranks from q0 on: of features 8h + g, the
-    // 8 ranks c*8 .. of each 32. Zero past the edges.
-    __device__ __forceinline__ void load_b(int i, int m0, int q0, int g, int c, uint4 (&w)[2][4]) const {
+    // B_i's values of the warp's 32 features (from m0 on), kHeld ranks from q0 on: of features 8h + g, the
+    // 8 ranks c*8 .. of each 32. Zero past the edges; nothing for i = -1.
+    __device__ __forceinline__ void load_b(int i, int m0, int q0, int g, int c, uint4 (&w)[NS][4]) const {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             const int m = m0 + h * 8 + g;
-            const __nv_bfloat16* at = b + ((int64_t)i * F + m) * r + q0 + c * 8;
+            const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q0 + c * 8;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                w[s][h] = m < F && q0 + s * 32 + c * 8 < r ? *reinterpret_cast<const uint4*>(at + s * 32) : make_uint4(0, 0, 0, 0);
+            for (int s = 0; s < NS; ++s)
+                w[s][h] = i >= 0 && m < F && q0 + s * 32 + c * 8 < r ? *reinterpret_cast<const uint4*>(at + s * 32)
+                                                                     : make_uint4(0, 0, 0, 0);
         }
     }
     // d += B_i times the terms of eight rows (`at`: this lane's piece of row g).
-    __device__ __forceinline__ void product(const uint4 (&w)[2][4], const unsigned char* at, float (&d)[2][4]) const {
-        const int pitch = stride(r);
+    __device__ __forceinline__ void product(const uint4 (&w)[NS][4], const unsigned char* at, float (&d)[2][4]) const {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (s * 32 >= staged(r)) break;
-            const uint4 hi = *reinterpret_cast<const uint4*>(at + s * 64), lo = *reinterpret_cast<const uint4*>(at + kRows * pitch + s * 64);
+        for (int s = 0; s < NS; ++s) {
+            const uint4 hi = *reinterpret_cast<const uint4*>(at + s * 64), lo = *reinterpret_cast<const uint4*>(at + kRows * kPitch + s * 64);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const uint4 x = w[s][2 * t], y = w[s][2 * t + 1];
@@ -434,60 +446,69 @@ struct AdapterWide : AdapterSide {
     }
     __device__ __forceinline__ void tile(uint32_t tmem, float* shared, unsigned char* terms, __nv_bfloat16* out, int64_t,
                                          int rows, int m0, int M, int half, int lane) const {
-        const int g = lane >> 2, c = lane & 3, pitch = stride(r);
-        const int* ids = reinterpret_cast<const int*>(shared);
-        const int* which = ids + kRows;
-        const int* one = which + kRows;
+        const int g = lane >> 2, c = lane & 3;
+        const int* which = reinterpret_cast<const int*>(shared);
+        const int* run_of = which + kRows;
+        const int* runs = run_of + kRows;
         const bool in = m0 + c * 8 < M;
         out += m0 + c * 8;
+        const int split = (rows + 31) / 32 * 16, begin = half * split, end = half ? rows : min(rows, split);
         for (int q0 = 0; q0 < r; q0 += kHeld) {
             const bool last = q0 + kHeld >= r;
-            int held = -1;
-            uint4 w[2][4];
             if (q0 > 0) {
                 epilogue_barrier<256>();
                 stage(which, terms, rows, q0);
                 epilogue_barrier<256>();
             }
+            if (begin >= end) continue;
+            int held = run_of[begin];
+            uint4 w[NS][4], next[NS][4];       // of the run at work and of the one after it
+            load_b(runs[held], m0, q0, g, c, w);
+            load_b(runs[run_of[rows - 1] > held ? held + 1 : held], m0, q0, g, c, next);
+            const auto hold = [&](int run) {
+                while (held < run) {
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) w[s][h] = next[s][h];
+                    ++held;
+                    load_b(runs[run_of[rows - 1] > held ? held + 1 : held], m0, q0, g, c, next);
+                }
+            };
 #pragma unroll 1
-            for (int n = half * 16; n < rows; n += 32) {
+            for (int n = begin; n < end; n += 16) {
                 float v[2][2][4];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     tmem_load_16x8(tmem + n + b * 8, v[b][0]);
                     tmem_load_16x8(tmem + n + b * 8 + (16u << 16), v[b][1]);
                 }
-                const int i = one[n >> 4];
-                const unsigned char* at = terms + (n + g) * pitch + c * 16;
-                if (i >= 0 && held != i) {
-                    load_b(i, m0, q0, g, c, w);
-                    held = i;
-                }
+                const int first = run_of[n];
+                const unsigned char* at = terms + (n + g) * kPitch + c * 16;
+                hold(first);
                 tmem_wait(v[0]);
                 tmem_wait(v[1]);
-                if (i >= 0) {
-                    product(w, at, v[0]);
-                    product(w, at + 8 * pitch, v[1]);
-                } else if (i == -2) {
+                if (run_of[min(n + 15, rows - 1)] == first) {
+                    if (runs[first] >= 0) {
+                        product(w, at, v[0]);
+                        product(w, at + 8 * kPitch, v[1]);
+                    }
+                } else {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const int id0 = ids[n + b * 8 + 2 * c], id1 = ids[n + b * 8 + 2 * c + 1];      // of this lane's columns
+                        if (n + b * 8 >= rows) break;
+                        const int run0 = run_of[n + b * 8 + 2 * c], run1 = run_of[n + b * 8 + 2 * c + 1];      // of this lane's columns
+                        const int to = run_of[min(n + b * 8 + 7, rows - 1)];
 #pragma unroll 1
-                        for (int j = 0; j < 8; ++j) {
-                            const int k = ids[n + b * 8 + j];
-                            bool seen = k < 0;
-                            for (int e = 0; e < j; ++e) seen = seen || ids[n + b * 8 + e] == k;
-                            if (seen) continue;
-                            if (held != k) {
-                                load_b(k, m0, q0, g, c, w);
-                                held = k;
-                            }
+                        for (int run = run_of[n + b * 8]; run <= to; ++run) {
+                            hold(run);
+                            if (runs[run] < 0) continue;
                             float d[2][4] = {};
-                            product(w, at + b * 8 * pitch, d);
+                            product(w, at + b * 8 * kPitch, d);
 #pragma unroll
                             for (int t = 0; t < 2; ++t) {
-                                if (id0 == k) v[b][t][0] += d[t][0], v[b][t][2] += d[t][2];
-                                if (id1 == k) v[b][t][1] += d[t][1], v[b][t][3] += d[t][3];
+                                if (run0 == run) v[b][t][0] += d[t][0], v[b][t][2] += d[t][2];
+                                if (run1 == run) v[b][t][1] += d[t][1], v[b][t][3] += d[t][3];
                             }
                         }
                     }
@@ -507,6 +528,16 @@ struct AdapterWide : AdapterSide {
         }
     }
 };
+
+template <int NS>
+cudaError_t launch_wide(const GemmMaps& maps, const GemmArgs& m, const AdapterSide& side, const int32_t* order,
+                        const int32_t* changes, int T, cudaStream_t stream) {
+    AdapterWide<NS> wide{side};
+    wide.order = order;
+    wide.changes = changes;
+    wide.T = T;
+    return launch_gemm<kForward>(maps, m, wide, AdapterFew{side}, stream);
+}
 
 ep_status check_adapter(const ep_adapter_shape* sh) {
     if (sh == nullptr) return EP_ERR_INVALID_ARG;
@@ -554,7 +585,7 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         m.M = sh->out_features;
         m.N = m.C = sh->in_features;
         m.err = launch->error_flags;
-        gemm_tiles(&m, false, AdapterWide::beside(sh->rank));
+        gemm_tiles(&m, false, sh->rank <= 32 ? AdapterWide<1>::kBeside : AdapterWide<2>::kBeside);
         const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, T = (uint64_t)sh->num_rows;
         const uint64_t da[3] = {K, F, 1}, db[2] = {K, T};
         const uint32_t ba[3] = {64, (uint32_t)kBM, 1};
@@ -595,11 +626,9 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
             if (e == cudaSuccess) e = launch_low_of<true>(g, launch->stream);
         }
         if (e == cudaSuccess) {
-            AdapterWide by_adapter{side};
-            by_adapter.order = wide && g.L > 0 ? order : nullptr;
-            by_adapter.changes = changes;
-            by_adapter.T = g.T;
-            e = launch_gemm<kForward>(maps, m, by_adapter, AdapterFew{side}, launch->stream);
+            const int32_t* by_adapter = wide && g.L > 0 ? order : nullptr;
+            e = g.r <= 32 ? launch_wide<1>(maps, m, side, by_adapter, changes, g.T, launch->stream)
+                          : launch_wide<2>(maps, m, side, by_adapter, changes, g.T, launch->stream);
         }
         if (e != cudaSuccess) return cuda_fail(e);
     }

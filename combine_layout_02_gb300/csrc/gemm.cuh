@@ -952,7 +952,7 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0) {
     const bool split = gemm_by_split(*a) && !wgrad;
     const int stage = (int)kABytes + (split ? bn * 128 : bn * 64), room = (split && bn <= 64 ? 96 : 200) * 1024;
     a->beside = split ? 0 : wgrad ? 8 * (int)kOutBytes : beside;
-    const int left = (wgrad ? 224 : 222) * 1024 - a->beside, most = split || left > room ? room : left;
+    const int left = (wgrad ? 224 : 220) * 1024 - a->beside, most = split || left > room ? room : left;
     a->stages = most / stage < kMaxStages ? most / stage : kMaxStages;
     a->smem = a->stages * stage + 1024 + a->beside;
 }
@@ -963,7 +963,7 @@ inline int64_t gemm_most_tiles(const GemmArgs& a, bool wgrad, int wide) {
     return mt * (wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn) : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows));
 }
 
-constexpr int kSplitSmemMax = 201 * 1024, kGemmSmemMax = 224 * 1024, kWgradSmemMax = 225 * 1024;
+constexpr int kSplitSmemMax = 201 * 1024, kGemmSmemMax = 222 * 1024, kWgradSmemMax = 225 * 1024;
 
 template <class Kernel, class Extra>
 cudaError_t launch_gemm_as(Kernel kernel, int smem_most, unsigned blocks, unsigned threads, unsigned cluster, cudaStream_t stream,
