@@ -268,6 +268,8 @@ struct AdapterSide {
 // rows at a time, fp32. Their B values
 // are requested before their low values are staged, and towards L2 while the projection is
 // computed. Loops, not unrolled code: a launch meets each instruction once, out of L2.
+// G: 8-rank pieces of B taken at a time (their latency is what a group of rows waits for).
+template <int G>
 struct AdapterFew : AdapterSide {
     static constexpr bool kFollows = true;
     static constexpr int kGroup = 4, kRows = 256;
@@ -291,14 +293,14 @@ struct AdapterFew : AdapterSide {
         const int* ids = reinterpret_cast<const int*>(shared + kIds) + c;
         const int tid = (threadIdx.x - 64) & 127;
         shared += half * kLow;
-        uint4 u[kGroup][2];
+        uint4 u[kGroup][G];
         const auto load_b = [&](int q0) {
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
                 const int i = c + j < rows && m < F ? ids[j] : -1;
                 const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q0;
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
+                for (int g = 0; g < G; ++g)
                     u[j][g] = i >= 0 && q0 + g * 8 < r ? *reinterpret_cast<const uint4*>(at + g * 8) : make_uint4(0, 0, 0, 0);
             }
         };
@@ -311,10 +313,10 @@ struct AdapterFew : AdapterSide {
         }
         epilogue_barrier<128>(2 + half);
 #pragma unroll 1
-        for (int q0 = 0; q0 < r; q0 += 16) {
+        for (int q0 = 0; q0 < r; q0 += 8 * G) {
             if (q0 > 0) load_b(q0);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+            for (int g = 0; g < G; ++g) {
                 if (q0 + g * 8 >= r) break;
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j) {
@@ -536,7 +538,8 @@ cudaError_t launch_wide(const GemmMaps& maps, const GemmArgs& m, const AdapterSi
     wide.order = order;
     wide.changes = changes;
     wide.T = T;
-    return launch_gemm<kForward>(maps, m, wide, AdapterFew{side}, stream);
+    return side.r <= 16 ? launch_gemm<kForward>(maps, m, wide, AdapterFew<2>{side}, stream)
+                        : launch_gemm<kForward>(maps, m, wide, AdapterFew<4>{side}, stream);
 }
 
 ep_status check_adapter(const ep_adapter_shape* sh) {

@@ -933,7 +933,8 @@ inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1;
 //          so that most experts are one tile. Up to 64 columns the weights' loads are what counts:
 //          two CTAs per SM, and the contraction split as long as all CTAs fit at once (one row,
 //          7168 x 7168: 4 parts 21 us, 8 parts, more CTAs than fit, 35 us); wider tiles are split only
-//          where there are fewer of them than SMs. A part keeps at least eight 64-deep steps.
+//          where there are fewer of them than SMs. A part keeps at least eight 64-deep steps
+//          (wider tiles: sixteen; below, pairs of CTAs are as fast and write faster).
 inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0) {
     int bn = 256;
     const int avg = (a->num_rows + a->E - 1) / a->E, wide = a->E > 1 ? 2 * (avg < 256 ? avg : 256) : avg;
@@ -947,7 +948,7 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0) {
         const int64_t tiles = (int64_t)ceil_div(a->M, kBM) * (a->E < a->num_rows ? a->E : a->num_rows) * ceil_div(avg, bn);
         const int64_t want = bn <= 64 ? 2 * sms : sms;
         const int steps = ceil_div(a->C, kBK);
-        while (a->split < 8 && tiles * a->split * 2 <= want && steps >= a->split * 16) a->split *= 2;
+        while (a->split < 8 && tiles * a->split * 2 <= want && steps >= a->split * (bn <= 64 ? 16 : 32)) a->split *= 2;
     }
     const bool split = gemm_by_split(*a) && !wgrad;
     const int stage = (int)kABytes + (split ? bn * 128 : bn * 64), room = (split && bn <= 64 ? 96 : 200) * 1024;

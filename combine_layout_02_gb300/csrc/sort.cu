@@ -369,6 +369,25 @@ __global__ void __launch_bounds__(kRowWarps * 32, MIN_BLOCKS) unsort_kernel(RowA
     pdl_trigger();
 }
 
+// Few rows: the four warps of a block share a row.
+template <int U, int P, bool V32>
+__global__ void __launch_bounds__(kRowWarps * 32) unsort_wide_kernel(RowArgs a) {
+    __shared__ int64_t s_row[EP_MAX_TOPK];
+    __shared__ float s_coef[EP_MAX_TOPK];
+    __shared__ int s_n;
+    pdl_wait();
+    const int64_t t = blockIdx.x;
+    if (threadIdx.x < 32) {
+        const int nd = placed_rows(a, t, threadIdx.x, s_row, s_coef, nullptr);
+        if (threadIdx.x == 0) s_n = nd;
+    }
+    __syncthreads();
+    char* out = a.out + t * (int64_t)a.H * 2;
+    if (V32) gather_reduce_row32<U, P>(a.y, s_row, s_coef, s_n, a.H, out, threadIdx.x, kRowWarps * 32);
+    else gather_reduce_row<U, P>(a.y, s_row, s_coef, s_n, a.H, out, threadIdx.x, kRowWarps * 32);
+    pdl_trigger();
+}
+
 using UnsortKernel = void (*)(RowArgs);
 UnsortKernel unsort_form(int H, int k, bool y32) {
     if (H <= 256) return unsort_kernel<1, 4, false, 10>;
@@ -378,36 +397,44 @@ UnsortKernel unsort_form(int H, int k, bool y32) {
     return unsort_kernel<2, 4, true>;
 }
 
-// One warp per row: its gradient dout[t] is read once per batch of P placed entries (from L1 / L2
+// SHARE warps per row: its gradient dout[t] is read once per batch of P placed entries (from L1 / L2
 // after the first), each entry's row of y once, each entry's dy written once; the weights'
-// gradients are summed in fp32, per lane over the row's units and then over the lanes by a fixed
-// tree. dy may be y: a lane reads its unit of y before it writes the same unit of dy.
-template <int P>
+// gradients are summed in fp32, per lane over the row's units, over the lanes by a fixed tree, and
+// over the warps in order. dy may be y: a lane reads its unit of y before it writes the same unit of dy.
+// Wide rows are shared by a block's four warps, so that few rows still keep enough loads in flight
+// (1528 rows of 6912 channels: 50 -> 25 us).
+template <int P, int SHARE>
 __global__ void __launch_bounds__(kRowWarps * 32) unsort_backward_kernel(RowArgs a) {
-    __shared__ int64_t s_row[kRowWarps][EP_MAX_TOPK];
-    __shared__ float s_coef[kRowWarps][EP_MAX_TOPK];
-    __shared__ int s_entry[kRowWarps][EP_MAX_TOPK];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kRows = kRowWarps / SHARE;     // of a block
+    __shared__ int64_t s_row[kRows][EP_MAX_TOPK];
+    __shared__ float s_coef[kRows][EP_MAX_TOPK];
+    __shared__ int s_entry[kRows][EP_MAX_TOPK], s_n[kRows];
+    __shared__ float s_sum[kRowWarps][EP_MAX_TOPK];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = warp / SHARE, first = threadIdx.x % (SHARE * 32);
     pdl_wait();
-    const int64_t t = (int64_t)blockIdx.x * kRowWarps + warp;
+    const int64_t t = (int64_t)blockIdx.x * kRows + slot;
+    if (t < a.N && warp % SHARE == 0) {
+        const int nd = placed_rows(a, t, lane, s_row[slot], s_coef[slot], s_entry[slot]);
+        if (lane == 0) s_n[slot] = nd;
+    }
+    __syncthreads();
     if (t < a.N) {
-        const int nd = placed_rows(a, t, lane, s_row[warp], s_coef[warp], s_entry[warp]);
-        __syncwarp();
+        const int nd = s_n[slot];
         const int64_t row_bytes = (int64_t)a.H * 2;
         const char* g = a.dout + t * row_bytes;
-        float mine = 0.0f;                       // lane j: the gradient of entry j's weight
         for (int p0 = 0; p0 < nd; p0 += P) {
             float acc[P];
 #pragma unroll
             for (int p = 0; p < P; ++p) acc[p] = 0.0f;
-            for (int u = lane; u < a.H >> 3; u += 32) {
+#pragma unroll 2
+            for (int u = first; u < a.H >> 3; u += SHARE * 32) {
                 const uint4 d4 = *reinterpret_cast<const uint4*>(g + (int64_t)u * 16);
                 const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w};
                 uint4 v[P];
                 if (a.dweights != nullptr) {
 #pragma unroll
                     for (int p = 0; p < P; ++p)
-                        if (p0 + p < nd) v[p] = *reinterpret_cast<const uint4*>(a.y + s_row[warp][p0 + p] * row_bytes + (int64_t)u * 16);
+                        if (p0 + p < nd) v[p] = *reinterpret_cast<const uint4*>(a.y + s_row[slot][p0 + p] * row_bytes + (int64_t)u * 16);
                 }
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
@@ -421,12 +448,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) unsort_backward_kernel(RowArgs
                         }
                     }
                     if (a.dy != nullptr) {
-                        const float c = s_coef[warp][p0 + p];
+                        const float c = s_coef[slot][p0 + p];
                         const uint4 o = make_uint4(pack_bf16x2(c * bf16_lo(d[0]), c * bf16_hi(d[0])),
                                                    pack_bf16x2(c * bf16_lo(d[1]), c * bf16_hi(d[1])),
                                                    pack_bf16x2(c * bf16_lo(d[2]), c * bf16_hi(d[2])),
                                                    pack_bf16x2(c * bf16_lo(d[3]), c * bf16_hi(d[3])));
-                        st_v4(a.dy + s_row[warp][p0 + p] * row_bytes + (int64_t)u * 16, o);
+                        st_v4(a.dy + s_row[slot][p0 + p] * row_bytes + (int64_t)u * 16, o);
                     }
                 }
             }
@@ -436,11 +463,23 @@ __global__ void __launch_bounds__(kRowWarps * 32) unsort_backward_kernel(RowArgs
                     float s = acc[p];
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-                    if (p0 + p < nd && lane == s_entry[warp][p0 + p]) mine = s;
+                    if (p0 + p < nd && lane == 0) s_sum[warp][p0 + p] = s;
                 }
             }
         }
-        if (a.dweights != nullptr && lane < a.k) a.dweights[t * a.k + lane] = mine;
+    }
+    __syncthreads();
+    if (t < a.N && a.dweights != nullptr && warp % SHARE == 0) {
+        // lane j: the gradient of entry j's weight, zero unless placed
+        const int nd = s_n[slot];
+        float mine = 0.0f;
+        for (int p = 0; p < nd; ++p) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < SHARE; ++w) s += s_sum[warp + w][p];
+            if (lane == s_entry[slot][p]) mine = s;
+        }
+        if (lane < a.k) a.dweights[t * a.k + lane] = mine;
     }
     pdl_trigger();
 }
@@ -608,8 +647,12 @@ ep_status ep_unsort_rows(const ep_shape* sh, const void* y, const float* topk_we
     a.topk_weights = topk_weights;
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (N > 0) {
-        cudaError_t e = launch_pdl(unsort_form(a.H, a.k, ((uintptr_t)y & 31) == 0), dim3(row_blocks(N, kRowWarps)),
-                                   dim3(kRowWarps * 32), 0, launch->stream, a);
+        // One warp per row needs about eight rows per SM to have its loads in flight.
+        const bool y32 = ((uintptr_t)y & 31) == 0, share = a.H >= 2048 && N < 8 * sm_count();
+        cudaError_t e = launch_pdl(share ? (y32 ? unsort_wide_kernel<1, 8, true> : unsort_wide_kernel<2, 4, false>)
+                                         : unsort_form(a.H, a.k, y32),
+                                   dim3(share ? (unsigned)N : row_blocks(N, kRowWarps)), dim3(kRowWarps * 32), 0,
+                                   launch->stream, a);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return end_call(launch);
@@ -633,7 +676,9 @@ ep_status ep_unsort_rows_backward(const ep_shape* sh, const void* dout, const vo
     a.topk_weights = topk_weights;
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (N > 0) {
-        cudaError_t e = launch_pdl(unsort_backward_kernel<4>, dim3(row_blocks(N, kRowWarps)), dim3(kRowWarps * 32), 0,
+        const bool share = a.H >= 2048;
+        cudaError_t e = launch_pdl(share ? unsort_backward_kernel<4, kRowWarps> : unsort_backward_kernel<4, 1>,
+                                   dim3(share ? (unsigned)N : row_blocks(N, kRowWarps)), dim3(kRowWarps * 32), 0,
                                    launch->stream, a);
         if (e != cudaSuccess) return cuda_fail(e);
     }
