@@ -15,8 +15,11 @@ struct AdapterArgs {
     const int64_t* idx;
     const int32_t* order;      // rows by adapter, and [L + 1] where each adapter's begin (many rows)
     const int32_t* prefix;
+    const int32_t* changes;    // wide: scattered rows' x is copied to sorted_x in that order, by
+    char* sorted_x;            // the blocks from copy_from on (one warp per row)
     float* low;                // [parts][T][r]
     int T, K, L, r, parts;
+    unsigned copy_from;
     uint32_t* err;
 };
 
@@ -55,6 +58,51 @@ inline int low_parts(int T, int L, int K) {
     return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 
+// Rows in many short runs of one adapter (under sixteen on average): the projection then takes them by
+// adapter, out of a copy in that order, and scatters its results. (8191 rows in any order of 16
+// adapters, rank 64: 820 -> 440 us; a run's rows are read where they are.)
+__device__ __forceinline__ bool scattered(int changes, int T) { return changes > T / 16; }
+
+// One warp: block number -> adapter and up to 32 of its rows in the order, 32 adapters at a time; -1
+// past the last.
+__device__ __forceinline__ int find_rows(const AdapterArgs& a, int lane, int& from, int& to) {
+    int first = 0;
+    for (int i0 = 0; i0 < a.L; i0 += 32) {
+        int begin = 0, end = 0;
+        if (i0 + lane < a.L) {
+            begin = a.prefix[i0 + lane];
+            end = a.prefix[i0 + lane + 1];
+        }
+        const int tiles = (end - begin + kLowRows - 1) / kLowRows;
+        int upto = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += up;
+        }
+        const int start = first + upto - tiles, b = (int)blockIdx.x;
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, b >= start && b < start + tiles);
+        if (hit != 0) {
+            const int src = __ffs(hit) - 1;
+            from = __shfl_sync(0xFFFFFFFFu, begin + (b - start) * kLowRows, src);
+            to = min(from + kLowRows, __shfl_sync(0xFFFFFFFFu, end, src));
+            return i0 + src;
+        }
+        first += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    from = to = 0;
+    return -1;
+}
+
+// The blocks from copy_from on: one warp copies a row to its place in the order. True for them.
+__device__ __forceinline__ bool copy_block(const AdapterArgs& a, int warp, int lane) {
+    if (blockIdx.x < a.copy_from) return false;
+    const int64_t p = (int64_t)(blockIdx.x - a.copy_from) * kLowWarps + warp, row_bytes = (int64_t)a.K * 2;
+    if (blockIdx.y == 0 && p < a.T && scattered(*a.changes, a.T))
+        scatter_copy_row<4>(reinterpret_cast<const char*>(a.x) + a.order[p] * row_bytes, a.sorted_x, &p, 1, row_bytes, lane, 32);
+    return true;
+}
+
 // low[part][t][q] = scales[i] * sum over the part's k of x[t][k] A_i[q][k], for up to 32 rows of one
 // adapter; NT * 8 ranks at a time. The warps share the part and join in shared memory in warp order;
 // the parts are added up by the projection's epilogue. Operands come straight from memory: a
@@ -77,34 +125,13 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapter_low_kernel(AdapterA
         pdl_wait();
         pdl_trigger();
     }
+    if (SORTED && copy_block(a, warp, lane)) return;
     if (warp == 0) {
         int adapter = -1, row = -1;
         if (SORTED) {
-            // block number -> adapter and which of its 32 rows, 32 adapters at a time
-            int first = 0;
-            for (int i0 = 0; i0 < a.L && adapter < 0; i0 += 32) {
-                int begin = 0, count = 0;
-                if (i0 + lane < a.L) {
-                    begin = a.prefix[i0 + lane];
-                    count = a.prefix[i0 + lane + 1] - begin;
-                }
-                const int tiles = (count + kLowRows - 1) / kLowRows;
-                int upto = tiles;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int up = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-                    if (lane >= o) upto += up;
-                }
-                const int start = first + upto - tiles, b = (int)blockIdx.x;
-                const unsigned hit = __ballot_sync(0xFFFFFFFFu, b >= start && b < start + tiles);
-                if (hit != 0) {
-                    const int src = __ffs(hit) - 1;
-                    adapter = i0 + src;
-                    const int at = __shfl_sync(0xFFFFFFFFu, begin + (b - start) * kLowRows, src) + lane;
-                    if (at < __shfl_sync(0xFFFFFFFFu, begin + count, src)) row = a.order[at];
-                }
-                first += __shfl_sync(0xFFFFFFFFu, upto, 31);
-            }
+            int begin, end;
+            adapter = find_rows(a, lane, begin, end);
+            if (adapter >= 0 && begin + lane < end) row = a.order[begin + lane];
         } else {
             if (blockIdx.x == 0 && blockIdx.y == 0)
                 for (int t = lane; t < a.T; t += 32) adapter_of(a, t, true);
@@ -184,9 +211,9 @@ cudaError_t launch_low(const AdapterArgs& g, cudaStream_t stream) {
         cudaError_t e = cudaFuncSetAttribute(adapter_low_kernel<NT, SORTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    const int64_t blocks = low_blocks(g.T, g.L);
-    return launch_pdl(adapter_low_kernel<NT, SORTED>, dim3((unsigned)(blocks > 0 ? blocks : 1), (unsigned)g.parts),
-                      dim3(kLowWarps * 32), smem, stream, g);
+    const unsigned copies = SORTED && g.sorted_x != nullptr ? (unsigned)ceil_div(g.T, kLowWarps) : 0u;
+    const unsigned blocks = SORTED ? g.copy_from + copies : (unsigned)(low_blocks(g.T, g.L) > 0 ? low_blocks(g.T, g.L) : 1);
+    return launch_pdl(adapter_low_kernel<NT, SORTED>, dim3(blocks, (unsigned)g.parts), dim3(kLowWarps * 32), smem, stream, g);
 }
 
 template <bool SORTED>
@@ -218,21 +245,6 @@ AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
         w.bytes = w.x + (sh->num_rows > 64 ? T * sh->in_features * 2 : 0);
     }
     return w;
-}
-
-// Rows in many short runs of one adapter (under sixteen on average): the projection then takes them by
-// adapter, out of a copy in that order, and scatters its results. (8191 rows in any order of 16
-// adapters, rank 64: 820 -> 440 us; a run's rows are read where they are.)
-__device__ __forceinline__ bool scattered(int changes, int T) { return changes > T / 16; }
-
-// x in the order of the adapters, one warp per row.
-__global__ void __launch_bounds__(256) adapter_gather_kernel(const char* x, const int32_t* order, const int32_t* changes,
-                                                             char* out, int T, int64_t row_bytes) {
-    pdl_wait();
-    const int64_t p = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (p < T && scattered(*changes, T))
-        scatter_copy_row<8>(x + order[p] * row_bytes, out, &p, 1, row_bytes, threadIdx.x & 31, 32);
-    pdl_trigger();
 }
 
 // The epilogue's part: y += B_i low. A row only ever meets its own adapter's values.
@@ -612,8 +624,9 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         int32_t* prefix = reinterpret_cast<int32_t*>(base + ws.prefix);
         int32_t* changes = reinterpret_cast<int32_t*>(base + ws.changes);
         const AdapterArgs g{reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(a), scales,
-                            adapter_idx, order, prefix, reinterpret_cast<float*>(workspace), sh->num_rows,
-                            sh->in_features, sh->num_adapters, sh->rank, ws.parts, launch->error_flags};
+                            adapter_idx, order, prefix, changes, wide ? base + ws.x : nullptr,
+                            reinterpret_cast<float*>(workspace), sh->num_rows, sh->in_features, sh->num_adapters, sh->rank,
+                            ws.parts, (unsigned)low_blocks(sh->num_rows, sh->num_adapters), launch->error_flags};
         const AdapterSide side{reinterpret_cast<const __nv_bfloat16*>(b), g.low, adapter_idx, (int64_t)g.T * g.r, g.parts,
                                sh->out_features, g.L, g.r};
         cudaError_t e = cudaSuccess;
@@ -622,10 +635,6 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         } else {
             e = launch_sort_ids(adapter_idx, g.T, g.L + 1, g.T, nullptr, order, prefix, base + ws.scratch,
                                 EP_DEVERR_BAD_ADAPTER, launch->error_flags, launch->stream, g.L, changes);
-            if (e == cudaSuccess && wide)
-                e = launch_pdl(adapter_gather_kernel, dim3((unsigned)((g.T + 7) / 8)), dim3(256), 0, launch->stream,
-                               reinterpret_cast<const char*>(x), (const int32_t*)order, (const int32_t*)changes,
-                               base + ws.x, g.T, (int64_t)g.K * 2);
             if (e == cudaSuccess) e = launch_low_of<true>(g, launch->stream);
         }
         if (e == cudaSuccess) {

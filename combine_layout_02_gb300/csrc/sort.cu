@@ -402,7 +402,7 @@ UnsortKernel unsort_form(int H, int k, bool y32) {
 // gradients are summed in fp32, per lane over the row's units, over the lanes by a fixed tree, and
 // over the warps in order. dy may be y: a lane reads its unit of y before it writes the same unit of dy.
 // Wide rows are shared by a block's four warps, so that few rows still keep enough loads in flight
-// (1528 rows of 6912 channels: 50 -> 25 us).
+// (both gradients of 1528 rows of 6912 channels: 62.5 -> 38.6 us).
 template <int P, int SHARE>
 __global__ void __launch_bounds__(kRowWarps * 32) unsort_backward_kernel(RowArgs a) {
     constexpr int kRows = kRowWarps / SHARE;     // of a block
