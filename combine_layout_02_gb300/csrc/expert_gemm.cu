@@ -15,24 +15,32 @@ namespace {
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using CurrentFn = CUresult (*)(CUcontext*);
 
-// The driver's encoder, looked up once (the library does not link the driver library).
-EncodeFn encoder() {
-    static const EncodeFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
+// A driver function, looked up once (the library does not link the driver library).
+void* driver_function(const char* name) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        p = nullptr;
+    return p;
+}
+
+// The encoder wants a current context, which a thread that has only been given a device (an
+// autograd thread's first call, for one) does not have yet.
+bool bind_context() {
+    static const CurrentFn current = reinterpret_cast<CurrentFn>(driver_function("cuCtxGetCurrent"));
+    CUcontext ctx = nullptr;
+    if (current != nullptr && current(&ctx) == CUDA_SUCCESS && ctx != nullptr) return true;
+    int device = 0;
+    return cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess;
 }
 }  // namespace
 
 ep_status encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint32_t* box) {
-    const EncodeFn fn = encoder();
-    if (fn == nullptr) return cuda_fail(cudaErrorNotSupported);
+    static const EncodeFn fn = reinterpret_cast<EncodeFn>(driver_function("cuTensorMapEncodeTiled"));
+    if (fn == nullptr || !bind_context()) return cuda_fail(cudaErrorNotSupported);
     cuuint64_t d[3], strides[2];
     cuuint32_t b[3], ones[3] = {1, 1, 1};
     uint64_t stride = 2;
@@ -45,7 +53,8 @@ ep_status encode_map(CUtensorMap* map, const void* base, int rank, const uint64_
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, strides, b,
                           ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? EP_OK : EP_ERR_UNSUPPORTED;
+    if (r == CUDA_ERROR_INVALID_VALUE) return EP_ERR_UNSUPPORTED;
+    return r == CUDA_SUCCESS ? EP_OK : cuda_fail(cudaErrorUnknown);
 }
 
 namespace {

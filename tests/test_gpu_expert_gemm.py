@@ -178,3 +178,25 @@ def test_rows_beyond_32_bit_offsets():
     want = (y[-33:].double() @ w[1].double())
     mags = (y[-33:].double().abs() @ w[1].double().abs())
     assert_within(dx[-33:], want, sum_bound(F, mags, 2 * U32), U16)
+
+
+def test_a_threads_first_call():
+    """A thread that has made no CUDA call before (as autograd's has not)."""
+    import threading
+    x, dy, w, prefix, n = data([40, 30], 128, 64, 10, integers)
+    want, got = Products(x, dy, w, prefix, n), []
+    sh, y = ep.ep_gemm_shape(n, 2, 128, 64), torch.empty_like(dy)
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call():
+        try:
+            ep.ep_expert_gemm(sh, x, w, prefix, y, ep.ep_launch(stream or None, None, None, None))
+            got.append(None)
+        except Exception as e:
+            got.append(e)
+
+    t = threading.Thread(target=call)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert got == [None] and torch.equal(y, want.y)
