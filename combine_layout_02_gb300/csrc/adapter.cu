@@ -5,6 +5,7 @@
 // the projection starts while low is still computed; its epilogue waits for it.
 #include "gemm.cuh"
 #include "rowops.cuh"
+#include "sort.cuh"
 
 namespace ep {
 namespace {

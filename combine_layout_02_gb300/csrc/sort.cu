@@ -14,6 +14,7 @@
 // and combine. Everything is bound by memory: each row is read once and each sorted row written
 // (or read) once.
 #include "rowops.cuh"
+#include "sort.cuh"
 
 namespace ep {
 namespace {
