@@ -6,7 +6,8 @@
 // and within a segment a warp takes 32 entries at a time: an entry's rank among them is the
 // number of lower lanes with the same expert (__match_any_sync), on top of the warp's running
 // count in shared memory. Counts only, no global atomics: the placement is the same in every
-// run. Few entries: one block does all of it (sort_small_kernel). More: count, scan (one warp
+// run. These kernels let the next one launch as soon as it has itself waited (the next waits for its end
+// before it reads): the launch is then over by that end. Few entries: one block does all of it (sort_small_kernel). More: count, scan (one block
 // per expert over the segments' counts) and place, three kernels without any inter-block wait.
 //
 // Rows (ep_sort_rows, ep_unsort_rows, ep_unsort_rows_backward): one warp per row in row order,
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(SortArgs a) {
     for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) tables[i] = 0;
     __syncthreads();
     pdl_wait();
+    pdl_trigger();
     const int changes = warp < a.warps ? count_segment(a, warp, tables + warp * a.E, lane) : 0;
     __shared__ int s_changes;
     if (threadIdx.x == 0) s_changes = 0;
@@ -168,7 +170,6 @@ __global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(SortArgs a) {
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.expert_prefix[e] = e < a.E ? first[e] : total;
     __syncthreads();
     if (warp < a.warps) place_segment(a, warp, tables + warp * a.E, lane);
-    pdl_trigger();
 }
 
 __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(SortArgs a) {
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(SortArgs a)
     for (int i = threadIdx.x; i < a.warps * a.E; i += blockDim.x) tables[i] = 0;
     __syncthreads();
     pdl_wait();
+    pdl_trigger();
     const int seg0 = blockIdx.x * a.warps;
     if (warp < a.warps && seg0 + warp < a.S) {
         const int changes = warp_sum(count_segment(a, seg0 + warp, tables + warp * a.E, lane));
@@ -187,43 +189,48 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(SortArgs a)
         const int e = i / a.warps, w = i - e * a.warps;
         if (seg0 + w < a.S) a.ws[(int64_t)e * a.S + seg0 + w] = tables[w * a.E + e];
     }
-    pdl_trigger();
 }
 
-// One warp per expert: its segments' counts -> exclusive prefix in place, and their total (one warp
-// more for the changes, which stand like an expert's after the last one's).
+// One block per expert: its segments' counts -> exclusive prefix in place, and their total (one block
+// more for the changes, which stand like an expert's after the last one's). A thread has a run of
+// up to kRun counts, all loaded before the first is used.
 __global__ void __launch_bounds__(kSortWarps * 32) sort_scan_kernel(SortArgs a) {
-    const int e = blockIdx.x * kSortWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    constexpr int kRun = (kMaxSegments + kSortWarps * 32 - 1) / (kSortWarps * 32);
+    __shared__ int s_sum[kSortWarps];
+    const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
-    const int columns = a.E + (a.changes != nullptr);
-    if (e < columns) {
-        int32_t* v = a.ws + (int64_t)e * a.S;
-        int run = 0;
-        constexpr int B = 8;                     // loads in flight per lane
-        for (int s0 = 0; s0 < a.S; s0 += 32 * B) {
-            int c[B];
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int s = s0 + b * 32 + lane;
-                c[b] = s < a.S ? v[s] : 0;
-            }
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                int inc = c[b];
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-                    if (lane >= o) inc += up;
-                }
-                const int s = s0 + b * 32 + lane;
-                if (s < a.S) v[s] = run + inc - c[b];
-                run += __shfl_sync(0xFFFFFFFFu, inc, 31);
-            }
-        }
-        if (lane == 0 && e < a.E) a.ws[(int64_t)columns * a.S + e] = run;
-        if (lane == 0 && e == a.E) *a.changes = run;
-    }
     pdl_trigger();
+    const int columns = a.E + (a.changes != nullptr);
+    int32_t* v = a.ws + (int64_t)e * a.S;
+    const int per = (a.S + kSortWarps * 32 - 1) / (kSortWarps * 32), first = threadIdx.x * per;
+    int c[kRun], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) c[i] = i < per && first + i < a.S ? v[first + i] : 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) sum += c[i];
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += up;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    int run = upto - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        if (w < warp) run += s_sum[w];
+        total += s_sum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+        if (i < per && first + i < a.S) v[first + i] = run;
+        run += c[i];
+    }
+    if (threadIdx.x == 0) {
+        if (e < a.E) a.ws[(int64_t)columns * a.S + e] = total;
+        else *a.changes = total;
+    }
 }
 
 __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(SortArgs a) {
@@ -232,6 +239,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(SortArgs a)
     int* tables = smem + a.E;          // [warps][E]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
+    pdl_trigger();
     const int seg0 = blockIdx.x * a.warps;
     for (int e = threadIdx.x; e < a.E; e += blockDim.x)
         first[e] = a.ws[(int64_t)(a.E + (a.changes != nullptr)) * a.S + e];
@@ -246,7 +254,6 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(SortArgs a)
         for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.expert_prefix[e] = e < a.E ? first[e] : total;
     __syncthreads();
     if (warp < a.warps && seg0 + warp < a.S) place_segment(a, seg0 + warp, tables + warp * a.E, lane);
-    pdl_trigger();
 }
 
 // ------------------------------------------------------------------ rows
@@ -542,7 +549,8 @@ cudaError_t launch_sort_ids(const int64_t* ids, int n, int E, int64_t num_rows, 
         a.seg_len = ceil_div(ceil_div(n > 0 ? n : 1, a.warps), 32) * 32;
         a.S = a.warps;
         const size_t smem = (size_t)(a.warps + 1) * E * sizeof(int);
-        e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
+        if (smem > 48 * 1024)
+            e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
         if (e == cudaSuccess) e = launch_pdl(sort_small_kernel, dim3(1), dim3(kSmallThreads), smem, stream, a);
     } else {
         a.warps = table_warps(E, kSortWarps);
@@ -550,11 +558,12 @@ cudaError_t launch_sort_ids(const int64_t* ids, int n, int E, int64_t num_rows, 
         a.S = ceil_div(n, a.seg_len);
         const unsigned blocks = (unsigned)ceil_div(a.S, a.warps);
         const size_t tables = (size_t)a.warps * E * sizeof(int), smem = tables + (size_t)E * sizeof(int);
-        e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
+        if (smem > 48 * 1024)
+            e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
         if (e == cudaSuccess) e = launch_pdl(sort_count_kernel, dim3(blocks), dim3(kSortWarps * 32), tables, stream, a);
         if (e == cudaSuccess)
-            e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div(E + (changes != nullptr), kSortWarps)),
-                           dim3(kSortWarps * 32), 0, stream, a);
+            e = launch_pdl(sort_scan_kernel, dim3((unsigned)(E + (changes != nullptr))), dim3(kSortWarps * 32), 0,
+                           stream, a);
         if (e == cudaSuccess) e = launch_pdl(sort_place_kernel, dim3(blocks), dim3(kSortWarps * 32), smem, stream, a);
     }
     return e;
@@ -620,7 +629,8 @@ ep_status ep_sort_rows(const ep_shape* sh, const void* x, ep_dtype x_dtype, cons
         const size_t smem = (size_t)kTmaWarps * a.row_bytes;
         cudaError_t e = cudaSuccess;
         if (smem <= (size_t)kTmaSmemMax) {
-            e = cudaFuncSetAttribute(sort_rows_tma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTmaSmemMax);
+            if (smem > 48 * 1024)
+                e = cudaFuncSetAttribute(sort_rows_tma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTmaSmemMax);
             if (e == cudaSuccess)
                 e = launch_pdl(sort_rows_tma_kernel, dim3(row_blocks(N, kTmaWarps)), dim3(kTmaWarps * 32), smem,
                                launch->stream, a);
@@ -649,9 +659,10 @@ ep_status ep_unsort_rows(const ep_shape* sh, const void* y, const float* topk_we
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (N > 0) {
         // One warp per row needs about eight rows per SM to have its loads in flight.
+        const bool few = sort->num_rows <= 2 * (int64_t)N;          // at most two entries a row on average
         const bool y32 = ((uintptr_t)y & 31) == 0, share = a.H >= 2048 && N < 8 * sm_count();
         cudaError_t e = launch_pdl(share ? (y32 ? unsort_wide_kernel<1, 8, true> : unsort_wide_kernel<2, 4, false>)
-                                         : unsort_form(a.H, a.k, y32),
+                                         : unsort_form(a.H, few ? 2 : a.k, y32),
                                    dim3(share ? (unsigned)N : row_blocks(N, kRowWarps)), dim3(kRowWarps * 32), 0,
                                    launch->stream, a);
         if (e != cudaSuccess) return cuda_fail(e);
