@@ -268,33 +268,39 @@ __device__ __forceinline__ void tma_load2_3d(uint32_t dst, const CUtensorMap* ma
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    tma_load_2d_at(smem_addr(dst), map, x, y, smem_addr(bar));
+}
+
 // wgrad: the last `left` < 64 rows of an expert, 64 columns from x on. A product takes 16 rows at a time,
 // and the rows that follow are another expert's, whose values may be infinite: so exactly the
 // expert's rows are loaded, in boxes of powers of two, and the rest of the last 16 in boxes that lie beyond the tensor, which reads as zero. (Clearing them with stores and ordering
 // those between the two CTAs cost a third of the whole product's time.)
+template <bool PAIR>
 __device__ __forceinline__ void load_tail_chunk(uint32_t at, const CUtensorMap* part, int x, int row, int left,
                                                 int num_rows, uint32_t bar) {
     const int none = -left & 15;
     for (int bit = 5; bit >= 0; --bit)
         if (left >> bit & 1) {
-            tma_load2_2d(at, &part[bit], x, row, bar);
+            if (PAIR) tma_load2_2d(at, &part[bit], x, row, bar);
+            else tma_load_2d_at(at, &part[bit], x, row, bar);
             at += 128 << bit;
             row += 1 << bit;
         }
     for (int bit = 3; bit >= 0; --bit)
         if (none >> bit & 1) {
-            tma_load2_2d(at, &part[bit], x, num_rows, bar);
+            if (PAIR) tma_load2_2d(at, &part[bit], x, num_rows, bar);
+            else tma_load_2d_at(at, &part[bit], x, num_rows, bar);
             at += 128 << bit;
         }
 }
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
-}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -586,7 +592,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
                         const int chunks = warp == 0 ? 2 : boxes, left = depth - whole;
                         mbar_expect_peer(bar, (uint32_t)(chunks * ((left + 15) & ~15)) * 128);
                         for (int b = 0; b < chunks; ++b)
-                            load_tail_chunk(at + b * kMnChunk, warp == 0 ? maps.part_a : maps.part_b,
+                            load_tail_chunk<true>(at + b * kMnChunk, warp == 0 ? maps.part_a : maps.part_b,
                                             (warp == 0 ? m0 : n0) + b * 64, t.begin + whole, left, a.num_rows, bar);
                     }
                     __syncwarp();
@@ -725,10 +731,22 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
 
 // ------------------------------------------------------------------ few rows: split contraction
 
-// One warp: tile number i of all experts (forward / dgrad, as TileWalk counts them), 32 experts at a
-// time; false past the last one.
+// One warp: tile number i of all experts, M tiles of 128 innermost; forward / dgrad: 32 experts at a time;
+// false past the last one.
+template <Direction D>
 __device__ __forceinline__ bool find_tile(const GemmArgs& a, int i, int lane, Tile& out) {
     const int mt = (a.M + kBM - 1) / kBM;
+    if (D == kWgrad) {
+        const int nt = (a.N + a.bn - 1) / a.bn, e = i / (mt * nt), c = i / mt % nt;
+        if (e >= a.E) return false;
+        out.e = e;
+        out.m0 = i % mt * kBM;
+        out.n0 = c * a.bn;
+        out.n = (min(a.bn, a.N - out.n0) + 15) & ~15;
+        out.begin = expert_begin(a, e);
+        out.end = max(out.begin, expert_end(a, e));
+        return true;
+    }
     int first = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
@@ -767,7 +785,8 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& a, int i, int lane, Ti
 
 constexpr int kSplitThreads = 320;
 
-// forward / dgrad where rows are few and the weights are what is read: a cluster of `split` CTAs per
+// Where rows are few and the weights are what is read (forward, dgrad), or where tiles are few and the
+// rows many (wgrad): a cluster of `split` CTAs per
 // tile, each over its part of the contraction, so that enough CTAs stream weights at the same time
 // (and two fit an SM, one filling its pipeline while the other runs). Each CTA leaves its fp32 part
 // in its own shared memory; after a cluster barrier each adds up, in rank order, the parts of
@@ -782,7 +801,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     __shared__ __align__(16) float s_extra[Extra::kFloats];
     __shared__ Tile s_tile;
     __shared__ int s_has;
-    constexpr bool kAMn = D != kForward;
+    constexpr bool kAMn = D != kForward, kBMn = D == kWgrad;
     unsigned char* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const uint32_t stage_bytes = kABytes + (uint32_t)a.bn * 128;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -802,7 +821,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     if (!Extra::kFollows) pdl_wait();
     if (warp == 2) {
         Tile t{};
-        const bool has = find_tile(a, blockIdx.x / a.split, lane, t);
+        const bool has = find_tile<D>(a, blockIdx.x / a.split, lane, t);
         if (lane == 0) {
             s_tile = t;
             s_has = has;
@@ -815,7 +834,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     const uint32_t tmem = s_tmem;
     const Tile t = s_tile;
     const bool has = s_has;            // the same in all CTAs of a cluster
-    const int blocks = (a.C + kBK - 1) / kBK;
+    const int depth = D == kWgrad ? t.end - t.begin : a.C, blocks = (depth + kBK - 1) / kBK;
     const int kb0 = (int)((int64_t)blocks * rank / a.split), kb1 = (int)((int64_t)blocks * (rank + 1) / a.split);
 
     if (has && warp == 0 && lane == 0) {
@@ -828,49 +847,68 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
             if (!(ok = mbar_wait(&empty[s], ((it / a.stages) & 1) ^ 1, &dead, a.err))) break;
             unsigned char* sa = smem + s * stage_bytes;
             unsigned char* sb = sa + kABytes;
-            const int k0 = kb * kBK;
+            const int k0 = kb * kBK, left = depth - k0;
+            if (D == kWgrad && left < kBK && (left & 15) != 0) {
+                mbar_expect_bytes(&full[s], (uint32_t)((2 + boxes) * ((left + 15) & ~15)) * 128);
+                for (int c = 0; c < 2 + boxes; ++c)
+                    load_tail_chunk<false>(smem_addr(sa) + c * kMnChunk, c < 2 ? maps.part_a : maps.part_b,
+                                           c < 2 ? t.m0 + c * 64 : t.n0 + (c - 2) * 64, t.begin + k0, left, a.num_rows,
+                                           smem_addr(&full[s]));
+                continue;
+            }
             mbar_expect_bytes(&full[s], bytes);
             if (D == kForward) {
                 tma_load_3d(sa, &maps.a, k0, t.m0, t.e, &full[s]);
-            } else {
+            } else if (D == kDgrad) {
                 tma_load_3d(sa, &maps.a, t.m0, k0, t.e, &full[s]);
                 tma_load_3d(sa + kMnChunk, &maps.a, t.m0 + 64, k0, t.e, &full[s]);
+            } else {
+                tma_load_2d(sa, &maps.a, t.m0, t.begin + k0, &full[s]);
+                tma_load_2d(sa + kMnChunk, &maps.a, t.m0 + 64, t.begin + k0, &full[s]);
             }
-            for (int b = 0; b < boxes; ++b) tma_load_2d(sb + b * a.box * 128, &maps.b, k0, t.n0 + b * a.box, &full[s]);
+            for (int b = 0; b < boxes; ++b) {
+                if (kBMn) tma_load_2d(sb + b * kMnChunk, &maps.b, t.n0 + b * 64, t.begin + k0, &full[s]);
+                else tma_load_2d(sb + b * a.box * 128, &maps.b, k0, t.n0 + b * a.box, &full[s]);
+            }
         }
         if (!ok) {     // wait, with a limit, for the copies still in flight
             for (uint32_t q = it > (uint32_t)a.stages ? it - a.stages : 0; q < it; ++q)
                 mbar_wait_bounded(&full[q % a.stages], (q / a.stages) & 1, kGemmWaitNs / 8);
         }
     } else if (has && warp == 1 && lane == 0) {
-        const uint32_t idesc = instr_desc(kBM, t.n, kAMn, false);
+        const uint32_t idesc = instr_desc(kBM, t.n, kAMn, kBMn);
         uint32_t it = 0;
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
             const uint32_t s = it % a.stages;
             if (!mbar_wait(&full[s], (it / a.stages) & 1, &dead, a.err)) break;
             tc_fence_after();
             const uint32_t sa = smem_addr(smem + s * stage_bytes), sb = sa + kABytes;
-            const uint64_t da = smem_desc(sa, kAMn), db = smem_desc(sb, false);
+            const uint64_t da = smem_desc(sa, kAMn), db = smem_desc(sb, kBMn);
+            const int left = depth - kb * kBK;
 #pragma unroll
-            for (int k = 0; k < kBK; k += 16)
-                tc_mma(tmem, da + (kAMn ? k * 128 : k * 2) / 16, db + k * 2 / 16, idesc, (it | k) != 0);
+            for (int k = 0; k < kBK; k += 16) {
+                if (D == kWgrad && k >= left) break;
+                tc_mma(tmem, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, (it | k) != 0);
+            }
             tc_commit(&empty[s]);
         }
         tc_commit(&done);
     }
     __syncwarp();
     const int quarter = warp & 3, half = (warp - 2) >> 2, m_local = quarter * 32 + lane, m = t.m0 + m_local;
-    const int rows = min(t.n, t.end - t.n0);
-    const int share = (rows + a.split - 1) / a.split, lo = rank * share, hi = min(rows, lo + share);   // of the rows
+    // Columns of the tile (rows; wgrad: in_features, eight at a time), and this CTA's share of them.
+    const int rows = D == kWgrad ? min(t.n, a.N - t.n0) : min(t.n, t.end - t.n0), unit = D == kWgrad ? 8 : 1;
+    const int share = (rows + a.split * unit - 1) / (a.split * unit) * unit, lo = rank * share, hi = min(rows, lo + share);
     bool ok = has;
     if (has && warp >= 2) {
-        extra.ahead(s_extra, t.n0 + lo, hi - lo, m, half);
+        if (D != kWgrad) extra.ahead(s_extra, t.n0 + lo, hi - lo, m, half);
         ok = epilogue_all<256>(mbar_wait(&done, 0, &dead, a.err));
         tc_fence_after();
     }
     if (Extra::kFollows && warp >= 2) pdl_wait();
     constexpr int G = Extra::kGroup;
-    if (a.split == 1) {
+    const bool some = kb1 > kb0;
+    if (D != kWgrad && a.split == 1) {
         if (ok && warp >= 2) {
             for (int c = half * G; c < rows; c += 2 * G) {
                 float v[G];
@@ -881,7 +919,6 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         }
     } else {
         float* part = reinterpret_cast<float*>(smem);      // [columns][128]; every product has read its stage
-        const bool some = kb1 > kb0;
         if (ok && warp >= 2) {
             for (int c = half * 8; c < rows; c += 16) {
                 float v[8];
@@ -897,8 +934,19 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         }
         __syncwarp();
         cluster_barrier();
-        if (ok && warp >= 2 && lo < hi) {
-            const uint32_t at = smem_addr(part);
+        const uint32_t at = smem_addr(part);
+        if constexpr (D == kWgrad) {
+            for (int c = lo + half * 8; ok && warp >= 2 && m < a.M && c < hi; c += 16) {
+                float v[8] = {};
+                for (int r = 0; r < a.split; ++r) {
+                    const uint32_t peer = peer_addr(at, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += peer_value(peer + ((c + j) * kBM + m_local) * 4);
+                }
+                st_v4(a.out + ((int64_t)t.e * a.M + m) * a.N + t.n0 + c,
+                      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+            }
+        } else if (ok && warp >= 2 && lo < hi) {
             for (int c = lo + half * G; c < hi; c += 2 * G) {
                 float v[G];
 #pragma unroll
@@ -924,11 +972,19 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
 
 // ------------------------------------------------------------------ host
 
-// Whether gemm_split_kernel runs (else gemm_kernel).
+// How many tiles of `wide` M indices there can be at most.
+inline int64_t gemm_most_tiles(const GemmArgs& a, bool wgrad, int wide) {
+    const int64_t mt = ceil_div(a.M, wide);
+    return mt * (wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn) : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows));
+}
+
+// Whether gemm_split_kernel runs (else gemm_kernel). (In clusters of at least two also for wgrad.)
 inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1; }
 
 // Column tile width, stages and split.
-//   wgrad: tiles of 256 columns, a pair of CTAs each.
+//   wgrad: tiles of 256 columns, a pair of CTAs each; where those are less than half of the pairs
+//          and experts have many rows, tiles of 128 x 128 whose rows are split (one expert of 7568 rows,
+//          672 -> 392 features: 40 -> 15 us).
 //   else:  tiles of twice the average rows of an expert (one group: of its rows), within [32, 256],
 //          so that most experts are one tile. Up to 64 columns the weights' loads are what counts:
 //          two CTAs per SM, and the contraction split as long as all CTAs fit at once (one row,
@@ -950,18 +1006,19 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0) {
         const int steps = ceil_div(a->C, kBK);
         while (a->split < 8 && tiles * a->split * 2 <= want && steps >= a->split * (bn <= 64 ? 16 : 32)) a->split *= 2;
     }
-    const bool split = gemm_by_split(*a) && !wgrad;
+    if (wgrad && 2 * gemm_most_tiles(*a, true, 2 * kBM) <= sms / 2 && avg >= 16 * kBK) {
+        a->bn = 128;
+        const int64_t tiles = gemm_most_tiles(*a, true, kBM);
+        while (a->split < 8 && tiles * a->split * 2 <= sms && avg >= a->split * 8 * kBK) a->split *= 2;
+        if (a->split == 1) a->bn = 256;
+    }
+    bn = a->bn;
+    const bool split = gemm_by_split(*a);
     const int stage = (int)kABytes + (split ? bn * 128 : bn * 64), room = (split && bn <= 64 ? 96 : 200) * 1024;
     a->beside = split ? 0 : wgrad ? 8 * (int)kOutBytes : beside;
     const int left = (wgrad ? 224 : 220) * 1024 - a->beside, most = split || left > room ? room : left;
     a->stages = most / stage < kMaxStages ? most / stage : kMaxStages;
     a->smem = a->stages * stage + 1024 + a->beside;
-}
-
-// How many tiles of `wide` M indices there can be at most.
-inline int64_t gemm_most_tiles(const GemmArgs& a, bool wgrad, int wide) {
-    const int64_t mt = ceil_div(a.M, wide);
-    return mt * (wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn) : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows));
 }
 
 constexpr int kSplitSmemMax = 201 * 1024, kGemmSmemMax = 222 * 1024, kWgradSmemMax = 225 * 1024;
@@ -992,13 +1049,11 @@ cudaError_t launch_gemm_as(Kernel kernel, int smem_most, unsigned blocks, unsign
 // Launches the product (a.num_rows > 0) as gemm_tiles has laid it out.
 template <Direction D, class Wide, class Few>
 cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Wide& wide, const Few& few, cudaStream_t stream) {
-    if constexpr (D != kWgrad) {
-        if (gemm_by_split(a)) {
-            const int64_t tiles = gemm_most_tiles(a, false, kBM);
-            if (tiles * a.split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-            return launch_gemm_as(gemm_split_kernel<D, Few>, kSplitSmemMax, (unsigned)(tiles * a.split), kSplitThreads,
-                                  (unsigned)a.split, stream, maps, a, few);
-        }
+    if (gemm_by_split(a)) {
+        const int64_t tiles = gemm_most_tiles(a, D == kWgrad, kBM);
+        if (tiles * a.split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+        return launch_gemm_as(gemm_split_kernel<D, Few>, kSplitSmemMax, (unsigned)(tiles * a.split), kSplitThreads,
+                              (unsigned)a.split, stream, maps, a, few);
     }
     const int64_t tiles = gemm_most_tiles(a, D == kWgrad, 2 * kBM), pairs = sm_count() / 2;
     return launch_gemm_as(gemm_kernel<D, Wide>, D == kWgrad ? kWgradSmemMax : kGemmSmemMax, 2u * (unsigned)(tiles < pairs ? tiles : pairs),

@@ -21,6 +21,8 @@ CASES = {
     "many_experts": ([(7 * e) % 5 for e in range(300)], 64, 128),
     "one_each": ([1] * 32, 520, 392),
     "few_rows_deep": ([3, 0, 2, 5, 1, 0, 4, 1], 4096, 256),
+    "many_rows_few_features": ([3000, 0, 1111, 1], 136, 200),
+    "one_long_expert": ([4099], 264, 392),
     "decode": ([16, 30, 8, 15, 2, 40, 0, 9], 1024, 1024),
 }
 
