@@ -68,9 +68,8 @@ __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Pair forms (cta_group::2): one thread of the leader CTA multiplies for both.
@@ -252,6 +251,9 @@ __device__ __forceinline__ void mbar_expect_peer(uint32_t at, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(at), "r"(bytes)
                  : "memory");
 }
+__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 // Pair loads: into this CTA's shared memory, completing on a barrier of either CTA (cluster address).
 __device__ __forceinline__ void tma_load2_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
@@ -274,10 +276,6 @@ __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap* 
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    tma_load_2d_at(smem_addr(dst), map, x, y, smem_addr(bar));
-}
-
 // wgrad: the last `left` < 64 rows of an expert, 64 columns from x on. A product takes 16 rows at a time,
 // and the rows that follow are another expert's, whose values may be infinite: so exactly the
 // expert's rows are loaded, in boxes of powers of two, and the rest of the last 16 in boxes that lie beyond the tensor, which reads as zero. (Clearing them with stores and ordering
@@ -301,11 +299,10 @@ __device__ __forceinline__ void load_tail_chunk(uint32_t at, const CUtensorMap* 
         }
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
@@ -837,62 +834,63 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     const int depth = D == kWgrad ? t.end - t.begin : a.C, blocks = (depth + kBK - 1) / kBK;
     const int kb0 = (int)((int64_t)blocks * rank / a.split), kb1 = (int)((int64_t)blocks * (rank + 1) / a.split);
 
-    if (has && warp == 0 && lane == 0) {
+    if (has && warp == 0) {
         const int boxes = (t.n + a.box - 1) / a.box;
-        const uint32_t bytes = kABytes + (uint32_t)boxes * a.box * 128;
-        uint32_t it = 0;
+        const uint32_t bytes = kABytes + (uint32_t)boxes * a.box * 128, smem0 = smem_addr(smem);
+        const uint32_t full0 = smem_addr(full), empty0 = smem_addr(empty);
+        Ring ring(a.stages);
         bool ok = true;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-            const uint32_t s = it % a.stages;
-            if (!(ok = mbar_wait(&empty[s], ((it / a.stages) & 1) ^ 1, &dead, a.err))) break;
-            unsigned char* sa = smem + s * stage_bytes;
-            unsigned char* sb = sa + kABytes;
+        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+            if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a.err))) break;
+            const uint32_t sa = smem0 + ring.s * stage_bytes, sb = sa + kABytes, bar = full0 + ring.s * 8;
             const int k0 = kb * kBK, left = depth - k0;
-            if (D == kWgrad && left < kBK && (left & 15) != 0) {
-                mbar_expect_bytes(&full[s], (uint32_t)((2 + boxes) * ((left + 15) & ~15)) * 128);
-                for (int c = 0; c < 2 + boxes; ++c)
-                    load_tail_chunk<false>(smem_addr(sa) + c * kMnChunk, c < 2 ? maps.part_a : maps.part_b,
-                                           c < 2 ? t.m0 + c * 64 : t.n0 + (c - 2) * 64, t.begin + k0, left, a.num_rows,
-                                           smem_addr(&full[s]));
-                continue;
+            if (elect_one()) {
+                if (D == kWgrad && left < kBK && (left & 15) != 0) {
+                    mbar_expect_at(bar, (uint32_t)((2 + boxes) * ((left + 15) & ~15)) * 128);
+                    for (int c = 0; c < 2 + boxes; ++c)
+                        load_tail_chunk<false>(sa + c * kMnChunk, c < 2 ? maps.part_a : maps.part_b,
+                                               c < 2 ? t.m0 + c * 64 : t.n0 + (c - 2) * 64, t.begin + k0, left, a.num_rows, bar);
+                } else {
+                    mbar_expect_at(bar, bytes);
+                    if (D == kForward) {
+                        tma_load_3d_at(sa, &maps.a, k0, t.m0, t.e, bar);
+                    } else if (D == kDgrad) {
+                        tma_load_3d_at(sa, &maps.a, t.m0, k0, t.e, bar);
+                        tma_load_3d_at(sa + kMnChunk, &maps.a, t.m0 + 64, k0, t.e, bar);
+                    } else {
+                        tma_load_2d_at(sa, &maps.a, t.m0, t.begin + k0, bar);
+                        tma_load_2d_at(sa + kMnChunk, &maps.a, t.m0 + 64, t.begin + k0, bar);
+                    }
+                    for (int b = 0; b < boxes; ++b) {
+                        if (kBMn) tma_load_2d_at(sb + b * kMnChunk, &maps.b, t.n0 + b * 64, t.begin + k0, bar);
+                        else tma_load_2d_at(sb + b * a.box * 128, &maps.b, k0, t.n0 + b * a.box, bar);
+                    }
+                }
             }
-            mbar_expect_bytes(&full[s], bytes);
-            if (D == kForward) {
-                tma_load_3d(sa, &maps.a, k0, t.m0, t.e, &full[s]);
-            } else if (D == kDgrad) {
-                tma_load_3d(sa, &maps.a, t.m0, k0, t.e, &full[s]);
-                tma_load_3d(sa + kMnChunk, &maps.a, t.m0 + 64, k0, t.e, &full[s]);
-            } else {
-                tma_load_2d(sa, &maps.a, t.m0, t.begin + k0, &full[s]);
-                tma_load_2d(sa + kMnChunk, &maps.a, t.m0 + 64, t.begin + k0, &full[s]);
-            }
-            for (int b = 0; b < boxes; ++b) {
-                if (kBMn) tma_load_2d(sb + b * kMnChunk, &maps.b, t.n0 + b * 64, t.begin + k0, &full[s]);
-                else tma_load_2d(sb + b * a.box * 128, &maps.b, k0, t.n0 + b * a.box, &full[s]);
-            }
+            __syncwarp();
         }
-        if (!ok) {     // wait, with a limit, for the copies still in flight
-            for (uint32_t q = it > (uint32_t)a.stages ? it - a.stages : 0; q < it; ++q)
-                mbar_wait_bounded(&full[q % a.stages], (q / a.stages) & 1, kGemmWaitNs / 8);
-        }
-    } else if (has && warp == 1 && lane == 0) {
-        const uint32_t idesc = instr_desc(kBM, t.n, kAMn, kBMn);
-        uint32_t it = 0;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-            const uint32_t s = it % a.stages;
-            if (!mbar_wait(&full[s], (it / a.stages) & 1, &dead, a.err)) break;
+        if (!ok)     // wait, with a limit, for the copies still in flight
+            for (int s = 0; s < a.stages; ++s, ring.next()) mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, kGemmWaitNs / 64);
+    } else if (has && warp == 1) {
+        const uint32_t idesc = instr_desc(kBM, t.n, kAMn, kBMn), full0 = smem_addr(full), empty0 = smem_addr(empty);
+        const uint64_t da0 = smem_desc(smem_addr(smem), kAMn), db0 = smem_desc(smem_addr(smem) + kABytes, kBMn);
+        Ring ring(a.stages);
+        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+            if (!mbar_wait_at(full0 + ring.s * 8, ring.phase, &dead, a.err)) break;
             tc_fence_after();
-            const uint32_t sa = smem_addr(smem + s * stage_bytes), sb = sa + kABytes;
-            const uint64_t da = smem_desc(sa, kAMn), db = smem_desc(sb, kBMn);
+            const uint64_t at = (uint64_t)((ring.s * stage_bytes) >> 4), da = da0 + at, db = db0 + at;
             const int left = depth - kb * kBK;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kBK; k += 16) {
-                if (D == kWgrad && k >= left) break;
-                tc_mma(tmem, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, (it | k) != 0);
+                for (int k = 0; k < kBK; k += 16) {
+                    if (D == kWgrad && k >= left) break;
+                    tc_mma(tmem, da + (kAMn ? k * 128 : k * 2) / 16, db + (kBMn ? k * 128 : k * 2) / 16, idesc, kb > kb0 || k > 0);
+                }
+                tc_commit(empty0 + ring.s * 8);
             }
-            tc_commit(&empty[s]);
+            __syncwarp();
         }
-        tc_commit(&done);
+        if (elect_one()) tc_commit(smem_addr(&done));
     }
     __syncwarp();
     const int quarter = warp & 3, half = (warp - 2) >> 2, m_local = quarter * 32 + lane, m = t.m0 + m_local;
@@ -984,7 +982,7 @@ inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1;
 // Column tile width, stages and split.
 //   wgrad: tiles of 256 columns, a pair of CTAs each; where those are less than half of the pairs
 //          and experts have many rows, tiles of 128 x 128 whose rows are split (one expert of 7568 rows,
-//          672 -> 392 features: 40 -> 15 us).
+//          672 -> 392 features: 40 -> 17 us).
 //   else:  tiles of twice the average rows of an expert (one group: of its rows), within [32, 256],
 //          so that most experts are one tile. Up to 64 columns the weights' loads are what counts:
 //          two CTAs per SM, and the contraction split as long as all CTAs fit at once (one row,
