@@ -1,6 +1,6 @@
 // adapter.cu -- a projection that all rows share plus each row's own low-rank adapter:
 //   y[t] = W x[t] + scales[i] * B_i (A_i x[t]),  i = adapter_idx[t]
-// low[t] = scales[i] * A_i x[t] in fp32 (more than 32 rows: by adapter, after a sort of the rows),
+// low[t] = scales[i] * A_i x[t] in fp32 (many rows: by adapter, after a sort of the rows),
 // then the projection with B_i low[t] added to its fp32 sums before the one rounding. With few rows
 // the projection starts while low is still computed; its epilogue waits for it.
 #include "gemm.cuh"
@@ -21,6 +21,7 @@ struct AdapterArgs {
     float* low;                // [parts][T][r]
     int T, K, L, r, parts;
     unsigned copy_from;
+    int slots;                 // blocks per 32 rows, where they are taken as they are
     uint32_t* err;
 };
 
@@ -41,17 +42,20 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 }
 
 constexpr int kLowRows = 32, kLowWarps = 8, kLowPartsMost = 16, kLowBlocks = 304;
+constexpr int kLowPlain = 128;          // rows up to which they are taken as they are
 
-// Blocks of the low-rank kernel: up to 32 rows are looked through for their distinct adapters
-// (one block per adapter, by its position among them); more are sorted by adapter first, and each
-// adapter's rows are cut into 32 at a time.
-inline int64_t low_blocks(int T, int L) {
-    return T <= kLowRows ? (T < L ? T : L) : (int64_t)T / kLowRows + (T < L ? T : L);
+// Blocks of the low-rank kernel. As the rows are: 32 rows are looked through for their distinct
+// adapters, a block for each by its position among them. By adapter: after a sort of the rows, each
+// adapter's rows cut into 32 at a time. Up to 128 rows the first saves the sort's time (61 rows of as
+// many adapters, 7168 x 7168: 37 us with it); with more it would start too many idle blocks.
+inline int low_slots(int T, int L) { return (T < L ? T : L) < kLowRows ? (T < L ? T : L) : kLowRows; }
+inline int64_t low_blocks(int T, int L, bool by_adapter) {
+    return by_adapter ? (int64_t)T / kLowRows + (T < L ? T : L) : (int64_t)ceil_div(T, kLowRows) * low_slots(T, L);
 }
 // Parts of the contraction, for as many blocks as two per SM: every part is at least four steps of
 // 32 for each warp.
-inline int low_parts(int T, int L, int K) {
-    const int64_t blocks = low_blocks(T, L);
+inline int low_parts(int T, int L, int K, bool by_adapter) {
+    const int64_t blocks = low_blocks(T, L, by_adapter);
     if (blocks == 0) return 1;
     int most = ceil_div(K, 32 * kLowWarps * 4);
     if (most > kLowPartsMost) most = kLowPartsMost;
@@ -136,12 +140,13 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapter_low_kernel(AdapterA
         } else {
             if (blockIdx.x == 0 && blockIdx.y == 0)
                 for (int t = lane; t < a.T; t += 32) adapter_of(a, t, true);
-            const int id = lane < a.T ? adapter_of(a, lane, false) : -1;
+            const int slots = a.slots, t0 = (int)blockIdx.x / slots * kLowRows, slot = (int)blockIdx.x % slots;
+            const int id = t0 + lane < a.T ? adapter_of(a, t0 + lane, false) : -1;
             const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
             unsigned firsts = __ballot_sync(0xFFFFFFFFu, id >= 0 && (same & lanemask_lt()) == 0);
-            for (unsigned d = 0; d < blockIdx.x && firsts != 0; ++d) firsts &= firsts - 1;
+            for (int d = 0; d < slot && firsts != 0; ++d) firsts &= firsts - 1;
             if (firsts != 0) adapter = __shfl_sync(0xFFFFFFFFu, id, __ffs(firsts) - 1);
-            if (adapter >= 0 && id == adapter) row = lane;
+            if (adapter >= 0 && id == adapter) row = t0 + lane;
         }
         s_row[lane] = row;
         if (lane == 0) s_adapter = adapter;
@@ -213,7 +218,7 @@ cudaError_t launch_low(const AdapterArgs& g, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     const unsigned copies = SORTED && g.sorted_x != nullptr ? (unsigned)ceil_div(g.T, kLowWarps) : 0u;
-    const unsigned blocks = SORTED ? g.copy_from + copies : (unsigned)(low_blocks(g.T, g.L) > 0 ? low_blocks(g.T, g.L) : 1);
+    const unsigned blocks = SORTED ? g.copy_from + copies : g.L > 0 ? (unsigned)low_blocks(g.T, g.L, false) : 1u;
     return launch_pdl(adapter_low_kernel<NT, SORTED>, dim3(blocks, (unsigned)g.parts), dim3(kLowWarps * 32), smem, stream, g);
 }
 
@@ -225,25 +230,26 @@ cudaError_t launch_low_of(const AdapterArgs& g, cudaStream_t stream) {
                        : launch_low<8, SORTED>(g, stream);
 }
 
-// Workspace: low; more than 32 rows: the order, where each adapter's rows begin, the changes, the sort's
-// scratch; more than 64 rows: room for x in that order.
+// Workspace: low; more than 64 rows: the order, where each adapter's rows begin, the changes, the sort's
+// scratch and room for x in that order.
 struct AdapterWorkspace {
     size_t order, prefix, changes, scratch, x, bytes;
-    int parts;
+    int parts[2];          // of the contraction: rows as they are, by adapter
 };
 AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
     AdapterWorkspace w{};
     const auto round = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t T = (size_t)sh->num_rows, L = (size_t)sh->num_adapters;
-    w.parts = low_parts(sh->num_rows, sh->num_adapters, sh->in_features);
-    w.order = round((size_t)w.parts * T * sh->rank * sizeof(float));
+    for (int i = 0; i < 2; ++i) w.parts[i] = low_parts(sh->num_rows, sh->num_adapters, sh->in_features, i);
+    const int parts = T <= kLowPlain && w.parts[0] > w.parts[1] ? w.parts[0] : w.parts[1];
+    w.order = round((size_t)parts * T * sh->rank * sizeof(float));
     w.prefix = w.changes = w.scratch = w.x = w.bytes = w.order;
-    if (sh->num_rows > kLowRows && L > 0) {
+    if (sh->num_rows > 64 && L > 0) {
         w.prefix = w.order + round(T * 4);
         w.changes = w.prefix + round((L + 2) * 4);
         w.scratch = w.changes + 256;
         w.x = w.scratch + round(sort_ids_workspace_changes(sh->num_rows, sh->num_adapters + 1));
-        w.bytes = w.x + (sh->num_rows > 64 ? T * sh->in_features * 2 : 0);
+        w.bytes = w.x + T * sh->in_features * 2;
     }
     return w;
 }
@@ -620,6 +626,7 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
+        const bool by_adapter = (wide || sh->num_rows > kLowPlain) && sh->num_adapters > 0;
         char* base = reinterpret_cast<char*>(workspace);
         int32_t* order = reinterpret_cast<int32_t*>(base + ws.order);
         int32_t* prefix = reinterpret_cast<int32_t*>(base + ws.prefix);
@@ -627,11 +634,13 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         const AdapterArgs g{reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(a), scales,
                             adapter_idx, order, prefix, changes, wide ? base + ws.x : nullptr,
                             reinterpret_cast<float*>(workspace), sh->num_rows, sh->in_features, sh->num_adapters, sh->rank,
-                            ws.parts, (unsigned)low_blocks(sh->num_rows, sh->num_adapters), launch->error_flags};
+                            ws.parts[by_adapter], (unsigned)low_blocks(sh->num_rows, sh->num_adapters, true),
+                            low_slots(sh->num_rows, sh->num_adapters) > 0 ? low_slots(sh->num_rows, sh->num_adapters) : 1,
+                            launch->error_flags};
         const AdapterSide side{reinterpret_cast<const __nv_bfloat16*>(b), g.low, adapter_idx, (int64_t)g.T * g.r, g.parts,
                                sh->out_features, g.L, g.r};
         cudaError_t e = cudaSuccess;
-        if (g.T <= kLowRows || g.L == 0) {
+        if (!by_adapter) {
             e = launch_low_of<false>(g, launch->stream);
         } else {
             e = launch_sort_ids(adapter_idx, g.T, g.L + 1, g.T, nullptr, order, prefix, base + ws.scratch,
@@ -639,9 +648,9 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
             if (e == cudaSuccess) e = launch_low_of<true>(g, launch->stream);
         }
         if (e == cudaSuccess) {
-            const int32_t* by_adapter = wide && g.L > 0 ? order : nullptr;
-            e = g.r <= 32 ? launch_wide<1>(maps, m, side, by_adapter, changes, g.T, launch->stream)
-                          : launch_wide<2>(maps, m, side, by_adapter, changes, g.T, launch->stream);
+            const int32_t* sorted = by_adapter ? order : nullptr;
+            e = g.r <= 32 ? launch_wide<1>(maps, m, side, sorted, changes, g.T, launch->stream)
+                          : launch_wide<2>(maps, m, side, sorted, changes, g.T, launch->stream);
         }
         if (e != cudaSuccess) return cuda_fail(e);
     }
