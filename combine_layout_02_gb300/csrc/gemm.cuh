@@ -515,7 +515,7 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
 // the M side and half of the columns; the tensor cores of both read both halves, which halves the
 // shared memory traffic of the columns. Warp 0 loads the M side (TMA), warp 1 of the leader multiplies (tcgen05.mma, fp32 sums in tensor
 // memory, two accumulators of 256 columns in turn), warp 3 loads the columns, warps 4 on write the tile before
-// meanwhile.
+// meanwhile; wgrad: warp 2 loads the tails.
 //   full[s]   leader's: both CTAs' loads (an arrival of each loading warp, and the bytes)
 //   empty[s]  each CTA's: the products that read stage s are done
 template <Direction D, class Extra>
@@ -532,15 +532,15 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
-    // wgrad keeps its last stage for the tails: their loads are issued early in a tile, since their many
-    // small boxes take longer than the ring is ahead (32 experts of 511 rows: 397 -> 330 us).
+    // wgrad keeps its last stage for the tails, whose many small boxes a warp of its own issues: they take
+    // longer than the ring is ahead (32 experts of 511 rows, 7168 x 2048: 397 -> 334 us).
     const uint32_t ring_stages = D == kWgrad ? a.stages - 1 : a.stages;
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&maps.a);
         tma_prefetch_map(&maps.b);
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(&full[s], 4);
+            mbar_init(&full[s], D == kWgrad && s == a.stages - 1 ? 2 : 4);
             mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -566,7 +566,6 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         Tile t;
         Ring ring(ring_stages);
         bool ok = true;
-        uint32_t tails = 0;
         const uint32_t full0 = peer_addr(smem_addr(full), 0);
         const uint32_t empty0 = smem_addr(empty), smem0 = smem_addr(smem) + (warp == 0 ? 0 : kABytes);
         const bool reordered = extra.reordered();
@@ -578,23 +577,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             const int box = kBMn ? 64 : half > 64 ? 2 * a.box : a.box, boxes = (half + box - 1) / box;
             const uint32_t bytes = warp == 0 ? kABytes : (uint32_t)(boxes * box) * 128;
             const int whole = D == kWgrad ? depth & ~(kBK - 1) : depth;
-            const int tail_at = depth > whole ? min(whole, (int)ring_stages * kBK) : -1;
-            for (int k0 = 0; k0 < whole || k0 == tail_at; k0 += kBK, ring.next()) {
-                if (D == kWgrad && k0 == tail_at) {
-                    // By now the products of the tile before have freed the tail's stage.
-                    const uint32_t bar = full0 + ring_stages * 8, at = smem0 + ring_stages * stage_bytes;
-                    if (!(ok = mbar_wait_at(empty0 + ring_stages * 8, (tails & 1) ^ 1, &dead, a.err))) break;
-                    ++tails;
-                    if (elect_one()) {
-                        const int chunks = warp == 0 ? 2 : boxes, left = depth - whole;
-                        mbar_expect_peer(bar, (uint32_t)(chunks * ((left + 15) & ~15)) * 128);
-                        for (int b = 0; b < chunks; ++b)
-                            load_tail_chunk<true>(at + b * kMnChunk, warp == 0 ? maps.part_a : maps.part_b,
-                                            (warp == 0 ? m0 : n0) + b * 64, t.begin + whole, left, a.num_rows, bar);
-                    }
-                    __syncwarp();
-                    if (k0 >= whole) break;
-                }
+            for (int k0 = 0; k0 < whole; k0 += kBK, ring.next()) {
                 if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a.err))) break;
                 const uint32_t at = smem0 + ring.s * stage_bytes, bar = full0 + ring.s * 8;
                 if (elect_one()) {
@@ -623,8 +606,30 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         if (warp == 0) {
             for (uint32_t q = 0; q < ring_stages; ++q, ring.next())
                 mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
-            if (D == kWgrad) mbar_wait_bounded(&empty[ring_stages], (tails & 1) ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
         }
+    } else if (D == kWgrad && warp == 2) {
+        // The tails, into their own stage as soon as the tile before has been multiplied.
+        TileWalk<D> walk(a);
+        Tile t;
+        uint32_t tails = 0;
+        bool ok = true;
+        const uint32_t bar = peer_addr(smem_addr(&full[ring_stages]), 0), at = smem_addr(smem) + ring_stages * stage_bytes;
+        for (int i = first; ok && walk.at(i, t); i += step) {
+            const int depth = t.end - t.begin, left = depth > 0 ? depth % kBK : 0;
+            if (left == 0) continue;
+            if (!(ok = mbar_wait(&empty[ring_stages], (tails & 1) ^ 1, &dead, a.err))) break;
+            ++tails;
+            if (elect_one()) {
+                const int half = t.n / 2, boxes = (half + 63) / 64;
+                mbar_expect_peer(bar, (uint32_t)((2 + boxes) * ((left + 15) & ~15)) * 128);
+                for (int c = 0; c < 2 + boxes; ++c)
+                    load_tail_chunk<true>(at + c * kMnChunk, c < 2 ? maps.part_a : maps.part_b,
+                                          c < 2 ? t.m0 + (int)rank * kBM + c * 64 : t.n0 + (int)rank * half + (c - 2) * 64,
+                                          t.end - left, left, a.num_rows, bar);
+            }
+            __syncwarp();
+        }
+        mbar_wait_bounded(&empty[ring_stages], (tails & 1) ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
     } else if (warp == 1 && rank == 0) {
         TileWalk<D> walk(a);
         Tile t;
