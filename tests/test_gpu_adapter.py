@@ -10,7 +10,8 @@ pytestmark = pytest.mark.gpu
 # rows, in_features, out_features, adapters, rank
 CASES = [(1, 8, 8, 1, 8), (1, 4096, 512, 8, 16), (2, 72, 200, 3, 24), (7, 520, 136, 2, 64), (16, 1024, 256, 16, 8),
          (33, 256, 392, 64, 16), (61, 2048, 640, 5, 32), (130, 640, 264, 4, 128), (257, 128, 256, 3, 256),
-         (300, 384, 128, 300, 8), (1000, 512, 520, 6, 16), (700, 264, 776, 2, 64), (2100, 1024, 384, 40, 40)]
+         (300, 384, 128, 300, 8), (1000, 512, 520, 6, 16), (700, 264, 776, 2, 64), (2100, 1024, 384, 40, 40),
+         (9001, 64, 136, 5, 8), (8193, 72, 264, 700, 16), (200, 64, 72, 2000, 8), (100, 4096, 256, 3, 24), (65, 72, 4104, 30, 72)]
 
 
 def normal(g, *shape):
