@@ -284,9 +284,10 @@ struct AdapterSide {
 };
 
 // gemm_split_kernel, few rows, each usually with another adapter: one output feature per lane, four
-// rows at a time, fp32. Their B values
-// are requested before their low values are staged, and towards L2 while the projection is
-// computed. Loops, not unrolled code: a launch meets each instruction once, out of L2.
+// rows at a time, fp32. Their B values are requested before their low values are staged, and towards
+// L2 while the projection is computed. G lanes share G features: each takes 8 of 8G ranks of all G (so
+// that a load of the warp covers whole runs of B, 16 bytes times G, not 32 far lines), and they
+// exchange their sums.
 // G: 8-rank pieces of B taken at a time (their latency is what a group of rows waits for).
 template <int G>
 struct AdapterFew : AdapterSide {
@@ -294,17 +295,22 @@ struct AdapterFew : AdapterSide {
     static constexpr int kGroup = 4, kRows = 256;
     // shared: low of each half, then the rows' adapters
     static constexpr int kLow = kGroup * EP_ADAPTER_MAX_RANK, kIds = 2 * kLow, kFloats = kIds + kRows;
+    int together;          // groups whose low is held at a time: a power of two, one with 256 ranks
 
+    explicit AdapterFew(const AdapterSide& side) : AdapterSide(side), together(1) {
+        while (together * 2 * r <= EP_ADAPTER_MAX_RANK) together *= 2;
+    }
     __device__ __forceinline__ void ahead(float* shared, int64_t row0, int rows, int m, int half) const {
         int* ids = reinterpret_cast<int*>(shared + kIds);
         const int tid = threadIdx.x - 64;
         if (tid < rows) ids[tid] = adapter(row0 + tid);
         epilogue_barrier<256>();
-        if (m >= F) return;
+        const int lane = threadIdx.x & 31, m0 = m - lane, bytes = min(32, F - m0) * r * 2;          // <= 0: none
         for (int j = half; j < rows; j += 2) {
             if (ids[j] < 0) continue;
-            const char* at = reinterpret_cast<const char*>(b + ((int64_t)ids[j] * F + m) * r);
-            for (int q = 0; q < r * 2; q += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + q));
+            const char* at = reinterpret_cast<const char*>(b + ((int64_t)ids[j] * F + m0) * r);
+            for (int o = lane * 128; o < bytes + 127; o += 32 * 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + min(o, bytes - 1)));
         }
     }
     __device__ __forceinline__ void apply(float* shared, float (&v)[kGroup], int64_t row0, int rows, int c, int m,
@@ -312,45 +318,69 @@ struct AdapterFew : AdapterSide {
         const int* ids = reinterpret_cast<const int*>(shared + kIds) + c;
         const int tid = (threadIdx.x - 64) & 127;
         shared += half * kLow;
+        // low of as many of this half's groups at a time as there is room for.
+        const int nth = c / (2 * kGroup) & (together - 1);
+        int id[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) id[j] = c + j < rows ? ids[j] : -1;
+        const int p = threadIdx.x % G, m0 = m - p;          // this lane's piece of each of G features
         uint4 u[kGroup][G];
         const auto load_b = [&](int q0) {
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
-                const int i = c + j < rows && m < F ? ids[j] : -1;
-                const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q0;
+                const __nv_bfloat16* at = b + ((int64_t)max(id[j], 0) * F + m0) * r + q0 + p * 8;
+                const bool has = id[j] >= 0 && q0 + p * 8 < r;
 #pragma unroll
                 for (int g = 0; g < G; ++g)
-                    u[j][g] = i >= 0 && q0 + g * 8 < r ? *reinterpret_cast<const uint4*>(at + g * 8) : make_uint4(0, 0, 0, 0);
+                    u[j][g] = has && m0 + g < F ? *reinterpret_cast<const uint4*>(at + g * r) : make_uint4(0, 0, 0, 0);
             }
         };
-        load_b(0);
-        epilogue_barrier<128>(2 + half);          // the four rows before have been read
-        for (int e = tid; e < r; e += 128) {          // four rows of r / 4 float4
-            const int j = e / (r / 4), q = (e % (r / 4)) * 4;
-            const float4 x = c + j < rows && ids[j] >= 0 ? low4(row0 + c + j, q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            *reinterpret_cast<float4*>(shared + j * r + q) = x;
+        const bool any = max(max(id[0], id[1]), max(id[2], id[3])) >= 0;          // for all of this half alike
+        if (any) load_b(0);
+        if (nth == 0) {
+            epilogue_barrier<128>(2 + half);          // the groups before have been read
+            const int pieces = r / 4;
+            for (int e = tid; e < together * kGroup * pieces; e += 128) {
+                const int n = e / pieces, q = (e - n * pieces) * 4, j = (n / kGroup) * 2 * kGroup + n % kGroup;
+                const bool has = c + j < rows && ids[j] >= 0;
+                *reinterpret_cast<float4*>(shared + n * r + q) = has ? low4(row0 + c + j, q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            epilogue_barrier<128>(2 + half);
         }
-        epilogue_barrier<128>(2 + half);
+        if (!any) return;
+        shared += nth * kGroup * r;
 #pragma unroll 1
         for (int q0 = 0; q0 < r; q0 += 8 * G) {
             if (q0 > 0) load_b(q0);
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                if (q0 + g * 8 >= r) break;
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j) {
-                    if (c + j >= rows || ids[j] < 0) continue;
-                    const float4* l = reinterpret_cast<const float4*>(shared + j * r + q0 + g * 8);
-                    const float4 x = l[0], y = l[1];
-                    v[j] = fmaf(x.x, bf16_lo(u[j][g].x), v[j]);
-                    v[j] = fmaf(x.y, bf16_hi(u[j][g].x), v[j]);
-                    v[j] = fmaf(x.z, bf16_lo(u[j][g].y), v[j]);
-                    v[j] = fmaf(x.w, bf16_hi(u[j][g].y), v[j]);
-                    v[j] = fmaf(y.x, bf16_lo(u[j][g].z), v[j]);
-                    v[j] = fmaf(y.y, bf16_hi(u[j][g].z), v[j]);
-                    v[j] = fmaf(y.z, bf16_lo(u[j][g].w), v[j]);
-                    v[j] = fmaf(y.w, bf16_hi(u[j][g].w), v[j]);
+            for (int j = 0; j < kGroup; ++j) {
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+                if (q0 + p * 8 < r) {
+                    const float4* l = reinterpret_cast<const float4*>(shared + j * r + q0 + p * 8);
+                    x = l[0], y = l[1];
                 }
+                float sum[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const uint4 w = u[j][g];
+                    float d = x.x * bf16_lo(w.x);
+                    d = fmaf(x.y, bf16_hi(w.x), d);
+                    d = fmaf(x.z, bf16_lo(w.y), d);
+                    d = fmaf(x.w, bf16_hi(w.y), d);
+                    d = fmaf(y.x, bf16_lo(w.z), d);
+                    d = fmaf(y.y, bf16_hi(w.z), d);
+                    d = fmaf(y.z, bf16_lo(w.w), d);
+                    sum[g] = fmaf(y.w, bf16_hi(w.w), d);
+                }
+                // Lane p of G keeps feature p's sum.
+#pragma unroll
+                for (int h = G / 2; h > 0; h /= 2)
+#pragma unroll
+                    for (int g = 0; g < h; ++g) {
+                        const float give = p & h ? sum[g] : sum[g + h], keep = p & h ? sum[g + h] : sum[g];
+                        sum[g] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, h);
+                    }
+                v[j] += sum[0];
             }
         }
     }
@@ -372,6 +402,11 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
     const float x = a - bf16_lo(hi), y = b - bf16_hi(hi);
     lo = pack_bf16x2(isinf(a) ? 0.0f : x, isinf(b) ? 0.0f : y);
 }
+
+// Rows of a split tile of more than 64 up to which AdapterFew is the faster: its time grows with
+// rows x ranks, AdapterWide's hardly does. (Rank 16: 240 rows 4096 -> 1024, 60 a CTA, 23 us, else 39;
+// 2560 -> 4096, 120 a CTA, 34 and 33. Rank 64: 60 a CTA 43 us, else 48; 120 a CTA 71 and 39.)
+inline int few_rows(int rank) { return 7168 / (rank + 48); }
 
 // NS: 32 ranks at a time, or 64.
 template <int NS>
@@ -607,7 +642,7 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         m.M = sh->out_features;
         m.N = m.C = sh->in_features;
         m.err = launch->error_flags;
-        gemm_tiles(&m, false, sh->rank <= 32 ? AdapterWide<1>::kBeside : AdapterWide<2>::kBeside);
+        gemm_tiles(&m, false, sh->rank <= 32 ? AdapterWide<1>::kBeside : AdapterWide<2>::kBeside, few_rows(sh->rank));
         const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, T = (uint64_t)sh->num_rows;
         const uint64_t da[3] = {K, F, 1}, db[2] = {K, T};
         const uint32_t ba[3] = {64, (uint32_t)kBM, 1};

@@ -993,8 +993,9 @@ inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1;
 //          two CTAs per SM, and the contraction split as long as all CTAs fit at once (one row,
 //          7168 x 7168: 4 parts 21 us, 8 parts, more CTAs than fit, 35 us); wider tiles are split only
 //          where there are fewer of them than SMs. A part keeps at least eight 64-deep steps
-//          (wider tiles: sixteen; below, pairs of CTAs are as fast and write faster).
-inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0) {
+//          (wider tiles: sixteen; below, pairs of CTAs are as fast and write faster), and of a wider
+//          tile at most most_rows rows.
+inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 256) {
     int bn = 256;
     const int avg = (a->num_rows + a->E - 1) / a->E, wide = a->E > 1 ? 2 * (avg < 256 ? avg : 256) : avg;
     if (!wgrad)
@@ -1008,6 +1009,7 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0) {
         const int64_t want = bn <= 64 ? 2 * sms : sms;
         const int steps = ceil_div(a->C, kBK);
         while (a->split < 8 && tiles * a->split * 2 <= want && steps >= a->split * (bn <= 64 ? 16 : 32)) a->split *= 2;
+        if (bn > 64 && (avg < bn ? avg : bn) > most_rows * a->split) a->split = 1;
     }
     if (wgrad && 2 * gemm_most_tiles(*a, true, 2 * kBM) <= sms / 2 && avg >= 16 * kBK) {
         a->bn = 128;
