@@ -292,7 +292,7 @@ struct AdapterSide {
 template <int G>
 struct AdapterFew : AdapterSide {
     static constexpr bool kFollows = true;
-    static constexpr int kGroup = 4, kRows = 256;
+    static constexpr int kGroup = 4, kRows = 256, kTaken = 8 / G;          // rows whose B is in registers at a time
     // shared: low of each half, then the rows' adapters
     static constexpr int kLow = kGroup * EP_ADAPTER_MAX_RANK, kIds = 2 * kLow, kFloats = kIds + kRows;
     int together;          // groups whose low is held at a time: a power of two, one with 256 ranks
@@ -324,19 +324,19 @@ struct AdapterFew : AdapterSide {
 #pragma unroll
         for (int j = 0; j < kGroup; ++j) id[j] = c + j < rows ? ids[j] : -1;
         const int p = threadIdx.x % G, m0 = m - p;          // this lane's piece of each of G features
-        uint4 u[kGroup][G];
-        const auto load_b = [&](int q0) {
+        uint4 u[kTaken][G];
+        const auto load_b = [&](int q0, int j0) {
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
-                const __nv_bfloat16* at = b + ((int64_t)max(id[j], 0) * F + m0) * r + q0 + p * 8;
-                const bool has = id[j] >= 0 && q0 + p * 8 < r;
+            for (int j = 0; j < kTaken; ++j) {
+                const __nv_bfloat16* at = b + ((int64_t)max(id[j0 + j], 0) * F + m0) * r + q0 + p * 8;
+                const bool has = id[j0 + j] >= 0 && q0 + p * 8 < r;
 #pragma unroll
                 for (int g = 0; g < G; ++g)
                     u[j][g] = has && m0 + g < F ? *reinterpret_cast<const uint4*>(at + g * r) : make_uint4(0, 0, 0, 0);
             }
         };
         const bool any = max(max(id[0], id[1]), max(id[2], id[3])) >= 0;          // for all of this half alike
-        if (any) load_b(0);
+        if (any) load_b(0, 0);
         if (nth == 0) {
             epilogue_barrier<128>(2 + half);          // the groups before have been read
             const int pieces = r / 4;
@@ -351,9 +351,9 @@ struct AdapterFew : AdapterSide {
         shared += nth * kGroup * r;
 #pragma unroll 1
         for (int q0 = 0; q0 < r; q0 += 8 * G) {
-            if (q0 > 0) load_b(q0);
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
+                if (j % kTaken == 0 && q0 + j > 0) load_b(q0, j);
                 float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
                 if (q0 + p * 8 < r) {
                     const float4* l = reinterpret_cast<const float4*>(shared + j * r + q0 + p * 8);
@@ -362,7 +362,7 @@ struct AdapterFew : AdapterSide {
                 float sum[G];
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const uint4 w = u[j][g];
+                    const uint4 w = u[j % kTaken][g];
                     float d = x.x * bf16_lo(w.x);
                     d = fmaf(x.y, bf16_hi(w.x), d);
                     d = fmaf(x.z, bf16_lo(w.y), d);
@@ -404,9 +404,16 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
 }
 
 // Rows of a split tile of more than 64 up to which AdapterFew is the faster: its time grows with
-// rows x ranks, AdapterWide's hardly does. (Rank 16: 240 rows 4096 -> 1024, 60 a CTA, 23 us, else 39;
-// 2560 -> 4096, 120 a CTA, 34 and 33. Rank 64: 60 a CTA 43 us, else 48; 120 a CTA 71 and 39.)
+// rows x ranks, AdapterWide's hardly does. (Rank 16: 320 rows 4096 -> 1024, 64 a CTA, 22 us, else 34;
+// 2560 -> 4096, 128 a CTA, 31 and 28. Rank 64: 240 rows 4096 -> 1024, 60 a CTA, 43 and 48; 2560 -> 4096,
+// 120 a CTA, 71 and 39.)
 inline int few_rows(int rank) { return 7168 / (rank + 48); }
+// Tiles of at most 64 rows, AdapterFew's, where there are few: more CTAs share its work, and up to 128
+// rows nothing is sorted. (Rank 16: 128 rows 1024 -> 648 13 us, else 23; 7168 -> 7168 39 and 38. 200 rows
+// 2048 -> 2048, 64 tiles, 16 and 29; 7168 -> 4096, 128 tiles, 37 and 30.)
+inline int widest_tile(int T, int F) {
+    return T <= 128 || (T <= 256 && (int64_t)ceil_div(T, 64) * ceil_div(F, kBM) <= sm_count() / 2) ? 64 : 256;
+}
 
 // NS: 32 ranks at a time, or 64.
 template <int NS>
@@ -642,7 +649,8 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         m.M = sh->out_features;
         m.N = m.C = sh->in_features;
         m.err = launch->error_flags;
-        gemm_tiles(&m, false, sh->rank <= 32 ? AdapterWide<1>::kBeside : AdapterWide<2>::kBeside, few_rows(sh->rank));
+        gemm_tiles(&m, false, sh->rank <= 32 ? AdapterWide<1>::kBeside : AdapterWide<2>::kBeside, few_rows(sh->rank),
+                   widest_tile(sh->num_rows, sh->out_features));
         const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, T = (uint64_t)sh->num_rows;
         const uint64_t da[3] = {K, F, 1}, db[2] = {K, T};
         const uint32_t ba[3] = {64, (uint32_t)kBM, 1};

@@ -794,7 +794,7 @@ constexpr int kSplitThreads = 320;
 // in its own shared memory; after a cluster barrier each adds up, in rank order, the parts of
 // its share of the rows. Warp 0 loads, warp 1 multiplies, warps 2 to 9 write.
 template <Direction D, class Extra>
-__global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_constant__ GemmMaps maps,
+__global__ void __launch_bounds__(kSplitThreads, 2) gemm_split_kernel(const __grid_constant__ GemmMaps maps,
                                                                    const GemmArgs a, const Extra extra) {
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done;
@@ -995,11 +995,11 @@ inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1;
 //          where there are fewer of them than SMs. A part keeps at least eight 64-deep steps
 //          (wider tiles: sixteen; below, pairs of CTAs are as fast and write faster), and of a wider
 //          tile at most most_rows rows.
-inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 256) {
+inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 256, int widest = 256) {
     int bn = 256;
     const int avg = (a->num_rows + a->E - 1) / a->E, wide = a->E > 1 ? 2 * (avg < 256 ? avg : 256) : avg;
     if (!wgrad)
-        for (bn = 32; bn < 256 && bn < wide; bn *= 2) {}
+        for (bn = 32; bn < widest && bn < wide; bn *= 2) {}
     a->bn = bn;
     a->box = bn < 64 ? bn : 64;
     a->split = 1;
