@@ -25,6 +25,7 @@ constexpr int kSmallEntries = 8192;            // up to here one block sorts eve
 constexpr int kSmallThreads = 1024;
 constexpr int kTableInts = 48 * 1024 / 4;      // per-warp counts of a block, in shared memory
 constexpr int kSortSmemMax = (kTableInts + EP_MAX_EXPERTS + 8) * 4;
+constexpr size_t kSmemPlain = 40 * 1024;       // dynamic shared memory without opting in: 48 KB with the static
 constexpr int kSegment = 128;                  // entries per segment, at least
 constexpr int kMaxSegments = 152 * 16;
 
@@ -549,7 +550,7 @@ cudaError_t launch_sort_ids(const int64_t* ids, int n, int E, int64_t num_rows, 
         a.seg_len = ceil_div(ceil_div(n > 0 ? n : 1, a.warps), 32) * 32;
         a.S = a.warps;
         const size_t smem = (size_t)(a.warps + 1) * E * sizeof(int);
-        if (smem > 48 * 1024)
+        if (smem > kSmemPlain)
             e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
         if (e == cudaSuccess) e = launch_pdl(sort_small_kernel, dim3(1), dim3(kSmallThreads), smem, stream, a);
     } else {
@@ -558,8 +559,10 @@ cudaError_t launch_sort_ids(const int64_t* ids, int n, int E, int64_t num_rows, 
         a.S = ceil_div(n, a.seg_len);
         const unsigned blocks = (unsigned)ceil_div(a.S, a.warps);
         const size_t tables = (size_t)a.warps * E * sizeof(int), smem = tables + (size_t)E * sizeof(int);
-        if (smem > 48 * 1024)
+        if (smem > kSmemPlain)
             e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
+        if (e == cudaSuccess && tables > kSmemPlain)
+            e = cudaFuncSetAttribute(sort_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemMax);
         if (e == cudaSuccess) e = launch_pdl(sort_count_kernel, dim3(blocks), dim3(kSortWarps * 32), tables, stream, a);
         if (e == cudaSuccess)
             e = launch_pdl(sort_scan_kernel, dim3((unsigned)(E + (changes != nullptr))), dim3(kSortWarps * 32), 0,
@@ -629,7 +632,7 @@ ep_status ep_sort_rows(const ep_shape* sh, const void* x, ep_dtype x_dtype, cons
         const size_t smem = (size_t)kTmaWarps * a.row_bytes;
         cudaError_t e = cudaSuccess;
         if (smem <= (size_t)kTmaSmemMax) {
-            if (smem > 48 * 1024)
+            if (smem > kSmemPlain)
                 e = cudaFuncSetAttribute(sort_rows_tma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTmaSmemMax);
             if (e == cudaSuccess)
                 e = launch_pdl(sort_rows_tma_kernel, dim3(row_blocks(N, kTmaWarps)), dim3(kTmaWarps * 32), smem,

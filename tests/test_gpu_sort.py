@@ -100,6 +100,18 @@ def test_rows_beyond_the_buffers_are_skipped_and_flagged(N):
     assert bool((out[room:] == 5.0).all())
 
 
+# Just below and at 48 KB of dynamic shared memory, which static shared memory adds to.
+@pytest.mark.parametrize("N,E,k", [(300, 372, 4), (300, 384, 4), (3000, 1365, 4), (3000, 1536, 4)])
+def test_placement_with_tables_of_48_kilobytes(N, E, k):
+    test_placement(N, E, k, 0.9)
+
+
+@pytest.mark.parametrize("H", [5888, 6016, 6144])
+def test_rows_of_which_a_block_holds_48_kilobytes(H):
+    test_bf16_rows_move_bit_for_bit(526, H, 16, 2, 1.0)
+    test_e4m3_rows_move_with_their_scales(526, 2 * H, 16, 2, 1.0, False)
+
+
 @pytest.mark.parametrize("N,H,E,k,share", [(1, 128, 4, 2, 1.0), (33, 7168, 32, 8, 0.125), (517, 384, 16, 3, 0.5),
                                            (64, 25728, 8, 2, 0.6), (3000, 256, 128, 6, 1.0)])
 def test_bf16_rows_move_bit_for_bit(N, H, E, k, share):
