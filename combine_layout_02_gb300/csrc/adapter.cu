@@ -52,14 +52,20 @@ inline int low_slots(int T, int L) { return (T < L ? T : L) < kLowRows ? (T < L 
 inline int64_t low_blocks(int T, int L, bool by_adapter) {
     return by_adapter ? (int64_t)T / kLowRows + (T < L ? T : L) : (int64_t)ceil_div(T, kLowRows) * low_slots(T, L);
 }
+// Ranks that a block takes at a time, in eights: few while there are few blocks, others then take the rest
+// (one row 4096 -> 1024, rank 128: 12 us, else 20), up to 64, which read x once for all of them.
+inline int low_tiles(int64_t blocks, int r) {
+    int nt = r <= 8 ? 1 : 2;
+    while (nt < 8 && nt * 8 < r && blocks * ceil_div(r, nt * 8) > kLowBlocks) nt *= 2;
+    return nt;
+}
 // Parts of the contraction, for as many blocks as two per SM: every part is at least four steps of
 // 32 for each warp.
-inline int low_parts(int T, int L, int K, bool by_adapter) {
-    const int64_t blocks = low_blocks(T, L, by_adapter);
+inline int low_parts(int64_t blocks, int K, int r) {
     if (blocks == 0) return 1;
     int most = ceil_div(K, 32 * kLowWarps * 4);
     if (most > kLowPartsMost) most = kLowPartsMost;
-    const int64_t want = kLowBlocks / blocks;
+    const int64_t want = kLowBlocks / (blocks * ceil_div(r, low_tiles(blocks, r) * 8));
     return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 
@@ -103,13 +109,13 @@ __device__ __forceinline__ int find_rows(const AdapterArgs& a, int lane, int& fr
 __device__ __forceinline__ bool copy_block(const AdapterArgs& a, int warp, int lane) {
     if (blockIdx.x < a.copy_from) return false;
     const int64_t p = (int64_t)(blockIdx.x - a.copy_from) * kLowWarps + warp, row_bytes = (int64_t)a.K * 2;
-    if (blockIdx.y == 0 && p < a.T && scattered(*a.changes, a.T))
+    if (blockIdx.y == 0 && blockIdx.z == 0 && p < a.T && scattered(*a.changes, a.T))
         scatter_copy_row<4>(reinterpret_cast<const char*>(a.x) + a.order[p] * row_bytes, a.sorted_x, &p, 1, row_bytes, lane, 32);
     return true;
 }
 
 // low[part][t][q] = scales[i] * sum over the part's k of x[t][k] A_i[q][k], for up to 32 rows of one
-// adapter; NT * 8 ranks at a time. The warps share the part and join in shared memory in warp order;
+// adapter; NT * 8 ranks at a time (blockIdx.z: which, where there are blocks for all). The warps share the part and join in shared memory in warp order;
 // the parts are added up by the projection's epilogue. Operands come straight from memory: a
 // lane of quad position c loads the 8 values c*8 .. c*8+7 of a 32-deep step with one 16-byte load,
 // for a row of x and for a rank of A alike; which of them a product calls its k-th is immaterial as
@@ -138,7 +144,7 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapter_low_kernel(AdapterA
             adapter = find_rows(a, lane, begin, end);
             if (adapter >= 0 && begin + lane < end) row = a.order[begin + lane];
         } else {
-            if (blockIdx.x == 0 && blockIdx.y == 0)
+            if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
                 for (int t = lane; t < a.T; t += 32) adapter_of(a, t, true);
             const int slots = a.slots, t0 = (int)blockIdx.x / slots * kLowRows, slot = (int)blockIdx.x % slots;
             const int id = t0 + lane < a.T ? adapter_of(a, t0 + lane, false) : -1;
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapter_low_kernel(AdapterA
         xr[h] = a.x + (int64_t)max(row, 0) * a.K;
     }
     const float scale = a.scales[i];
-    for (int q0 = 0; q0 < a.r; q0 += NT * 8) {
+    for (int q0 = blockIdx.z * NT * 8; q0 < a.r; q0 += gridDim.z * NT * 8) {
         float acc[2][NT][4] = {};
         const __nv_bfloat16* ar = a.a + ((int64_t)i * a.r + q0 + g) * a.K;
         const int ranks = a.r - q0;
@@ -219,32 +225,35 @@ cudaError_t launch_low(const AdapterArgs& g, cudaStream_t stream) {
     }
     const unsigned copies = SORTED && g.sorted_x != nullptr ? (unsigned)ceil_div(g.T, kLowWarps) : 0u;
     const unsigned blocks = SORTED ? g.copy_from + copies : g.L > 0 ? (unsigned)low_blocks(g.T, g.L, false) : 1u;
-    return launch_pdl(adapter_low_kernel<NT, SORTED>, dim3(blocks, (unsigned)g.parts), dim3(kLowWarps * 32), smem, stream, g);
+    const unsigned ranks = NT < 8 ? (unsigned)ceil_div(g.r, NT * 8) : 1u;
+    return launch_pdl(adapter_low_kernel<NT, SORTED>, dim3(blocks, (unsigned)g.parts, ranks), dim3(kLowWarps * 32), smem, stream, g);
 }
 
 template <bool SORTED>
 cudaError_t launch_low_of(const AdapterArgs& g, cudaStream_t stream) {
-    return g.r <= 8    ? launch_low<1, SORTED>(g, stream)
-           : g.r <= 16 ? launch_low<2, SORTED>(g, stream)
-           : g.r <= 32 ? launch_low<4, SORTED>(g, stream)
-                       : launch_low<8, SORTED>(g, stream);
+    switch (low_tiles(low_blocks(g.T, g.L, SORTED), g.r)) {
+        case 1: return launch_low<1, SORTED>(g, stream);
+        case 2: return launch_low<2, SORTED>(g, stream);
+        case 4: return launch_low<4, SORTED>(g, stream);
+        default: return launch_low<8, SORTED>(g, stream);
+    }
 }
 
-// Workspace: low; more than 64 rows: the order, where each adapter's rows begin, the changes, the sort's
-// scratch and room for x in that order.
+// Workspace: low; more than kLowPlain rows: the order, where each adapter's rows begin, the changes,
+// the sort's scratch and room for x in that order.
 struct AdapterWorkspace {
     size_t order, prefix, changes, scratch, x, bytes;
-    int parts[2];          // of the contraction: rows as they are, by adapter
+    int parts;             // of the contraction
 };
 AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
     AdapterWorkspace w{};
     const auto round = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t T = (size_t)sh->num_rows, L = (size_t)sh->num_adapters;
-    for (int i = 0; i < 2; ++i) w.parts[i] = low_parts(sh->num_rows, sh->num_adapters, sh->in_features, i);
-    const int parts = T <= kLowPlain && w.parts[0] > w.parts[1] ? w.parts[0] : w.parts[1];
-    w.order = round((size_t)parts * T * sh->rank * sizeof(float));
+    const bool by_adapter = sh->num_rows > kLowPlain;
+    w.parts = low_parts(low_blocks(sh->num_rows, sh->num_adapters, by_adapter), sh->in_features, sh->rank);
+    w.order = round((size_t)w.parts * T * sh->rank * sizeof(float));
     w.prefix = w.changes = w.scratch = w.x = w.bytes = w.order;
-    if (sh->num_rows > 64 && L > 0) {
+    if (by_adapter && L > 0) {
         w.prefix = w.order + round(T * 4);
         w.changes = w.prefix + round((L + 2) * 4);
         w.scratch = w.changes + 256;
@@ -412,7 +421,7 @@ inline int few_rows(int rank) { return 7168 / (rank + 48); }
 // rows nothing is sorted. (Rank 16: 128 rows 1024 -> 648 13 us, else 23; 7168 -> 7168 39 and 38. 200 rows
 // 2048 -> 2048, 64 tiles, 16 and 29; 7168 -> 4096, 128 tiles, 37 and 30.)
 inline int widest_tile(int T, int F) {
-    return T <= 128 || (T <= 256 && (int64_t)ceil_div(T, 64) * ceil_div(F, kBM) <= sm_count() / 2) ? 64 : 256;
+    return T <= kLowPlain || (T <= 256 && (int64_t)ceil_div(T, 64) * ceil_div(F, kBM) <= sm_count() / 2) ? 64 : 256;
 }
 
 // NS: 32 ranks at a time, or 64.
@@ -650,7 +659,7 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         m.N = m.C = sh->in_features;
         m.err = launch->error_flags;
         gemm_tiles(&m, false, sh->rank <= 32 ? AdapterWide<1>::kBeside : AdapterWide<2>::kBeside, few_rows(sh->rank),
-                   widest_tile(sh->num_rows, sh->out_features));
+                   widest_tile(sh->num_rows, sh->out_features), 4);
         const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, T = (uint64_t)sh->num_rows;
         const uint64_t da[3] = {K, F, 1}, db[2] = {K, T};
         const uint32_t ba[3] = {64, (uint32_t)kBM, 1};
@@ -669,7 +678,7 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
-        const bool by_adapter = (wide || sh->num_rows > kLowPlain) && sh->num_adapters > 0;
+        const bool by_adapter = sh->num_rows > kLowPlain && sh->num_adapters > 0;
         char* base = reinterpret_cast<char*>(workspace);
         int32_t* order = reinterpret_cast<int32_t*>(base + ws.order);
         int32_t* prefix = reinterpret_cast<int32_t*>(base + ws.prefix);
@@ -677,7 +686,7 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         const AdapterArgs g{reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<const __nv_bfloat16*>(a), scales,
                             adapter_idx, order, prefix, changes, wide ? base + ws.x : nullptr,
                             reinterpret_cast<float*>(workspace), sh->num_rows, sh->in_features, sh->num_adapters, sh->rank,
-                            ws.parts[by_adapter], (unsigned)low_blocks(sh->num_rows, sh->num_adapters, true),
+                            ws.parts, (unsigned)low_blocks(sh->num_rows, sh->num_adapters, true),
                             low_slots(sh->num_rows, sh->num_adapters) > 0 ? low_slots(sh->num_rows, sh->num_adapters) : 1,
                             launch->error_flags};
         const AdapterSide side{reinterpret_cast<const __nv_bfloat16*>(b), g.low, adapter_idx, (int64_t)g.T * g.r, g.parts,

@@ -975,10 +975,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) gemm_split_kernel(const __gr
 
 // ------------------------------------------------------------------ host
 
-// How many tiles of `wide` M indices there can be at most.
+// How many tiles of `wide` M indices there can be at most: one for each expert's first row, one more for
+// every bn rows.
 inline int64_t gemm_most_tiles(const GemmArgs& a, bool wgrad, int wide) {
-    const int64_t mt = ceil_div(a.M, wide);
-    return mt * (wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn) : a.num_rows / a.bn + (a.E < a.num_rows ? a.E : a.num_rows));
+    const int64_t mt = ceil_div(a.M, wide), some = a.E < a.num_rows ? a.E : a.num_rows;
+    return mt * (wgrad ? (int64_t)a.E * ceil_div(a.N, a.bn) : some + (a.num_rows - some) / a.bn);
 }
 
 // Whether gemm_split_kernel runs (else gemm_kernel). (In clusters of at least two also for wgrad.)
@@ -988,14 +989,19 @@ inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1;
 //   wgrad: tiles of 256 columns, a pair of CTAs each; where those are less than half of the pairs
 //          and experts have many rows, tiles of 128 x 128 whose rows are split (one expert of 7568 rows,
 //          672 -> 392 features: 40 -> 17 us).
-//   else:  tiles of twice the average rows of an expert (one group: of its rows), within [32, 256],
+//   else:  tiles of twice the average rows of an expert (one group: of its rows), within [32, widest],
 //          so that most experts are one tile. Up to 64 columns the weights' loads are what counts:
 //          two CTAs per SM, and the contraction split as long as all CTAs fit at once (one row,
 //          7168 x 7168: 4 parts 21 us, 8 parts, more CTAs than fit, 35 us); wider tiles are split only
-//          where there are fewer of them than SMs. A part keeps at least eight 64-deep steps
-//          (wider tiles: sixteen; below, pairs of CTAs are as fast and write faster), and of a wider
-//          tile at most most_rows rows.
-inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 256, int widest = 256) {
+//          where there are fewer of them than SMs. Before it is split further, a part has sixteen
+//          64-deep steps or more (wider tiles: 32; below, pairs of CTAs are as fast and write faster).
+//   Adapters, whose work for the rows counts too, pass: the most rows of a wider tile that a part may
+//          have; the fewest steps (`least`) with which CTAs for up to half of the SMs are split further (24
+//          rows 512 -> 512, rank 64: 4 steps 11 us, 16 steps 17).
+// Narrow tiles that are few take an SM each: 128 KB, so that two do not share one while others are
+// idle (128 rows 1024 -> 4096 with adapters of rank 64, 128 CTAs: 23 us, else 31). Not in clusters of
+// eight: an SM each, not all of them fit at once (70 rows 4096 -> 1024: 17 us, else 12).
+inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 256, int widest = 256, int least = 16) {
     int bn = 256;
     const int avg = (a->num_rows + a->E - 1) / a->E, wide = a->E > 1 ? 2 * (avg < 256 ? avg : 256) : avg;
     if (!wgrad)
@@ -1008,7 +1014,9 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 
         const int64_t tiles = (int64_t)ceil_div(a->M, kBM) * (a->E < a->num_rows ? a->E : a->num_rows) * ceil_div(avg, bn);
         const int64_t want = bn <= 64 ? 2 * sms : sms;
         const int steps = ceil_div(a->C, kBK);
-        while (a->split < 8 && tiles * a->split * 2 <= want && steps >= a->split * (bn <= 64 ? 16 : 32)) a->split *= 2;
+        while (a->split < 8 && tiles * a->split * 2 <= want &&
+               steps >= a->split * (bn > 64 ? 32 : tiles * a->split * 2 <= sms / 2 ? least : 16))
+            a->split *= 2;
         if (bn > 64 && (avg < bn ? avg : bn) > most_rows * a->split) a->split = 1;
     }
     if (wgrad && 2 * gemm_most_tiles(*a, true, 2 * kBM) <= sms / 2 && avg >= 16 * kBK) {
@@ -1019,7 +1027,8 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 
     }
     bn = a->bn;
     const bool split = gemm_by_split(*a);
-    const int stage = (int)kABytes + (split ? bn * 128 : bn * 64), room = (split && bn <= 64 ? 96 : 200) * 1024;
+    const bool spread = a->split <= 4 && gemm_most_tiles(*a, wgrad, kBM) * a->split <= sms;
+    const int stage = (int)kABytes + (split ? bn * 128 : bn * 64), room = (split && bn <= 64 ? spread ? 128 : 96 : 200) * 1024;
     a->beside = split ? 0 : wgrad ? 8 * (int)kOutBytes : beside;
     const int left = (wgrad ? 224 : 220) * 1024 - a->beside, most = split || left > room ? room : left;
     a->stages = most / stage < kMaxStages ? most / stage : kMaxStages;
