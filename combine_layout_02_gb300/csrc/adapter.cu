@@ -3,6 +3,8 @@
 // low[t] = scales[i] * A_i x[t] in fp32 (many rows: by adapter, after a sort of the rows),
 // then the projection with B_i low[t] added to its fp32 sums before the one rounding. With few rows
 // the projection starts while low is still computed; its epilogue waits for it.
+#include <type_traits>
+
 #include "gemm.cuh"
 #include "rowops.cuh"
 #include "sort.cuh"
@@ -424,21 +426,23 @@ inline int widest_tile(int T, int F) {
     return T <= kLowPlain || (T <= 256 && (int64_t)ceil_div(T, 64) * ceil_div(F, kBM) <= sm_count() / 2) ? 64 : 256;
 }
 
-// NS: 32 ranks at a time, or 64.
-template <int NS>
+// RANKS: 16, 32 or 64 at a time, in pieces of 16 or 32.
+template <int RANKS>
 struct AdapterWide : AdapterSide {
     static constexpr bool kFollows = false;
     // shared: which rows the tile has, the run each is in, and each run's adapter (and one -1 after)
-    static constexpr int kRows = 256, kHeld = 32 * NS, kFloats = 3 * kRows + 4 + 8;
+    static constexpr int kRows = 256, kHeld = RANKS, kFloats = 3 * kRows + 4 + 8;
+    static constexpr int NS = RANKS < 32 ? 1 : RANKS / 32, kLane = RANKS < 32 ? 4 : 8;          // ranks of a lane in a piece
+    using Piece = typename std::conditional<RANKS < 32, uint2, uint4>::type;
     const int32_t* order;
     const int32_t* changes;
     int T;
 
     __device__ __forceinline__ bool reordered() const { return order != nullptr && scattered(*changes, T); }
 
-    // Bytes from one row's terms to the next's (16 more than a multiple of 32: eight rows' pieces of one
-    // column lie in different banks).
-    static constexpr int kPitch = 2 * kHeld + 16, kBeside = 2 * kRows * kPitch;
+    // Bytes from one row's terms to the next's: the rows' pieces that are read together lie in
+    // different banks.
+    static constexpr int kPitch = 2 * kHeld + (RANKS < 32 ? 0 : 16), kBeside = 2 * kRows * kPitch;
 
     // hi and lo terms of the tile's rows, kHeld ranks from q0 on, zero past the last rank.
     __device__ __forceinline__ void stage(const int* which, unsigned char* terms, int rows, int q0) const {
@@ -489,30 +493,31 @@ struct AdapterWide : AdapterSide {
     }
 
     // B_i's values of the warp's 32 features (from m0 on), kHeld ranks from q0 on: of features 8h + g, the
-    // 8 ranks c*8 .. of each 32. Zero past the edges; nothing for i = -1.
-    __device__ __forceinline__ void load_b(int i, int m0, int q0, int g, int c, uint4 (&w)[NS][4]) const {
+    // kLane ranks c*kLane .. of each piece. Zero past the edges; nothing for i = -1.
+    __device__ __forceinline__ void load_b(int i, int m0, int q0, int g, int c, Piece (&w)[NS][4]) const {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             const int m = m0 + h * 8 + g;
-            const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q0 + c * 8;
+            const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q0 + c * kLane;
 #pragma unroll
             for (int s = 0; s < NS; ++s)
-                w[s][h] = i >= 0 && m < F && q0 + s * 32 + c * 8 < r ? *reinterpret_cast<const uint4*>(at + s * 32)
-                                                                     : make_uint4(0, 0, 0, 0);
+                w[s][h] = i >= 0 && m < F && q0 + s * 32 + c * kLane < r ? *reinterpret_cast<const Piece*>(at + s * 32) : Piece{};
         }
     }
     // d += B_i times the terms of eight rows (`at`: this lane's piece of row g).
-    __device__ __forceinline__ void product(const uint4 (&w)[NS][4], const unsigned char* at, float (&d)[2][4]) const {
+    __device__ __forceinline__ void product(const Piece (&w)[NS][4], const unsigned char* at, float (&d)[2][4]) const {
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            const uint4 hi = *reinterpret_cast<const uint4*>(at + s * 64), lo = *reinterpret_cast<const uint4*>(at + kRows * kPitch + s * 64);
+            const Piece hi = *reinterpret_cast<const Piece*>(at + s * 64), lo = *reinterpret_cast<const Piece*>(at + kRows * kPitch + s * 64);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const uint4 x = w[s][2 * t], y = w[s][2 * t + 1];
+                const Piece x = w[s][2 * t], y = w[s][2 * t + 1];
                 mma_16816(d[t], x.x, y.x, x.y, y.y, hi.x, hi.y);
-                mma_16816(d[t], x.z, y.z, x.w, y.w, hi.z, hi.w);
                 mma_16816(d[t], x.x, y.x, x.y, y.y, lo.x, lo.y);
-                mma_16816(d[t], x.z, y.z, x.w, y.w, lo.z, lo.w);
+                if constexpr (kLane == 8) {
+                    mma_16816(d[t], x.z, y.z, x.w, y.w, hi.z, hi.w);
+                    mma_16816(d[t], x.z, y.z, x.w, y.w, lo.z, lo.w);
+                }
             }
         }
     }
@@ -534,7 +539,7 @@ struct AdapterWide : AdapterSide {
             }
             if (begin >= end) continue;
             int held = run_of[begin];
-            uint4 w[NS][4], next[NS][4];       // of the run at work and of the one after it
+            Piece w[NS][4], next[NS][4];       // of the run at work and of the one after it
             load_b(runs[held], m0, q0, g, c, w);
             load_b(runs[run_of[rows - 1] > held ? held + 1 : held], m0, q0, g, c, next);
             const auto hold = [&](int run) {
@@ -556,7 +561,7 @@ struct AdapterWide : AdapterSide {
                     tmem_load_16x8(tmem + n + b * 8 + (16u << 16), v[b][1]);
                 }
                 const int first = run_of[n];
-                const unsigned char* at = terms + (n + g) * kPitch + c * 16;
+                const unsigned char* at = terms + (n + g) * kPitch + c * (int)sizeof(Piece);
                 hold(first);
                 tmem_wait(v[0]);
                 tmem_wait(v[1]);
@@ -601,15 +606,14 @@ struct AdapterWide : AdapterSide {
     }
 };
 
-template <int NS>
+template <int RANKS>
 cudaError_t launch_wide(const GemmMaps& maps, const GemmArgs& m, const AdapterSide& side, const int32_t* order,
                         const int32_t* changes, int T, cudaStream_t stream) {
-    AdapterWide<NS> wide{side};
+    AdapterWide<RANKS> wide{side};
     wide.order = order;
     wide.changes = changes;
     wide.T = T;
-    return side.r <= 16 ? launch_gemm<kForward>(maps, m, wide, AdapterFew<2>{side}, stream)
-                        : launch_gemm<kForward>(maps, m, wide, AdapterFew<4>{side}, stream);
+    return launch_gemm<kForward>(maps, m, wide, AdapterFew<(RANKS < 32 ? 2 : 4)>{side}, stream);
 }
 
 ep_status check_adapter(const ep_adapter_shape* sh) {
@@ -658,7 +662,9 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         m.M = sh->out_features;
         m.N = m.C = sh->in_features;
         m.err = launch->error_flags;
-        gemm_tiles(&m, false, sh->rank <= 32 ? AdapterWide<1>::kBeside : AdapterWide<2>::kBeside, few_rows(sh->rank),
+        gemm_tiles(&m, false, sh->rank <= 16   ? AdapterWide<16>::kBeside
+                              : sh->rank <= 32 ? AdapterWide<32>::kBeside
+                                               : AdapterWide<64>::kBeside, few_rows(sh->rank),
                    widest_tile(sh->num_rows, sh->out_features), 4);
         const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, T = (uint64_t)sh->num_rows;
         const uint64_t da[3] = {K, F, 1}, db[2] = {K, T};
@@ -701,8 +707,9 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         }
         if (e == cudaSuccess) {
             const int32_t* sorted = by_adapter ? order : nullptr;
-            e = g.r <= 32 ? launch_wide<1>(maps, m, side, sorted, changes, g.T, launch->stream)
-                          : launch_wide<2>(maps, m, side, sorted, changes, g.T, launch->stream);
+            e = g.r <= 16   ? launch_wide<16>(maps, m, side, sorted, changes, g.T, launch->stream)
+                : g.r <= 32 ? launch_wide<32>(maps, m, side, sorted, changes, g.T, launch->stream)
+                            : launch_wide<64>(maps, m, side, sorted, changes, g.T, launch->stream);
         }
         if (e != cudaSuccess) return cuda_fail(e);
     }
