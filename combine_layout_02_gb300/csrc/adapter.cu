@@ -504,21 +504,30 @@ struct AdapterWide : AdapterSide {
                 w[s][h] = i >= 0 && m < F && q0 + s * 32 + c * kLane < r ? *reinterpret_cast<const Piece*>(at + s * 32) : Piece{};
         }
     }
-    // d += B_i times the terms of eight rows (`at`: this lane's piece of row g).
-    __device__ __forceinline__ void product(const Piece (&w)[NS][4], const unsigned char* at, float (&d)[2][4]) const {
+    // d[n] += B_i times the terms of eight rows (`at`: this lane's piece of row g), for N times eight rows. Products
+    // that wait for one another are far apart: each waits for those of the tile that are at work.
+    template <int N>
+    __device__ __forceinline__ void product(const Piece (&w)[NS][4], const unsigned char* at, float (&d)[N][2][4]) const {
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            const Piece hi = *reinterpret_cast<const Piece*>(at + s * 64), lo = *reinterpret_cast<const Piece*>(at + kRows * kPitch + s * 64);
+            Piece hi[N], lo[N];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const Piece x = w[s][2 * t], y = w[s][2 * t + 1];
-                mma_16816(d[t], x.x, y.x, x.y, y.y, hi.x, hi.y);
-                mma_16816(d[t], x.x, y.x, x.y, y.y, lo.x, lo.y);
-                if constexpr (kLane == 8) {
-                    mma_16816(d[t], x.z, y.z, x.w, y.w, hi.z, hi.w);
-                    mma_16816(d[t], x.z, y.z, x.w, y.w, lo.z, lo.w);
-                }
+            for (int n = 0; n < N; ++n) {
+                hi[n] = *reinterpret_cast<const Piece*>(at + n * 8 * kPitch + s * 64);
+                lo[n] = *reinterpret_cast<const Piece*>(at + (kRows + n * 8) * kPitch + s * 64);
             }
+#pragma unroll
+            for (int part = 0; part < kLane / 4; ++part)
+#pragma unroll
+                for (int term = 0; term < 2; ++term)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            const uint32_t *x = &w[s][2 * t].x + 2 * part, *y = &w[s][2 * t + 1].x + 2 * part;
+                            const uint32_t* l = (term ? &lo[n].x : &hi[n].x) + 2 * part;
+                            mma_16816(d[n][t], x[0], y[0], x[1], y[1], l[0], l[1]);
+                        }
         }
     }
     __device__ __forceinline__ void tile(uint32_t tmem, float* shared, unsigned char* terms, __nv_bfloat16* out, int64_t,
@@ -566,10 +575,7 @@ struct AdapterWide : AdapterSide {
                 tmem_wait(v[0]);
                 tmem_wait(v[1]);
                 if (run_of[min(n + 15, rows - 1)] == first) {
-                    if (runs[first] >= 0) {
-                        product(w, at, v[0]);
-                        product(w, at + 8 * kPitch, v[1]);
-                    }
+                    if (runs[first] >= 0) product(w, at, v);
                 } else {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
@@ -580,12 +586,12 @@ struct AdapterWide : AdapterSide {
                         for (int run = run_of[n + b * 8]; run <= to; ++run) {
                             hold(run);
                             if (runs[run] < 0) continue;
-                            float d[2][4] = {};
+                            float d[1][2][4] = {};
                             product(w, at + b * 8 * kPitch, d);
 #pragma unroll
                             for (int t = 0; t < 2; ++t) {
-                                if (run0 == run) v[b][t][0] += d[t][0], v[b][t][2] += d[t][2];
-                                if (run1 == run) v[b][t][1] += d[t][1], v[b][t][3] += d[t][3];
+                                if (run0 == run) v[b][t][0] += d[0][t][0], v[b][t][2] += d[0][t][2];
+                                if (run1 == run) v[b][t][1] += d[0][t][1], v[b][t][3] += d[0][t][3];
                             }
                         }
                     }
