@@ -117,12 +117,14 @@ __device__ __forceinline__ bool copy_block(const AdapterArgs& a, int warp, int l
 }
 
 // low[part][t][q] = scales[i] * sum over the part's k of x[t][k] A_i[q][k], for up to 32 rows of one
-// adapter; NT * 8 ranks at a time (blockIdx.z: which, where there are blocks for all). The warps share the part and join in shared memory in warp order;
-// the parts are added up by the projection's epilogue. Operands come straight from memory: a
+// adapter; NT * 8 ranks at a time (blockIdx.z: which, where there are blocks for all). The warps
+// share the part and join in shared memory in warp order; the parts are added up by the
+// projection's epilogue. Operands come straight from memory: a
 // lane of quad position c loads the 8 values c*8 .. c*8+7 of a 32-deep step with one 16-byte load,
 // for a row of x and for a rank of A alike; which of them a product calls its k-th is immaterial as
 // long as both agree, so the lane's four words feed two products. Rows of other adapters are not
-// read (zero) and not written.
+// read (zero) and not written. Bound by the loads' latency at two blocks per SM and by the warp-level
+// tensor rate (8191 rows of 7168, rank 64: 57 us, the tensor pipe 26 % active).
 template <int NT, bool SORTED>
 __global__ void __launch_bounds__(kLowWarps * 32, 2) adapter_low_kernel(AdapterArgs a) {
     extern __shared__ float parts[];                    // [warps][32][NT * 8]
@@ -298,7 +300,8 @@ struct AdapterSide {
 // rows at a time, fp32. Their B values are requested before their low values are staged, and towards
 // L2 while the projection is computed. G lanes share G features: each takes 8 of 8G ranks of all G (so
 // that a load of the warp covers whole runs of B, 16 bytes times G, not 32 far lines), and they
-// exchange their sums.
+// exchange their sums. Bound by latency (61 rows of 64 adapters, 7168 -> 7168, rank 16: 33 us, where W alone
+// takes 21): low has to be there first.
 // G: 8-rank pieces of B taken at a time (their latency is what a group of rows waits for).
 template <int G>
 struct AdapterFew : AdapterSide {
@@ -406,7 +409,9 @@ struct AdapterFew : AdapterSide {
 // rows hold several runs, a product is taken of one run's adapter for eight rows and added to the
 // run's rows alone.
 // (One feature per lane with low broadcast out of shared memory was bound by that broadcast, and
-// low taken from memory row by row by its latency: 500 and 365 us where this is 290.)
+// low taken from memory row by row by its latency: 500 and 365 us where this is 290. Now these products
+// are what counts where the contraction is short: they share the tensor cores with the tiles at
+// work. 4096 rows 2048 -> 8192: 116 us with rank 16, 142 with 64, 75 without adapters.)
 // hi and lo terms of two fp32 values (an infinite one is its hi term).
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = pack_bf16x2(a, b);

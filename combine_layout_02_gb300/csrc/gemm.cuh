@@ -513,9 +513,12 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
 // tiles. The weights are the M side and the rows the N side, so that a tile has as many columns as
 // its expert has rows left (to a multiple of 32): no padding of the experts. Each CTA loads its 128 of
 // the M side and half of the columns; the tensor cores of both read both halves, which halves the
-// shared memory traffic of the columns. Warp 0 loads the M side (TMA), warp 1 of the leader multiplies (tcgen05.mma, fp32 sums in tensor
-// memory, two accumulators of 256 columns in turn), warp 3 loads the columns, warps 4 on write the tile before
-// meanwhile; wgrad: warp 2 loads the tails.
+// shared memory traffic of the columns. Warp 0 loads the M side (TMA), warp 1 of the leader
+// multiplies (tcgen05.mma, fp32 sums in tensor memory, two accumulators of 256 columns in turn),
+// warp 3 loads the columns, warps 4 on write the tile before meanwhile; wgrad: warp 2 loads the
+// tails. Full tiles are bound by the tensor cores (8192^3 1.90 PFLOP/s; 32771 rows of 32 experts,
+// 7168 -> 4096: 1.27 ms, tensor pipe 91 % active), narrower ones by filling shared memory (512 rows
+// an expert, 7168 -> 2048: dgrad 79 %, wgrad with its 8 steps a tile 62 %).
 //   full[s]   leader's: both CTAs' loads (an arrival of each loading warp, and the bytes)
 //   empty[s]  each CTA's: the products that read stage s are done
 template <Direction D, class Extra>
@@ -788,14 +791,16 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& a, int i, int lane, Ti
 constexpr int kSplitThreads = 320;
 
 // Where rows are few and the weights are what is read (forward, dgrad), or where tiles are few and the
-// rows many (wgrad): a cluster of `split` CTAs per
-// tile, each over its part of the contraction, so that enough CTAs stream weights at the same time
-// (and two fit an SM, one filling its pipeline while the other runs). Each CTA leaves its fp32 part
-// in its own shared memory; after a cluster barrier each adds up, in rank order, the parts of
-// its share of the rows. Warp 0 loads, warp 1 multiplies, warps 2 to 9 write.
+// rows many (wgrad): a cluster of `split` CTAs per tile, each over its part of the contraction, so
+// that enough CTAs stream weights at the same time (and two fit an SM, one filling its pipeline
+// while the other runs). Each CTA leaves its fp32 part in its own shared memory; after a cluster
+// barrier each adds up, in rank order, the parts of its share of the rows. Warp 0 loads, warp 1
+// multiplies, warps 2 to 9 write. Bound by the stream of weights (251 rows of 32 experts, 7168 ->
+// 2048: 136 us, 6.9 TB/s), a single small matrix by launch, pipeline fill and the join (one row 7168
+// x 7168: 21 us, 4096 x 4096: 10).
 template <Direction D, class Extra>
-__global__ void __launch_bounds__(kSplitThreads, 2) gemm_split_kernel(const __grid_constant__ GemmMaps maps,
-                                                                   const GemmArgs a, const Extra extra) {
+__global__ void __launch_bounds__(kSplitThreads, 2)
+    gemm_split_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done;
     __shared__ uint32_t s_tmem;

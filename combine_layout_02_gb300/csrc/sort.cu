@@ -6,14 +6,17 @@
 // and within a segment a warp takes 32 entries at a time: an entry's rank among them is the
 // number of lower lanes with the same expert (__match_any_sync), on top of the warp's running
 // count in shared memory. Counts only, no global atomics: the placement is the same in every
-// run. These kernels let the next one launch as soon as it has itself waited (the next waits for its end
-// before it reads): the launch is then over by that end. Few entries: one block does all of it (sort_small_kernel). More: count, scan (one block
-// per expert over the segments' counts) and place, three kernels without any inter-block wait.
+// run. These kernels let the next one launch as soon as it has itself waited (the next waits for
+// its end before it reads): the launch is then over by that end. Few entries: one block does all
+// of it (sort_small_kernel). More: count, scan (one block per expert over the segments' counts)
+// and place, three kernels without any inter-block wait.
 //
 // Rows (ep_sort_rows, ep_unsort_rows, ep_unsort_rows_backward): one warp per row in row order,
 // its placed entries' sorted rows as destinations or sources, as in the expert-major dispatch
 // and combine. Everything is bound by memory: each row is read once and each sorted row written
-// (or read) once.
+// (or read) once. 21673 rows of 7168 bf16 channels, 1.34 entries a row: placement 9 us beside
+// its launches, rows 103 us (666 MB, 6.5 TB/s), back 116 us (6.2); both gradients of 16384 rows
+// of 4096, top-6 of 128 experts: 261 us (1.75 GB, 6.7 TB/s) and 136 us for the rows' own.
 #include "rowops.cuh"
 #include "sort.cuh"
 

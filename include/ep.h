@@ -26,7 +26,8 @@
  *   - All pointers marked "dev" are device pointers owned by the caller; the library
  *     never allocates, frees or retains memory, and keeps no state between calls
  *     other than per-device caches (the SM count, a kernel's shared-memory limit set
- *     once, the static-scratch array's address per context) and a launch counter.
+ *     once, the static-scratch array's address per context), the address of the driver
+ *     call that encodes tensor maps, and a launch counter.
  *   - Calls are asynchronous on launch->stream and never synchronise the host,
  *     except the functions whose name ends in _sync.
  *   - Argument errors are detected on the host before anything is enqueued and
@@ -35,7 +36,9 @@
  *   - Problems only visible on the device (a topk_idx entry outside [-1, E), a row
  *     beyond its receive region, a low-latency slot beyond Nmax) skip the offending
  *     write and set a bit of *launch->error_flags (if non-NULL) with atomicOr. The
- *     kernels never trap, never spin and never wait on other blocks.
+ *     kernels never trap, every wait on an asynchronous copy or product has a time limit
+ *     (EP_DEVERR_TIMEOUT), and only blocks of one cluster wait for one another
+ *     (ep_expert_gemm* and ep_adapter_gemm, at cluster barriers).
  *   - Limits: 1 <= R <= 64; E % R == 0; 1 <= k <= 32; H % 128 == 0 and H >= 128;
  *     T >= 0; C >= 1; E <= 8192.
  */
@@ -497,7 +500,8 @@ EP_API ep_status ep_unsort_rows_backward(const ep_shape* shape, const void* dout
  * [expert_prefix[e], expert_prefix[e+1]). Values outside [0, num_rows] are clipped and
  * flagged (EP_DEVERR_RECV_OVERFLOW). Rows of no expert are neither read nor written.
  * bf16 operands, fp32 accumulation, one bf16 rounding; every pointer 16-byte aligned;
- * outputs must not overlap inputs. */
+ * outputs must not overlap inputs. An operand that has not arrived after 2 s sets
+ * EP_DEVERR_TIMEOUT and its tile is not written. */
 typedef struct ep_gemm_shape {
     int32_t num_rows;
     int32_t num_experts;
@@ -551,8 +555,9 @@ EP_API size_t ep_adapter_workspace_size(const ep_adapter_shape* shape);
  *   scales dev [L] fp32; adapter_idx dev [T] int64 (any order; -1 = none; others outside
  *   [0, L): EP_DEVERR_BAD_ADAPTER, treated as none). a, b, scales may be NULL with L = 0.
  *   workspace dev, >= ep_adapter_workspace_size bytes, 16-byte aligned
- * fp32 accumulation, A_i x[t] is kept in fp32, one bf16 rounding of the sum. Values of one
- * adapter never reach another adapter's rows. */
+ * fp32 accumulation, A_i x[t] is kept in fp32, one bf16 rounding of the sum; with many rows
+ * A_i x[t] meets B_i as the sum of two bf16 values, which leaves up to 2^-17 of it. Values of
+ * one adapter never reach another adapter's rows. EP_DEVERR_TIMEOUT as above. */
 EP_API ep_status ep_adapter_gemm(const ep_adapter_shape* shape, const void* x, const void* w,
                                  const void* a, const void* b, const float* scales,
                                  const int64_t* adapter_idx, void* y, void* workspace,
