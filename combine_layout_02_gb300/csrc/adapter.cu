@@ -411,7 +411,7 @@ struct AdapterFew : AdapterSide {
 // (One feature per lane with low broadcast out of shared memory was bound by that broadcast, and
 // low taken from memory row by row by its latency: 500 and 365 us where this is 290. Now these products
 // are what counts where the contraction is short: they share the tensor cores with the tiles at
-// work. 4096 rows 2048 -> 8192: 116 us with rank 16, 142 with 64, 75 without adapters.)
+// work. 4096 rows 2048 -> 8192: 116 us with rank 16, 142 with 64, 75 without adapters; PLAIN 107.)
 // hi and lo terms of two fp32 values (an infinite one is its hi term).
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = pack_bf16x2(a, b);
@@ -431,14 +431,24 @@ inline int widest_tile(int T, int F) {
     return T <= kLowPlain || (T <= 256 && (int64_t)ceil_div(T, 64) * ceil_div(F, kBM) <= sm_count() / 2) ? 64 : 256;
 }
 
-// RANKS: 16, 32 or 64 at a time, in pieces of 16 or 32.
-template <int RANKS>
+// d += a * b, both halves.
+__device__ __forceinline__ void fma_pair(float2& d, float2 a, float2 b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+}
+
+// RANKS: 16, 32 or 64 at a time.
+// PLAIN (16): multiply-adds in fp32 in the same layout, with low as it is and all 16 values of B of a lane's
+// four features in registers. They leave the tensor cores to the tiles, but take longer by themselves.
+template <int RANKS, bool PLAIN>
 struct AdapterWide : AdapterSide {
     static constexpr bool kFollows = false;
     // shared: which rows the tile has, the run each is in, and each run's adapter (and one -1 after)
     static constexpr int kRows = 256, kHeld = RANKS, kFloats = 3 * kRows + 4 + 8;
-    static constexpr int NS = RANKS < 32 ? 1 : RANKS / 32, kLane = RANKS < 32 ? 4 : 8;          // ranks of a lane in a piece
-    using Piece = typename std::conditional<RANKS < 32, uint2, uint4>::type;
+    // A lane's pieces of B, and its ranks in one.
+    using Piece = typename std::conditional<RANKS == 16 && !PLAIN, uint2, uint4>::type;
+    static constexpr int kPer = sizeof(Piece) / 2, NS = PLAIN ? 2 : RANKS / (4 * kPer);
     const int32_t* order;
     const int32_t* changes;
     int T;
@@ -447,24 +457,28 @@ struct AdapterWide : AdapterSide {
 
     // Bytes from one row's terms to the next's: the rows' pieces that are read together lie in
     // different banks.
-    static constexpr int kPitch = 2 * kHeld + (RANKS < 32 ? 0 : 16), kBeside = 2 * kRows * kPitch;
+    static constexpr int kPitch = PLAIN ? 80 : 2 * kHeld + (RANKS == 16 ? 0 : 16), kBeside = (PLAIN ? 1 : 2) * kRows * kPitch;
 
-    // hi and lo terms of the tile's rows, kHeld ranks from q0 on, zero past the last rank.
+    // The tile's rows' low, or its hi and lo terms: kHeld ranks from q0 on, zero past the last rank.
     __device__ __forceinline__ void stage(const int* which, unsigned char* terms, int rows, int q0) const {
-        constexpr int kPieces = kHeld / 8;
+        constexpr int kPieces = kHeld / (PLAIN ? 4 : 8);
 #pragma unroll 2
         for (int e = threadIdx.x - 128; e < rows * kPieces; e += 256) {
-            const int j = e / kPieces, q = e % kPieces * 8;
-            uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-            if (q0 + q < r) {
-                const float4 x = low4(which[j], q0 + q), y = low4(which[j], q0 + q + 4);
+            const int j = e / kPieces, q = e % kPieces * (PLAIN ? 4 : 8);
+            const bool has = q0 + q < r;
+            const float4 x = has ? low4(which[j], q0 + q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if constexpr (PLAIN) {
+                *reinterpret_cast<float4*>(terms + j * kPitch + q * 4) = x;
+            } else {
+                const float4 y = has ? low4(which[j], q0 + q + 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                uint4 hi, lo;
                 split_pair(x.x, x.y, hi.x, lo.x);
                 split_pair(x.z, x.w, hi.y, lo.y);
                 split_pair(y.x, y.y, hi.z, lo.z);
                 split_pair(y.z, y.w, hi.w, lo.w);
+                *reinterpret_cast<uint4*>(terms + j * kPitch + q * 2) = hi;
+                *reinterpret_cast<uint4*>(terms + (kRows + j) * kPitch + q * 2) = lo;
             }
-            *reinterpret_cast<uint4*>(terms + j * kPitch + q * 2) = hi;
-            *reinterpret_cast<uint4*>(terms + (kRows + j) * kPitch + q * 2) = lo;
         }
     }
     __device__ __forceinline__ void prepare(float* shared, unsigned char* terms, int64_t row0, int rows) const {
@@ -498,41 +512,78 @@ struct AdapterWide : AdapterSide {
     }
 
     // B_i's values of the warp's 32 features (from m0 on), kHeld ranks from q0 on: of features 8h + g, the
-    // kLane ranks c*kLane .. of each piece. Zero past the edges; nothing for i = -1.
+    // quarter c of each 4 * kPer ranks (PLAIN: all ranks). Zero past the edges; nothing for i = -1.
     __device__ __forceinline__ void load_b(int i, int m0, int q0, int g, int c, Piece (&w)[NS][4]) const {
+        const int q = q0 + (PLAIN ? 0 : c * kPer);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             const int m = m0 + h * 8 + g;
-            const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q0 + c * kLane;
+            const __nv_bfloat16* at = b + ((int64_t)max(i, 0) * F + m) * r + q;
 #pragma unroll
-            for (int s = 0; s < NS; ++s)
-                w[s][h] = i >= 0 && m < F && q0 + s * 32 + c * kLane < r ? *reinterpret_cast<const Piece*>(at + s * 32) : Piece{};
+            for (int s = 0; s < NS; ++s) {
+                const int on = s * (PLAIN ? kPer : 4 * kPer);
+                w[s][h] = i >= 0 && m < F && q + on < r ? *reinterpret_cast<const Piece*>(at + on) : Piece{};
+            }
         }
     }
-    // d[n] += B_i times the terms of eight rows (`at`: this lane's piece of row g), for N times eight rows. Products
+    // Where a lane begins to read for eight rows from n on.
+    __device__ __forceinline__ const unsigned char* row_terms(const unsigned char* terms, int n, int g, int c) const {
+        return PLAIN ? terms + (n + 2 * c) * kPitch : terms + (n + g) * kPitch + c * (int)sizeof(Piece);
+    }
+    // d[n] += B_i times low of eight rows (`at`: row_terms), for N times eight rows. Products
     // that wait for one another are far apart: each waits for those of the tile that are at work.
     template <int N>
     __device__ __forceinline__ void product(const Piece (&w)[NS][4], const unsigned char* at, float (&d)[N][2][4]) const {
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            Piece hi[N], lo[N];
+        if constexpr (PLAIN) {
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                hi[n] = *reinterpret_cast<const Piece*>(at + n * 8 * kPitch + s * 64);
-                lo[n] = *reinterpret_cast<const Piece*>(at + (kRows + n * 8) * kPitch + s * 64);
-            }
+                float2 sum[2][4] = {};          // over even and over odd ranks
 #pragma unroll
-            for (int part = 0; part < kLane / 4; ++part)
+                for (int s = 0; s < NS; ++s) {
+                    if (s * kPer >= r) break;
 #pragma unroll
-                for (int term = 0; term < 2; ++term)
+                    for (int part = 0; part < 2; ++part) {
+                        const unsigned char* low_at = at + n * 8 * kPitch + (s * 2 + part) * 16;
+                        const float4 l0 = *reinterpret_cast<const float4*>(low_at), l1 = *reinterpret_cast<const float4*>(low_at + kPitch);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int n = 0; n < N; ++n) {
-                            const uint32_t *x = &w[s][2 * t].x + 2 * part, *y = &w[s][2 * t + 1].x + 2 * part;
-                            const uint32_t* l = (term ? &lo[n].x : &hi[n].x) + 2 * part;
-                            mma_16816(d[n][t], x[0], y[0], x[1], y[1], l[0], l[1]);
+                        for (int h = 0; h < 4; ++h) {
+                            const uint32_t u = part ? w[s][h].z : w[s][h].x, v = part ? w[s][h].w : w[s][h].y;
+                            const float2 x = make_float2(bf16_lo(u), bf16_hi(u)), y = make_float2(bf16_lo(v), bf16_hi(v));
+                            fma_pair(sum[0][h], x, make_float2(l0.x, l0.y));
+                            fma_pair(sum[1][h], x, make_float2(l1.x, l1.y));
+                            fma_pair(sum[0][h], y, make_float2(l0.z, l0.w));
+                            fma_pair(sum[1][h], y, make_float2(l1.z, l1.w));
                         }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) d[n][h >> 1][(h & 1) * 2 + i] += sum[i][h].x + sum[i][h].y;
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                Piece hi[N], lo[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    hi[n] = *reinterpret_cast<const Piece*>(at + n * 8 * kPitch + s * 64);
+                    lo[n] = *reinterpret_cast<const Piece*>(at + (kRows + n * 8) * kPitch + s * 64);
+                }
+#pragma unroll
+                for (int part = 0; part < kPer / 4; ++part)
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int n = 0; n < N; ++n) {
+                                const Piece x = w[s][2 * t], y = w[s][2 * t + 1], l = term ? lo[n] : hi[n];
+                                if (part == 0) mma_16816(d[n][t], x.x, y.x, x.y, y.y, l.x, l.y);
+                                if constexpr (kPer == 8)
+                                    if (part == 1) mma_16816(d[n][t], x.z, y.z, x.w, y.w, l.z, l.w);
+                            }
+            }
         }
     }
     __device__ __forceinline__ void tile(uint32_t tmem, float* shared, unsigned char* terms, __nv_bfloat16* out, int64_t,
@@ -553,17 +604,22 @@ struct AdapterWide : AdapterSide {
             }
             if (begin >= end) continue;
             int held = run_of[begin];
-            Piece w[NS][4], next[NS][4];       // of the run at work and of the one after it
+            Piece w[NS][4], next[PLAIN ? 1 : NS][4];       // of the run at work and of the one after it
             load_b(runs[held], m0, q0, g, c, w);
-            load_b(runs[run_of[rows - 1] > held ? held + 1 : held], m0, q0, g, c, next);
+            if constexpr (!PLAIN) load_b(runs[run_of[rows - 1] > held ? held + 1 : held], m0, q0, g, c, next);
             const auto hold = [&](int run) {
-                while (held < run) {
+                if constexpr (PLAIN) {          // (no registers for the one after)
+                    if (held < run) load_b(runs[run], m0, q0, g, c, w);
+                    held = run;
+                } else {
+                    while (held < run) {
 #pragma unroll
-                    for (int s = 0; s < NS; ++s)
+                        for (int s = 0; s < NS; ++s)
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) w[s][h] = next[s][h];
-                    ++held;
-                    load_b(runs[run_of[rows - 1] > held ? held + 1 : held], m0, q0, g, c, next);
+                            for (int h = 0; h < 4; ++h) w[s][h] = next[s][h];
+                        ++held;
+                        load_b(runs[run_of[rows - 1] > held ? held + 1 : held], m0, q0, g, c, next);
+                    }
                 }
             };
 #pragma unroll 1
@@ -575,7 +631,7 @@ struct AdapterWide : AdapterSide {
                     tmem_load_16x8(tmem + n + b * 8 + (16u << 16), v[b][1]);
                 }
                 const int first = run_of[n];
-                const unsigned char* at = terms + (n + g) * kPitch + c * (int)sizeof(Piece);
+                const unsigned char* at = row_terms(terms, n, g, c);
                 hold(first);
                 tmem_wait(v[0]);
                 tmem_wait(v[1]);
@@ -617,14 +673,22 @@ struct AdapterWide : AdapterSide {
     }
 };
 
-template <int RANKS>
+template <int RANKS, bool PLAIN>
 cudaError_t launch_wide(const GemmMaps& maps, const GemmArgs& m, const AdapterSide& side, const int32_t* order,
                         const int32_t* changes, int T, cudaStream_t stream) {
-    AdapterWide<RANKS> wide{side};
+    AdapterWide<RANKS, PLAIN> wide{side};
     wide.order = order;
     wide.changes = changes;
     wide.T = T;
     return launch_gemm<kForward>(maps, m, wide, AdapterFew<(RANKS < 32 ? 2 : 4)>{side}, stream);
+}
+
+// Few ranks by plain multiply-adds (AdapterWide's PLAIN) where a tile's own products are long enough to
+// hide them, and where there are tiles after it that do. (4096 rows -> 8192, plain and not, us: rank 8, K 512
+// 70 and 62, 1024 77 and 80, 2048 93 and 115; rank 16, 1536 102 and 99, 2048 107 and 116, 4096 166 and 185. 600
+// rows 2048 -> 4096, rank 16, 48 tiles: 28 and 24.)
+inline bool plain_low(int T, int K, int F, int rank) {
+    return rank <= 16 && K >= 128 * rank && (int64_t)ceil_div(T, 256) * ceil_div(F, 2 * kBM) >= sm_count();
 }
 
 ep_status check_adapter(const ep_adapter_shape* sh) {
@@ -673,9 +737,11 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         m.M = sh->out_features;
         m.N = m.C = sh->in_features;
         m.err = launch->error_flags;
-        gemm_tiles(&m, false, sh->rank <= 16   ? AdapterWide<16>::kBeside
-                              : sh->rank <= 32 ? AdapterWide<32>::kBeside
-                                               : AdapterWide<64>::kBeside, few_rows(sh->rank),
+        const int beside = plain_low(sh->num_rows, sh->in_features, sh->out_features, sh->rank) ? AdapterWide<16, true>::kBeside
+                           : sh->rank <= 16 ? AdapterWide<16, false>::kBeside
+                           : sh->rank <= 32 ? AdapterWide<32, false>::kBeside
+                                            : AdapterWide<64, false>::kBeside;
+        gemm_tiles(&m, false, beside, few_rows(sh->rank),
                    widest_tile(sh->num_rows, sh->out_features), 4);
         const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, T = (uint64_t)sh->num_rows;
         const uint64_t da[3] = {K, F, 1}, db[2] = {K, T};
@@ -718,9 +784,10 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
         }
         if (e == cudaSuccess) {
             const int32_t* sorted = by_adapter ? order : nullptr;
-            e = g.r <= 16   ? launch_wide<16>(maps, m, side, sorted, changes, g.T, launch->stream)
-                : g.r <= 32 ? launch_wide<32>(maps, m, side, sorted, changes, g.T, launch->stream)
-                            : launch_wide<64>(maps, m, side, sorted, changes, g.T, launch->stream);
+            e = plain_low(g.T, g.K, sh->out_features, g.r) ? launch_wide<16, true>(maps, m, side, sorted, changes, g.T, launch->stream)
+                : g.r <= 16         ? launch_wide<16, false>(maps, m, side, sorted, changes, g.T, launch->stream)
+                : g.r <= 32         ? launch_wide<32, false>(maps, m, side, sorted, changes, g.T, launch->stream)
+                                    : launch_wide<64, false>(maps, m, side, sorted, changes, g.T, launch->stream);
         }
         if (e != cudaSuccess) return cuda_fail(e);
     }

@@ -72,6 +72,29 @@ def test_random_numbers(case, order):
     assert torch.equal(got, call(d))
 
 
+# Many tiles of a long contraction with few ranks.
+FEW_RANKS = [(2100, 1032, 4360, 5, 8), (2307, 2056, 4104, 40, 16)]
+
+
+@pytest.mark.parametrize("case", FEW_RANKS)
+@pytest.mark.parametrize("order", ["any", "sorted"])
+def test_few_ranks_many_tiles(case, order):
+    test_random_numbers(case, order)
+
+
+@pytest.mark.parametrize("case", FEW_RANKS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_few_ranks_many_tiles_stay_their_own(case, bad):
+    T, L = case[0], case[3]
+    for order in ("any", "sorted"):
+        d = make(case, order, 4, lambda g, *s: integers(g, *s, most=1))
+        y, delta = plain(d)
+        d["a"][1], d["b"][1], d["s"][1] = bad, bad, bad
+        got, others = call(d), d["ids"] != 1
+        assert torch.equal(got[others], (y + delta).float().bfloat16()[others])
+        assert bool(torch.isnan(got[~others]).all())
+
+
 @pytest.mark.parametrize("case", [(5, 72, 136, 3, 8), (61, 264, 392, 7, 16), (300, 136, 264, 4, 64), (90, 1024, 128, 2, 128)])
 def test_whole_numbers(case):
     d = make(case, "any", 2, lambda g, *s: integers(g, *s, most=1))
