@@ -100,6 +100,12 @@ def test_rows_beyond_the_buffers_are_skipped_and_flagged(N):
     assert bool((out[room:] == 5.0).all())
 
 
+# Where one block's sort ends, and around the 32 and 256 entries that a warp takes at a time.
+@pytest.mark.parametrize("N,E,k", [(640, 17, 8), (5121, 64, 1), (8191, 5, 1), (8193, 65, 1), (255, 3, 1), (257, 8, 1), (2050, 8192, 2)])
+def test_placement_around_the_steps(N, E, k):
+    test_placement(N, E, k, 0.9)
+
+
 # Just below and at 48 KB of dynamic shared memory, which static shared memory adds to.
 @pytest.mark.parametrize("N,E,k", [(300, 372, 4), (300, 384, 4), (3000, 1365, 4), (3000, 1536, 4)])
 def test_placement_with_tables_of_48_kilobytes(N, E, k):
