@@ -31,7 +31,8 @@ __all__ = [
     "ep_buffer_size_hint", "ep_size_hint",
     "ep_dispatch", "ep_combine", "ep_dispatch_expert_major", "ep_combine_expert_major",
     "ep_ll_dispatch", "ep_ll_combine", "ep_clean_ll_buffer", "ep_read_recv_counts_sync",
-    "ep_read_error_flags_sync", "ep_selftest_wait_timeout", "ep_kernel_launch_count",
+    "ep_read_error_flags_sync", "ep_selftest_wait_timeout", "ep_selftest_gemm_timeout",
+    "ep_kernel_launch_count",
     "ep_abi_version", "EXPORTED_SYMBOLS",
     "ep_sort", "ep_gemm_shape", "ep_adapter_shape", "ep_sort_workspace_size", "ep_sort_layout",
     "ep_sort_rows", "ep_unsort_rows", "ep_unsort_rows_backward", "ep_expert_gemm",
@@ -57,7 +58,7 @@ EXPORTED_SYMBOLS = (
     "ep_buffer_size_hint",
     "ep_dispatch", "ep_combine", "ep_dispatch_expert_major", "ep_combine_expert_major",
     "ep_ll_dispatch", "ep_ll_combine", "ep_clean_ll_buffer", "ep_read_recv_counts_sync",
-    "ep_read_error_flags_sync", "ep_selftest_wait_timeout", "ep_status_string",
+    "ep_read_error_flags_sync", "ep_selftest_wait_timeout", "ep_selftest_gemm_timeout", "ep_status_string",
     "ep_last_cuda_error", "ep_kernel_launch_count", "ep_abi_version",
     "ep_sort_workspace_size", "ep_sort_layout", "ep_sort_rows", "ep_unsort_rows",
     "ep_unsort_rows_backward", "ep_expert_gemm", "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad",
@@ -195,6 +196,8 @@ def lib():
         L.ep_unsort_rows.argtypes = [S(ep_shape), _P, _P, S(ep_sort), _P, S(ep_launch)]
         L.ep_unsort_rows_backward.argtypes = [S(ep_shape), _P, _P, _P, S(ep_sort), _P, _P,
                                               S(ep_launch)]
+        L.ep_selftest_gemm_timeout.argtypes = [S(ep_gemm_shape), _I32, _P, _P, _P, _P, _I32, _I32, S(ep_launch)]
+        L.ep_selftest_gemm_timeout.restype = _I32
         for name in ("ep_expert_gemm", "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad"):
             getattr(L, name).argtypes = [S(ep_gemm_shape), _P, _P, _P, _P, S(ep_launch)]
         L.ep_adapter_workspace_size.argtypes = [S(ep_adapter_shape)]
@@ -458,6 +461,13 @@ def ep_selftest_wait_timeout(src16, timeout_ms: int, elapsed_us=None,
     _check("ep_selftest_wait_timeout",
            lib().ep_selftest_wait_timeout(_ptr(src16), timeout_ms, _ptr(elapsed_us),
                                           ctypes.byref(launch or make_launch())))
+
+
+def ep_selftest_gemm_timeout(shape: ep_gemm_shape, product: int, rows, other, expert_prefix, out, loads: int,
+                             timeout_ms: int, launch: Optional[ep_launch] = None) -> None:
+    _check("ep_selftest_gemm_timeout",
+           lib().ep_selftest_gemm_timeout(ctypes.byref(shape), product, _ptr(rows), _ptr(other), _ptr(expert_prefix),
+                                          _ptr(out), loads, timeout_ms, ctypes.byref(_launch(launch))))
 
 
 def ep_read_error_flags_sync(error_flags, stream=None) -> int:

@@ -78,7 +78,7 @@ ep_status check_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* ot
 
 template <Direction D>
 ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* other, const int32_t* prefix, void* out,
-                   const ep_launch* launch) {
+                   const ep_launch* launch, int loads = GemmArgs{}.loads, uint64_t wait_ns = GemmArgs{}.wait_ns) {
     ep_status st = check_gemm(sh, rows_a, other, D == kWgrad, prefix, out, D != kWgrad, launch);
     if (st != EP_OK) return st;
     const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, E = (uint64_t)sh->num_experts,
@@ -98,6 +98,8 @@ ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* othe
     a.N = sh->in_features;
     a.C = D == kForward ? sh->in_features : sh->out_features;
     a.err = launch->error_flags;
+    a.loads = loads;
+    a.wait_ns = wait_ns;
     gemm_tiles(&a, D == kWgrad);
     GemmMaps maps{};
     if (rows > 0) {
@@ -150,6 +152,22 @@ ep_status ep_expert_gemm_dgrad(const ep_gemm_shape* sh, const void* dy, const vo
 ep_status ep_expert_gemm_wgrad(const ep_gemm_shape* sh, const void* dy, const void* x, const int32_t* expert_prefix,
                                void* dw, const ep_launch* launch) {
     return ep::run_gemm<ep::kWgrad>(sh, dy, x, expert_prefix, dw, launch);
+}
+
+ep_status ep_selftest_gemm_timeout(const ep_gemm_shape* sh, int32_t product, const void* rows, const void* other,
+                                   const int32_t* expert_prefix, void* out, int32_t loads, int32_t timeout_ms,
+                                   const ep_launch* launch) {
+    using namespace ep;
+    if (launch == nullptr || launch->error_flags == nullptr || loads < 0 || loads % kBK != 0 || timeout_ms < 1 ||
+        timeout_ms > 10000)
+        return EP_ERR_INVALID_ARG;
+    const uint64_t ns = (uint64_t)timeout_ms * 1000000ull;
+    switch (product) {
+        case 0: return run_gemm<kForward>(sh, rows, other, expert_prefix, out, launch, loads, ns);
+        case 1: return run_gemm<kDgrad>(sh, rows, other, expert_prefix, out, launch, loads, ns);
+        case 2: return run_gemm<kWgrad>(sh, rows, other, expert_prefix, out, launch, loads, ns);
+        default: return EP_ERR_INVALID_ARG;
+    }
 }
 
 }  // extern "C"

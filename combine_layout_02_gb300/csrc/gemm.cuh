@@ -20,6 +20,8 @@ struct GemmArgs {
     int split;                 // CTAs that share a tile's contraction
     int smem;                  // bytes of dynamic shared memory
     int beside;                // of them beside the stages, for gemm_kernel's epilogue
+    int loads = 0x7FFFFFFF;    // contracted values of a tile that are loaded: all, but in the self-test
+    uint64_t wait_ns = 2000000000ull;      // bound on one barrier wait: 2 s, but in the self-test
     uint32_t* err;
 };
 
@@ -174,12 +176,11 @@ __device__ __forceinline__ bool mbar_try_at(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
-constexpr uint64_t kGemmWaitNs = 2000000000ull;   // bound on one barrier wait: 2 s
-
-// Waits for a phase. Gives up when another role has (*dead), or after kGemmWaitNs (then flags
+// Waits for a phase. Gives up when another role has (*dead), or after a.wait_ns (then flags
 // EP_DEVERR_TIMEOUT and sets *dead): every role then leaves its loop. The global timer is first read
 // after many tries.
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead, uint32_t* err) {
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead, uint32_t* err,
+                                                   uint64_t wait_ns) {
     uint64_t t0 = 0;
     for (uint32_t n = 0;; ++n) {
         for (int i = 0; i < 64; ++i)
@@ -187,19 +188,19 @@ static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity
         if (*dead) return false;
         if ((n & 255) != 255) continue;
         if (t0 == 0) t0 = global_ns();
-        if (global_ns() - t0 > kGemmWaitNs) {
+        if (global_ns() - t0 > wait_ns) {
             raise_flag(err, EP_DEVERR_TIMEOUT);
             *dead = 1;
             return false;
         }
     }
 }
-__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, volatile int* dead, uint32_t* err) {
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, volatile int* dead, const GemmArgs& a) {
     if (mbar_try_at(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity, dead, err);
+    return mbar_wait_slow(bar, parity, dead, a.err, a.wait_ns);
 }
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* dead, uint32_t* err) {
-    return mbar_wait_at(smem_addr(bar), parity, dead, err);
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* dead, const GemmArgs& a) {
+    return mbar_wait_at(smem_addr(bar), parity, dead, a);
 }
 
 // True in one lane of the (converged) warp.
@@ -241,6 +242,11 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ float peer_value(uint32_t at) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ int peer_word(uint32_t at) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
 
@@ -579,9 +585,9 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             const int half = t.n / 2, m0 = t.m0 + (int)rank * kBM, n0 = t.n0 + (int)rank * half;
             const int box = kBMn ? 64 : half > 64 ? 2 * a.box : a.box, boxes = (half + box - 1) / box;
             const uint32_t bytes = warp == 0 ? kABytes : (uint32_t)(boxes * box) * 128;
-            const int whole = D == kWgrad ? depth & ~(kBK - 1) : depth;
-            for (int k0 = 0; k0 < whole; k0 += kBK, ring.next()) {
-                if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a.err))) break;
+            const int whole = D == kWgrad ? depth & ~(kBK - 1) : depth, upto = min(whole, a.loads);
+            for (int k0 = 0; k0 < upto; k0 += kBK, ring.next()) {
+                if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a))) break;
                 const uint32_t at = smem0 + ring.s * stage_bytes, bar = full0 + ring.s * 8;
                 if (elect_one()) {
                     mbar_expect_peer(bar, bytes);
@@ -603,12 +609,13 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
                 }
                 __syncwarp();
             }
+            ok = ok && upto == whole;
         }
         // The last loads' stages are free: nothing more arrives at this CTA's barriers. (Where a role has
         // given up, that is waited for as long as copies in flight may take.)
         if (warp == 0) {
             for (uint32_t q = 0; q < ring_stages; ++q, ring.next())
-                mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
+                ok = mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, ok ? a.wait_ns : a.wait_ns / 64) && ok;
         }
     } else if (D == kWgrad && warp == 2) {
         // The tails, into their own stage as soon as the tile before has been multiplied.
@@ -620,7 +627,8 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         for (int i = first; ok && walk.at(i, t); i += step) {
             const int depth = t.end - t.begin, left = depth > 0 ? depth % kBK : 0;
             if (left == 0) continue;
-            if (!(ok = mbar_wait(&empty[ring_stages], (tails & 1) ^ 1, &dead, a.err))) break;
+            if (!(ok = depth <= a.loads)) break;
+            if (!(ok = mbar_wait(&empty[ring_stages], (tails & 1) ^ 1, &dead, a))) break;
             ++tails;
             if (elect_one()) {
                 const int half = t.n / 2, boxes = (half + 63) / 64;
@@ -632,7 +640,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             }
             __syncwarp();
         }
-        mbar_wait_bounded(&empty[ring_stages], (tails & 1) ^ 1, ok ? kGemmWaitNs : kGemmWaitNs / 64);
+        mbar_wait_bounded(&empty[ring_stages], (tails & 1) ^ 1, ok ? a.wait_ns : a.wait_ns / 64);
     } else if (warp == 1 && rank == 0) {
         TileWalk<D> walk(a);
         Tile t;
@@ -645,7 +653,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             const int depth = D == kWgrad ? t.end - t.begin : a.C;
             if (depth <= 0) continue;
             const uint32_t acc = used & 1;
-            if (!(ok = mbar_wait(&acc_empty[acc], ((used >> 1) & 1) ^ 1, &dead, a.err))) break;
+            if (!(ok = mbar_wait(&acc_empty[acc], ((used >> 1) & 1) ^ 1, &dead, a))) break;
             tc_fence_after();
             const uint32_t d = tmem + acc * 256, idesc = instr_desc(2 * kBM, t.n, kAMn, kBMn);
             for (int k0 = 0; k0 < depth; k0 += kBK) {
@@ -653,7 +661,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
                 uint32_t s = ring.s, phase = ring.phase;
                 if (D == kWgrad && left < kBK) s = ring_stages, phase = tails++ & 1;
                 else ring.next();
-                if (!(ok = mbar_wait_at(full0 + s * 8, phase, &dead, a.err))) break;
+                if (!(ok = mbar_wait_at(full0 + s * 8, phase, &dead, a))) break;
                 tc_fence_after();
                 const uint64_t at = (uint64_t)((s * stage_bytes) >> 4), da = da0 + at, db = db0 + at;
                 if (elect_one()) {
@@ -666,13 +674,15 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
                 }
                 __syncwarp();
             }
+            if (!ok) break;          // the tile is not complete: neither CTA may write it
             if (elect_one()) tc_commit2(smem_addr(&acc_full[acc]));
             __syncwarp();
             ++used;
         }
         if (!ok) {
             if (elect_one()) tc_commit2(smem_addr(&drain));
-            mbar_wait_bounded(&drain, 0, kGemmWaitNs / 8);
+            __syncwarp();
+            mbar_wait_bounded(&drain, 0, a.wait_ns / 8);
         }
     } else if (warp >= 4) {
         TileWalk<D> walk(a);
@@ -686,7 +696,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             const int rows = min(t.n, t.end - t.n0);
             if (D != kWgrad) extra.prepare(s_extra, smem + a.stages * stage_bytes, t.n0, rows);
             if (some) {
-                if (!epilogue_all<32 * kTileWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a.err))) break;
+                if (!epilogue_all<32 * kTileWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a))) break;
                 tc_fence_after();
             }
             const int m = t.m0 + (int)rank * kBM + quarter * 32 + lane;
@@ -790,6 +800,19 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& a, int i, int lane, Ti
 
 constexpr int kSplitThreads = 320;
 
+// The writing warps of a CTA that has given up: NaN for its whole part, once copies in flight have had
+// time to land (they share the memory).
+static __device__ __noinline__ void spoil_part(float* part, int columns, uint64_t* done, uint64_t wait_ns) {
+    mbar_wait_bounded(done, 0, wait_ns);
+    for (int i = threadIdx.x - 64; i < columns * kBM; i += kSplitThreads - 64) part[i] = __int_as_float(0x7FFFFFFF);
+}
+// Whether all parts of the tile are complete (`complete`: this CTA's word of that).
+static __device__ __noinline__ bool parts_complete(const int* complete, int split) {
+    bool all = true;
+    for (int r = 0; r < split; ++r) all = all && peer_word(peer_addr(smem_addr(complete), r)) != 0;
+    return all;
+}
+
 // Where rows are few and the weights are what is read (forward, dgrad), or where tiles are few and the
 // rows many (wgrad): a cluster of `split` CTAs per tile, each over its part of the contraction, so
 // that enough CTAs stream weights at the same time (and two fit an SM, one filling its pipeline
@@ -802,12 +825,13 @@ template <Direction D, class Extra>
 __global__ void __launch_bounds__(kSplitThreads, 2)
     gemm_split_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done;
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done, drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int dead;
     __shared__ __align__(16) float s_extra[Extra::kFloats];
     __shared__ Tile s_tile;
     __shared__ int s_has;
+    __shared__ int s_complete;             // this CTA's part is
     constexpr bool kAMn = D != kForward, kBMn = D == kWgrad;
     unsigned char* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const uint32_t stage_bytes = kABytes + (uint32_t)a.bn * 128;
@@ -822,6 +846,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             mbar_init(&empty[s], 1);
         }
         mbar_init(&done, 1);
+        mbar_init(&drain, 1);
         dead = 0;
     }
     if (warp == 1) tmem_alloc(&s_tmem, (uint32_t)a.bn);
@@ -850,8 +875,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         const uint32_t full0 = smem_addr(full), empty0 = smem_addr(empty);
         Ring ring(a.stages);
         bool ok = true;
-        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-            if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a.err))) break;
+        const int upto = min(kb1, a.loads / kBK);
+        for (int kb = kb0; kb < upto; ++kb, ring.next()) {
+            if (!(ok = mbar_wait_at(empty0 + ring.s * 8, ring.phase ^ 1, &dead, a))) break;
             const uint32_t sa = smem0 + ring.s * stage_bytes, sb = sa + kABytes, bar = full0 + ring.s * 8;
             const int k0 = kb * kBK, left = depth - k0;
             if (elect_one()) {
@@ -879,14 +905,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             }
             __syncwarp();
         }
-        if (!ok)     // wait, with a limit, for the copies still in flight
-            for (int s = 0; s < a.stages; ++s, ring.next()) mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, kGemmWaitNs / 64);
+        if (!ok || upto < kb1)     // wait, with a limit, for the copies still in flight
+            for (int s = 0; s < a.stages; ++s, ring.next()) mbar_wait_bounded(&empty[ring.s], ring.phase ^ 1, a.wait_ns / 64);
     } else if (has && warp == 1) {
         const uint32_t idesc = instr_desc(kBM, t.n, kAMn, kBMn), full0 = smem_addr(full), empty0 = smem_addr(empty);
         const uint64_t da0 = smem_desc(smem_addr(smem), kAMn), db0 = smem_desc(smem_addr(smem) + kABytes, kBMn);
         Ring ring(a.stages);
+        bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-            if (!mbar_wait_at(full0 + ring.s * 8, ring.phase, &dead, a.err)) break;
+            if (!(ok = mbar_wait_at(full0 + ring.s * 8, ring.phase, &dead, a))) break;
             tc_fence_after();
             const uint64_t at = (uint64_t)((ring.s * stage_bytes) >> 4), da = da0 + at, db = db0 + at;
             const int left = depth - kb * kBK;
@@ -900,7 +927,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             }
             __syncwarp();
         }
-        if (elect_one()) tc_commit(smem_addr(&done));
+        if (elect_one()) tc_commit(smem_addr(ok ? &done : &drain));      // done: this part is complete
+        __syncwarp();
+        if (!ok) mbar_wait_bounded(&drain, 0, a.wait_ns / 8);
     }
     __syncwarp();
     const int quarter = warp & 3, half = (warp - 2) >> 2, m_local = quarter * 32 + lane, m = t.m0 + m_local;
@@ -910,7 +939,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     bool ok = has;
     if (has && warp >= 2) {
         if (D != kWgrad) extra.ahead(s_extra, t.n0 + lo, hi - lo, m, half);
-        ok = epilogue_all<256>(mbar_wait(&done, 0, &dead, a.err));
+        ok = epilogue_all<256>(mbar_wait(&done, 0, &dead, a));
         tc_fence_after();
     }
     if (Extra::kFollows && warp >= 2) pdl_wait();
@@ -940,6 +969,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 for (int j = 0; j < 8; ++j) part[(c + j) * kBM + m_local] = v[j];     // up to bn columns
             }
         }
+        // The tile is written where every part is complete. A CTA that has given up leaves NaN as its part,
+        // so that the others ask for its word only then: asking every time, before or beside the sums,
+        // took 0.2 to 0.4 us of the 10 that one row 4096 x 4096 takes.
+        if (threadIdx.x == 64) s_complete = ok;          // (warp 2's ok is that of all writing warps)
+        if (has && !ok && warp >= 2) spoil_part(part, a.bn, &done, a.wait_ns / 64);
         __syncwarp();
         cluster_barrier();
         const uint32_t at = smem_addr(part);
@@ -951,6 +985,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] += peer_value(peer + ((c + j) * kBM + m_local) * 4);
                 }
+                if (isnan(v[0]) && !parts_complete(&s_complete, a.split)) break;
                 st_v4(a.out + ((int64_t)t.e * a.M + m) * a.N + t.n0 + c,
                       make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
             }
@@ -965,8 +1000,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                     for (int j = 0; j < G; ++j)
                         if (c + j < hi) v[j] += peer_value(peer + ((c + j) * kBM + m_local) * 4);
                 }
+                const bool failed = isnan(v[0]) && !parts_complete(&s_complete, a.split);          // for all alike
                 extra.apply(s_extra, v, t.n0 + lo, hi - lo, c - lo, m, half);
-                store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
+                if (!__any_sync(0xFFFFFFFFu, failed)) store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
             }
         }
         __syncwarp();

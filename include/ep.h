@@ -622,6 +622,17 @@ EP_API ep_status ep_read_error_flags_sync(const uint32_t* error_flags, uint32_t*
 EP_API ep_status ep_selftest_wait_timeout(const void* src16, int32_t timeout_ms, uint32_t* elapsed_us,
                                           const ep_launch* launch);
 
+/* The same for the waits of the products: an ep_expert_gemm (product 0), _dgrad (1) or
+ * _wgrad (2) of the same arguments whose tiles load no more than the first `loads` (>= 0, a
+ * multiple of 64) of their contracted values (features; wgrad: rows of an expert), as if the
+ * others had not arrived, and whose waits give up after timeout_ms (1 to 10000). Tiles of
+ * a longer contraction are not written and EP_DEVERR_TIMEOUT is set in launch->error_flags
+ * (required); with no longer one it is the product. Nothing faults or hangs, and the
+ * context stays usable. */
+EP_API ep_status ep_selftest_gemm_timeout(const ep_gemm_shape* shape, int32_t product, const void* rows,
+                                          const void* other, const int32_t* expert_prefix, void* out,
+                                          int32_t loads, int32_t timeout_ms, const ep_launch* launch);
+
 /* Static description of a status code. */
 EP_API const char* ep_status_string(ep_status status);
 
