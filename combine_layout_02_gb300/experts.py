@@ -33,7 +33,9 @@ class ExpertSort:
         self.shape = make_shape(1, self.N, hidden, num_experts, self.k)
         self.buffers = SortBuffers(self.shape, rows, topk_idx.device)
         ep_sort_layout(self.shape, topk_idx, self.buffers.handle(), self.buffers.workspace, self.launch())
-        self.rows = int(self.buffers.expert_prefix[-1].item()) if rows is None else int(rows)
+        if rows is None:
+            self.buffers.rows = int(self.buffers.expert_prefix[-1].item())      # what sorted rows are sized by
+        self.rows = self.buffers.rows
         self.handle = self.buffers.handle()
 
     @property
