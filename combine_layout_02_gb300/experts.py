@@ -4,7 +4,8 @@ the C ABI: rows into expert order and back (``ep_sort_*`` / ``ep_unsort_*``), th
 (``ep_adapter_gemm``); and ``MoELayer``, a layer that runs all of it together with a ``Buffer``.
 
 Like the rest of the package this module only allocates tensors and calls the library, on the
-current stream. Tensors are bf16 unless stated.
+current stream. Tensors are bf16 unless stated. The library takes pointers, so each function first
+checks its tensors' types and shapes and raises ValueError where they are others.
 """
 from __future__ import annotations
 
@@ -21,6 +22,21 @@ from .buffers import SortBuffers
 __all__ = ["ExpertSort", "sort_rows", "unsort_rows", "expert_product", "adapter_projection", "MoELayer"]
 
 
+def _check(what: str, t: torch.Tensor, dtype: torch.dtype, *shape: Optional[int]) -> None:
+    """t has to be a tensor of this type and shape (None: any length)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise ValueError(f"{what} has to be a tensor of {dtype}, not {getattr(t, 'dtype', type(t))}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        wants = ", ".join("any" if n is None else str(n) for n in shape)
+        raise ValueError(f"{what} has to be [{wants}], not {list(t.shape)}")
+
+
+def _check_err(err: Optional[torch.Tensor]) -> None:
+    if err is not None and (not isinstance(err, torch.Tensor) or err.dtype not in (torch.int32, torch.uint32) or
+                            err.numel() < 1):
+        raise ValueError("err has to be a tensor of one int32 error word")
+
+
 class ExpertSort:
     """The placement of rows by expert: ``topk_idx`` [N][k] int64, -1 masked, experts 0 to E - 1.
     ``rows``: how many sorted rows there are, where the caller knows (from the counts of a
@@ -28,6 +44,8 @@ class ExpertSort:
 
     def __init__(self, topk_idx: torch.Tensor, num_experts: int, hidden: int, rows: Optional[int] = None,
                  err: Optional[torch.Tensor] = None):
+        _check("topk_idx", topk_idx, torch.int64, None, None)
+        _check_err(err)
         self.N, self.k = topk_idx.shape
         self.E, self.H, self.err = num_experts, hidden, err
         self.shape = make_shape(1, self.N, hidden, num_experts, self.k)
@@ -104,13 +122,17 @@ class _ExpertProduct(torch.autograd.Function):
 
 
 def sort_rows(x: torch.Tensor, sort: ExpertSort) -> torch.Tensor:
-    """x [N][H] -> [rows][H] in expert order; gradient to x."""
+    """x [N][H] -> [rows][H] in expert order; gradient to x. (Quantised rows: ``ep_sort_rows``.)"""
+    _check("x", x, torch.bfloat16, sort.N, sort.H)
     return _SortRows.apply(x, sort)
 
 
 def unsort_rows(y: torch.Tensor, sort: ExpertSort, weights: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [rows][H] -> [N][H], the sum of each row's entries, scaled by weights [N][k] fp32 if given;
     gradients to y and weights."""
+    _check("y", y, torch.bfloat16, sort.rows, sort.H)
+    if weights is not None:
+        _check("weights", weights, torch.float32, sort.N, sort.k)
     return _UnsortRows.apply(y, weights, sort)
 
 
@@ -118,6 +140,10 @@ def expert_product(x: torch.Tensor, weight: torch.Tensor, expert_prefix: torch.T
                    err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [rows][in] in expert order, weight [E][out][in] -> [rows][out]; gradients to both. Every
     row has to belong to an expert (expert_prefix runs from 0 to rows)."""
+    _check("weight", weight, torch.bfloat16, None, None, None)
+    _check("x", x, torch.bfloat16, None, weight.shape[2])
+    _check("expert_prefix", expert_prefix, torch.int32, weight.shape[0] + 1)
+    _check_err(err)
     return _ExpertProduct.apply(x, weight, expert_prefix, err)
 
 
@@ -127,8 +153,17 @@ def adapter_projection(x: torch.Tensor, weight: torch.Tensor, a: Optional[torch.
                        err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [T][in], weight [out][in], a [L][r][in], b [L][out][r], scales [L] fp32, adapter_idx [T]
     int64 (-1 none) -> [T][out]. For serving: no gradient."""
+    _check("x", x, torch.bfloat16, None, None)
+    _check("weight", weight, torch.bfloat16, None, x.shape[1])
     (T, K), F = x.shape, weight.shape[0]
-    L, r = (0, 8) if a is None else (a.shape[0], a.shape[1])
+    L, r = 0, 8
+    if a is not None:
+        _check("a", a, torch.bfloat16, None, None, K)
+        L, r = a.shape[0], a.shape[1]
+        _check("b", b, torch.bfloat16, L, F, r)
+        _check("scales", scales, torch.float32, L)
+    _check("adapter_idx", adapter_idx, torch.int64, T)
+    _check_err(err)
     shape = ep_adapter_shape(T, K, F, L, r)
     workspace = torch.empty(max(16, ep_adapter_workspace_size(shape)), dtype=torch.uint8, device=x.device)
     y = torch.empty((T, F), dtype=x.dtype, device=x.device)
@@ -191,6 +226,9 @@ class MoELayer(torch.nn.Module):
         """x [R][T][H], topk_idx / topk_weights [R][T][k]; adapters: (a, b, scales, adapter_idx [R][T])
         of the shared projection (without gradients) or None -> [R][T][H]."""
         buf, out = self.buf, {}
+        _check("x", x, torch.bfloat16, buf.R, None, buf.H)
+        _check("topk_idx", topk_idx, torch.int64, buf.R, x.shape[1], buf.k)
+        _check("topk_weights", topk_weights, torch.float32, buf.R, x.shape[1], buf.k)
         rows, weights = _Dispatch.apply(x, topk_weights, topk_idx, buf, out)
         off: List[int] = out["handle"].row_offset
         local = out["recv_idx"][:off[-1]]
