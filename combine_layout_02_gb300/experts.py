@@ -5,13 +5,15 @@ the C ABI: rows into expert order and back (``ep_sort_*`` / ``ep_unsort_*``), th
 
 Like the rest of the package this module only allocates tensors and calls the library, on the
 current stream. Tensors are bf16 unless stated. The library takes pointers, so each function first
-checks its tensors' types and shapes and raises ValueError where they are others.
+checks its tensors' types and shapes and raises ValueError where they are others. The gradients are
+the library's too and have no gradients of their own: differentiating them raises.
 """
 from __future__ import annotations
 
 from typing import List, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (EP_BF16, ep_adapter_gemm, ep_adapter_shape, ep_adapter_workspace_size, ep_expert_gemm,
                ep_expert_gemm_dgrad, ep_expert_gemm_wgrad, ep_gemm_shape, ep_sort_layout, ep_sort_rows,
@@ -73,6 +75,7 @@ class _SortRows(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         sort = ctx.sort
         dx = torch.empty((sort.N, sort.H), dtype=grad.dtype, device=grad.device)
@@ -90,6 +93,7 @@ class _UnsortRows(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         sort, (y, weights) = ctx.sort, ctx.saved_tensors
         dy = torch.empty_like(y)
@@ -109,6 +113,7 @@ class _ExpertProduct(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         x, weight, prefix = ctx.saved_tensors
         grad, launch, dx, dw = grad.contiguous(), make_launch(error_flags=ctx.err), None, None
@@ -185,6 +190,7 @@ class _Dispatch(torch.autograd.Function):
         return buf._rows_tensor(recv_x, off)[:rows], buf._rows_tensor(recv_w, off)[:rows]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dx, dw):
         gx, gw, _ = ctx.buf.combine(dx.contiguous(), ctx.handle, topk_weights=dw.contiguous())
         return gx, gw, None, None, None
@@ -200,6 +206,7 @@ class _Combine(torch.autograd.Function):
         return buf.combine(y, handle)[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         recv_x = ctx.buf.dispatch(grad.contiguous(), handle=ctx.handle)[0]
         off = ctx.handle.row_offset
