@@ -126,6 +126,23 @@ class _ExpertProduct(torch.autograd.Function):
         return dx, dw, None, None
 
 
+class _AdapterProjection(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, a, b, scales, adapter_idx, err):
+        (T, K), F = x.shape, weight.shape[0]
+        L, r = (0, 8) if a is None else (a.shape[0], a.shape[1])
+        shape = ep_adapter_shape(T, K, F, L, r)
+        workspace = torch.empty(max(16, ep_adapter_workspace_size(shape)), dtype=torch.uint8, device=x.device)
+        y = torch.empty((T, F), dtype=x.dtype, device=x.device)
+        ep_adapter_gemm(shape, x, weight, a, b, scales, adapter_idx, y, workspace, make_launch(error_flags=err))
+        return y
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError("adapter_projection is for serving and has no gradient: call it under torch.no_grad(), or "
+                           "detach its inputs where the gradient may leave it out")
+
+
 def sort_rows(x: torch.Tensor, sort: ExpertSort) -> torch.Tensor:
     """x [N][H] -> [rows][H] in expert order; gradient to x. (Quantised rows: ``ep_sort_rows``.)"""
     _check("x", x, torch.bfloat16, sort.N, sort.H)
@@ -152,16 +169,14 @@ def expert_product(x: torch.Tensor, weight: torch.Tensor, expert_prefix: torch.T
     return _ExpertProduct.apply(x, weight, expert_prefix, err)
 
 
-@torch.no_grad()
 def adapter_projection(x: torch.Tensor, weight: torch.Tensor, a: Optional[torch.Tensor], b: Optional[torch.Tensor],
                        scales: Optional[torch.Tensor], adapter_idx: torch.Tensor,
                        err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [T][in], weight [out][in], a [L][r][in], b [L][out][r], scales [L] fp32, adapter_idx [T]
-    int64 (-1 none) -> [T][out]. For serving: no gradient."""
+    int64 (-1 none) -> [T][out]. For serving: a backward pass that reaches it raises."""
     _check("x", x, torch.bfloat16, None, None)
     _check("weight", weight, torch.bfloat16, None, x.shape[1])
     (T, K), F = x.shape, weight.shape[0]
-    L, r = 0, 8
     if a is not None:
         _check("a", a, torch.bfloat16, None, None, K)
         L, r = a.shape[0], a.shape[1]
@@ -169,11 +184,7 @@ def adapter_projection(x: torch.Tensor, weight: torch.Tensor, a: Optional[torch.
         _check("scales", scales, torch.float32, L)
     _check("adapter_idx", adapter_idx, torch.int64, T)
     _check_err(err)
-    shape = ep_adapter_shape(T, K, F, L, r)
-    workspace = torch.empty(max(16, ep_adapter_workspace_size(shape)), dtype=torch.uint8, device=x.device)
-    y = torch.empty((T, F), dtype=x.dtype, device=x.device)
-    ep_adapter_gemm(shape, x, weight, a, b, scales, adapter_idx, y, workspace, make_launch(error_flags=err))
-    return y
+    return _AdapterProjection.apply(x, weight, a, b, scales, adapter_idx, err)
 
 
 class _Dispatch(torch.autograd.Function):
@@ -231,7 +242,8 @@ class MoELayer(torch.nn.Module):
     def forward(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
                 adapters: Optional[tuple] = None) -> torch.Tensor:
         """x [R][T][H], topk_idx / topk_weights [R][T][k]; adapters: (a, b, scales, adapter_idx [R][T])
-        of the shared projection (without gradients) or None -> [R][T][H]."""
+        of the shared projection (serving: under torch.no_grad(), a backward pass raises) or None
+        -> [R][T][H]."""
         buf, out = self.buf, {}
         _check("x", x, torch.bfloat16, buf.R, None, buf.H)
         _check("topk_idx", topk_idx, torch.int64, buf.R, x.shape[1], buf.k)
