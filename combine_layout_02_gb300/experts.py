@@ -6,7 +6,9 @@ the C ABI: rows into expert order and back (``ep_sort_*`` / ``ep_unsort_*``), th
 Like the rest of the package this module only allocates tensors and calls the library, on the
 current stream. Tensors are bf16 unless stated. The library takes pointers, so each function first
 checks its tensors' types and shapes and raises ValueError where they are others. The gradients are
-the library's too and have no gradients of their own: differentiating them raises.
+the library's too and have no gradients of their own: differentiating them raises. What only the
+device sees (ids out of range, rows beyond their buffer, a wait that gave up: EP_DEVERR_*) goes to
+the error word that a call is given as ``err``, else to the module's own, which check_errors() reads.
 """
 from __future__ import annotations
 
@@ -16,12 +18,13 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (EP_BF16, ep_adapter_gemm, ep_adapter_shape, ep_adapter_workspace_size, ep_expert_gemm,
-               ep_expert_gemm_dgrad, ep_expert_gemm_wgrad, ep_gemm_shape, ep_sort_layout, ep_sort_rows,
+               ep_expert_gemm_dgrad, ep_expert_gemm_wgrad, ep_gemm_shape, ep_read_error_flags_sync, ep_sort_layout, ep_sort_rows,
                ep_unsort_rows, ep_unsort_rows_backward, make_launch, make_shape)
 from .api import Buffer
 from .buffers import SortBuffers
 
-__all__ = ["ExpertSort", "sort_rows", "unsort_rows", "expert_product", "adapter_projection", "MoELayer"]
+__all__ = ["ExpertSort", "sort_rows", "unsort_rows", "expert_product", "adapter_projection", "check_errors",
+           "MoELayer"]
 
 
 def _check(what: str, t: torch.Tensor, dtype: torch.dtype, *shape: Optional[int]) -> None:
@@ -39,6 +42,34 @@ def _check_err(err: Optional[torch.Tensor]) -> None:
         raise ValueError("err has to be a tensor of one int32 error word")
 
 
+_words: dict = {}           # device index -> the error word of calls without one
+
+
+def _error_word(err: Optional[torch.Tensor], device: torch.device) -> Optional[torch.Tensor]:
+    if err is not None or device.type != "cuda":
+        return err
+    if device.index not in _words and not torch.cuda.is_current_stream_capturing():
+        word = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.current_stream(device).synchronize()            # any stream may use it from here on
+        _words[device.index] = word
+    return _words.get(device.index)          # none where a graph captures the very first call
+
+
+def check_errors(device="cuda") -> int:
+    """Waits for the device, then returns the EP_DEVERR_* bits that calls without an error word of
+    their own have seen since the last check_errors."""
+    device = torch.device(device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    if index not in _words:
+        return 0
+    torch.cuda.synchronize(index)
+    seen = ep_read_error_flags_sync(_words[index])
+    if seen:
+        _words[index].zero_()
+        torch.cuda.synchronize(index)
+    return seen
+
+
 class ExpertSort:
     """The placement of rows by expert: ``topk_idx`` [N][k] int64, -1 masked, experts 0 to E - 1.
     ``rows``: how many sorted rows there are, where the caller knows (from the counts of a
@@ -49,7 +80,7 @@ class ExpertSort:
         _check("topk_idx", topk_idx, torch.int64, None, None)
         _check_err(err)
         self.N, self.k = topk_idx.shape
-        self.E, self.H, self.err = num_experts, hidden, err
+        self.E, self.H, self.err = num_experts, hidden, _error_word(err, topk_idx.device)
         self.shape = make_shape(1, self.N, hidden, num_experts, self.k)
         self.buffers = SortBuffers(self.shape, rows, topk_idx.device)
         ep_sort_layout(self.shape, topk_idx, self.buffers.handle(), self.buffers.workspace, self.launch())
@@ -166,7 +197,7 @@ def expert_product(x: torch.Tensor, weight: torch.Tensor, expert_prefix: torch.T
     _check("x", x, torch.bfloat16, None, weight.shape[2])
     _check("expert_prefix", expert_prefix, torch.int32, weight.shape[0] + 1)
     _check_err(err)
-    return _ExpertProduct.apply(x, weight, expert_prefix, err)
+    return _ExpertProduct.apply(x, weight, expert_prefix, _error_word(err, x.device))
 
 
 def adapter_projection(x: torch.Tensor, weight: torch.Tensor, a: Optional[torch.Tensor], b: Optional[torch.Tensor],
@@ -184,7 +215,7 @@ def adapter_projection(x: torch.Tensor, weight: torch.Tensor, a: Optional[torch.
         _check("scales", scales, torch.float32, L)
     _check("adapter_idx", adapter_idx, torch.int64, T)
     _check_err(err)
-    return _AdapterProjection.apply(x, weight, a, b, scales, adapter_idx, err)
+    return _AdapterProjection.apply(x, weight, a, b, scales, adapter_idx, _error_word(err, x.device))
 
 
 class _Dispatch(torch.autograd.Function):
