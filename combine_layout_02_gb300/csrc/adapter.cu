@@ -412,11 +412,12 @@ struct AdapterFew : AdapterSide {
 // low taken from memory row by row by its latency: 500 and 365 us where this is 290. Now these products
 // are what counts where the contraction is short: they share the tensor cores with the tiles at
 // work. 4096 rows 2048 -> 8192: 116 us with rank 16, 142 with 64, 75 without adapters; PLAIN 107.)
-// hi and lo terms of two fp32 values (an infinite one is its hi term).
+// hi and lo terms of two fp32 values. hi stays finite: a value that rounds beyond bf16's largest has that
+// as its hi term and what is left as lo (an infinity is left whole; a NaN is in lo).
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16x2(a, b);
-    const float x = a - bf16_lo(hi), y = b - bf16_hi(hi);
-    lo = pack_bf16x2(isinf(a) ? 0.0f : x, isinf(b) ? 0.0f : y);
+    constexpr float kMost = 0x1.FEp127f;
+    hi = pack_bf16x2(fminf(fmaxf(a, -kMost), kMost), fminf(fmaxf(b, -kMost), kMost));
+    lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
 }
 
 // Rows of a split tile of more than 64 up to which AdapterFew is the faster: its time grows with

@@ -1,0 +1,52 @@
+"""The projection with adapters at the edges of its types, in every form it takes: few rows, many rows
+by warp-level products of low's two bf16 terms, and many rows by fp32 multiply-adds."""
+import pytest
+import torch
+
+from rows_util import U16, assert_within
+from test_gpu_adapter import call, ids_of, plain
+
+pytestmark = pytest.mark.gpu
+
+# rows, in_features, out_features, adapters, rank
+FORMS = {
+    "one": (1, 136, 264, 3, 16),
+    "few": (40, 136, 264, 3, 16),
+    "few_64": (90, 72, 136, 3, 64),
+    "many_8": (700, 72, 264, 3, 8),
+    "many_16": (700, 136, 264, 5, 16),
+    "many_24": (1000, 72, 520, 40, 24),
+    "many_64": (600, 264, 136, 3, 64),
+    "many_72": (520, 72, 264, 4, 72),
+    "many_short_runs": (2100, 72, 136, 700, 16),
+    "plain": (2307, 2056, 4104, 7, 16),
+}
+
+
+def zeros(case, order, seed):
+    """No projection, no adapters yet; every row's x is 1 in the first place and 0 elsewhere."""
+    T, K, F, L, r = FORMS[case]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    d = dict(x=bf(T, K), w=bf(F, K), a=bf(L, r, K), b=bf(L, F, r), s=torch.ones(L, device="cuda"), ids=ids_of(T, L, order, g))
+    d["x"][:, 0] = 1
+    d["ids"][0] = 0
+    return d
+
+
+@pytest.mark.parametrize("case", FORMS)
+@pytest.mark.parametrize("order", ["any", "sorted"])
+def test_low_at_the_end_of_fp32(case, order):
+    """low values between bf16's and fp32's largest, scaled back by B: finite results. Everything
+    but their one rounding, and where two bf16 terms stand for low its 2^-17, is exact."""
+    d = zeros(case, order, 1)
+    L, r = FORMS[case][3], FORMS[case][4]
+    values = torch.tensor([3.39e38, 3.3961775e38, 3.397e38, 3.4e38, 3.4028234e38], device="cuda")
+    d["s"] = values[torch.arange(L, device="cuda") % 5]
+    rank = torch.arange(L, device="cuda") % r
+    d["a"][torch.arange(L, device="cuda"), rank, 0] = torch.where(torch.arange(L, device="cuda") % 2 == 0, 1.0, -1.0).bfloat16()
+    d["b"][torch.arange(L, device="cuda"), :, rank] = 2.0 ** -9
+    got = call(d)
+    y, delta = plain(d)
+    assert bool(torch.isfinite(delta).all())
+    assert_within(got, y + delta, 2.0 ** -17 * delta.abs(), U16)
