@@ -20,7 +20,7 @@ struct AdapterArgs {
     const int32_t* prefix;
     const int32_t* changes;    // wide: scattered rows' x is copied to sorted_x in that order, by
     char* sorted_x;            // the blocks from copy_from on (one warp per row)
-    float* low;                // [parts][T][r]
+    float* low;                // [parts][T][r], scaled if there is one part
     int T, K, L, r, parts;
     unsigned copy_from;
     int slots;                 // blocks per 32 rows, where they are taken as they are
@@ -116,8 +116,8 @@ __device__ __forceinline__ bool copy_block(const AdapterArgs& a, int warp, int l
     return true;
 }
 
-// low[part][t][q] = scales[i] * sum over the part's k of x[t][k] A_i[q][k], for up to 32 rows of one
-// adapter; NT * 8 ranks at a time (blockIdx.z: which, where there are blocks for all). The warps
+// low[part][t][q] = sum over the part's k of x[t][k] A_i[q][k], times scales[i] if it is the only part (a part's
+// own product may overflow where that of the sum does not), for up to 32 rows of one adapter; NT * 8 ranks at a time (blockIdx.z: which, where there are blocks for all). The warps
 // share the part and join in shared memory in warp order; the parts are added up by the
 // projection's epilogue. Operands come straight from memory: a
 // lane of quad position c loads the 8 values c*8 .. c*8+7 of a 32-deep step with one 16-byte load,
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapter_low_kernel(AdapterA
         take[h] = row >= 0;
         xr[h] = a.x + (int64_t)max(row, 0) * a.K;
     }
-    const float scale = a.scales[i];
+    const float scale = gridDim.y > 1 ? 1.0f : a.scales[i];
     for (int q0 = blockIdx.z * NT * 8; q0 < a.r; q0 += gridDim.z * NT * 8) {
         float acc[2][NT][4] = {};
         const __nv_bfloat16* ar = a.a + ((int64_t)i * a.r + q0 + g) * a.K;
@@ -271,6 +271,7 @@ AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
 struct AdapterSide {
     const __nv_bfloat16* b;
     const float* low;
+    const float* scales;
     const int64_t* idx;
     int64_t part;          // floats from one part of low to the next
     int parts, F, L, r;
@@ -280,9 +281,11 @@ struct AdapterSide {
         const int64_t i = idx[t];
         return i >= 0 && i < L ? (int)i : -1;
     }
-    // Four low values of row t, ranks from q on: the sum of the parts.
-    __device__ __forceinline__ float4 low4(int64_t t, int q) const {
+    // Four low values of row t, ranks from q on: the sum of the parts, times the scale of its adapter (not looked
+    // at if there is one part).
+    __device__ __forceinline__ float4 low4(int64_t t, int q, const float* scale) const {
         const float* at = low + t * r + q;
+        const float s = parts > 1 ? *scale : 1.0f;
         float4 v = *reinterpret_cast<const float4*>(at);
         for (int p0 = 1; p0 < parts; p0 += 4) {
             float4 x[4];
@@ -292,7 +295,7 @@ struct AdapterSide {
 #pragma unroll
             for (int p = 0; p < 4; ++p) v.x += x[p].x, v.y += x[p].y, v.z += x[p].z, v.w += x[p].w;
         }
-        return v;
+        return make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
     }
 };
 
@@ -357,7 +360,7 @@ struct AdapterFew : AdapterSide {
             for (int e = tid; e < together * kGroup * pieces; e += 128) {
                 const int n = e / pieces, q = (e - n * pieces) * 4, j = (n / kGroup) * 2 * kGroup + n % kGroup;
                 const bool has = c + j < rows && ids[j] >= 0;
-                *reinterpret_cast<float4*>(shared + n * r + q) = has ? low4(row0 + c + j, q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                *reinterpret_cast<float4*>(shared + n * r + q) = has ? low4(row0 + c + j, q, scales + ids[j]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
             epilogue_barrier<128>(2 + half);
         }
@@ -445,8 +448,9 @@ __device__ __forceinline__ void fma_pair(float2& d, float2 a, float2 b) {
 template <int RANKS, bool PLAIN>
 struct AdapterWide : AdapterSide {
     static constexpr bool kFollows = false;
-    // shared: which rows the tile has, the run each is in, and each run's adapter (and one -1 after)
-    static constexpr int kRows = 256, kHeld = RANKS, kFloats = 3 * kRows + 4 + 8;
+    // shared: which rows the tile has, the run each is in, each run's adapter (and one -1 after), the warps'
+    // counts of runs, and the rows' scales
+    static constexpr int kRows = 256, kHeld = RANKS, kScale = 3 * kRows + 4 + 8, kFloats = kScale + kRows;
     // A lane's pieces of B, and its ranks in one.
     using Piece = typename std::conditional<RANKS == 16 && !PLAIN, uint2, uint4>::type;
     static constexpr int kPer = sizeof(Piece) / 2, NS = PLAIN ? 2 : RANKS / (4 * kPer);
@@ -462,16 +466,17 @@ struct AdapterWide : AdapterSide {
 
     // The tile's rows' low, or its hi and lo terms: kHeld ranks from q0 on, zero past the last rank.
     __device__ __forceinline__ void stage(const int* which, unsigned char* terms, int rows, int q0) const {
+        const float* scale_of = reinterpret_cast<const float*>(which) + kScale;
         constexpr int kPieces = kHeld / (PLAIN ? 4 : 8);
 #pragma unroll 2
         for (int e = threadIdx.x - 128; e < rows * kPieces; e += 256) {
             const int j = e / kPieces, q = e % kPieces * (PLAIN ? 4 : 8);
             const bool has = q0 + q < r;
-            const float4 x = has ? low4(which[j], q0 + q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float4 x = has ? low4(which[j], q0 + q, scale_of + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if constexpr (PLAIN) {
                 *reinterpret_cast<float4*>(terms + j * kPitch + q * 4) = x;
             } else {
-                const float4 y = has ? low4(which[j], q0 + q + 4) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const float4 y = has ? low4(which[j], q0 + q + 4, scale_of + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 uint4 hi, lo;
                 split_pair(x.x, x.y, hi.x, lo.x);
                 split_pair(x.z, x.w, hi.y, lo.y);
@@ -495,8 +500,10 @@ struct AdapterWide : AdapterSide {
         const int before = tid < rows && tid > 0 ? adapter(row_at(tid - 1)) : -2;
         const bool starts = tid < rows && mine != before;
         const unsigned mask = __ballot_sync(0xFFFFFFFFu, starts);
+        const float scale = parts > 1 && mine >= 0 ? scales[mine] : 0.0f;
         epilogue_barrier<256>();          // the tile before has been read
         which[tid] = row;
+        shared[kScale + tid] = scale;
         if (lane == 0) counts[warp] = __popc(mask);
         epilogue_barrier<256>();
         int run = __popc(mask & (lanemask_lt() | 1u << lane)) - 1, all = 0;
@@ -773,7 +780,7 @@ ep_status ep_adapter_gemm(const ep_adapter_shape* sh, const void* x, const void*
                             ws.parts, (unsigned)low_blocks(sh->num_rows, sh->num_adapters, true),
                             low_slots(sh->num_rows, sh->num_adapters) > 0 ? low_slots(sh->num_rows, sh->num_adapters) : 1,
                             launch->error_flags};
-        const AdapterSide side{reinterpret_cast<const __nv_bfloat16*>(b), g.low, adapter_idx, (int64_t)g.T * g.r, g.parts,
+        const AdapterSide side{reinterpret_cast<const __nv_bfloat16*>(b), g.low, scales, adapter_idx, (int64_t)g.T * g.r, g.parts,
                                sh->out_features, g.L, g.r};
         cudaError_t e = cudaSuccess;
         if (!by_adapter) {

@@ -20,6 +20,12 @@ FORMS = {
     "many_72": (520, 72, 264, 4, 72),
     "many_short_runs": (2100, 72, 136, 700, 16),
     "plain": (2307, 2056, 4104, 7, 16),
+    # contractions that several blocks share
+    "one_shared": (1, 4096, 264, 3, 16),
+    "few_shared": (40, 4104, 264, 3, 40),
+    "hundred_shared": (100, 7168, 136, 30, 64),
+    "many_shared": (300, 7168, 520, 3, 16),
+    "many_64_shared": (520, 4096, 264, 4, 64),
 }
 
 
@@ -50,3 +56,30 @@ def test_low_at_the_end_of_fp32(case, order):
     y, delta = plain(d)
     assert bool(torch.isfinite(delta).all())
     assert_within(got, y + delta, 2.0 ** -17 * delta.abs(), U16)
+
+
+@pytest.mark.parametrize("case", FORMS)
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_low_not_finite(case, value):
+    """An infinite low gives infinities of B's sign and NaN where B is zero; a NaN gives NaN."""
+    d = zeros(case, "any", 2)
+    F = FORMS[case][2]
+    d["s"][0] = value
+    d["a"][:, :, 0] = 1
+    d["b"][:] = (torch.arange(F, device="cuda") % 3 - 1).bfloat16().view(1, F, 1)
+    y, delta = plain(d)
+    assert_within(call(d), y + delta, 0.0)
+
+
+@pytest.mark.parametrize("case", FORMS)
+def test_the_scale_is_of_the_whole_sum(case):
+    """A x whose terms cancel over the contraction: times the scale they would be infinite, their sum is not."""
+    d = zeros(case, "any", 3)
+    K = FORMS[case][1]
+    d["x"][:, K - 1] = 1
+    d["s"][:] = 1e37
+    d["a"][:, :, 0], d["a"][:, :, K - 1] = 100, -99
+    d["b"][:, :, 0] = 2.0 ** -9
+    y, delta = plain(d)
+    assert bool(torch.isfinite(delta).all()) and bool((delta > 0).any())
+    assert_within(call(d), y + delta, 2.0 ** -17 * delta.abs(), U16)
