@@ -556,8 +556,9 @@ EP_API size_t ep_adapter_workspace_size(const ep_adapter_shape* shape);
  *   [0, L): EP_DEVERR_BAD_ADAPTER, treated as none). a, b, scales may be NULL with L = 0.
  *   workspace dev, >= ep_adapter_workspace_size bytes, 16-byte aligned
  * fp32 accumulation, A_i x[t] is kept in fp32, one bf16 rounding of the sum; with many rows
- * A_i x[t] may meet B_i as the sum of two bf16 values, which leaves up to 2^-17 of it. Values of
- * one adapter never reach another adapter's rows. EP_DEVERR_TIMEOUT as above. */
+ * A_i x[t] may meet B_i as the sum of two bf16 values, which leaves up to 2^-17 of it, and an
+ * infinite value of B_i may then give NaN in place of an infinity. Values of one adapter never
+ * reach another adapter's rows. EP_DEVERR_TIMEOUT as above. */
 EP_API ep_status ep_adapter_gemm(const ep_adapter_shape* shape, const void* x, const void* w,
                                  const void* a, const void* b, const float* scales,
                                  const int64_t* adapter_idx, void* y, void* workspace,

@@ -83,3 +83,31 @@ def test_the_scale_is_of_the_whole_sum(case):
     y, delta = plain(d)
     assert bool(torch.isfinite(delta).all()) and bool((delta > 0).any())
     assert_within(call(d), y + delta, 2.0 ** -17 * delta.abs(), U16)
+
+
+@pytest.mark.parametrize("case", FORMS)
+@pytest.mark.parametrize("order", ["any", "sorted"])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_b_not_finite(case, order, value):
+    """An infinite value of B gives infinities of low's sign, NaN where low is zero, and leaves the features
+    beside it alone."""
+    d = zeros(case, order, 4)
+    T, K, F, L, r = FORMS[case]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    lows = torch.tensor([1.0, -2.0, 1.00390625, -1.01171875, 0.0, 1.0048828125, -3.0048828125], device="cuda")
+    d["x"][:, 0] = 1
+    d["x"][:, 1] = torch.randint(0, 7, (T,), generator=g, device="cuda").bfloat16()
+    d["x"][:, 0] = lows[d["x"][:, 1].long()].bfloat16()
+    d["x"][:, 1] = 0
+    d["x"][:, 2] = (lows[torch.randint(0, 7, (T,), generator=g, device="cuda")] * 2.0 ** -11).bfloat16()
+    d["a"][:, r - 1, 0], d["a"][:, r - 1, 2], d["a"][:, 0, 0] = 1, 1, 1
+    d["b"][:, :, 0] = 1                                     # every feature: low of the first rank
+    d["b"][0, 5, r - 1], d["b"][L - 1, F - 1, r - 1], d["b"][L // 2, 70, 0] = value, value, value
+    y, delta = plain(d)
+    _, mdelta = plain(d, absolute=True)
+    got, slack = call(d), 2.0 ** -17 * torch.nan_to_num(mdelta, posinf=0.0)
+    if case.startswith("many"):          # two terms of low: not finite, but NaN as well as an infinity
+        bad = ~torch.isfinite(delta)
+        assert torch.equal(~torch.isfinite(got), bad)
+        got, delta = torch.where(bad, 0, got), torch.where(bad, 0, delta)
+    assert_within(got, y + delta, slack, U16)
