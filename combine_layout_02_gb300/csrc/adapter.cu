@@ -141,6 +141,9 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapter_low_kernel(AdapterA
         pdl_trigger();
     }
     if (SORTED && copy_block(a, warp, lane)) return;
+    if (!SORTED && blockIdx.y == 0 && blockIdx.z == 0)
+        for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < a.T; t += (int64_t)gridDim.x * blockDim.x)
+            adapter_of(a, t, true);
     if (warp == 0) {
         int adapter = -1, row = -1;
         if (SORTED) {
@@ -148,8 +151,6 @@ __global__ void __launch_bounds__(kLowWarps * 32, 2) adapter_low_kernel(AdapterA
             adapter = find_rows(a, lane, begin, end);
             if (adapter >= 0 && begin + lane < end) row = a.order[begin + lane];
         } else {
-            if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-                for (int t = lane; t < a.T; t += 32) adapter_of(a, t, true);
             const int slots = a.slots, t0 = (int)blockIdx.x / slots * kLowRows, slot = (int)blockIdx.x % slots;
             const int id = t0 + lane < a.T ? adapter_of(a, t0 + lane, false) : -1;
             const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
@@ -228,7 +229,10 @@ cudaError_t launch_low(const AdapterArgs& g, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     const unsigned copies = SORTED && g.sorted_x != nullptr ? (unsigned)ceil_div(g.T, kLowWarps) : 0u;
-    const unsigned blocks = SORTED ? g.copy_from + copies : g.L > 0 ? (unsigned)low_blocks(g.T, g.L, false) : 1u;
+    // Without adapters the ids are only looked at: a thread for each.
+    const unsigned blocks = SORTED ? g.copy_from + copies
+                            : g.L > 0 ? (unsigned)low_blocks(g.T, g.L, false)
+                                      : (unsigned)ceil_div(g.T, kLowWarps * 32);
     const unsigned ranks = NT < 8 ? (unsigned)ceil_div(g.r, NT * 8) : 1u;
     return launch_pdl(adapter_low_kernel<NT, SORTED>, dim3(blocks, (unsigned)g.parts, ranks), dim3(kLowWarps * 32), smem, stream, g);
 }

@@ -3,7 +3,8 @@ by warp-level products of low's two bf16 terms, and many rows by fp32 multiply-a
 import pytest
 import torch
 
-from rows_util import U16, assert_within
+import combine_layout_02_gb300 as ep
+from rows_util import U16, assert_within, integers
 from test_gpu_adapter import call, ids_of, plain
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +112,19 @@ def test_b_not_finite(case, order, value):
         assert torch.equal(~torch.isfinite(got), bad)
         got, delta = torch.where(bad, 0, got), torch.where(bad, 0, delta)
     assert_within(got, y + delta, slack, U16)
+
+
+@pytest.mark.parametrize("T", [1, 32, 128, 129, 257, 70001])
+def test_ids_without_any_adapter(T):
+    """L = 0: the projection alone, every id but -1 flagged wherever it stands."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, w = integers(g, T, 64), integers(g, 72, 64)
+    d = dict(x=x, w=w, a=None, b=None, s=None, ids=torch.full((T,), -1, device="cuda"))
+    want = (x.double() @ w.double().t()).float().bfloat16()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert torch.equal(call(d, err=err), want) and int(err.item()) == 0
+    for at in sorted({0, T // 2, T - 1}):
+        d["ids"].fill_(-1)
+        d["ids"][at] = 0
+        err.zero_()
+        assert torch.equal(call(d, err=err), want) and int(err.item()) == ep.EP_DEVERR_BAD_ADAPTER
