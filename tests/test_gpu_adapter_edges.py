@@ -4,8 +4,8 @@ import pytest
 import torch
 
 import combine_layout_02_gb300 as ep
-from rows_util import U16, assert_within, integers
-from test_gpu_adapter import call, ids_of, plain
+from rows_util import U16, U32, assert_within, integers, sum_bound
+from test_gpu_adapter import call, ids_of, make, normal, plain
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,23 @@ def test_ids_without_any_adapter(T):
         d["ids"][at] = 0
         err.zero_()
         assert torch.equal(call(d, err=err), want) and int(err.item()) == ep.EP_DEVERR_BAD_ADAPTER
+
+
+# many rows of a short contraction, where what two bf16 terms leave of low shows beside the sums' bounds
+SHORT = [(300, 8, 264, 3, 16), (700, 8, 264, 2, 64), (9001, 8, 136, 5, 8), (1000, 16, 520, 6, 24), (600, 24, 136, 300, 72),
+         (2100, 32, 384, 40, 256), (513, 40, 776, 2, 32)]
+
+
+@pytest.mark.parametrize("case", SHORT)
+@pytest.mark.parametrize("order", ["any", "sorted", "one"])
+def test_short_contractions(case, order):
+    T, K, F, L, r = case
+    d = make(case, order, 7, normal)
+    (y, delta), (my, mdelta) = plain(d), plain(d, absolute=True)
+    # as for longer ones (K products; the adapter's K products, scale and r products), and of low * B the part that
+    # low's two terms leave: of a low in [1, 2) the first leaves less than 2^-8, whose unit in bf16 is 2^-16 or
+    # smaller, and the second half a unit of that
+    slack = sum_bound(K + 1, my, 2 * U32) + sum_bound(K + r + 3, mdelta, 2 * U32) + 2.0 ** -17 * mdelta
+    got = call(d)
+    assert_within(got, y + delta, slack, U16)
+    assert torch.equal(got, call(d))
