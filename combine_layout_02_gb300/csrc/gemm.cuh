@@ -199,8 +199,13 @@ __device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, vola
     if (mbar_try_at(bar, parity)) return true;
     return mbar_wait_slow(bar, parity, dead, a.err, a.wait_ns);
 }
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* dead, const GemmArgs& a) {
-    return mbar_wait_at(smem_addr(bar), parity, dead, a);
+// `depth`: contracted values whose products are waited for too, each given kValueNs (a step of 64 takes a
+// microsecond or less). 2^30 rows of one expert, 8 x 8 features: 3.9 s for the one tile of their wgrad.
+constexpr uint64_t kValueNs = 64;
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* dead, const GemmArgs& a,
+                                          int64_t depth = 0) {
+    if (mbar_try_at(smem_addr(bar), parity)) return true;
+    return mbar_wait_slow(smem_addr(bar), parity, dead, a.err, a.wait_ns + (depth > 0 ? (uint64_t)depth * kValueNs : 0));
 }
 
 // True in one lane of the (converged) warp.
@@ -622,13 +627,17 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         TileWalk<D> walk(a);
         Tile t;
         uint32_t tails = 0;
+        int64_t rows = 0, pending = 0;          // of the tiles since the last tail's, and up to that one's
         bool ok = true;
         const uint32_t bar = peer_addr(smem_addr(&full[ring_stages]), 0), at = smem_addr(smem) + ring_stages * stage_bytes;
         for (int i = first; ok && walk.at(i, t); i += step) {
             const int depth = t.end - t.begin, left = depth > 0 ? depth % kBK : 0;
+            rows += max(depth, 0);
             if (left == 0) continue;
             if (!(ok = depth <= a.loads)) break;
-            if (!(ok = mbar_wait(&empty[ring_stages], (tails & 1) ^ 1, &dead, a))) break;
+            if (!(ok = mbar_wait(&empty[ring_stages], (tails & 1) ^ 1, &dead, a, pending))) break;
+            pending = rows;
+            rows = 0;
             ++tails;
             if (elect_one()) {
                 const int half = t.n / 2, boxes = (half + 63) / 64;
@@ -696,7 +705,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             const int rows = min(t.n, t.end - t.n0);
             if (D != kWgrad) extra.prepare(s_extra, smem + a.stages * stage_bytes, t.n0, rows);
             if (some) {
-                if (!epilogue_all<32 * kTileWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a))) break;
+                if (!epilogue_all<32 * kTileWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a, D == kWgrad ? t.end - t.begin : a.C))) break;
                 tc_fence_after();
             }
             const int m = t.m0 + (int)rank * kBM + quarter * 32 + lane;
@@ -939,7 +948,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     bool ok = has;
     if (has && warp >= 2) {
         if (D != kWgrad) extra.ahead(s_extra, t.n0 + lo, hi - lo, m, half);
-        ok = epilogue_all<256>(mbar_wait(&done, 0, &dead, a));
+        ok = epilogue_all<256>(mbar_wait(&done, 0, &dead, a, (kb1 - kb0) * kBK));
         tc_fence_after();
     }
     if (Extra::kFollows && warp >= 2) pdl_wait();

@@ -500,8 +500,9 @@ EP_API ep_status ep_unsort_rows_backward(const ep_shape* shape, const void* dout
  * [expert_prefix[e], expert_prefix[e+1]). Values outside [0, num_rows] are clipped and
  * flagged (EP_DEVERR_RECV_OVERFLOW). Rows of no expert are neither read nor written.
  * bf16 operands, fp32 accumulation, one bf16 rounding; every pointer 16-byte aligned;
- * outputs must not overlap inputs. An operand that has not arrived after 2 s sets
- * EP_DEVERR_TIMEOUT and its tile is not written. */
+ * outputs must not overlap inputs. An operand that has not arrived after 2 s (and 64 ns more for
+ * each contracted value that is worked on meanwhile) sets EP_DEVERR_TIMEOUT and its tile is not
+ * written. */
 typedef struct ep_gemm_shape {
     int32_t num_rows;
     int32_t num_experts;

@@ -62,3 +62,32 @@ def test_tiles_without_their_operands_are_not_written(case):
     assert flags == 0 and torch.equal(out, want)
     out, flags = run(lambda out, la: CALLS[product](sh, a, b, prefix, out, la), shape)
     assert flags == 0 and torch.equal(out, want)
+
+
+# One tile's products take longer than the limit of a wait, but nothing is missing: rows of one expert
+# beside many empty ones (pairs), of one expert (a cluster), with and without a tail. (The limit is first
+# looked at after many tries, about 0.1 s.)
+LONG = [([0] * 30 + [64_000_000] + [0] * 41, 8, 8), ([0] * 30 + [60_000_037, 1_000_001] + [0] * 41, 16, 8),
+        ([400_000_001], 8, 8)]
+
+
+@pytest.mark.parametrize("counts,K,F", LONG)
+def test_long_products_are_not_given_up(counts, K, F):
+    rows, E = sum(counts), len(counts)
+    x = torch.ones(rows, K, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros(rows, F, dtype=torch.bfloat16, device="cuda")
+    dy[::9973] = 1
+    prefix = torch.tensor([0] + counts).cumsum(0).int().cuda()
+    want = torch.stack([torch.full((F, K), float(dy[a:b, 0].float().sum()), device="cuda")
+                        for a, b in zip(prefix.tolist()[:-1], prefix.tolist()[1:])]).bfloat16()
+    sh = ep.ep_gemm_shape(rows, E, K, F)
+    start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+
+    def call(out, launch):
+        start.record()
+        ep.ep_selftest_gemm_timeout(sh, WGRAD, dy, x, prefix, out, 1 << 30, 1, launch)
+        stop.record()
+
+    out, flags = run(call, (E, F, K))
+    assert start.elapsed_time(stop) > 120                 # ms: longer than it takes to give up
+    assert flags == 0 and torch.equal(out, want)
