@@ -24,8 +24,10 @@ namespace ep {
 namespace {
 
 constexpr int kSortWarps = 8;                  // warps per block of the count / place kernels
-// Up to here one block sorts everything, in less time than three kernels (64 experts, us: 4096 entries 8.2 and
-// 8.3, 8192 12.0 and 8.6; 17: 5000 7.2 and 7.5; 256: 5000 10.6 and 11.3, 8192 14.0 and 11.5).
+// Up to here one block sorts everything, in less time than three kernels or hardly more, 1 to 8192 experts (us, one
+// block and three: 8 experts, 5120 entries 5.9 and 6.3; 64, 4096 8.0 and 7.7, 5120 9.0 and 7.7, 8192 12.0 and 8.6; 256,
+// 5120 10.4 and 10.6, 8192 14.0 and 11.5; 1024, 5120 11.9 and 24; 4096, 5120 27 and 43; 8192, where the table has
+// room for one warp, 2048 33 and 58, 5120 71 and 65).
 constexpr int kSmallEntries = 5120;
 constexpr int kSmallThreads = 1024;
 constexpr int kTableInts = 48 * 1024 / 4;      // per-warp counts of a block, in shared memory

@@ -29,11 +29,14 @@ __all__ = ["ExpertSort", "sort_rows", "unsort_rows", "expert_product", "adapter_
 
 def _check(what: str, t: torch.Tensor, dtype: torch.dtype, *shape: Optional[int]) -> None:
     """t has to be a tensor of this type and shape (None: any length)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise ValueError(f"{what} has to be a tensor of {dtype}, not {getattr(t, 'dtype', type(t))}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    has = t.shape
+    if has == shape:
+        return
+    if len(has) != len(shape) or any(n is not None and n != m for n, m in zip(shape, has)):
         wants = ", ".join("any" if n is None else str(n) for n in shape)
-        raise ValueError(f"{what} has to be [{wants}], not {list(t.shape)}")
+        raise ValueError(f"{what} has to be [{wants}], not {list(has)}")
 
 
 def _check_err(err: Optional[torch.Tensor]) -> None:
@@ -157,15 +160,9 @@ class _ExpertProduct(torch.autograd.Function):
         return dx, dw, None, None
 
 
-class _AdapterProjection(torch.autograd.Function):
+class _NoGradient(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, a, b, scales, adapter_idx, err):
-        (T, K), F = x.shape, weight.shape[0]
-        L, r = (0, 8) if a is None else (a.shape[0], a.shape[1])
-        shape = ep_adapter_shape(T, K, F, L, r)
-        workspace = torch.empty(max(16, ep_adapter_workspace_size(shape)), dtype=torch.uint8, device=x.device)
-        y = torch.empty((T, F), dtype=x.dtype, device=x.device)
-        ep_adapter_gemm(shape, x, weight, a, b, scales, adapter_idx, y, workspace, make_launch(error_flags=err))
+    def forward(ctx, y, *inputs):
         return y
 
     @staticmethod
@@ -208,6 +205,7 @@ def adapter_projection(x: torch.Tensor, weight: torch.Tensor, a: Optional[torch.
     _check("x", x, torch.bfloat16, None, None)
     _check("weight", weight, torch.bfloat16, None, x.shape[1])
     (T, K), F = x.shape, weight.shape[0]
+    L, r = 0, 8
     if a is not None:
         _check("a", a, torch.bfloat16, None, None, K)
         L, r = a.shape[0], a.shape[1]
@@ -215,7 +213,16 @@ def adapter_projection(x: torch.Tensor, weight: torch.Tensor, a: Optional[torch.
         _check("scales", scales, torch.float32, L)
     _check("adapter_idx", adapter_idx, torch.int64, T)
     _check_err(err)
-    return _AdapterProjection.apply(x, weight, a, b, scales, adapter_idx, _error_word(err, x.device))
+    shape = ep_adapter_shape(T, K, F, L, r)
+    workspace = torch.empty(max(16, ep_adapter_workspace_size(shape)), dtype=torch.uint8, device=x.device)
+    y = torch.empty((T, F), dtype=x.dtype, device=x.device)
+    ep_adapter_gemm(shape, x, weight, a, b, scales, adapter_idx, y, workspace,
+                    make_launch(error_flags=_error_word(err, x.device)))
+    if torch.is_grad_enabled():
+        inputs = [t for t in (x, weight, a, b, scales) if t is not None and t.requires_grad]
+        if inputs:
+            return _NoGradient.apply(y, *inputs)
+    return y
 
 
 class _Dispatch(torch.autograd.Function):
