@@ -37,6 +37,9 @@ __all__ = [
     "ep_sort", "ep_gemm_shape", "ep_adapter_shape", "ep_sort_workspace_size", "ep_sort_layout",
     "ep_sort_rows", "ep_unsort_rows", "ep_unsort_rows_backward", "ep_expert_gemm",
     "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad", "ep_adapter_workspace_size", "ep_adapter_gemm",
+    "ep_checkpoint", "make_checkpoint", "ep_checkpoint_rows", "ep_restore_rows",
+    "ep_wgrad_checkpoint_workspace_size", "ep_expert_gemm_wgrad_checkpoint",
+    "EP_CHECKPOINT_GROUP", "EP_ACT_SILU", "EP_ACT_GELU_TANH", "ep_expert_gated", "ep_expert_gated_dgrad",
 ]
 
 EP_OK, EP_ERR_INVALID_ARG, EP_ERR_CUDA, EP_ERR_UNSUPPORTED = 0, 1, 2, 3
@@ -51,6 +54,8 @@ EP_MAX_RANKS = 64
 EP_MAX_TOPK = 32
 EP_EXPERT_MAJOR_MAX_EXPERTS = 4096
 EP_ADAPTER_MAX_RANK = 256
+EP_CHECKPOINT_GROUP = 16
+EP_ACT_SILU, EP_ACT_GELU_TANH = 0, 1
 
 # Every function include/ep.h declares (checked by the ABI test).
 EXPORTED_SYMBOLS = (
@@ -63,6 +68,8 @@ EXPORTED_SYMBOLS = (
     "ep_sort_workspace_size", "ep_sort_layout", "ep_sort_rows", "ep_unsort_rows",
     "ep_unsort_rows_backward", "ep_expert_gemm", "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad",
     "ep_adapter_workspace_size", "ep_adapter_gemm",
+    "ep_checkpoint_rows", "ep_restore_rows", "ep_wgrad_checkpoint_workspace_size",
+    "ep_expert_gemm_wgrad_checkpoint", "ep_expert_gated", "ep_expert_gated_dgrad",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -142,6 +149,10 @@ class ep_adapter_shape(ctypes.Structure):
                 ("num_adapters", _I32), ("rank", _I32)]
 
 
+class ep_checkpoint(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("values", _P), ("scales", _P)]
+
+
 _lib = None
 
 
@@ -204,9 +215,19 @@ def lib():
         L.ep_adapter_workspace_size.restype = ctypes.c_size_t
         L.ep_adapter_gemm.argtypes = [S(ep_adapter_shape), _P, _P, _P, _P, _P, _P, _P, _P,
                                       ctypes.c_size_t, S(ep_launch)]
+        L.ep_checkpoint_rows.argtypes = [_I32, _I32, _P, S(ep_checkpoint), S(ep_launch)]
+        L.ep_restore_rows.argtypes = [_I32, _I32, S(ep_checkpoint), _P, S(ep_launch)]
+        L.ep_wgrad_checkpoint_workspace_size.argtypes = [S(ep_gemm_shape)]
+        L.ep_wgrad_checkpoint_workspace_size.restype = ctypes.c_size_t
+        L.ep_expert_gemm_wgrad_checkpoint.argtypes = [S(ep_gemm_shape), _P, S(ep_checkpoint), _P, _P, _P,
+                                                      ctypes.c_size_t, S(ep_launch)]
+        L.ep_expert_gated.argtypes = [S(ep_gemm_shape), _P, _P, _P, _I32, _P, S(ep_checkpoint), S(ep_launch)]
+        L.ep_expert_gated_dgrad.argtypes = [S(ep_gemm_shape), _P, _P, _P, _I32, S(ep_checkpoint), _P, _P,
+                                            S(ep_launch)]
         for name in ("ep_sort_layout", "ep_sort_rows", "ep_unsort_rows", "ep_unsort_rows_backward",
                      "ep_expert_gemm", "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad",
-                     "ep_adapter_gemm"):
+                     "ep_adapter_gemm", "ep_checkpoint_rows", "ep_restore_rows",
+                     "ep_expert_gemm_wgrad_checkpoint", "ep_expert_gated", "ep_expert_gated_dgrad"):
             getattr(L, name).restype = _I32
         for name in ("ep_get_layout", "ep_get_layout_static_scratch", "ep_dispatch", "ep_combine",
                      "ep_dispatch_expert_major", "ep_combine_expert_major", "ep_ll_dispatch",
@@ -446,6 +467,54 @@ def ep_adapter_gemm(shape: ep_adapter_shape, x, w, a, b, scales, adapter_idx, y,
                                0 if workspace is None else workspace.numel() * workspace.element_size(),
                                ctypes.byref(_launch(launch)))
     _check("ep_adapter_gemm", st)
+
+
+def make_checkpoint(values, scales=None) -> ep_checkpoint:
+    """Rows kept for a backward pass: e4m3 bytes with their scales, or bf16 without."""
+    return ep_checkpoint(EP_BF16 if scales is None else EP_FP8_E4M3, _ptr(values), _ptr(scales))
+
+
+def _checkpoint(c: Optional[ep_checkpoint]):
+    return None if c is None else ctypes.byref(c)
+
+
+def ep_checkpoint_rows(num_rows: int, features: int, x, out: ep_checkpoint,
+                       launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_checkpoint_rows(num_rows, features, _ptr(x), _checkpoint(out), ctypes.byref(_launch(launch)))
+    _check("ep_checkpoint_rows", st)
+
+
+def ep_restore_rows(num_rows: int, features: int, checkpoint: ep_checkpoint, x,
+                    launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_restore_rows(num_rows, features, _checkpoint(checkpoint), _ptr(x),
+                               ctypes.byref(_launch(launch)))
+    _check("ep_restore_rows", st)
+
+
+def ep_wgrad_checkpoint_workspace_size(shape: ep_gemm_shape) -> int:
+    return int(lib().ep_wgrad_checkpoint_workspace_size(ctypes.byref(shape)))
+
+
+def ep_expert_gemm_wgrad_checkpoint(shape: ep_gemm_shape, dy, x: ep_checkpoint, expert_prefix, dw, workspace,
+                                    launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_expert_gemm_wgrad_checkpoint(
+        ctypes.byref(shape), _ptr(dy), _checkpoint(x), _ptr(expert_prefix), _ptr(dw), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), ctypes.byref(_launch(launch)))
+    _check("ep_expert_gemm_wgrad_checkpoint", st)
+
+
+def ep_expert_gated(shape: ep_gemm_shape, x, w, expert_prefix, activation: int, h,
+                    keep: Optional[ep_checkpoint] = None, launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_expert_gated(ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(expert_prefix), activation, _ptr(h),
+                               _checkpoint(keep), ctypes.byref(_launch(launch)))
+    _check("ep_expert_gated", st)
+
+
+def ep_expert_gated_dgrad(shape: ep_gemm_shape, dy, w, expert_prefix, activation: int, kept: ep_checkpoint, dgu, h,
+                          launch: Optional[ep_launch] = None) -> None:
+    st = lib().ep_expert_gated_dgrad(ctypes.byref(shape), _ptr(dy), _ptr(w), _ptr(expert_prefix), activation,
+                                     _checkpoint(kept), _ptr(dgu), _ptr(h), ctypes.byref(_launch(launch)))
+    _check("ep_expert_gated_dgrad", st)
 
 
 def ep_read_recv_counts_sync(shape: ep_shape, handle: ep_handle, stream=None) -> list:

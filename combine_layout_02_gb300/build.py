@@ -18,8 +18,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libep.so")
 SOURCES = ["ep_api.cu", "layout.cu", "layout_static.cu", "dispatch.cu", "combine.cu", "ll.cu",
-           "expert_major.cu", "sort.cu", "expert_gemm.cu", "adapter.cu"]
-HEADERS = ["ep_internal.cuh", "rowops.cuh", "gemm.cuh", "sort.cuh"]
+           "expert_major.cu", "sort.cu", "expert_gemm.cu", "adapter.cu",
+           "checkpoint.cu", "gated.cu"]
+HEADERS = ["ep_internal.cuh", "rowops.cuh", "gemm.cuh", "sort.cuh", "checkpoint.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-Werror", "all-warnings"]

@@ -273,6 +273,7 @@ AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
 
 // The epilogue's part: y += B_i low. A row only ever meets its own adapter's values.
 struct AdapterSide {
+    static constexpr bool kStores = false, kPairs = false;
     const __nv_bfloat16* b;
     const float* low;
     const float* scales;

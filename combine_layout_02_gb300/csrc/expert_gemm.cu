@@ -7,6 +7,7 @@
 //   forward  W_e, out_features, K-major      x, rows, K-major             in_features
 //   dgrad    W_e, in_features, MN-major      dy, rows, K-major            out_features
 //   wgrad    dy, out_features, MN-major      x, in_features, MN-major     the expert's rows
+#include "checkpoint.cuh"
 #include "gemm.cuh"
 
 namespace ep {
@@ -38,17 +39,28 @@ bool bind_context() {
 }
 }  // namespace
 
-ep_status encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint32_t* box) {
+ep_status check_gemm_shape(const ep_gemm_shape* sh) {
+    if (sh == nullptr) return EP_ERR_INVALID_ARG;
+    if (sh->num_rows < 0 || sh->num_experts < 1 || !features_ok(sh->in_features) || !features_ok(sh->out_features))
+        return EP_ERR_INVALID_ARG;
+    if (sh->num_experts > EP_MAX_EXPERTS || sh->in_features > EP_GEMM_MAX_FEATURES ||
+        sh->out_features > EP_GEMM_MAX_FEATURES || sh->num_rows > 1 << 30)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+ep_status encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint32_t* box,
+                     const uint64_t* given) {
     static const EncodeFn fn = reinterpret_cast<EncodeFn>(driver_function("cuTensorMapEncodeTiled"));
     if (fn == nullptr || !bind_context()) return cuda_fail(cudaErrorNotSupported);
-    cuuint64_t d[3], strides[2];
-    cuuint32_t b[3], ones[3] = {1, 1, 1};
+    cuuint64_t d[5], strides[4];
+    cuuint32_t b[5], ones[5] = {1, 1, 1, 1, 1};
     uint64_t stride = 2;
     for (int i = 0; i < rank; ++i) {
         d[i] = dims[i];
         b[i] = box[i];
         stride *= dims[i];
-        if (i + 1 < rank) strides[i] = stride;
+        if (i + 1 < rank) strides[i] = given != nullptr ? given[i] : stride;
     }
     const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, strides, b,
                           ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -61,12 +73,9 @@ namespace {
 
 ep_status check_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* other, bool other_rows,
                      const int32_t* prefix, const void* out, bool out_rows, const ep_launch* launch) {
-    if (sh == nullptr || launch == nullptr) return EP_ERR_INVALID_ARG;
-    if (sh->num_rows < 0 || sh->num_experts < 1 || !features_ok(sh->in_features) || !features_ok(sh->out_features))
-        return EP_ERR_INVALID_ARG;
-    if (sh->num_experts > EP_MAX_EXPERTS || sh->in_features > EP_GEMM_MAX_FEATURES ||
-        sh->out_features > EP_GEMM_MAX_FEATURES || sh->num_rows > 1 << 30)
-        return EP_ERR_UNSUPPORTED;
+    if (launch == nullptr) return EP_ERR_INVALID_ARG;
+    const ep_status st = check_gemm_shape(sh);
+    if (st != EP_OK) return st;
     const bool rows = sh->num_rows > 0;
     if (prefix == nullptr || (rows && rows_a == nullptr)) return EP_ERR_INVALID_ARG;
     if ((rows || !other_rows) && other == nullptr) return EP_ERR_INVALID_ARG;
@@ -152,6 +161,30 @@ ep_status ep_expert_gemm_dgrad(const ep_gemm_shape* sh, const void* dy, const vo
 ep_status ep_expert_gemm_wgrad(const ep_gemm_shape* sh, const void* dy, const void* x, const int32_t* expert_prefix,
                                void* dw, const ep_launch* launch) {
     return ep::run_gemm<ep::kWgrad>(sh, dy, x, expert_prefix, dw, launch);
+}
+
+size_t ep_wgrad_checkpoint_workspace_size(const ep_gemm_shape* sh) {
+    if (ep::check_gemm_shape(sh) != EP_OK) return 0;
+    const size_t bytes = (size_t)sh->num_rows * sh->in_features * 2;
+    return bytes > 16 ? bytes : 16;
+}
+
+ep_status ep_expert_gemm_wgrad_checkpoint(const ep_gemm_shape* sh, const void* dy, const ep_checkpoint* x,
+                                          const int32_t* expert_prefix, void* dw, void* workspace, size_t workspace_bytes,
+                                          const ep_launch* launch) {
+    using namespace ep;
+    ep_status st = check_gemm(sh, dy, workspace, true, expert_prefix, dw, false, launch);
+    if (st != EP_OK) return st;
+    if ((st = check_checkpoint(x, sh->num_rows > 0, false)) != EP_OK) return st;
+    if (workspace == nullptr || workspace_bytes < ep_wgrad_checkpoint_workspace_size(sh)) return EP_ERR_INVALID_ARG;
+    ep_launch inner = *launch;          // the rows wait for the event, the product is recorded
+    inner.record_event = nullptr;
+    if ((st = begin_call(&inner)) != EP_OK) return st;
+    const cudaError_t e = launch_restore(sh->num_rows, sh->in_features, x->values, x->scales, workspace, launch->stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    inner = *launch;
+    inner.wait_event = nullptr;
+    return run_gemm<kWgrad>(sh, dy, workspace, expert_prefix, dw, &inner);
 }
 
 ep_status ep_selftest_gemm_timeout(const ep_gemm_shape* sh, int32_t product, const void* rows, const void* other,

@@ -33,8 +33,10 @@ struct GemmMaps {
 
 inline bool features_ok(int f) { return f >= 8 && f % 8 == 0; }
 
-// Encodes a tiled bf16 map of up to three dimensions (innermost first), 128-byte swizzle.
-ep_status encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint32_t* box);
+// Encodes a tiled bf16 map of up to five dimensions (innermost first), 128-byte swizzle. `strides`: bytes from
+// one index of dimension i + 1 to the next; without them the dimensions follow one another.
+ep_status encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint32_t* box,
+                     const uint64_t* strides = nullptr);
 
 // ------------------------------------------------------------------ expert rows
 
@@ -281,6 +283,14 @@ __device__ __forceinline__ void tma_load2_3d(uint32_t dst, const CUtensorMap* ma
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load2_5d(uint32_t dst, const CUtensorMap* map, int x, int group, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %5, %5, %3, %4}], [%6];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(group), "r"(z), "r"(0), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -314,6 +324,12 @@ __device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap* 
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_at(uint32_t dst, const CUtensorMap* map, int x, int group, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %5, %5, %3, %4}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(group), "r"(z), "r"(0), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
@@ -417,17 +433,8 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
     return t;
 }
-// Sums of 32 features x 8 rows in the layout of tmem_load_16x8 (lane 4g + c: rows 2c, 2c+1 of features
-// g, 8 + g in v[0], 16 + g, 24 + g in v[1]) -> bf16, lane 4g + c the eight features 8c .. 8c+7 of row
-// g: a transposition within 8 x 8 blocks and one within quads of lanes. A lane then stores 16
-// bytes, a warp 64 bytes of eight rows.
-__device__ __forceinline__ uint4 rows_of_features(const float (&v)[2][4], int c) {
-    uint32_t p[4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        p[2 * t] = transpose_8x8(pack_bf16x2(v[t][0], v[t][1]));
-        p[2 * t + 1] = transpose_8x8(pack_bf16x2(v[t][2], v[t][3]));
-    }
+// Within quads of lanes: lane c has word h of its own in p[h], and gets word c of lane h in place h.
+__device__ __forceinline__ uint4 transpose_quad(uint32_t (&p)[4], int c) {
 #pragma unroll
     for (int bit = 1; bit <= 2; bit *= 2)
 #pragma unroll
@@ -439,6 +446,19 @@ __device__ __forceinline__ uint4 rows_of_features(const float (&v)[2][4], int c)
             else p[h | bit] = got;
         }
     return make_uint4(p[0], p[1], p[2], p[3]);
+}
+// Sums of 32 features x 8 rows in the layout of tmem_load_16x8 (lane 4g + c: rows 2c, 2c+1 of features
+// g, 8 + g in v[0], 16 + g, 24 + g in v[1]) -> bf16, lane 4g + c the eight features 8c .. 8c+7 of row
+// g: a transposition within 8 x 8 blocks and one within quads of lanes. A lane then stores 16
+// bytes, a warp 64 bytes of eight rows.
+__device__ __forceinline__ uint4 rows_of_features(const float (&v)[2][4], int c) {
+    uint32_t p[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        p[2 * t] = transpose_8x8(pack_bf16x2(v[t][0], v[t][1]));
+        p[2 * t + 1] = transpose_8x8(pack_bf16x2(v[t][2], v[t][3]));
+    }
+    return transpose_quad(p, c);
 }
 
 // wgrad: a lane holds 64 consecutive columns of one row of dW; a warp stages its 32 rows x 64 columns
@@ -471,9 +491,12 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 //                       the products run. Both get a.beside bytes of shared memory
 //   gemm_split_kernel:  ahead for the CTA's rows while the products run (before that wait), then apply
 //                       for each kGroup of them: v[j] belongs to row row0 + c + j. Two halves of 128
-//                       threads take groups in turn
+//                       threads take groups in turn. kStores: store writes the group instead, v[0]
+//                       being row row0's
+// kPairs (forward): the M side is two projections of out_features each, eight rows of one and eight of the
+// other in turn (maps.a has five dimensions: in_features, 8, 2, out_features / 8, experts).
 struct NoExtra {
-    static constexpr bool kFollows = false;
+    static constexpr bool kFollows = false, kStores = false, kPairs = false;
     static constexpr int kFloats = 4, kGroup = 32;
     __device__ __forceinline__ bool reordered() const { return false; }
     __device__ __forceinline__ void prepare(float*, unsigned char*, int64_t, int) const {}
@@ -501,6 +524,7 @@ struct NoExtra {
     }
     __device__ __forceinline__ void ahead(float*, int64_t, int, int, int) const {}
     __device__ __forceinline__ void apply(float*, float (&)[32], int64_t, int, int, int, int) const {}
+    __device__ __forceinline__ void store(const float (&)[32], __nv_bfloat16*, int64_t, int, int, int, int) const {}
 };
 
 // The epilogue's THREADS: a barrier, and whether all of them have `mine` (the same answer to all, so
@@ -597,7 +621,9 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
                 if (elect_one()) {
                     mbar_expect_peer(bar, bytes);
                     if (warp == 0) {
-                        if (D == kForward) {
+                        if constexpr (Extra::kPairs) {
+                            tma_load2_5d(at, map, k0, m0 / 16, t.e, bar);
+                        } else if (D == kForward) {
                             tma_load2_3d(at, map, k0, m0, t.e, bar);
                         } else if (D == kDgrad) {
                             tma_load2_3d(at, map, m0, k0, t.e, bar);
@@ -897,7 +923,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                                                c < 2 ? t.m0 + c * 64 : t.n0 + (c - 2) * 64, t.begin + k0, left, a.num_rows, bar);
                 } else {
                     mbar_expect_at(bar, bytes);
-                    if (D == kForward) {
+                    if (Extra::kPairs) {
+                        tma_load_5d_at(sa, &maps.a, k0, t.m0 / 16, t.e, bar);
+                    } else if (D == kForward) {
                         tma_load_3d_at(sa, &maps.a, k0, t.m0, t.e, bar);
                     } else if (D == kDgrad) {
                         tma_load_3d_at(sa, &maps.a, t.m0, k0, t.e, bar);
@@ -960,7 +988,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 float v[G];
                 tmem_load(tmem + c + ((uint32_t)quarter << 21), v);
                 extra.apply(s_extra, v, t.n0, rows, c, m, half);
-                store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
+                if constexpr (Extra::kStores) extra.store(v, a.out, t.n0 + c, rows - c, m, a.M, lane);
+                else store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
             }
         }
     } else {
@@ -1011,7 +1040,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 }
                 const bool failed = isnan(v[0]) && !parts_complete(&s_complete, a.split);          // for all alike
                 extra.apply(s_extra, v, t.n0 + lo, hi - lo, c - lo, m, half);
-                if (!__any_sync(0xFFFFFFFFu, failed)) store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
+                if (__any_sync(0xFFFFFFFFu, failed)) continue;
+                if constexpr (Extra::kStores) extra.store(v, a.out, t.n0 + c, hi - c, m, a.M, lane);
+                else store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
             }
         }
         __syncwarp();

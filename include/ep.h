@@ -38,7 +38,7 @@
  *     write and set a bit of *launch->error_flags (if non-NULL) with atomicOr. The
  *     kernels never trap, every wait on an asynchronous copy or product has a time limit
  *     (EP_DEVERR_TIMEOUT), and only blocks of one cluster wait for one another
- *     (ep_expert_gemm* and ep_adapter_gemm, at cluster barriers).
+ *     (ep_expert_gemm*, ep_expert_gated* and ep_adapter_gemm, at cluster barriers).
  *   - Limits: 1 <= R <= 64; E % R == 0; 1 <= k <= 32; H % 128 == 0 and H >= 128;
  *     T >= 0; C >= 1; E <= 8192.
  */
@@ -528,6 +528,76 @@ EP_API ep_status ep_expert_gemm_dgrad(const ep_gemm_shape* shape, const void* dy
 EP_API ep_status ep_expert_gemm_wgrad(const ep_gemm_shape* shape, const void* dy, const void* x,
                                       const int32_t* expert_prefix, void* dw,
                                       const ep_launch* launch);
+
+/* ---------------------------------------------------------------- checkpoints in 8 bits */
+
+/* Rows of activations that a backward pass needs again, kept in 8 bits: e4m3 values with a power of
+ * two for each EP_CHECKPOINT_GROUP features of a row, the least 2^k (k >= -126) with
+ * amax <= 448 * 2^k (amax: the group's largest magnitude, NaN left out); q = e4m3(x / 2^k), to
+ * nearest even, and k + 127 in a byte. x comes back as q * 2^k: within 2^-4 of it relatively
+ * (2^-10 * 2^k absolutely where that is more), exact in bf16 but for magnitudes below 2^-133.
+ * NaN stays NaN; an infinity stays one, and what else its group has is held on that scale; above
+ * 1.9375 * 2^127 a value comes back as an infinity.
+ *   dtype   EP_FP8_E4M3, or EP_BF16 where a call says so: bf16 values, scales NULL
+ *   values  dev, 16-byte aligned: e4m3 [rows][features, padded with zeros to a multiple of
+ *           EP_CHECKPOINT_GROUP], bf16 [rows][features]
+ *   scales  dev uint8 [rows][padded features / EP_CHECKPOINT_GROUP] (bytes 1 to 254)
+ * A row of several parts (ep_expert_gated's two) has each part padded. */
+#define EP_CHECKPOINT_GROUP 16
+
+typedef struct ep_checkpoint {
+    int32_t dtype;
+    void* values;
+    uint8_t* scales;
+} ep_checkpoint;
+
+/* Rows into a checkpoint, and back. num_rows >= 0; features a multiple of 8, 8 to
+ * EP_GEMM_MAX_FEATURES; x dev [num_rows][features] bf16, 16-byte aligned; a checkpoint of dtype
+ * EP_FP8_E4M3. */
+EP_API ep_status ep_checkpoint_rows(int32_t num_rows, int32_t features, const void* x,
+                                    const ep_checkpoint* out, const ep_launch* launch);
+EP_API ep_status ep_restore_rows(int32_t num_rows, int32_t features, const ep_checkpoint* checkpoint,
+                                 void* x, const ep_launch* launch);
+
+/* ep_expert_gemm_wgrad with x as its checkpoint has it: dw[e] = sum over expert e's rows of
+ * dy[i] x~[i]^T. x: a checkpoint (EP_FP8_E4M3) of [num_rows][in_features]. workspace dev,
+ * >= ep_wgrad_checkpoint_workspace_size bytes, 16-byte aligned. */
+EP_API ep_status ep_expert_gemm_wgrad_checkpoint(const ep_gemm_shape* shape, const void* dy,
+                                                 const ep_checkpoint* x, const int32_t* expert_prefix,
+                                                 void* dw, void* workspace, size_t workspace_bytes,
+                                                 const ep_launch* launch);
+
+/* Bytes of dev scratch it needs (0 for a bad shape). */
+EP_API size_t ep_wgrad_checkpoint_workspace_size(const ep_gemm_shape* shape);
+
+/* ---------------------------------------------------------------- gated feed-forward block */
+
+typedef enum ep_activation { EP_ACT_SILU = 0, EP_ACT_GELU_TANH = 1 } ep_activation;
+
+/* Both projections of a gated feed-forward block, the activation and the product, for each row i of
+ * expert e (rules as for ep_expert_gemm, out_features = F):
+ *   g = Wg x[i], u = Wu x[i], h[i] = act(g) * u
+ *   EP_ACT_SILU       act(g) = g / (1 + exp(-g))
+ *   EP_ACT_GELU_TANH  act(g) = g / 2 * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3)))
+ *   x  dev [num_rows][in_features]
+ *   w  dev [E][2][F][in_features]: Wg, then Wu
+ *   h  dev [num_rows][F], from the fp32 sums, rounded once; NULL to leave out (with keep)
+ *   keep  nullable: g and u, rounded to bf16, for ep_expert_gated_dgrad: a checkpoint of rows of two
+ *         parts [num_rows][2][F], EP_BF16 or EP_FP8_E4M3 */
+EP_API ep_status ep_expert_gated(const ep_gemm_shape* shape, const void* x, const void* w,
+                                 const int32_t* expert_prefix, int32_t activation, void* h,
+                                 const ep_checkpoint* keep, const ep_launch* launch);
+
+/* Gradient of the block's down projection y[i] = Wd h[i] to g and u, with g and u as they were kept:
+ *   dh = Wd^T dy[i]  (fp32),  dgu[i] = (dh * u * act'(g), dh * act(g)),  h[i] = act(g) * u
+ * shape is the down projection's: in_features = F, out_features those of y.
+ *   dy dev [num_rows][out_features], w dev [E][out_features][F]
+ *   dgu dev [num_rows][2][F]: dy of the gate and up projections as one product of 2F features
+ *   h  dev [num_rows][F], what Wd's gradient wants; NULL to leave out */
+EP_API ep_status ep_expert_gated_dgrad(const ep_gemm_shape* shape, const void* dy, const void* w,
+                                       const int32_t* expert_prefix, int32_t activation,
+                                       const ep_checkpoint* kept, void* dgu, void* h,
+                                       const ep_launch* launch);
 
 /* ---------------------------------------------------------------- adapters */
 
