@@ -276,13 +276,9 @@ struct GatedBackFew : NoExtra {
 
 ep_status check_block(const ep_gemm_shape* sh, const void* rows_in, const void* w, const int32_t* prefix, int32_t act,
                       const ep_launch* launch) {
-    if (sh == nullptr || launch == nullptr) return EP_ERR_INVALID_ARG;
-    if (sh->num_rows < 0 || sh->num_experts < 1 || !features_ok(sh->in_features) || !features_ok(sh->out_features))
-        return EP_ERR_INVALID_ARG;
-    if (act != EP_ACT_SILU && act != EP_ACT_GELU_TANH) return EP_ERR_INVALID_ARG;
-    if (sh->num_experts > EP_MAX_EXPERTS || sh->in_features > EP_GEMM_MAX_FEATURES ||
-        sh->out_features > EP_GEMM_MAX_FEATURES || sh->num_rows > 1 << 30)
-        return EP_ERR_UNSUPPORTED;
+    if (launch == nullptr || (act != EP_ACT_SILU && act != EP_ACT_GELU_TANH)) return EP_ERR_INVALID_ARG;
+    const ep_status st = check_gemm_shape(sh);
+    if (st != EP_OK) return st;
     if (prefix == nullptr || ((uintptr_t)prefix & 3) != 0) return EP_ERR_INVALID_ARG;
     if (sh->num_rows > 0 && (rows_in == nullptr || w == nullptr)) return EP_ERR_INVALID_ARG;
     return (((uintptr_t)rows_in | (uintptr_t)w) & 15) != 0 ? EP_ERR_INVALID_ARG : EP_OK;

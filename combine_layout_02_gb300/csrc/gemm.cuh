@@ -32,6 +32,7 @@ struct GemmMaps {
 };
 
 inline bool features_ok(int f) { return f >= 8 && f % 8 == 0; }
+ep_status check_gemm_shape(const ep_gemm_shape* sh);
 
 // Encodes a tiled bf16 map of up to five dimensions (innermost first), 128-byte swizzle. `strides`: bytes from
 // one index of dimension i + 1 to the next; without them the dimensions follow one another.

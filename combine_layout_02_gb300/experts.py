@@ -1,6 +1,8 @@
 """What a model does with the rows between dispatch and combine, as PyTorch autograd functions over
 the C ABI: rows into expert order and back (``ep_sort_*`` / ``ep_unsort_*``), the experts' products
-(``ep_expert_gemm*``) and a shared projection with each row's own low-rank adapter
+(``ep_expert_gemm*``), the experts' gated feed-forward block in one function with the activations that its
+backward pass needs kept in bf16, in 8 bits or not at all (``ep_expert_gated*``,
+``ep_checkpoint_rows``), and a shared projection with each row's own low-rank adapter
 (``ep_adapter_gemm``); and ``MoELayer``, a layer that runs all of it together with a ``Buffer``.
 
 Like the rest of the package this module only allocates tensors and calls the library, on the
@@ -17,14 +19,16 @@ from typing import List, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (EP_BF16, ep_adapter_gemm, ep_adapter_shape, ep_adapter_workspace_size, ep_expert_gemm,
-               ep_expert_gemm_dgrad, ep_expert_gemm_wgrad, ep_gemm_shape, ep_read_error_flags_sync, ep_sort_layout, ep_sort_rows,
-               ep_unsort_rows, ep_unsort_rows_backward, make_launch, make_shape)
+from . import (EP_ACT_GELU_TANH, EP_ACT_SILU, EP_BF16, EP_CHECKPOINT_GROUP, ep_adapter_gemm, ep_adapter_shape,
+               ep_adapter_workspace_size, ep_checkpoint_rows, ep_expert_gated, ep_expert_gated_dgrad, ep_expert_gemm,
+               ep_expert_gemm_dgrad, ep_expert_gemm_wgrad, ep_expert_gemm_wgrad_checkpoint, ep_gemm_shape,
+               ep_read_error_flags_sync, ep_restore_rows, ep_sort_layout, ep_sort_rows, ep_unsort_rows,
+               ep_unsort_rows_backward, ep_wgrad_checkpoint_workspace_size, make_checkpoint, make_launch, make_shape)
 from .api import Buffer
 from .buffers import SortBuffers
 
-__all__ = ["ExpertSort", "sort_rows", "unsort_rows", "expert_product", "adapter_projection", "check_errors",
-           "MoELayer"]
+__all__ = ["ExpertSort", "sort_rows", "unsort_rows", "expert_product", "expert_feed_forward", "checkpoint_rows",
+           "restore_rows", "adapter_projection", "check_errors", "MoELayer"]
 
 
 def _check(what: str, t: torch.Tensor, dtype: torch.dtype, *shape: Optional[int]) -> None:
@@ -37,6 +41,11 @@ def _check(what: str, t: torch.Tensor, dtype: torch.dtype, *shape: Optional[int]
     if len(has) != len(shape) or any(n is not None and n != m for n, m in zip(shape, has)):
         wants = ", ".join("any" if n is None else str(n) for n in shape)
         raise ValueError(f"{what} has to be [{wants}], not {list(has)}")
+
+
+def _one_of(what: str, value, names) -> None:
+    if value not in names:
+        raise ValueError(f"{what} has to be one of {', '.join(map(repr, names))}, not {value!r}")
 
 
 def _check_err(err: Optional[torch.Tensor]) -> None:
@@ -136,6 +145,37 @@ class _UnsortRows(torch.autograd.Function):
         return dy, dw, None
 
 
+def _checkpoint_like(rows: int, features: int, parts: int, device):
+    """Empty buffers of a checkpoint in 8 bits."""
+    width = -(-features // EP_CHECKPOINT_GROUP) * EP_CHECKPOINT_GROUP * parts
+    return (torch.empty((rows, width), dtype=torch.uint8, device=device),
+            torch.empty((rows, width // EP_CHECKPOINT_GROUP), dtype=torch.uint8, device=device))
+
+
+class _UnsortRowsKept(torch.autograd.Function):
+    """_UnsortRows with y in 8 bits until the weights' gradient needs it."""
+
+    @staticmethod
+    def forward(ctx, y, weights, sort: ExpertSort):
+        ctx.sort = sort
+        kept = checkpoint_rows(y) if ctx.needs_input_grad[1] else (None, None)
+        ctx.save_for_backward(weights, *kept)
+        out = torch.empty((sort.N, sort.H), dtype=y.dtype, device=y.device)
+        ep_unsort_rows(sort.shape, y, weights, sort.handle, out, sort.launch())
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        sort, (weights, values, scales) = ctx.sort, ctx.saved_tensors
+        y, dw = None, None
+        if ctx.needs_input_grad[1]:
+            y, dw = restore_rows(values, scales, sort.H), torch.empty_like(weights)
+        dy = y if y is not None else grad.new_empty((sort.rows, sort.H))          # in place: y is this call's own
+        ep_unsort_rows_backward(sort.shape, grad.contiguous(), y, weights, sort.handle, dy, dw, sort.launch())
+        return dy, dw, None
+
+
 class _ExpertProduct(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, prefix, err):
@@ -160,6 +200,57 @@ class _ExpertProduct(torch.autograd.Function):
         return dx, dw, None, None
 
 
+class _FeedForward(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate_up, down, prefix, act, checkpoint, err):
+        (rows, K), (E, H, F) = x.shape, down.shape
+        launch, new = make_launch(error_flags=err), x.new_empty
+        ctx.act, ctx.checkpoint, ctx.err = act, checkpoint, err
+        for_x, for_gate_up, for_down = ctx.needs_input_grad[:3]
+        kept, rows_kept = (None, None), (None, None)
+        if (for_x or for_gate_up or for_down) and checkpoint != "recompute":
+            kept = (new((rows, 2 * F)), None) if checkpoint == "bf16" else _checkpoint_like(rows, F, 2, x.device)
+            if for_gate_up:
+                rows_kept = (x, None) if checkpoint == "bf16" else checkpoint_rows(x)
+        elif for_x or for_gate_up or for_down:
+            rows_kept = (x, None)
+        h, y = new((rows, F)), new((rows, H))
+        ep_expert_gated(ep_gemm_shape(rows, E, K, F), x, gate_up, prefix, act, h,
+                        None if kept[0] is None else make_checkpoint(*kept), launch)
+        ep_expert_gemm(ep_gemm_shape(rows, E, F, H), h, down, prefix, y, launch)
+        ctx.save_for_backward(gate_up, down, prefix, *kept, *rows_kept)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        gate_up, down, prefix, values, scales, x, x_scales = ctx.saved_tensors
+        (rows, H), (E, _, F), K = grad.shape, down.shape, gate_up.shape[2]
+        grad, launch, new = grad.contiguous(), make_launch(error_flags=ctx.err), grad.new_empty
+        for_x, for_gate_up, for_down = ctx.needs_input_grad[:3]
+        if ctx.checkpoint == "recompute":
+            values = new((rows, 2 * F))
+            ep_expert_gated(ep_gemm_shape(rows, E, K, F), x, gate_up, prefix, ctx.act, None, make_checkpoint(values), launch)
+        dgu, h = new((rows, 2 * F)), new((rows, F)) if for_down else None
+        down_shape, up_shape = ep_gemm_shape(rows, E, F, H), ep_gemm_shape(rows, E, K, 2 * F)
+        ep_expert_gated_dgrad(down_shape, grad, down, prefix, ctx.act, make_checkpoint(values, scales), dgu, h, launch)
+        dx = dgate_up = ddown = None
+        if for_down:
+            ddown = torch.empty_like(down)
+            ep_expert_gemm_wgrad(down_shape, grad, h, prefix, ddown, launch)
+        if for_x:
+            dx = new((rows, K))
+            ep_expert_gemm_dgrad(up_shape, dgu, gate_up, prefix, dx, launch)
+        if for_gate_up:
+            dgate_up = torch.empty_like(gate_up)
+            if x_scales is None:
+                ep_expert_gemm_wgrad(up_shape, dgu, x, prefix, dgate_up, launch)
+            else:
+                workspace = new(max(16, ep_wgrad_checkpoint_workspace_size(up_shape)), dtype=torch.uint8)
+                ep_expert_gemm_wgrad_checkpoint(up_shape, dgu, make_checkpoint(x, x_scales), prefix, dgate_up, workspace, launch)
+        return dx, dgate_up, ddown, None, None, None, None
+
+
 class _NoGradient(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, *inputs):
@@ -177,12 +268,36 @@ def sort_rows(x: torch.Tensor, sort: ExpertSort) -> torch.Tensor:
     return _SortRows.apply(x, sort)
 
 
-def unsort_rows(y: torch.Tensor, sort: ExpertSort, weights: Optional[torch.Tensor] = None) -> torch.Tensor:
+def checkpoint_rows(x: torch.Tensor):
+    """x [rows][features] bf16 -> (values, scales): the rows in 8 bits, uint8 [rows][features padded to
+    16] of e4m3 and uint8 [rows][groups of 16], for a backward pass (see ep_checkpoint in ep.h)."""
+    _check("x", x, torch.bfloat16, None, None)
+    kept = _checkpoint_like(*x.shape, 1, x.device)
+    ep_checkpoint_rows(*x.shape, x, make_checkpoint(*kept), make_launch())
+    return kept
+
+
+def restore_rows(values: torch.Tensor, scales: torch.Tensor, features: int) -> torch.Tensor:
+    """The rows [rows][features] in bf16 that checkpoint_rows has kept."""
+    groups = -(-features // EP_CHECKPOINT_GROUP)
+    _check("values", values, torch.uint8, None, groups * EP_CHECKPOINT_GROUP)
+    _check("scales", scales, torch.uint8, values.shape[0], groups)
+    x = torch.empty((values.shape[0], features), dtype=torch.bfloat16, device=values.device)
+    ep_restore_rows(*x.shape, make_checkpoint(values, scales), x, make_launch())
+    return x
+
+
+def unsort_rows(y: torch.Tensor, sort: ExpertSort, weights: Optional[torch.Tensor] = None,
+                checkpoint: str = "bf16") -> torch.Tensor:
     """y [rows][H] -> [N][H], the sum of each row's entries, scaled by weights [N][k] fp32 if given;
-    gradients to y and weights."""
+    gradients to y and weights. The weights' gradient needs y: with checkpoint "e4m3" it is kept in
+    8 bits until then."""
+    _one_of("checkpoint", checkpoint, ("bf16", "e4m3"))
     _check("y", y, torch.bfloat16, sort.rows, sort.H)
     if weights is not None:
         _check("weights", weights, torch.float32, sort.N, sort.k)
+        if checkpoint == "e4m3":
+            return _UnsortRowsKept.apply(y, weights, sort)
     return _UnsortRows.apply(y, weights, sort)
 
 
@@ -195,6 +310,32 @@ def expert_product(x: torch.Tensor, weight: torch.Tensor, expert_prefix: torch.T
     _check("expert_prefix", expert_prefix, torch.int32, weight.shape[0] + 1)
     _check_err(err)
     return _ExpertProduct.apply(x, weight, expert_prefix, _error_word(err, x.device))
+
+
+_ACTIVATIONS = {"silu": EP_ACT_SILU, "gelu": EP_ACT_GELU_TANH}
+
+
+def expert_feed_forward(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, expert_prefix: torch.Tensor,
+                        activation: str = "silu", checkpoint: str = "bf16",
+                        err: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The experts' gated feed-forward block: x [rows][in] in expert order, gate_up [E][2 * features][in]
+    (gate, then up), down [E][out][features] -> down (act(gate x) * (up x)) [rows][out]; gradients to
+    all three. activation: "silu" or "gelu" (with a hyperbolic tangent). checkpoint: what is kept for
+    the backward pass, which computes the product of activation and up again in any case:
+      "bf16"       x and both projections' results, 2 bytes a value
+      "e4m3"       the same in 8 bits (1.0625 bytes); the matrices' gradients and act' then go by
+                   those values, the result and the gradient's way through down do not
+      "recompute"  x; both projections run again
+    Every row has to belong to an expert (expert_prefix runs from 0 to rows)."""
+    _check("down", down, torch.bfloat16, None, None, None)
+    _check("gate_up", gate_up, torch.bfloat16, down.shape[0], 2 * down.shape[2], None)
+    _check("x", x, torch.bfloat16, None, gate_up.shape[2])
+    _check("expert_prefix", expert_prefix, torch.int32, gate_up.shape[0] + 1)
+    _one_of("activation", activation, tuple(_ACTIVATIONS))
+    _one_of("checkpoint", checkpoint, ("bf16", "e4m3", "recompute"))
+    _check_err(err)
+    return _FeedForward.apply(x, gate_up, down, expert_prefix, _ACTIVATIONS[activation], checkpoint,
+                              _error_word(err, x.device))
 
 
 def adapter_projection(x: torch.Tensor, weight: torch.Tensor, a: Optional[torch.Tensor], b: Optional[torch.Tensor],
@@ -267,11 +408,19 @@ class MoELayer(torch.nn.Module):
     order, gate / up products, silu(gate) * up, down product, back with the routing weights,
     combine; plus a projection that every token passes, with each token's own adapter when
     serving. All ranks' experts live on this GPU, so one sort and one product cover all of
-    them: rank d's local expert e is expert d * E_loc + e."""
+    them: rank d's local expert e is expert d * E_loc + e.
 
-    def __init__(self, buf: Buffer, features: int, device="cuda"):
+    checkpoint: None runs the experts product by product and keeps every step's result in bf16;
+    "bf16", "e4m3" and "recompute" run them as expert_feed_forward does, the activation and the
+    product in the projections' kernel ("e4m3" keeps the experts' outputs in 8 bits too, for the
+    routing weights' gradient). activation: "silu", or with a checkpoint "gelu"."""
+
+    def __init__(self, buf: Buffer, features: int, device="cuda", checkpoint: Optional[str] = None,
+                 activation: str = "silu"):
         super().__init__()
-        self.buf = buf
+        _one_of("checkpoint", checkpoint, (None, "bf16", "e4m3", "recompute"))
+        _one_of("activation", activation, tuple(_ACTIVATIONS) if checkpoint is not None else ("silu",))
+        self.buf, self.checkpoint, self.activation = buf, checkpoint, activation
         H, E = buf.H, buf.E
         new = lambda *shape: torch.nn.Parameter(  # noqa: E731
             (torch.randn(*shape, device=device) * shape[-1] ** -0.5).bfloat16())
@@ -293,10 +442,15 @@ class MoELayer(torch.nn.Module):
         rank = torch.repeat_interleave(torch.arange(buf.R, device=x.device), sizes, output_size=off[-1])
         expert = torch.where(local >= 0, local + (rank * (buf.E // buf.R)).unsqueeze(1), local)
         sort = ExpertSort(expert, buf.E, buf.H, err=buf.err)
-        h = expert_product(sort_rows(rows, sort), self.gate_up, sort.expert_prefix, buf.err)
-        gate, up = h.chunk(2, dim=1)
-        y = expert_product(torch.nn.functional.silu(gate) * up, self.down, sort.expert_prefix, buf.err)
-        routed = _Combine.apply(unsort_rows(y, sort, weights), buf, out["handle"])
+        if self.checkpoint is None:
+            h = expert_product(sort_rows(rows, sort), self.gate_up, sort.expert_prefix, buf.err)
+            gate, up = h.chunk(2, dim=1)
+            y = expert_product(torch.nn.functional.silu(gate) * up, self.down, sort.expert_prefix, buf.err)
+        else:
+            y = expert_feed_forward(sort_rows(rows, sort), self.gate_up, self.down, sort.expert_prefix, self.activation,
+                                    self.checkpoint, buf.err)
+        back = unsort_rows(y, sort, weights, "e4m3" if self.checkpoint == "e4m3" else "bf16")
+        routed = _Combine.apply(back, buf, out["handle"])
         flat = x.reshape(-1, buf.H)
         if adapters is None:
             one = torch.tensor([0, flat.shape[0]], dtype=torch.int32, device=x.device)

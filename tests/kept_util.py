@@ -43,7 +43,7 @@ def quantised(x: torch.Tensor):
     code, value = torch.where(nan, torch.full_like(code, 127), code), torch.where(nan, at, value)
     sign = torch.signbit(at)
     code, value = code + 128 * (sign & ~nan), torch.where(sign, -value, value)
-    return (code.view(rows, -1).to(torch.uint8), (k + 127).to(torch.uint8), value.view(rows, -1)[:, :features])
+    return (code.flatten(1).to(torch.uint8), (k + 127).to(torch.uint8), value.flatten(1)[:, :features])
 
 
 def stands_for(values: torch.Tensor, scales: torch.Tensor, features: int) -> torch.Tensor:
