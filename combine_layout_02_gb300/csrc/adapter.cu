@@ -273,7 +273,8 @@ AdapterWorkspace adapter_workspace(const ep_adapter_shape* sh) {
 
 // The epilogue's part: y += B_i low. A row only ever meets its own adapter's values.
 struct AdapterSide {
-    static constexpr bool kStores = false, kPairs = false;
+    static constexpr bool kWrites = false, kPairs = false;
+    static constexpr int kWarps = kTileWarps;
     const __nv_bfloat16* b;
     const float* low;
     const float* scales;
@@ -494,7 +495,7 @@ struct AdapterWide : AdapterSide {
             }
         }
     }
-    __device__ __forceinline__ void prepare(float* shared, unsigned char* terms, int64_t row0, int rows) const {
+    __device__ __forceinline__ void prepare(float* shared, unsigned char* terms, int64_t row0, int rows, int) const {
         int* which = reinterpret_cast<int*>(shared);
         int* run_of = which + kRows;
         int* runs = run_of + kRows;

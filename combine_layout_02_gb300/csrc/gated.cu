@@ -35,13 +35,16 @@ __device__ __forceinline__ Activated activate_both(float g, int act) {
 
 // ------------------------------------------------------------------ what is kept
 
-// g and u of a row: bf16 [rows][2][F], or e4m3 [rows][2][F padded to 16] with a byte for each 16.
+// g and u of a row: bf16 [rows][2][F], or e4m3 [rows][2][F padded to 16] with a byte for each 16
+// features, [groups][rows][2]: what a warp writes of them lies side by side (by rows, single bytes of 32 lines
+// took 16 us of 53 for 4229 rows 560 -> 2616).
 enum Keep { kNone, kBf16, kE4m3 };
 
 struct Kept {
     void* values;
     uint8_t* scales;
     int F, padded, act;
+    int64_t rows;
     __device__ __forceinline__ __nv_bfloat16* halves(int64_t row, int side) const {
         return reinterpret_cast<__nv_bfloat16*>(values) + (2 * row + side) * F;
     }
@@ -49,130 +52,120 @@ struct Kept {
         return reinterpret_cast<uint8_t*>(values) + (2 * row + side) * padded;
     }
     __device__ __forceinline__ uint8_t* exponent(int64_t row, int side, int feature) const {
-        return scales + (2 * row + side) * (padded / kKeptGroup) + feature / kKeptGroup;
+        return scales + ((feature / kKeptGroup) * rows + row) * 2 + side;
     }
 };
-
-__device__ __forceinline__ void store_half(__nv_bfloat16* at, float v) { *at = __float2bfloat16_rn(v); }
 
 // ------------------------------------------------------------------ forward
 
 // The M side has eight rows of Wg and eight of Wu in turn, so that a warp has both sums of a feature
 // in the same place of two sets of eight lanes, and a tile of 256 covers 128 features.
 template <Keep KEEP>
-struct GatedWide : NoExtra {
-    static constexpr bool kPairs = true;
+struct Gated : NoExtra {
+    static constexpr bool kPairs = true, kWrites = true;
     Kept kept;
-    // g and u of those 16 rows; `row` is this lane's.
-    __device__ __forceinline__ void keep_block(const float (&v)[2][2][4], int64_t row, bool there, int f0, int F, int c) const {
-        uint32_t side[2][4];          // g, u: block b's features 8t + 2c, 2c+1 of row g in 2b + t
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float(&s)[4] = v[i >> 1][i & 1];
-            side[0][i] = transpose_8x8(pack_bf16x2(s[0], s[1]));
-            side[1][i] = transpose_8x8(pack_bf16x2(s[2], s[3]));
-        }
-        if constexpr (KEEP == kBf16) {
-            const int f = f0 + (c & 1) * 8;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 q = transpose_quad(side[h], c);
-                if (there && f < F) st_v4(kept.halves(row, h) + f, q);
-            }
-        } else {
-            uint32_t p[4], e[4];          // 2b + h
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const uint32_t mg = larger_bf16x2(side[0][2 * b], side[0][2 * b + 1]);
-                const uint32_t mu = larger_bf16x2(side[1][2 * b], side[1][2 * b + 1]);
-                uint32_t m = larger_bf16x2(__byte_perm(mg, mu, 0x5410), __byte_perm(mg, mu, 0x7632));
-                m = larger_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                m = larger_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                e[2 * b] = kept_exponent(m & 0xFFFFu);
-                e[2 * b + 1] = kept_exponent(m >> 16);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float inv = kept_inverse(e[2 * b + h]);
-                    p[2 * b + h] = keep_pair(side[h][2 * b], inv) | keep_pair(side[h][2 * b + 1], inv) << 16;
-                }
-            }
-            const uint4 q = transpose_quad(p, c);          // lane c: all 16 features of block c / 2, side c & 1
-            if (there) {
-                st_v4(kept.bytes(row, c & 1) + f0, make_uint4(__byte_perm(q.x, q.y, 0x5410), __byte_perm(q.z, q.w, 0x5410),
-                                                              __byte_perm(q.x, q.y, 0x7632), __byte_perm(q.z, q.w, 0x7632)));
-                *kept.exponent(row, c & 1, f0) = (uint8_t)(c < 2 ? (c == 0 ? e[0] : e[1]) : (c == 2 ? e[2] : e[3]));
-            }
-        }
-    }
-    // 16 features x 16 rows at a time. Lane 4g + c has rows 2c, 2c+1 of features g (t = 0) and 8 + g
-    // (t = 1); after the transpositions the four lanes of row g have eight features each of both blocks
-    // of rows.
     __device__ __forceinline__ void tile(uint32_t tmem, float*, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows,
                                          int m0, int M, int half, int lane) const {
+        write<kWarps / 4>(tmem, out, row0, rows, m0, M, half, lane);
+    }
+    __device__ __forceinline__ void prefetch(int64_t, int, int, int, int) const {}
+    // 16 features x 32 rows at a time, in sets s of 16, each step for all of them before the next (a step's
+    // results take tens of cycles, and there are two warps a scheduler). Lane 4g + c has rows 2c, 2c+1 of
+    // features g (t = 0) and 8 + g (t = 1) of both blocks b of a set; after the transpositions the four
+    // lanes of row g have eight features each of both blocks.
+    static constexpr int kSets = 2;
+    template <int PARTS>          // how many warps share the rows
+    __device__ __forceinline__ void write(uint32_t tmem, __nv_bfloat16* out, int64_t row0, int rows, int m0, int M, int part,
+                                          int lane) const {
         const int g = lane >> 2, c = lane & 3, F = M / 2, f0 = m0 / 2;
         if (f0 >= F) return;
         const int f = f0 + (c & 1) * 8, at = (c >> 1) * 8 + g;
-        for (int n = half * 16; n < rows; n += 32) {
-            float v[2][2][4];
+        for (int n = part * 16 * kSets; n < rows; n += PARTS * 16 * kSets) {
+            float v[kSets][2][2][4];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                tmem_load_16x8(tmem + n + b * 8, v[b][0]);
-                tmem_load_16x8(tmem + n + b * 8 + (16u << 16), v[b][1]);
-            }
-            tmem_wait(v[0]);
-            tmem_wait(v[1]);
-            const bool there = n + at < rows;
+            for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    tmem_load_16x8(tmem + n + s * 16 + b * 8, v[s][b][0]);
+                    tmem_load_16x8(tmem + n + s * 16 + b * 8 + (16u << 16), v[s][b][1]);
+                }
+#pragma unroll
+            for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) tmem_wait(v[s][b]);
             const int64_t row = row0 + n + at;
             if (out != nullptr) {
-                uint32_t p[4];
+                uint32_t p[kSets][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float(&s)[4] = v[i >> 1][i & 1];
-                    p[i] = transpose_8x8(pack_bf16x2(activate(s[0], kept.act) * s[2], activate(s[1], kept.act) * s[3]));
-                }
-                const uint4 q = transpose_quad(p, c);
-                if (there && f < F) st_v4(out + row * F + f, q);
+                for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float(&w)[4] = v[s][i >> 1][i & 1];
+                        p[s][i] = transpose_8x8(pack_bf16x2(activate(w[0], kept.act) * w[2], activate(w[1], kept.act) * w[3]));
+                    }
+                transpose_quads(p, c);
+#pragma unroll
+                for (int s = 0; s < kSets; ++s)
+                    if (n + s * 16 + at < rows && f < F) st_v4(out + (row + s * 16) * F + f, words(p[s]));
             }
-            if constexpr (KEEP != kNone) keep_block(v, row, there, f0, F, c);
+            if constexpr (KEEP != kNone) keep_rows(v, row, rows - n - at, f0, F, c);
         }
     }
-};
-
-// Few rows: a lane has one sum of G rows; the other projection's is eight lanes on.
-template <Keep KEEP>
-struct GatedFew : NoExtra {
-    static constexpr bool kPairs = true, kStores = true;
-    Kept kept;
-    __device__ __forceinline__ void store(const float (&v)[kGroup], __nv_bfloat16* out, int64_t row0, int rows, int m, int M,
-                                          int lane) const {
-        const int side = lane >> 3 & 1, f = (m >> 4) * 8 + (m & 7), F = M / 2;
-        const bool in = f < F;
+    // g and u of those rows; `row` is this lane's of the first set, `left` how many there are from it on.
+    __device__ __forceinline__ void keep_rows(const float (&v)[kSets][2][2][4], int64_t row, int left, int f0, int F, int c) const {
+        uint32_t side[2][kSets][4];          // g, u: block b's features 8t + 2c, 2c+1 of row g in 2b + t
 #pragma unroll
-        for (int j = 0; j < kGroup; j += 2) {
-            if (j >= rows) break;
-            // Lanes of Wg take row j, lanes of Wu row j + 1.
-            const float other = __shfl_xor_sync(0xFFFFFFFFu, side ? v[j] : v[j + 1], 8);
-            const float h = side ? activate(other, kept.act) * v[j + 1] : activate(v[j], kept.act) * other;
-            if (out != nullptr && in && j + side < rows) store_half(out + (row0 + j + side) * F + f, h);
-            if constexpr (KEEP == kBf16) {
-                if (in) store_half(kept.halves(row0 + j, side) + f, v[j]);
-                if (in && j + 1 < rows) store_half(kept.halves(row0 + j + 1, side) + f, v[j + 1]);
-            } else if constexpr (KEEP == kE4m3) {
-                // A group's 16 features are the lanes of one side.
-                const uint32_t pair = pack_bf16x2(v[j], v[j + 1]);
-                uint32_t most = larger_bf16x2(pair, pair);
+        for (int s = 0; s < kSets; ++s)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) most = larger_bf16x2(most, __shfl_xor_sync(0xFFFFFFFFu, most, i < 3 ? 1 << i : 16));
-                const uint32_t e0 = kept_exponent(most & 0xFFFFu), e1 = kept_exponent(most >> 16);
-                const uint32_t q = pack_e4m3x2(bf16_lo(pair) * kept_inverse(e0), bf16_hi(pair) * kept_inverse(e1));
-                if (f < kept.padded) {
-                    *(kept.bytes(row0 + j, side) + f) = (uint8_t)q;
-                    if (j + 1 < rows) *(kept.bytes(row0 + j + 1, side) + f) = (uint8_t)(q >> 8);
-                    if ((lane & 0x17) == 0) {
-                        *kept.exponent(row0 + j, side, f) = (uint8_t)e0;
-                        if (j + 1 < rows) *kept.exponent(row0 + j + 1, side, f) = (uint8_t)e1;
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const float(&w)[4] = v[s][i >> 1][i & 1];
+                side[0][s][i] = transpose_8x8(pack_bf16x2(w[0], w[1]));
+                side[1][s][i] = transpose_8x8(pack_bf16x2(w[2], w[3]));
+            }
+        if constexpr (KEEP == kBf16) {
+            const int f = f0 + (c & 1) * 8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) transpose_quads(side[h], c);
+#pragma unroll
+            for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (s * 16 < left && f < F) st_v4(kept.halves(row + s * 16, h) + f, words(side[h][s]));
+        } else {
+            uint32_t p[kSets][4], m[kSets][2];
+#pragma unroll
+            for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {          // g's and u's maximum
+                    const uint32_t mg = larger_bf16x2(side[0][s][2 * b], side[0][s][2 * b + 1]);
+                    const uint32_t mu = larger_bf16x2(side[1][s][2 * b], side[1][s][2 * b + 1]);
+                    m[s][b] = larger_bf16x2(__byte_perm(mg, mu, 0x5410), __byte_perm(mg, mu, 0x7632));
                 }
+#pragma unroll
+            for (int bit = 1; bit <= 2; bit *= 2)
+#pragma unroll
+                for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) m[s][b] = larger_bf16x2(m[s][b], __shfl_xor_sync(0xFFFFFFFFu, m[s][b], bit));
+#pragma unroll
+            for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {          // block i / 2, side i & 1
+                    const int b = i >> 1, h = i & 1;
+                    const float inv = kept_inverse(kept_exponent(h ? m[s][b] >> 16 : m[s][b] & 0xFFFFu));
+                    p[s][i] = keep_pair(side[h][s][2 * b], inv) | keep_pair(side[h][s][2 * b + 1], inv) << 16;
+                }
+            transpose_quads(p, c);          // lane c: all 16 features of block c / 2, side c & 1
+#pragma unroll
+            for (int s = 0; s < kSets; ++s) {
+                if (s * 16 >= left) break;
+                const uint32_t(&q)[4] = p[s];
+                st_v4(kept.bytes(row + s * 16, c & 1) + f0, make_uint4(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                                                                       __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632)));
+                if (c & 1) continue;
+                const uint32_t most = c & 2 ? m[s][1] : m[s][0];
+                *reinterpret_cast<uint16_t*>(kept.exponent(row + s * 16, 0, f0)) =
+                    (uint16_t)(kept_exponent(most & 0xFFFFu) | kept_exponent(most >> 16) << 8);
             }
         }
     }
@@ -188,86 +181,89 @@ struct Back {
 // The sums are dh. What was kept is read by rows, eight features a lane, and brought into the sums'
 // layout by the transpositions of rows_of_features in reverse (its values are exact in bf16).
 template <Keep KEEP>
-struct GatedBackWide : NoExtra {
+struct GatedBack : NoExtra {
+    static constexpr bool kWrites = true;
+    static constexpr int kWarps = 16;
     Kept kept;
     Back to;
-    // Eight features of one side, as four bf16 pairs.
-    __device__ __forceinline__ uint4 load(int64_t row, int side, int f) const {
-        if (KEEP == kBf16) return *reinterpret_cast<const uint4*>(kept.halves(row, side) + f);
-        const uint2 q = *reinterpret_cast<const uint2*>(kept.bytes(row, side) + f);
-        const float s = kept_scale(*kept.exponent(row, side, f));
-        return make_uint4(kept_pair(q.x, s), kept_pair(q.x >> 16, s), kept_pair(q.y, s), kept_pair(q.y >> 16, s));
+    // Eight features of one row's side as they are stored, and as four bf16 pairs.
+    struct Raw {
+        uint4 q;          // e4m3: two words, and the power of two's byte in the third
+    };
+    __device__ __forceinline__ Raw load(int64_t row, int side, int f) const {
+        if constexpr (KEEP == kBf16) return {ld_stream_v4(kept.halves(row, side) + f)};
+        uint2 q;
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "l"(kept.bytes(row, side) + f));
+        return {make_uint4(q.x, q.y, __ldg(kept.exponent(row, side, f)), 0)};
     }
-    __device__ __forceinline__ void tile(uint32_t tmem, float*, unsigned char*, __nv_bfloat16*, int64_t row0, int rows, int m0,
+    static __device__ __forceinline__ void pairs(const Raw& r, uint32_t (&p)[4]) {
+        if constexpr (KEEP == kBf16) {
+            p[0] = r.q.x, p[1] = r.q.y, p[2] = r.q.z, p[3] = r.q.w;
+        } else {
+            const float s = kept_scale(r.q.z);
+            p[0] = kept_pair(r.q.x, s), p[1] = kept_pair(r.q.x >> 16, s), p[2] = kept_pair(r.q.y, s), p[3] = kept_pair(r.q.y >> 16, s);
+        }
+    }
+    __device__ __forceinline__ void prepare(float*, unsigned char*, int64_t row0, int rows, int m0) const {
+        prefetch(row0, rows, m0, threadIdx.x - 128, 32 * kWarps);
+    }
+    // What was kept of a tile, towards L2 while its products run: 128 features of both sides.
+    __device__ __forceinline__ void prefetch(int64_t row0, int rows, int m0, int thread, int threads) const {
+        const int bytes = KEEP == kBf16 ? 2 : 1, width = min(128, kept.F - m0) * bytes;
+        for (int i = thread; i < rows * 2; i += threads) {
+            const char* at = KEEP == kBf16 ? reinterpret_cast<const char*>(kept.halves(row0 + (i >> 1), i & 1) + m0)
+                                           : reinterpret_cast<const char*>(kept.bytes(row0 + (i >> 1), i & 1) + m0);
+            for (int o = 0; o < width; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + o));
+        }
+    }
+    __device__ __forceinline__ void tile(uint32_t tmem, float*, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows, int m0,
                                          int M, int half, int lane) const {
+        write<kWarps / 4>(tmem, out, row0, rows, m0, M, half, lane);
+    }
+    // 32 features x 8 rows at a time; the next rows' loads are under way meanwhile.
+    template <int PARTS>
+    __device__ __forceinline__ void write(uint32_t tmem, __nv_bfloat16*, int64_t row0, int rows, int m0, int M, int part,
+                                          int lane) const {
         if (m0 >= M) return;
         const int g = lane >> 2, c = lane & 3, f = m0 + c * 8;
-        for (int n = half * 8; n < rows; n += 16) {
+        Raw next[2] = {};
+        if (part * 8 + g < rows && f < M)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) next[h] = load(row0 + part * 8 + g, h, f);
+        for (int n = part * 8; n < rows; n += 8 * PARTS) {
             const bool there = n + g < rows && f < M;
             const int64_t row = row0 + n + g;
-            uint32_t side[2][4] = {};
+            uint32_t side[2][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (there) {
-                    const uint4 q = load(row, h, f);
-                    side[h][0] = q.x, side[h][1] = q.y, side[h][2] = q.z, side[h][3] = q.w;
-                }
+            for (int h = 0; h < 2; ++h) pairs(next[h], side[h]);
+            if (n + 8 * PARTS + g < rows && f < M)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) next[h] = load(row + 8 * PARTS, h, f);
             float v[2][4];
             tmem_load_16x8(tmem + n, v[0]);
             tmem_load_16x8(tmem + n + (16u << 16), v[1]);
-            tmem_wait(v);
-            float dg[2][4], du[2][4], again[2][4];
-            uint4 q[2];
+            transpose_quads(side, c);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) q[h] = transpose_quad(side[h], c);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) side[h][i] = transpose_8x8(side[h][i]);
+            tmem_wait(v);
+            uint32_t p[3][4];          // dg, du, h
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t gate = transpose_8x8(i < 2 ? (i == 0 ? q[0].x : q[0].y) : (i == 2 ? q[0].z : q[0].w));
-                const uint32_t up = transpose_8x8(i < 2 ? (i == 0 ? q[1].x : q[1].y) : (i == 2 ? q[1].z : q[1].w));
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float u = j ? bf16_hi(up) : bf16_lo(up), dh = v[i >> 1][(i & 1) * 2 + j];
-                    const Activated a = activate_both(j ? bf16_hi(gate) : bf16_lo(gate), kept.act);
-                    dg[i >> 1][(i & 1) * 2 + j] = dh * u * a.slope;
-                    du[i >> 1][(i & 1) * 2 + j] = dh * a.value;
-                    again[i >> 1][(i & 1) * 2 + j] = a.value * u;
-                }
+                const float d0 = v[i >> 1][(i & 1) * 2], d1 = v[i >> 1][(i & 1) * 2 + 1];
+                const float u0 = bf16_lo(side[1][i]), u1 = bf16_hi(side[1][i]);
+                const Activated a0 = activate_both(bf16_lo(side[0][i]), kept.act), a1 = activate_both(bf16_hi(side[0][i]), kept.act);
+                p[0][i] = transpose_8x8(pack_bf16x2(d0 * u0 * a0.slope, d1 * u1 * a1.slope));
+                p[1][i] = transpose_8x8(pack_bf16x2(d0 * a0.value, d1 * a1.value));
+                p[2][i] = transpose_8x8(pack_bf16x2(a0.value * u0, a1.value * u1));
             }
-            const uint4 pg = rows_of_features(dg, c), pu = rows_of_features(du, c);
+            transpose_quads(p, c);
             if (there) {
-                st_v4(to.dgu + 2 * row * M + f, pg);
-                st_v4(to.dgu + (2 * row + 1) * M + f, pu);
+                st_v4(to.dgu + 2 * row * M + f, words(p[0]));
+                st_v4(to.dgu + (2 * row + 1) * M + f, words(p[1]));
+                if (to.h != nullptr) st_v4(to.h + row * M + f, words(p[2]));
             }
-            if (to.h != nullptr) {
-                const uint4 ph = rows_of_features(again, c);
-                if (there) st_v4(to.h + row * M + f, ph);
-            }
-        }
-    }
-};
-
-template <Keep KEEP>
-struct GatedBackFew : NoExtra {
-    static constexpr bool kStores = true;
-    static constexpr int kGroup = 8;          // their loads are in flight together
-    Kept kept;
-    Back to;
-    __device__ __forceinline__ float load(int64_t row, int side, int f) const {
-        if (KEEP == kBf16) return __bfloat162float(*(kept.halves(row, side) + f));
-        return kept_values(*(kept.bytes(row, side) + f)).x * kept_scale(*kept.exponent(row, side, f));
-    }
-    __device__ __forceinline__ void apply(float*, float (&)[kGroup], int64_t, int, int, int, int) const {}
-    __device__ __forceinline__ void store(const float (&v)[kGroup], __nv_bfloat16*, int64_t row0, int rows, int m, int M, int) const {
-        if (m >= M) return;
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-            if (j >= rows) break;
-            const int64_t row = row0 + j;
-            const float u = load(row, 1, m);
-            const Activated a = activate_both(load(row, 0, m), kept.act);
-            store_half(to.dgu + 2 * row * M + m, v[j] * u * a.slope);
-            store_half(to.dgu + (2 * row + 1) * M + m, v[j] * a.value);
-            if (to.h != nullptr) store_half(to.h + row * M + m, a.value * u);
         }
     }
 };
@@ -284,16 +280,39 @@ ep_status check_block(const ep_gemm_shape* sh, const void* rows_in, const void* 
     return (((uintptr_t)rows_in | (uintptr_t)w) & 15) != 0 ? EP_ERR_INVALID_ARG : EP_OK;
 }
 
-Kept kept_of(const ep_checkpoint* c, int F, int act) {
-    Kept k{nullptr, nullptr, F, kept_features(F), act};
+// A checkpoint of g and u: a row's two bytes of scales are written together.
+ep_status check_sides(const ep_checkpoint* c, bool rows) {
+    const ep_status st = check_checkpoint(c, rows, true);
+    return st == EP_OK && ((uintptr_t)c->scales & 1) != 0 ? EP_ERR_INVALID_ARG : st;
+}
+
+Kept kept_of(const ep_checkpoint* c, int F, int act, int rows) {
+    Kept k{nullptr, nullptr, F, kept_features(F), act, rows};
     if (c != nullptr) k.values = c->values, k.scales = c->scales;
     return k;
 }
 
-template <Direction D, class Wide, class Few>
-ep_status run_block(const GemmMaps& maps, const GemmArgs& a, const Wide& wide, const Few& few, cudaStream_t stream) {
-    const cudaError_t e = launch_gemm<D>(maps, a, wide, few, stream);
+template <Direction D, class Extra>
+ep_status run_block(const GemmMaps& maps, const GemmArgs& a, const Extra& extra, cudaStream_t stream) {
+    const cudaError_t e = launch_gemm<D>(maps, a, extra, extra, stream);
     return e == cudaSuccess ? EP_OK : cuda_fail(e);
+}
+
+// Tiles and stages. Where the contraction is short and all tiles of 32 or 64 rows are on the GPU at once
+// (two an SM; of 64 rows over up to 8 steps of 64 also twice that), they are taken that narrow, not as
+// wide as gemm_tiles would: a pair's 256 x 256 costs 4 us more to set up, and its epilogue 4 (forward) to
+// 10 us (backward) that nothing hides. Forward keeping 8 bits / backward: 509 rows of 8 experts 256 -> 512
+// 9.0 / 11.7 us, with 32 rows 4.5 / 5.7; 1500 rows of 8, 1024 -> 512 14.7 / 19.8, with 64 and 32 rows
+// 9.2 / 9.3; 2048 rows of 16, 512 -> 512 14.3 / 19.3, 10.0 / 8.6. Longer contractions lose by it, as the
+// weights are read once for each tile (32 steps, 509 rows of 8 experts: 18.1 us, with 64 rows 24.2).
+void block_tiles(GemmArgs* a) {
+    const int steps = ceil_div(a->C, kBK), sms = sm_count();
+    int widest = 256;
+    for (int bn = 64; steps <= 16 && bn >= 32; bn /= 2) {
+        a->bn = bn;
+        if (gemm_most_tiles(*a, false, kBM) <= (bn == 64 && steps <= 8 ? 4 : 2) * sms) widest = bn;
+    }
+    gemm_tiles(a, false, 0, 256, widest);
 }
 
 // The maps of the rows, in boxes of a.box and of twice that.
@@ -308,19 +327,17 @@ ep_status encode_rows(GemmMaps* maps, const GemmArgs& a, const void* rows) {
 
 template <Keep KEEP>
 ep_status forward(const GemmMaps& maps, const GemmArgs& a, const Kept& kept, cudaStream_t stream) {
-    GatedWide<KEEP> wide;
-    GatedFew<KEEP> few;
-    wide.kept = few.kept = kept;
-    return run_block<kForward>(maps, a, wide, few, stream);
+    Gated<KEEP> extra;
+    extra.kept = kept;
+    return run_block<kForward>(maps, a, extra, stream);
 }
 
 template <Keep KEEP>
 ep_status backward(const GemmMaps& maps, const GemmArgs& a, const Kept& kept, const Back& to, cudaStream_t stream) {
-    GatedBackWide<KEEP> wide;
-    GatedBackFew<KEEP> few;
-    wide.kept = few.kept = kept;
-    wide.to = few.to = to;
-    return run_block<kDgrad>(maps, a, wide, few, stream);
+    GatedBack<KEEP> extra;
+    extra.kept = kept;
+    extra.to = to;
+    return run_block<kDgrad>(maps, a, extra, stream);
 }
 
 }  // namespace
@@ -334,7 +351,7 @@ ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w,
     ep_status st = check_block(sh, x, w, expert_prefix, activation, launch);
     if (st != EP_OK) return st;
     const bool rows = sh->num_rows > 0;
-    if (keep != nullptr && (st = check_checkpoint(keep, rows, true)) != EP_OK) return st;
+    if (keep != nullptr && (st = check_sides(keep, rows)) != EP_OK) return st;
     if ((rows && h == nullptr && keep == nullptr) || ((uintptr_t)h & 15) != 0) return EP_ERR_INVALID_ARG;
     const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, E = (uint64_t)sh->num_experts;
     GemmArgs a{};
@@ -345,7 +362,7 @@ ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w,
     a.M = 2 * sh->out_features;
     a.N = a.C = sh->in_features;
     a.err = launch->error_flags;
-    gemm_tiles(&a, false);
+    block_tiles(&a);
     GemmMaps maps{};
     if (rows) {
         const uint64_t d[5] = {K, 8, 2, F / 8, E}, strides[4] = {2 * K, 2 * F * K, 16 * K, 4 * F * K};
@@ -355,7 +372,7 @@ ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w,
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
-        const Kept kept = kept_of(keep, sh->out_features, activation);
+        const Kept kept = kept_of(keep, sh->out_features, activation, sh->num_rows);
         st = keep == nullptr              ? forward<kNone>(maps, a, kept, launch->stream)
              : keep->dtype == EP_BF16 ? forward<kBf16>(maps, a, kept, launch->stream)
                                           : forward<kE4m3>(maps, a, kept, launch->stream);
@@ -370,7 +387,7 @@ ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const v
     ep_status st = check_block(sh, dy, w, expert_prefix, activation, launch);
     if (st != EP_OK) return st;
     const bool rows = sh->num_rows > 0;
-    if ((st = check_checkpoint(kept, rows, true)) != EP_OK) return st;
+    if ((st = check_sides(kept, rows)) != EP_OK) return st;
     if ((rows && dgu == nullptr) || (((uintptr_t)dgu | (uintptr_t)h) & 15) != 0) return EP_ERR_INVALID_ARG;
     GemmArgs a{};
     a.prefix = expert_prefix;
@@ -379,7 +396,7 @@ ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const v
     a.M = a.N = sh->in_features;
     a.C = sh->out_features;
     a.err = launch->error_flags;
-    gemm_tiles(&a, false);
+    block_tiles(&a);
     GemmMaps maps{};
     if (rows) {
         const uint64_t d[3] = {(uint64_t)sh->in_features, (uint64_t)sh->out_features, (uint64_t)sh->num_experts};
@@ -389,7 +406,7 @@ ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const v
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
-        const Kept k = kept_of(kept, sh->in_features, activation);
+        const Kept k = kept_of(kept, sh->in_features, activation, sh->num_rows);
         const Back to{reinterpret_cast<__nv_bfloat16*>(dgu), reinterpret_cast<__nv_bfloat16*>(h)};
         st = kept->dtype == EP_BF16 ? backward<kBf16>(maps, a, k, to, launch->stream) : backward<kE4m3>(maps, a, k, to, launch->stream);
         if (st != EP_OK) return st;

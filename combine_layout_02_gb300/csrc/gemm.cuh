@@ -129,6 +129,12 @@ __device__ __forceinline__ void tmem_store_16x8(uint32_t at, const float (&v)[4]
                  "f"(v[3])
                  : "memory");
 }
+// 8 consecutive columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_store(uint32_t at, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "f"(v[0]), "f"(v[1]),
+                 "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 4, 8 consecutive columns of this warp's 32 lanes.
@@ -357,7 +363,7 @@ __device__ __forceinline__ uint32_t instr_desc(int m, int n, bool a_mn, bool b_m
 constexpr int kBM = 128, kBK = 64;
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr int kMaxStages = 8;
-constexpr int kTileWarps = 8;          // writing warps of gemm_kernel, two per quarter of the lanes
+constexpr int kTileWarps = 8;          // writing warps of gemm_kernel, two per quarter of the lanes, but for extras with more
 
 struct Tile {
     int e, m0, n0, n;          // expert, first M index, first column (row index or N index), columns
@@ -434,32 +440,36 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
     return t;
 }
-// Within quads of lanes: lane c has word h of its own in p[h], and gets word c of lane h in place h.
-__device__ __forceinline__ uint4 transpose_quad(uint32_t (&p)[4], int c) {
+// Within quads of lanes, N times: lane c has word h of its own in p[.][h], and gets word c of lane h in place h.
+template <int N>
+__device__ __forceinline__ void transpose_quads(uint32_t (&p)[N][4], int c) {
 #pragma unroll
     for (int bit = 1; bit <= 2; bit *= 2)
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            if (h & bit) continue;
-            const bool up = c & bit;
-            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? p[h] : p[h | bit], bit);
-            if (up) p[h] = got;
-            else p[h | bit] = got;
-        }
-    return make_uint4(p[0], p[1], p[2], p[3]);
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                if (h & bit) continue;
+                const bool up = c & bit;
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? p[n][h] : p[n][h | bit], bit);
+                if (up) p[n][h] = got;
+                else p[n][h | bit] = got;
+            }
 }
+__device__ __forceinline__ uint4 words(const uint32_t (&p)[4]) { return make_uint4(p[0], p[1], p[2], p[3]); }
 // Sums of 32 features x 8 rows in the layout of tmem_load_16x8 (lane 4g + c: rows 2c, 2c+1 of features
 // g, 8 + g in v[0], 16 + g, 24 + g in v[1]) -> bf16, lane 4g + c the eight features 8c .. 8c+7 of row
 // g: a transposition within 8 x 8 blocks and one within quads of lanes. A lane then stores 16
 // bytes, a warp 64 bytes of eight rows.
 __device__ __forceinline__ uint4 rows_of_features(const float (&v)[2][4], int c) {
-    uint32_t p[4];
+    uint32_t p[1][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        p[2 * t] = transpose_8x8(pack_bf16x2(v[t][0], v[t][1]));
-        p[2 * t + 1] = transpose_8x8(pack_bf16x2(v[t][2], v[t][3]));
+        p[0][2 * t] = transpose_8x8(pack_bf16x2(v[t][0], v[t][1]));
+        p[0][2 * t + 1] = transpose_8x8(pack_bf16x2(v[t][2], v[t][3]));
     }
-    return transpose_quad(p, c);
+    transpose_quads(p, c);
+    return words(p[0]);
 }
 
 // wgrad: a lane holds 64 consecutive columns of one row of dW; a warp stages its 32 rows x 64 columns
@@ -487,20 +497,21 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 // directly follows one of this library after which the call's inputs are complete; only the
 // epilogue waits for that kernel itself.
 //   gemm_kernel:        tile writes rows row0 .. row0 + rows - 1 of a tile, features m0 .. m0 + 31, out of
-//                       tensor memory; two warps do, `half` 0 and 1. reordered: the rows are loaded
-//                       through other_b. prepare is called by all 256 writing threads before, while
+//                       tensor memory; kWarps / 4 warps do, `half` 0, 1 and on. reordered: the rows are loaded
+//                       through other_b. prepare is called by all writing threads before, while
 //                       the products run. Both get a.beside bytes of shared memory
 //   gemm_split_kernel:  ahead for the CTA's rows while the products run (before that wait), then apply
 //                       for each kGroup of them: v[j] belongs to row row0 + c + j. Two halves of 128
-//                       threads take groups in turn. kStores: store writes the group instead, v[0]
-//                       being row row0's
+//                       threads take groups in turn. kWrites: what is written is not the sums alone:
+//                       write does it from tensor memory, as tile, where joined sums have gone back to,
+//                       and prefetch is called before for the rows, while the products run
 // kPairs (forward): the M side is two projections of out_features each, eight rows of one and eight of the
 // other in turn (maps.a has five dimensions: in_features, 8, 2, out_features / 8, experts).
 struct NoExtra {
-    static constexpr bool kFollows = false, kStores = false, kPairs = false;
-    static constexpr int kFloats = 4, kGroup = 32;
+    static constexpr bool kFollows = false, kWrites = false, kPairs = false;
+    static constexpr int kFloats = 4, kGroup = 32, kWarps = kTileWarps;
     __device__ __forceinline__ bool reordered() const { return false; }
-    __device__ __forceinline__ void prepare(float*, unsigned char*, int64_t, int) const {}
+    __device__ __forceinline__ void prepare(float*, unsigned char*, int64_t, int, int) const {}
     // Sixteen rows at a time, to have two blocks' steps in flight.
     __device__ __forceinline__ void tile(uint32_t tmem, float*, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows,
                                          int m0, int M, int half, int lane) const {
@@ -525,7 +536,6 @@ struct NoExtra {
     }
     __device__ __forceinline__ void ahead(float*, int64_t, int, int, int) const {}
     __device__ __forceinline__ void apply(float*, float (&)[32], int64_t, int, int, int, int) const {}
-    __device__ __forceinline__ void store(const float (&)[32], __nv_bfloat16*, int64_t, int, int, int, int) const {}
 };
 
 // The epilogue's THREADS: a barrier, and whether all of them have `mine` (the same answer to all, so
@@ -558,7 +568,7 @@ __device__ __forceinline__ bool epilogue_all(bool mine) {
 //   full[s]   leader's: both CTAs' loads (an arrival of each loading warp, and the bytes)
 //   empty[s]  each CTA's: the products that read stage s are done
 template <Direction D, class Extra>
-__global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
+__global__ void __launch_bounds__(128 + 32 * Extra::kWarps, 1)
     gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a, const Extra extra) {
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
@@ -584,7 +594,7 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 2 * kTileWarps);
+            mbar_init(&acc_empty[i], 2 * Extra::kWarps);
         }
         mbar_init(&drain, 1);
         dead = 0;
@@ -730,9 +740,9 @@ __global__ void __launch_bounds__(128 + 32 * kTileWarps, 1)
             const bool some = D != kWgrad || t.end > t.begin;
             const uint32_t acc = used & 1;
             const int rows = min(t.n, t.end - t.n0);
-            if (D != kWgrad) extra.prepare(s_extra, smem + a.stages * stage_bytes, t.n0, rows);
+            if (D != kWgrad) extra.prepare(s_extra, smem + a.stages * stage_bytes, t.n0, rows, t.m0 + (int)rank * kBM);
             if (some) {
-                if (!epilogue_all<32 * kTileWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a, D == kWgrad ? t.end - t.begin : a.C))) break;
+                if (!epilogue_all<32 * Extra::kWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a, D == kWgrad ? t.end - t.begin : a.C))) break;
                 tc_fence_after();
             }
             const int m = t.m0 + (int)rank * kBM + quarter * 32 + lane;
@@ -976,6 +986,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const int share = (rows + a.split * unit - 1) / (a.split * unit) * unit, lo = rank * share, hi = min(rows, lo + share);
     bool ok = has;
     if (has && warp >= 2) {
+        if constexpr (Extra::kWrites) extra.prefetch(t.n0 + lo, hi - lo, t.m0, threadIdx.x - 64, 256);
         if (D != kWgrad) extra.ahead(s_extra, t.n0 + lo, hi - lo, m, half);
         ok = epilogue_all<256>(mbar_wait(&done, 0, &dead, a, (kb1 - kb0) * kBK));
         tc_fence_after();
@@ -984,13 +995,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     constexpr int G = Extra::kGroup;
     const bool some = kb1 > kb0;
     if (D != kWgrad && a.split == 1) {
-        if (ok && warp >= 2) {
+        if constexpr (Extra::kWrites) {
+            if (ok && warp >= 2)
+                extra.template write<2>(tmem + ((uint32_t)quarter << 21), a.out, t.n0, rows, m - lane, a.M, half, lane);
+        } else if (ok && warp >= 2) {
             for (int c = half * G; c < rows; c += 2 * G) {
                 float v[G];
                 tmem_load(tmem + c + ((uint32_t)quarter << 21), v);
                 extra.apply(s_extra, v, t.n0, rows, c, m, half);
-                if constexpr (Extra::kStores) extra.store(v, a.out, t.n0 + c, rows - c, m, a.M, lane);
-                else store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
+                store_features(v, a.out, a.M, t.n0 + c, rows - c, m, a.M, lane);
             }
         }
     } else {
@@ -1028,6 +1041,27 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 st_v4(a.out + ((int64_t)t.e * a.M + m) * a.N + t.n0 + c,
                       make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
             }
+        } else if constexpr (Extra::kWrites) {
+            // The joined sums go back to tensor memory, from its first column on.
+            bool fine = ok;
+            for (int c = lo + half * 8; ok && warp >= 2 && c < hi; c += 16) {
+                float v[8] = {};
+                for (int r = 0; r < a.split; ++r) {
+                    const uint32_t peer = peer_addr(at, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (c + j < hi) v[j] += peer_value(peer + ((c + j) * kBM + m_local) * 4);
+                }
+                fine = fine && (!isnan(v[0]) || parts_complete(&s_complete, a.split));
+                tmem_store(tmem + c - lo + ((uint32_t)quarter << 21), v);
+            }
+            if (warp >= 2) {
+                tmem_store_wait();
+                tc_fence_before();
+                fine = epilogue_all<256>(fine);
+                tc_fence_after();
+                if (fine) extra.template write<2>(tmem + ((uint32_t)quarter << 21), a.out, t.n0 + lo, hi - lo, m - lane, a.M, half, lane);
+            }
         } else if (ok && warp >= 2 && lo < hi) {
             for (int c = lo + half * G; c < hi; c += 2 * G) {
                 float v[G];
@@ -1041,9 +1075,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 }
                 const bool failed = isnan(v[0]) && !parts_complete(&s_complete, a.split);          // for all alike
                 extra.apply(s_extra, v, t.n0 + lo, hi - lo, c - lo, m, half);
-                if (__any_sync(0xFFFFFFFFu, failed)) continue;
-                if constexpr (Extra::kStores) extra.store(v, a.out, t.n0 + c, hi - c, m, a.M, lane);
-                else store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
+                if (!__any_sync(0xFFFFFFFFu, failed)) store_features(v, a.out, a.M, t.n0 + c, hi - c, m, a.M, lane);
             }
         }
         __syncwarp();
@@ -1153,7 +1185,7 @@ cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Wide& wid
     }
     const int64_t tiles = gemm_most_tiles(a, D == kWgrad, 2 * kBM), pairs = sm_count() / 2;
     return launch_gemm_as(gemm_kernel<D, Wide>, D == kWgrad ? kWgradSmemMax : kGemmSmemMax, 2u * (unsigned)(tiles < pairs ? tiles : pairs),
-                          128 + 32 * kTileWarps, 2, stream,
+                          128 + 32 * Wide::kWarps, 2, stream,
                           maps, a, wide);
 }
 

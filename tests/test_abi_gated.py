@@ -43,7 +43,7 @@ def test_gated_refusals(ep):
     assert go(x=P + 8) == bad and go(w=P + 2) == bad and go(prefix=P + 2) == bad and go(h=P + 8) == bad
     assert go(act=2) == bad and go(act=-1) == bad
     for keep in (C(2, P, P), C(-1, P, P), C(ep.EP_FP8_E4M3, P, None), C(ep.EP_FP8_E4M3, None, P), C(ep.EP_BF16, None, None),
-                 C(ep.EP_BF16, P, P), C(ep.EP_FP8_E4M3, P + 8, P), C(ep.EP_BF16, P + 4, None)):
+                 C(ep.EP_BF16, P, P), C(ep.EP_FP8_E4M3, P + 8, P), C(ep.EP_FP8_E4M3, P, P + 1), C(ep.EP_BF16, P + 4, None)):
         assert go(keep=keep) == bad
 
     def back(shape=S(10, 2, 64, 64), dy=P, w=P, prefix=P, act=1, kept=b, dgu=P, h=P, launch=launch):
@@ -55,7 +55,7 @@ def test_gated_refusals(ep):
     assert back(dy=None) == bad and back(w=None) == bad and back(prefix=None) == bad and back(dgu=None) == bad
     assert back(dy=P + 8) == bad and back(w=P + 2) == bad and back(prefix=P + 2) == bad and back(dgu=P + 8) == bad and back(h=P + 2) == bad
     assert back(act=7) == bad
-    for kept in (C(2, P, P), C(ep.EP_FP8_E4M3, P, None), C(ep.EP_BF16, P, P), C(ep.EP_BF16, P + 2, None)):
+    for kept in (C(2, P, P), C(ep.EP_FP8_E4M3, P, None), C(ep.EP_BF16, P, P), C(ep.EP_BF16, P + 2, None), C(ep.EP_FP8_E4M3, P, P + 1)):
         assert back(kept=kept) == bad
 
 

@@ -38,6 +38,11 @@ def normal(g, *shape):
     return torch.randn(*shape, generator=g, device="cuda").bfloat16()
 
 
+def by_row(scales):
+    """[groups][rows][2] -> each side's [rows][groups]."""
+    return [scales[:, :, side].t().contiguous() for side in range(2)]
+
+
 class Block:
     """Rows of the experts with some of no expert around them: NaN where inputs, 7 where outputs."""
 
@@ -69,14 +74,14 @@ class Block:
         else:
             width = -(-self.F // GROUP) * GROUP
             values = torch.full((self.n, 2 * width), 0xA5, dtype=torch.uint8, device="cuda")
-            scales = torch.full((self.n, 2 * width // GROUP), 0xA5, dtype=torch.uint8, device="cuda")
+            scales = torch.full((width // GROUP, self.n, 2), 0xA5, dtype=torch.uint8, device="cuda")
         return values, scales, ep.make_checkpoint(values, scales)
 
     def parts(self, values, scales):
         """g and u as kept, in 64 bits."""
         if scales is None:
             return values.double().chunk(2, 1)
-        return [stands_for(v.contiguous(), s.contiguous(), self.F) for v, s in zip(values.chunk(2, 1), scales.chunk(2, 1))]
+        return [stands_for(v.contiguous(), s.contiguous(), self.F) for v, s in zip(values.chunk(2, 1), by_row(scales))]
 
     def forward(self, kind, keep=None, with_h=True):
         h = torch.full((self.n, self.F), 7.0, dtype=torch.bfloat16, device="cuda") if with_h else None
@@ -98,6 +103,7 @@ class Block:
         """Rows of no expert are as they were."""
         for t in outputs:
             if t is not None:
+                t = t.transpose(0, 1) if t.dim() == 3 else t
                 rest = torch.cat([t[:self.mine.start], t[self.mine.stop:]])
                 assert bool((rest == (0xA5 if t.dtype == torch.uint8 else 7)).all())
 
@@ -134,7 +140,7 @@ def test_kept_bytes_of_whole_numbers(name):
     b = Block(*CASES[name], seed=2, make=integers)
     h, values, scales = b.forward("silu", "e4m3", with_h=False)
     sums, _ = b.sums()
-    for side, (v, s) in enumerate(zip(values.chunk(2, 1), scales.chunk(2, 1))):
+    for side, (v, s) in enumerate(zip(values.chunk(2, 1), by_row(scales))):
         q, k, _ = quantised(sums[side][b.mine].float().bfloat16())
         assert torch.equal(v[b.mine].cpu(), q) and torch.equal(s[b.mine].cpu(), k)
     _, halves, _ = b.forward("silu", "bf16")
@@ -154,8 +160,8 @@ def backward(b, kind, keep, with_h=True, seed=9):
         for side, part in enumerate(made.chunk(2, 1)):
             q, k, _ = quantised(part)
             wide = q.shape[1]
-            values[:, side * wide:(side + 1) * wide], scales[:, side * wide // GROUP:(side + 1) * wide // GROUP] = q.cuda(), k.cuda()
-    for t in (values, scales):          # rows of no expert: not read
+            values[:, side * wide:(side + 1) * wide], scales[:, :, side] = q.cuda(), k.t().cuda()
+    for t in (values, None if scales is None else scales.transpose(0, 1)):          # rows of no expert: not read
         if t is not None:
             t[:b.mine.start], t[b.mine.stop:] = (math.nan, math.nan) if t.dtype == torch.bfloat16 else (0x7F, 0x7F)
     dgu = torch.full((b.n, 2 * b.F), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -286,7 +292,7 @@ def test_many_rows_beyond_two_to_the_31_values():
     assert_within(h[last], a * u, product_bound(a, a_off + STEEP * off[:, :F], u, off[:, F:]) + (a * u).abs() * U32, U16)
     dgu = torch.empty(n, 2 * F, dtype=torch.bfloat16, device="cuda")
     ep.ep_expert_gated_dgrad(b.down_shape, b.dy, b.down, b.prefix, ep.EP_ACT_SILU, ep.make_checkpoint(values, scales), dgu, None, b.launch)
-    g, u = (stands_for(v[last].contiguous(), s[last].contiguous(), F) for v, s in zip(values.chunk(2, 1), scales.chunk(2, 1)))
+    g, u = (stands_for(v[last].contiguous(), s[last].contiguous(), F) for v, s in zip(values.chunk(2, 1), by_row(scales)))
     dh = b.dy[last].double() @ b.down[0].double()
     off = sum_bound(K, b.dy[last].double().abs() @ b.down[0].double().abs(), 2 * U32)
     a, _, a_off, _ = act(g, "silu")
