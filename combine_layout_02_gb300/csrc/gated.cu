@@ -171,6 +171,107 @@ struct Gated : NoExtra {
     }
 };
 
+// ------------------------------------------------------------------ single tokens
+
+// One row, nothing kept: a stream of its expert's weights past it without tensor cores, whose set-up and
+// joining of parts are what such a call takes longest (1 row 4096 -> 4096: 15.4 us by gemm_split_kernel, so
+// 12.9; 1024 -> 1024 6.9, 2.8; two rows and more are as fast by tensor cores). Small blocks that ask
+// for all of their weights at once and leave: with many of them an SM 64 MB come in 10.7 us, where blocks that
+// stay and load ahead take 12.5. `team` warps have a feature's two rows of weights, AHEAD pieces of 16
+// bytes a thread and row at a time. fp32 sums: a thread's, of even and of odd values, then over the lanes,
+// then over the team's warps in order.
+constexpr int kTokenThreads = 256, kTokenWarps = kTokenThreads / 32;
+struct TokenArgs {
+    const __nv_bfloat16* x;
+    const __nv_bfloat16* w;
+    const int32_t* prefix;
+    __nv_bfloat16* h;
+    uint32_t* err;
+    int E, K, F, act;
+    int team;          // 1, 2, 4 or 8
+};
+
+// A bf16 pair as two fp32 values, and two multiply-adds at once.
+__device__ __forceinline__ uint64_t wide_pair(uint32_t w) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(w << 16), "r"(w & 0xFFFF0000u));
+    return r;
+}
+__device__ __forceinline__ void add_products(uint64_t& sum, const uint4& a, const uint4& b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(wide_pair(x[i])), "l"(wide_pair(y[i])));
+}
+
+template <int AHEAD>
+__global__ void __launch_bounds__(kTokenThreads, AHEAD == 2 ? 6 : 4) token_kernel(const TokenArgs a) {
+    __shared__ int s_expert;
+    __shared__ float s_sum[kTokenWarps][2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int in = warp & (a.team - 1), f = (int)blockIdx.x * (kTokenWarps / a.team) + warp / a.team;
+    const int width = a.team * 256, k_first = in * 256 + lane * 8;
+    const int64_t up = (int64_t)a.F * a.K;
+    uint4 q[AHEAD][2];
+    auto load = [&](int expert, int k0) {
+        const __nv_bfloat16* w = a.w + ((int64_t)expert * 2 * a.F + f) * a.K;
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d) {
+            const int k = k0 + d * width;
+            if (f < a.F && k < a.K) {
+                q[d][0] = ld_stream_v4(w + k);
+                q[d][1] = ld_stream_v4(w + up + k);
+            }
+        }
+    };
+    if (threadIdx.x == 0) s_expert = -1;
+    pdl_wait();
+    if (a.E == 1) load(0, k_first);          // (its weights are these whether or not it has the row)
+    __syncthreads();
+    bool bad = false;
+    for (int e = threadIdx.x; e < a.E; e += kTokenThreads) {
+        const int begin = a.prefix[e], end = a.prefix[e + 1];
+        bad |= begin < 0 || end > 1 || end < begin;
+        if (begin <= 0 && end >= 1) s_expert = e;
+    }
+    if (bad && blockIdx.x == 0) raise_flag(a.err, EP_DEVERR_RECV_OVERFLOW);
+    __syncthreads();
+    const int expert = s_expert;
+    if (expert >= 0) {
+        if (a.E > 1) load(expert, k_first);
+        uint64_t sum[2] = {};
+        for (int k0 = k_first;;) {
+#pragma unroll
+            for (int d = 0; d < AHEAD; ++d) {
+                const int k = k0 + d * width;
+                if (f >= a.F || k >= a.K) break;
+                const uint4 x = *reinterpret_cast<const uint4*>(a.x + k);
+                add_products(sum[0], q[d][0], x);
+                add_products(sum[1], q[d][1], x);
+            }
+            k0 += AHEAD * width;
+            if (k0 - k_first >= a.K) break;
+            load(expert, k0);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v = __uint_as_float((uint32_t)sum[h]) + __uint_as_float((uint32_t)(sum[h] >> 32));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            if (lane == 0) s_sum[warp][h] = v;
+        }
+        __syncthreads();
+        if (in == 0 && lane == 0 && f < a.F) {
+            float g = 0.0f, u = 0.0f;
+            for (int i = 0; i < a.team; ++i) {
+                g += s_sum[warp + i][0];
+                u += s_sum[warp + i][1];
+            }
+            a.h[f] = __float2bfloat16_rn(activate(g, a.act) * u);
+        }
+    }
+    pdl_trigger();
+}
+
 // ------------------------------------------------------------------ backward
 
 struct Back {
@@ -353,6 +454,18 @@ ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w,
     const bool rows = sh->num_rows > 0;
     if (keep != nullptr && (st = check_sides(keep, rows)) != EP_OK) return st;
     if ((rows && h == nullptr && keep == nullptr) || ((uintptr_t)h & 15) != 0) return EP_ERR_INVALID_ARG;
+    if (sh->num_rows == 1 && keep == nullptr) {
+        TokenArgs t{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(w), expert_prefix,
+                    static_cast<__nv_bfloat16*>(h), launch->error_flags, sh->num_experts, sh->in_features, sh->out_features,
+                    activation, kTokenWarps};
+        // Two pieces of 16 bytes a thread where the block's warps reach that far, else four at a time.
+        while (t.team > 1 && t.team * 256 >= t.K) t.team /= 2;
+        const dim3 grid((unsigned)(((int64_t)t.F * t.team + kTokenWarps - 1) / kTokenWarps));
+        if ((st = begin_call(launch)) != EP_OK) return st;
+        const cudaError_t e = launch_pdl(t.K <= kTokenWarps * 512 ? token_kernel<2> : token_kernel<4>, grid, dim3(kTokenThreads), 0,
+                                         launch->stream, t);
+        return e != cudaSuccess ? cuda_fail(e) : end_call(launch);
+    }
     const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, E = (uint64_t)sh->num_experts;
     GemmArgs a{};
     a.prefix = expert_prefix;
