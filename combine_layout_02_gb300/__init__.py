@@ -241,9 +241,12 @@ def lib():
 # ---------------------------------------------------------------- marshalling helpers
 
 def _ptr(t) -> Optional[int]:
-    """Device pointer of a tensor (None -> NULL). Requires a contiguous CUDA tensor."""
+    """Device pointer of a tensor (None -> NULL). Requires a contiguous CUDA tensor. (An address is
+    passed on: parts of one allocation.)"""
     if t is None:
         return None
+    if isinstance(t, int):
+        return t or None
     if not t.is_cuda:
         raise ValueError("libep takes device tensors")
     if not t.is_contiguous():
@@ -262,8 +265,8 @@ def _check(func: str, status: int):
 
 def _stream_handle(stream) -> Optional[int]:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:          # its handle alone: a Stream object takes longer than most calls of this module
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     return stream.cuda_stream or None
 
 

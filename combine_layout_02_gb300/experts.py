@@ -145,11 +145,17 @@ class _UnsortRows(torch.autograd.Function):
         return dy, dw, None
 
 
-def _checkpoint_like(rows: int, features: int, parts: int, device):
-    """Empty buffers of a checkpoint in 8 bits."""
-    width = -(-features // EP_CHECKPOINT_GROUP) * EP_CHECKPOINT_GROUP * parts
-    return (torch.empty((rows, width), dtype=torch.uint8, device=device),
-            torch.empty((rows, width // EP_CHECKPOINT_GROUP), dtype=torch.uint8, device=device))
+def _kept_width(features: int) -> int:
+    return -(-features // EP_CHECKPOINT_GROUP) * EP_CHECKPOINT_GROUP
+
+
+def _kept_bytes(rows: int, width: int) -> int:
+    """Bytes of a checkpoint in 8 bits, values, then scales, to the next multiple of 16."""
+    return (rows * width + rows * width // EP_CHECKPOINT_GROUP + 15) & ~15
+
+
+def _kept_at(address: int, rows: int, width: int):
+    return make_checkpoint(address, address + rows * width)
 
 
 class _UnsortRowsKept(torch.autograd.Function):
@@ -201,39 +207,58 @@ class _ExpertProduct(torch.autograd.Function):
 
 
 class _FeedForward(torch.autograd.Function):
+    # The host's part of a small call takes longer than the device's, so what is kept, and what only the
+    # backward pass uses, is one allocation each.
     @staticmethod
     def forward(ctx, x, gate_up, down, prefix, act, checkpoint, err):
         (rows, K), (E, H, F) = x.shape, down.shape
         launch, new = make_launch(error_flags=err), x.new_empty
-        ctx.act, ctx.checkpoint, ctx.err = act, checkpoint, err
         for_x, for_gate_up, for_down = ctx.needs_input_grad[:3]
-        kept, rows_kept = (None, None), (None, None)
-        if (for_x or for_gate_up or for_down) and checkpoint != "recompute":
-            kept = (new((rows, 2 * F)), None) if checkpoint == "bf16" else _checkpoint_like(rows, F, 2, x.device)
-            if for_gate_up:
-                rows_kept = (x, None) if checkpoint == "bf16" else checkpoint_rows(x)
-        elif for_x or for_gate_up or for_down:
-            rows_kept = (x, None)
+        wanted = for_x or for_gate_up or for_down
         h, y = new((rows, F)), new((rows, H))
-        ep_expert_gated(ep_gemm_shape(rows, E, K, F), x, gate_up, prefix, act, h,
-                        None if kept[0] is None else make_checkpoint(*kept), launch)
+        kept = rows_kept = keep = None
+        if wanted and checkpoint == "bf16":
+            kept, rows_kept = new((rows, 2 * F)), x if for_gate_up else None
+            keep = make_checkpoint(kept)
+        elif wanted and checkpoint == "e4m3":          # g and u, then the rows
+            wide, width = 2 * _kept_width(F), _kept_width(K)
+            own = _kept_bytes(rows, wide)
+            kept = new(own + (_kept_bytes(rows, width) if for_gate_up else 0), dtype=torch.uint8)
+            keep = _kept_at(kept.data_ptr(), rows, wide)
+            if for_gate_up:
+                ep_checkpoint_rows(rows, K, x, _kept_at(kept.data_ptr() + own, rows, width), launch)
+        elif wanted:
+            rows_kept = x
+        ep_expert_gated(ep_gemm_shape(rows, E, K, F), x, gate_up, prefix, act, h, keep, launch)
         ep_expert_gemm(ep_gemm_shape(rows, E, F, H), h, down, prefix, y, launch)
-        ctx.save_for_backward(gate_up, down, prefix, *kept, *rows_kept)
+        if wanted:
+            ctx.act, ctx.checkpoint, ctx.err = act, checkpoint, err
+            ctx.save_for_backward(gate_up, down, prefix, kept, rows_kept)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
-        gate_up, down, prefix, values, scales, x, x_scales = ctx.saved_tensors
+        gate_up, down, prefix, kept, x = ctx.saved_tensors
         (rows, H), (E, _, F), K = grad.shape, down.shape, gate_up.shape[2]
         grad, launch, new = grad.contiguous(), make_launch(error_flags=ctx.err), grad.new_empty
         for_x, for_gate_up, for_down = ctx.needs_input_grad[:3]
-        if ctx.checkpoint == "recompute":
-            values = new((rows, 2 * F))
-            ep_expert_gated(ep_gemm_shape(rows, E, K, F), x, gate_up, prefix, ctx.act, None, make_checkpoint(values), launch)
-        dgu, h = new((rows, 2 * F)), new((rows, F)) if for_down else None
         down_shape, up_shape = ep_gemm_shape(rows, E, F, H), ep_gemm_shape(rows, E, K, 2 * F)
-        ep_expert_gated_dgrad(down_shape, grad, down, prefix, ctx.act, make_checkpoint(values, scales), dgu, h, launch)
+        if ctx.checkpoint == "e4m3":
+            wide, width = 2 * _kept_width(F), _kept_width(K)
+            own = _kept_at(kept.data_ptr(), rows, wide)
+        else:
+            if ctx.checkpoint == "recompute":
+                kept = new((rows, 2 * F))
+                ep_expert_gated(ep_gemm_shape(rows, E, K, F), x, gate_up, prefix, ctx.act, None, make_checkpoint(kept), launch)
+            own = make_checkpoint(kept)
+        eight = ctx.checkpoint == "e4m3" and for_gate_up
+        room = max(16, ep_wgrad_checkpoint_workspace_size(up_shape)) if eight else 0
+        scratch = new(rows * F * (6 if for_down else 4) + room, dtype=torch.uint8)          # the workspace, dgu, h
+        workspace = scratch[:room] if eight else None
+        dgu = scratch.data_ptr() + room
+        h = dgu + rows * F * 4 if for_down else None
+        ep_expert_gated_dgrad(down_shape, grad, down, prefix, ctx.act, own, dgu, h, launch)
         dx = dgate_up = ddown = None
         if for_down:
             ddown = torch.empty_like(down)
@@ -241,13 +266,13 @@ class _FeedForward(torch.autograd.Function):
         if for_x:
             dx = new((rows, K))
             ep_expert_gemm_dgrad(up_shape, dgu, gate_up, prefix, dx, launch)
-        if for_gate_up:
+        if eight:
             dgate_up = torch.empty_like(gate_up)
-            if x_scales is None:
-                ep_expert_gemm_wgrad(up_shape, dgu, x, prefix, dgate_up, launch)
-            else:
-                workspace = new(max(16, ep_wgrad_checkpoint_workspace_size(up_shape)), dtype=torch.uint8)
-                ep_expert_gemm_wgrad_checkpoint(up_shape, dgu, make_checkpoint(x, x_scales), prefix, dgate_up, workspace, launch)
+            at = kept.data_ptr() + _kept_bytes(rows, wide)
+            ep_expert_gemm_wgrad_checkpoint(up_shape, dgu, _kept_at(at, rows, width), prefix, dgate_up, workspace, launch)
+        elif for_gate_up:
+            dgate_up = torch.empty_like(gate_up)
+            ep_expert_gemm_wgrad(up_shape, dgu, x, prefix, dgate_up, launch)
         return dx, dgate_up, ddown, None, None, None, None
 
 
@@ -272,16 +297,17 @@ def checkpoint_rows(x: torch.Tensor):
     """x [rows][features] bf16 -> (values, scales): the rows in 8 bits, uint8 [rows][features padded to
     16] of e4m3 and uint8 [rows][groups of 16], for a backward pass (see ep_checkpoint in ep.h)."""
     _check("x", x, torch.bfloat16, None, None)
-    kept = _checkpoint_like(*x.shape, 1, x.device)
-    ep_checkpoint_rows(*x.shape, x, make_checkpoint(*kept), make_launch())
-    return kept
+    (rows, features), width = x.shape, _kept_width(x.shape[1])
+    values, scales = (torch.empty((rows, n), dtype=torch.uint8, device=x.device) for n in (width, width // EP_CHECKPOINT_GROUP))
+    ep_checkpoint_rows(rows, features, x, make_checkpoint(values, scales), make_launch())
+    return values, scales
 
 
 def restore_rows(values: torch.Tensor, scales: torch.Tensor, features: int) -> torch.Tensor:
     """The rows [rows][features] in bf16 that checkpoint_rows has kept."""
-    groups = -(-features // EP_CHECKPOINT_GROUP)
-    _check("values", values, torch.uint8, None, groups * EP_CHECKPOINT_GROUP)
-    _check("scales", scales, torch.uint8, values.shape[0], groups)
+    width = _kept_width(features)
+    _check("values", values, torch.uint8, None, width)
+    _check("scales", scales, torch.uint8, values.shape[0], width // EP_CHECKPOINT_GROUP)
     x = torch.empty((values.shape[0], features), dtype=torch.bfloat16, device=values.device)
     ep_restore_rows(*x.shape, make_checkpoint(values, scales), x, make_launch())
     return x
