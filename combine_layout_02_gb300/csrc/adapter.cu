@@ -317,7 +317,7 @@ struct AdapterFew : AdapterSide {
     static constexpr bool kFollows = true;
     static constexpr int kGroup = 4, kRows = 256, kTaken = 8 / G;          // rows whose B is in registers at a time
     // shared: low of each half, then the rows' adapters
-    static constexpr int kLow = kGroup * EP_ADAPTER_MAX_RANK, kIds = 2 * kLow, kFloats = kIds + kRows;
+    static constexpr int kLow = kGroup * EP_ADAPTER_MAX_RANK, kIds = 2 * kLow, kFloats = kIds + kRows, kFewFloats = kFloats;
     int together;          // groups whose low is held at a time: a power of two, one with 256 ranks
 
     explicit AdapterFew(const AdapterSide& side) : AdapterSide(side), together(1) {

@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const uint4* __restrict_
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = larger_bf16x2(m, w[j]);
+        for (int j = 0; j < 8; ++j) m = larger_bf16x2(m, magnitudes(w[j]));
         const uint32_t e = kept_exponent(larger_bf16x2(m, m >> 16) & 0xFFFFu);
         const float inv = kept_inverse(e);
         uint32_t q[4];

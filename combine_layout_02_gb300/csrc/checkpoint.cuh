@@ -17,19 +17,17 @@ namespace ep {
 constexpr int kKeptGroup = EP_CHECKPOINT_GROUP;
 __host__ __device__ __forceinline__ int kept_features(int features) { return (features + kKeptGroup - 1) & ~(kKeptGroup - 1); }
 
-// Magnitudes of bf16 pairs and the larger of two, half by half; NaN gives way to a number.
+// Magnitudes of a bf16 pair, and the larger of two pairs' values, half by half; NaN gives way to a number.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t a) { return a & 0x7FFF7FFFu; }
 __device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
-    __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&a), y = *reinterpret_cast<__nv_bfloat162*>(&b);
-    const __nv_bfloat162 m = __hmax2(__habs2(x), __habs2(y));
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// k + 127 from a group's largest magnitude (the bits of a bf16 without its sign): 1 for zeros (2^-126),
-// 247 or less for an infinity, whose e4m3 value 448 * 2^120 comes back as one.
-__device__ __forceinline__ uint32_t kept_exponent(uint32_t amax) {
-    const int e = (int)(amax >> 7) - 8 + ((amax & 0x7Fu) > 0x60u ? 1 : 0);
-    return (uint32_t)(e > 1 ? e : 1);
-}
+// k + 127 from a group's largest magnitude (the bits of a bf16 without its sign): its exponent less 8, and one
+// more where its mantissa is above 1.75, which then carries over. 1 for zeros (2^-126), 247 or less for
+// an infinity, whose e4m3 value 448 * 2^120 comes back as one.
+__device__ __forceinline__ uint32_t kept_exponent(uint32_t amax) { return max((amax + 0x1Fu) >> 7, 9u) - 8; }
 __device__ __forceinline__ float kept_scale(uint32_t exponent) { return __uint_as_float(exponent << 23); }
 __device__ __forceinline__ float kept_inverse(uint32_t exponent) { return __uint_as_float((254u - exponent) << 23); }
 

@@ -19,18 +19,27 @@ struct Activated {
 };
 __device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 constexpr float kGelu = 1.5957691216057308f, kCubic = 0.044715f;
-__device__ __forceinline__ float activate(float g, int act) {
-    if (act == EP_ACT_SILU) return g * logistic(g);
-    const float t = fminf(fmaxf(g, -16.0f), 16.0f);
-    return g * logistic(kGelu * (t + kCubic * t * t * t));
-}
-__device__ __forceinline__ Activated activate_both(float g, int act) {
-    if (act == EP_ACT_SILU) {
-        const float s = logistic(g);
-        return {g * s, s * (1.0f + g * (1.0f - s))};
+template <int ACT>
+__device__ __forceinline__ float gate_slope_at(float& z, float g) {          // z, and its slope
+    if (ACT == EP_ACT_SILU) {
+        z = g;
+        return 1.0f;
     }
-    const float t = fminf(fmaxf(g, -16.0f), 16.0f), s = logistic(kGelu * (t + kCubic * t * t * t));
-    return {g * s, s + g * (s * (1.0f - s)) * (kGelu * (1.0f + 3.0f * kCubic * t * t))};
+    const float t = fminf(fmaxf(g, -16.0f), 16.0f), t2 = t * t;
+    z = kGelu * t * fmaf(kCubic, t2, 1.0f);
+    return kGelu * fmaf(3.0f * kCubic, t2, 1.0f);
+}
+template <int ACT>
+__device__ __forceinline__ float activate(float g) {
+    float z;
+    gate_slope_at<ACT>(z, g);
+    return g * logistic(z);
+}
+template <int ACT>
+__device__ __forceinline__ Activated activate_both(float g) {
+    float z;
+    const float dz = gate_slope_at<ACT>(z, g), s = logistic(z), v = g * s;
+    return {v, ACT == EP_ACT_SILU ? fmaf(v, 1.0f - s, s) : fmaf(v * (1.0f - s), dz, s)};
 }
 
 // ------------------------------------------------------------------ what is kept
@@ -43,7 +52,7 @@ enum Keep { kNone, kBf16, kE4m3 };
 struct Kept {
     void* values;
     uint8_t* scales;
-    int F, padded, act;
+    int F, padded;
     int64_t rows;
     __device__ __forceinline__ __nv_bfloat16* halves(int64_t row, int side) const {
         return reinterpret_cast<__nv_bfloat16*>(values) + (2 * row + side) * F;
@@ -60,113 +69,91 @@ struct Kept {
 
 // The M side has eight rows of Wg and eight of Wu in turn, so that a warp has both sums of a feature
 // in the same place of two sets of eight lanes, and a tile of 256 covers 128 features.
-template <Keep KEEP>
+template <Keep KEEP, int ACT>
 struct Gated : NoExtra {
     static constexpr bool kPairs = true, kWrites = true;
+    static constexpr int kStaged = 1024, kFloats = kWarps * kStaged / 4, kFewFloats = kFloats;
     Kept kept;
-    __device__ __forceinline__ void tile(uint32_t tmem, float*, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows,
+    __device__ __forceinline__ void tile(uint32_t tmem, float* shared, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows,
                                          int m0, int M, int half, int lane) const {
-        write<kWarps / 4>(tmem, out, row0, rows, m0, M, half, lane);
+        write<kWarps / 4>(tmem, smem_addr(shared) + ((threadIdx.x >> 5) - 4) * kStaged, out, row0, rows, m0, M, half, lane);
     }
     __device__ __forceinline__ void prefetch(int64_t, int, int, int, int) const {}
-    // 16 features x 32 rows at a time, in sets s of 16, each step for all of them before the next (a step's
-    // results take tens of cycles, and there are two warps a scheduler). Lane 4g + c has rows 2c, 2c+1 of
-    // features g (t = 0) and 8 + g (t = 1) of both blocks b of a set; after the transpositions the four
-    // lanes of row g have eight features each of both blocks.
-    static constexpr int kSets = 2;
-    template <int PARTS>          // how many warps share the rows
-    __device__ __forceinline__ void write(uint32_t tmem, __nv_bfloat16* out, int64_t row0, int rows, int m0, int M, int part,
-                                          int lane) const {
-        const int g = lane >> 2, c = lane & 3, F = M / 2, f0 = m0 / 2;
-        if (f0 >= F) return;
-        const int f = f0 + (c & 1) * 8, at = (c >> 1) * 8 + g;
-        for (int n = part * 16 * kSets; n < rows; n += PARTS * 16 * kSets) {
-            float v[kSets][2][2][4];
+
+    // 16 features x 32 rows at a time, blocks b of 8 rows. Lane 4g + c has rows 2c, 2c+1 of features 8t + g of
+    // each block. By way of shared memory a lane gets eight features, chunk lane & 1, of rows lane / 2 and
+    // 16 + lane / 2: 16 bytes in bf16. (Chunks of row r lie r from the first, the second ones' rows swapped
+    // by fours, so that neither direction meets in a bank. Exchanging registers between lanes instead
+    // took twice the instructions, which bound short contractions.)
+    static __device__ __forceinline__ void by_rows(const uint32_t (&p)[2][4], uint32_t stage, int lane, uint4 (&q)[2]) {
+        __syncwarp();          // what was there has been read
 #pragma unroll
-            for (int s = 0; s < kSets; ++s)
+        for (int t = 0; t < 2; ++t) store_blocks(stage + t * 512 + ((lane ^ (t * 4)) << 4), p[t]);
+        __syncwarp();
+        const int t = lane & 1, r = lane >> 1;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    tmem_load_16x8(tmem + n + s * 16 + b * 8, v[s][b][0]);
-                    tmem_load_16x8(tmem + n + s * 16 + b * 8 + (16u << 16), v[s][b][1]);
-                }
-#pragma unroll
-            for (int s = 0; s < kSets; ++s)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) tmem_wait(v[s][b]);
-            const int64_t row = row0 + n + at;
-            if (out != nullptr) {
-                uint32_t p[kSets][4];
-#pragma unroll
-                for (int s = 0; s < kSets; ++s)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float(&w)[4] = v[s][i >> 1][i & 1];
-                        p[s][i] = transpose_8x8(pack_bf16x2(activate(w[0], kept.act) * w[2], activate(w[1], kept.act) * w[3]));
-                    }
-                transpose_quads(p, c);
-#pragma unroll
-                for (int s = 0; s < kSets; ++s)
-                    if (n + s * 16 + at < rows && f < F) st_v4(out + (row + s * 16) * F + f, words(p[s]));
-            }
-            if constexpr (KEEP != kNone) keep_rows(v, row, rows - n - at, f0, F, c);
-        }
+        for (int j = 0; j < 2; ++j) q[j] = ld_shared_v4(stage + t * 512 + (((r + j * 16) ^ (t * 4)) << 4));
     }
-    // g and u of those rows; `row` is this lane's of the first set, `left` how many there are from it on.
-    __device__ __forceinline__ void keep_rows(const float (&v)[kSets][2][2][4], int64_t row, int left, int f0, int F, int c) const {
-        uint32_t side[2][kSets][4];          // g, u: block b's features 8t + 2c, 2c+1 of row g in 2b + t
+    template <int PARTS>          // how many warps share the rows
+    __device__ __forceinline__ void write(uint32_t tmem, uint32_t stage, __nv_bfloat16* out, int64_t row0, int rows, int m0, int M,
+                                          int part, int lane) const {
+        const int F = M / 2, f0 = m0 / 2, f = f0 + (lane & 1) * 8;
+        if (f0 >= F) return;
+        for (int n = part * 32; n < rows; n += PARTS * 32) {
+            float v[4][2][4];
 #pragma unroll
-        for (int s = 0; s < kSets; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float(&w)[4] = v[s][i >> 1][i & 1];
-                side[0][s][i] = transpose_8x8(pack_bf16x2(w[0], w[1]));
-                side[1][s][i] = transpose_8x8(pack_bf16x2(w[2], w[3]));
+            for (int b = 0; b < 4; ++b) {
+                tmem_load_16x8(tmem + n + b * 8, v[b][0]);
+                tmem_load_16x8(tmem + n + b * 8 + (16u << 16), v[b][1]);
             }
-        if constexpr (KEEP == kBf16) {
-            const int f = f0 + (c & 1) * 8;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) transpose_quads(side[h], c);
+            for (int b = 0; b < 4; ++b) tmem_wait(v[b]);
+            const int64_t row = row0 + n + (lane >> 1);
+            const int left = rows - n - (lane >> 1);          // of the rows from that one on
+            uint32_t p[2][4];
+            uint4 q[2];
+            if (out != nullptr) {
 #pragma unroll
-            for (int s = 0; s < kSets; ++s)
+                for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (s * 16 < left && f < F) st_v4(kept.halves(row + s * 16, h) + f, words(side[h][s]));
-        } else {
-            uint32_t p[kSets][4], m[kSets][2];
+                    for (int t = 0; t < 2; ++t)
+                        p[t][b] = pack_bf16x2(activate<ACT>(v[b][t][0]) * v[b][t][2], activate<ACT>(v[b][t][1]) * v[b][t][3]);
+                by_rows(p, stage, lane, q);
 #pragma unroll
-            for (int s = 0; s < kSets; ++s)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {          // g's and u's maximum
-                    const uint32_t mg = larger_bf16x2(side[0][s][2 * b], side[0][s][2 * b + 1]);
-                    const uint32_t mu = larger_bf16x2(side[1][s][2 * b], side[1][s][2 * b + 1]);
-                    m[s][b] = larger_bf16x2(__byte_perm(mg, mu, 0x5410), __byte_perm(mg, mu, 0x7632));
-                }
-#pragma unroll
-            for (int bit = 1; bit <= 2; bit *= 2)
-#pragma unroll
-                for (int s = 0; s < kSets; ++s)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) m[s][b] = larger_bf16x2(m[s][b], __shfl_xor_sync(0xFFFFFFFFu, m[s][b], bit));
-#pragma unroll
-            for (int s = 0; s < kSets; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {          // block i / 2, side i & 1
-                    const int b = i >> 1, h = i & 1;
-                    const float inv = kept_inverse(kept_exponent(h ? m[s][b] >> 16 : m[s][b] & 0xFFFFu));
-                    p[s][i] = keep_pair(side[h][s][2 * b], inv) | keep_pair(side[h][s][2 * b + 1], inv) << 16;
-                }
-            transpose_quads(p, c);          // lane c: all 16 features of block c / 2, side c & 1
-#pragma unroll
-            for (int s = 0; s < kSets; ++s) {
-                if (s * 16 >= left) break;
-                const uint32_t(&q)[4] = p[s];
-                st_v4(kept.bytes(row + s * 16, c & 1) + f0, make_uint4(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
-                                                                       __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632)));
-                if (c & 1) continue;
-                const uint32_t most = c & 2 ? m[s][1] : m[s][0];
-                *reinterpret_cast<uint16_t*>(kept.exponent(row + s * 16, 0, f0)) =
-                    (uint16_t)(kept_exponent(most & 0xFFFFu) | kept_exponent(most >> 16) << 8);
+                for (int j = 0; j < 2; ++j)
+                    if (j * 16 < left && f < F) st_v4(out + (row + j * 16) * F + f, q[j]);
             }
+            uint32_t exponent[2][2];          // by side, row
+#pragma unroll
+            for (int h = 0; h < (KEEP == kNone ? 0 : 2); ++h) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) p[t][b] = pack_bf16x2(v[b][t][2 * h], v[b][t][2 * h + 1]);
+                by_rows(p, stage, lane, q);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (KEEP == kBf16) {
+                        if (j * 16 < left && f < F) st_v4(kept.halves(row + j * 16, h) + f, q[j]);
+                        continue;
+                    }
+                    // The group is this lane's eight features and its neighbour's.
+                    uint32_t m = larger_bf16x2(magnitudes(q[j].x), magnitudes(q[j].y));
+                    m = larger_bf16x2(m, larger_bf16x2(magnitudes(q[j].z), magnitudes(q[j].w)));
+                    m = larger_bf16x2(m, __byte_perm(m, 0, 0x1032));
+                    m = larger_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                    const uint32_t e = exponent[h][j] = kept_exponent(m & 0xFFFFu);
+                    const float inv = kept_inverse(e);
+                    const uint2 eight = make_uint2(keep_pair(q[j].x, inv) | keep_pair(q[j].y, inv) << 16,
+                                                   keep_pair(q[j].z, inv) | keep_pair(q[j].w, inv) << 16);
+                    if (j * 16 < left) *reinterpret_cast<uint2*>(kept.bytes(row + j * 16, h) + f) = eight;
+                }
+            }
+            if (KEEP == kE4m3 && (lane & 1) == 0)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (j * 16 < left)
+                        *reinterpret_cast<uint16_t*>(kept.exponent(row + j * 16, 0, f0)) = (uint16_t)(exponent[0][j] | exponent[1][j] << 8);
         }
     }
 };
@@ -266,7 +253,7 @@ __global__ void __launch_bounds__(kTokenThreads, AHEAD == 2 ? 6 : 4) token_kerne
                 g += s_sum[warp + i][0];
                 u += s_sum[warp + i][1];
             }
-            a.h[f] = __float2bfloat16_rn(activate(g, a.act) * u);
+            a.h[f] = __float2bfloat16_rn((a.act == EP_ACT_SILU ? activate<EP_ACT_SILU>(g) : activate<EP_ACT_GELU_TANH>(g)) * u);
         }
     }
     pdl_trigger();
@@ -279,12 +266,12 @@ struct Back {
     __nv_bfloat16* h;            // [rows][F], NULL to leave out
 };
 
-// The sums are dh. What was kept is read by rows, eight features a lane, and brought into the sums'
-// layout by the transpositions of rows_of_features in reverse (its values are exact in bf16).
-template <Keep KEEP>
+// The sums are dh. What was kept is read by rows, eight features a lane, and comes into the sums' layout by way
+// of shared memory, as the results come out of it (its values are exact in bf16).
+template <Keep KEEP, int ACT>
 struct GatedBack : NoExtra {
     static constexpr bool kWrites = true;
-    static constexpr int kWarps = 16;
+    static constexpr int kWarps = 16, kStaged = 512, kFloats = kWarps * kStaged / 4, kFewFloats = 8 * kStaged / 4;
     Kept kept;
     Back to;
     // Eight features of one row's side as they are stored, and as four bf16 pairs.
@@ -297,13 +284,10 @@ struct GatedBack : NoExtra {
         asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "l"(kept.bytes(row, side) + f));
         return {make_uint4(q.x, q.y, __ldg(kept.exponent(row, side, f)), 0)};
     }
-    static __device__ __forceinline__ void pairs(const Raw& r, uint32_t (&p)[4]) {
-        if constexpr (KEEP == kBf16) {
-            p[0] = r.q.x, p[1] = r.q.y, p[2] = r.q.z, p[3] = r.q.w;
-        } else {
-            const float s = kept_scale(r.q.z);
-            p[0] = kept_pair(r.q.x, s), p[1] = kept_pair(r.q.x >> 16, s), p[2] = kept_pair(r.q.y, s), p[3] = kept_pair(r.q.y >> 16, s);
-        }
+    static __device__ __forceinline__ uint4 pairs(const Raw& r) {
+        if constexpr (KEEP == kBf16) return r.q;
+        const float s = kept_scale(r.q.z);
+        return make_uint4(kept_pair(r.q.x, s), kept_pair(r.q.x >> 16, s), kept_pair(r.q.y, s), kept_pair(r.q.y >> 16, s));
     }
     __device__ __forceinline__ void prepare(float*, unsigned char*, int64_t row0, int rows, int m0) const {
         prefetch(row0, rows, m0, threadIdx.x - 128, 32 * kWarps);
@@ -317,16 +301,19 @@ struct GatedBack : NoExtra {
             for (int o = 0; o < width; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + o));
         }
     }
-    __device__ __forceinline__ void tile(uint32_t tmem, float*, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows, int m0,
+    __device__ __forceinline__ void tile(uint32_t tmem, float* shared, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows, int m0,
                                          int M, int half, int lane) const {
-        write<kWarps / 4>(tmem, out, row0, rows, m0, M, half, lane);
+        write<kWarps / 4>(tmem, smem_addr(shared) + ((threadIdx.x >> 5) - 4) * kStaged, out, row0, rows, m0, M, half, lane);
     }
-    // 32 features x 8 rows at a time; the next rows' loads are under way meanwhile.
+    // 32 features x 8 rows at a time; the next rows' loads are under way meanwhile. In shared memory chunk t
+    // of eight features of row r is at 8t + (r ^ 2t), so that neither direction meets in a bank: `by_row` is
+    // where this lane's row lane / 4 and chunk lane & 3 are, `by_block` where row lane & 7 of block lane / 8 is.
     template <int PARTS>
-    __device__ __forceinline__ void write(uint32_t tmem, __nv_bfloat16*, int64_t row0, int rows, int m0, int M, int part,
+    __device__ __forceinline__ void write(uint32_t tmem, uint32_t stage, __nv_bfloat16*, int64_t row0, int rows, int m0, int M, int part,
                                           int lane) const {
         if (m0 >= M) return;
         const int g = lane >> 2, c = lane & 3, f = m0 + c * 8;
+        const uint32_t by_row = stage + ((c * 8 + (g ^ (2 * c))) << 4), by_block = stage + (((lane & ~7) + ((lane & 7) ^ (lane >> 3 << 1))) << 4);
         Raw next[2] = {};
         if (part * 8 + g < rows && f < M)
 #pragma unroll
@@ -336,34 +323,37 @@ struct GatedBack : NoExtra {
             const int64_t row = row0 + n + g;
             uint32_t side[2][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) pairs(next[h], side[h]);
+            for (int h = 0; h < 2; ++h) {
+                __syncwarp();
+                st_shared_v4(by_row, pairs(next[h]));
+                __syncwarp();
+                load_blocks(by_block, side[h]);
+            }
             if (n + 8 * PARTS + g < rows && f < M)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) next[h] = load(row + 8 * PARTS, h, f);
             float v[2][4];
             tmem_load_16x8(tmem + n, v[0]);
             tmem_load_16x8(tmem + n + (16u << 16), v[1]);
-            transpose_quads(side, c);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) side[h][i] = transpose_8x8(side[h][i]);
             tmem_wait(v);
             uint32_t p[3][4];          // dg, du, h
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float d0 = v[i >> 1][(i & 1) * 2], d1 = v[i >> 1][(i & 1) * 2 + 1];
                 const float u0 = bf16_lo(side[1][i]), u1 = bf16_hi(side[1][i]);
-                const Activated a0 = activate_both(bf16_lo(side[0][i]), kept.act), a1 = activate_both(bf16_hi(side[0][i]), kept.act);
-                p[0][i] = transpose_8x8(pack_bf16x2(d0 * u0 * a0.slope, d1 * u1 * a1.slope));
-                p[1][i] = transpose_8x8(pack_bf16x2(d0 * a0.value, d1 * a1.value));
-                p[2][i] = transpose_8x8(pack_bf16x2(a0.value * u0, a1.value * u1));
+                const Activated a0 = activate_both<ACT>(bf16_lo(side[0][i])), a1 = activate_both<ACT>(bf16_hi(side[0][i]));
+                p[0][i] = pack_bf16x2(d0 * u0 * a0.slope, d1 * u1 * a1.slope);
+                p[1][i] = pack_bf16x2(d0 * a0.value, d1 * a1.value);
+                p[2][i] = pack_bf16x2(a0.value * u0, a1.value * u1);
             }
-            transpose_quads(p, c);
-            if (there) {
-                st_v4(to.dgu + 2 * row * M + f, words(p[0]));
-                st_v4(to.dgu + (2 * row + 1) * M + f, words(p[1]));
-                if (to.h != nullptr) st_v4(to.h + row * M + f, words(p[2]));
+#pragma unroll
+            for (int h = 0; h < 3; ++h) {
+                if (h == 2 && to.h == nullptr) break;
+                __syncwarp();
+                store_blocks(by_block, p[h]);
+                __syncwarp();
+                const uint4 q = ld_shared_v4(by_row);
+                if (there) st_v4(h == 2 ? to.h + row * M + f : to.dgu + (2 * row + h) * M + f, q);
             }
         }
     }
@@ -387,8 +377,8 @@ ep_status check_sides(const ep_checkpoint* c, bool rows) {
     return st == EP_OK && ((uintptr_t)c->scales & 1) != 0 ? EP_ERR_INVALID_ARG : st;
 }
 
-Kept kept_of(const ep_checkpoint* c, int F, int act, int rows) {
-    Kept k{nullptr, nullptr, F, kept_features(F), act, rows};
+Kept kept_of(const ep_checkpoint* c, int F, int rows) {
+    Kept k{nullptr, nullptr, F, kept_features(F), rows};
     if (c != nullptr) k.values = c->values, k.scales = c->scales;
     return k;
 }
@@ -427,15 +417,26 @@ ep_status encode_rows(GemmMaps* maps, const GemmArgs& a, const void* rows) {
 }
 
 template <Keep KEEP>
-ep_status forward(const GemmMaps& maps, const GemmArgs& a, const Kept& kept, cudaStream_t stream) {
-    Gated<KEEP> extra;
+ep_status forward(const GemmMaps& maps, const GemmArgs& a, int act, const Kept& kept, cudaStream_t stream) {
+    if (act == EP_ACT_SILU) {
+        Gated<KEEP, EP_ACT_SILU> extra;
+        extra.kept = kept;
+        return run_block<kForward>(maps, a, extra, stream);
+    }
+    Gated<KEEP, EP_ACT_GELU_TANH> extra;
     extra.kept = kept;
     return run_block<kForward>(maps, a, extra, stream);
 }
 
 template <Keep KEEP>
-ep_status backward(const GemmMaps& maps, const GemmArgs& a, const Kept& kept, const Back& to, cudaStream_t stream) {
-    GatedBack<KEEP> extra;
+ep_status backward(const GemmMaps& maps, const GemmArgs& a, int act, const Kept& kept, const Back& to, cudaStream_t stream) {
+    if (act == EP_ACT_SILU) {
+        GatedBack<KEEP, EP_ACT_SILU> extra;
+        extra.kept = kept;
+        extra.to = to;
+        return run_block<kDgrad>(maps, a, extra, stream);
+    }
+    GatedBack<KEEP, EP_ACT_GELU_TANH> extra;
     extra.kept = kept;
     extra.to = to;
     return run_block<kDgrad>(maps, a, extra, stream);
@@ -485,10 +486,10 @@ ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w,
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
-        const Kept kept = kept_of(keep, sh->out_features, activation, sh->num_rows);
-        st = keep == nullptr              ? forward<kNone>(maps, a, kept, launch->stream)
-             : keep->dtype == EP_BF16 ? forward<kBf16>(maps, a, kept, launch->stream)
-                                          : forward<kE4m3>(maps, a, kept, launch->stream);
+        const Kept kept = kept_of(keep, sh->out_features, sh->num_rows);
+        st = keep == nullptr              ? forward<kNone>(maps, a, activation, kept, launch->stream)
+             : keep->dtype == EP_BF16 ? forward<kBf16>(maps, a, activation, kept, launch->stream)
+                                          : forward<kE4m3>(maps, a, activation, kept, launch->stream);
         if (st != EP_OK) return st;
     }
     return end_call(launch);
@@ -519,9 +520,9 @@ ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const v
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
-        const Kept k = kept_of(kept, sh->in_features, activation, sh->num_rows);
+        const Kept k = kept_of(kept, sh->in_features, sh->num_rows);
         const Back to{reinterpret_cast<__nv_bfloat16*>(dgu), reinterpret_cast<__nv_bfloat16*>(h)};
-        st = kept->dtype == EP_BF16 ? backward<kBf16>(maps, a, k, to, launch->stream) : backward<kE4m3>(maps, a, k, to, launch->stream);
+        st = kept->dtype == EP_BF16 ? backward<kBf16>(maps, a, activation, k, to, launch->stream) : backward<kE4m3>(maps, a, activation, k, to, launch->stream);
         if (st != EP_OK) return st;
     }
     return end_call(launch);

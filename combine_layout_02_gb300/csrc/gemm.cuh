@@ -440,36 +440,49 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
     return t;
 }
-// Within quads of lanes, N times: lane c has word h of its own in p[.][h], and gets word c of lane h in place h.
-template <int N>
-__device__ __forceinline__ void transpose_quads(uint32_t (&p)[N][4], int c) {
-#pragma unroll
-    for (int bit = 1; bit <= 2; bit *= 2)
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                if (h & bit) continue;
-                const bool up = c & bit;
-                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? p[n][h] : p[n][h | bit], bit);
-                if (up) p[n][h] = got;
-                else p[n][h | bit] = got;
-            }
+// Four 8 x 8 blocks of 16-bit values to and from shared memory, transposed: lane 4g + c has rows 2c, 2c+1 of
+// column g of block i in word i; lane 8i + r gives the address of row r (16 bytes) of block i.
+__device__ __forceinline__ void store_blocks(uint32_t at, const uint32_t (&v)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3])
+                 : "memory");
 }
-__device__ __forceinline__ uint4 words(const uint32_t (&p)[4]) { return make_uint4(p[0], p[1], p[2], p[3]); }
+__device__ __forceinline__ void load_blocks(uint32_t at, uint32_t (&v)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 // Sums of 32 features x 8 rows in the layout of tmem_load_16x8 (lane 4g + c: rows 2c, 2c+1 of features
 // g, 8 + g in v[0], 16 + g, 24 + g in v[1]) -> bf16, lane 4g + c the eight features 8c .. 8c+7 of row
 // g: a transposition within 8 x 8 blocks and one within quads of lanes. A lane then stores 16
 // bytes, a warp 64 bytes of eight rows.
 __device__ __forceinline__ uint4 rows_of_features(const float (&v)[2][4], int c) {
-    uint32_t p[1][4];
+    uint32_t p[4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        p[0][2 * t] = transpose_8x8(pack_bf16x2(v[t][0], v[t][1]));
-        p[0][2 * t + 1] = transpose_8x8(pack_bf16x2(v[t][2], v[t][3]));
+        p[2 * t] = transpose_8x8(pack_bf16x2(v[t][0], v[t][1]));
+        p[2 * t + 1] = transpose_8x8(pack_bf16x2(v[t][2], v[t][3]));
     }
-    transpose_quads(p, c);
-    return words(p[0]);
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit *= 2)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            if (h & bit) continue;
+            const bool up = c & bit;
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? p[h] : p[h | bit], bit);
+            if (up) p[h] = got;
+            else p[h | bit] = got;
+        }
+    return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
 // wgrad: a lane holds 64 consecutive columns of one row of dW; a warp stages its 32 rows x 64 columns
@@ -493,7 +506,7 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 }
 
 // What an epilogue adds to the sums before they are rounded; all 128 epilogue threads make the calls
-// together, each for output feature m. `shared`: kFloats floats of the block. kFollows: the kernel
+// together, each for output feature m. `shared`: kFloats floats of the block (gemm_split_kernel: kFewFloats). kFollows: the kernel
 // directly follows one of this library after which the call's inputs are complete; only the
 // epilogue waits for that kernel itself.
 //   gemm_kernel:        tile writes rows row0 .. row0 + rows - 1 of a tile, features m0 .. m0 + 31, out of
@@ -503,13 +516,14 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 //   gemm_split_kernel:  ahead for the CTA's rows while the products run (before that wait), then apply
 //                       for each kGroup of them: v[j] belongs to row row0 + c + j. Two halves of 128
 //                       threads take groups in turn. kWrites: what is written is not the sums alone:
-//                       write does it from tensor memory, as tile, where joined sums have gone back to,
+//                       write does it from tensor memory, as tile, where joined sums have gone back to
+//                       (each warp with kStaged of the shared bytes),
 //                       and prefetch is called before for the rows, while the products run
 // kPairs (forward): the M side is two projections of out_features each, eight rows of one and eight of the
 // other in turn (maps.a has five dimensions: in_features, 8, 2, out_features / 8, experts).
 struct NoExtra {
     static constexpr bool kFollows = false, kWrites = false, kPairs = false;
-    static constexpr int kFloats = 4, kGroup = 32, kWarps = kTileWarps;
+    static constexpr int kFloats = 4, kFewFloats = 4, kGroup = 32, kWarps = kTileWarps;
     __device__ __forceinline__ bool reordered() const { return false; }
     __device__ __forceinline__ void prepare(float*, unsigned char*, int64_t, int, int) const {}
     // Sixteen rows at a time, to have two blocks' steps in flight.
@@ -874,7 +888,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done, drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int dead;
-    __shared__ __align__(16) float s_extra[Extra::kFloats];
+    __shared__ __align__(16) float s_extra[Extra::kFewFloats];
     __shared__ Tile s_tile;
     __shared__ int s_has;
     __shared__ int s_complete;             // this CTA's part is
@@ -997,7 +1011,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     if (D != kWgrad && a.split == 1) {
         if constexpr (Extra::kWrites) {
             if (ok && warp >= 2)
-                extra.template write<2>(tmem + ((uint32_t)quarter << 21), a.out, t.n0, rows, m - lane, a.M, half, lane);
+                extra.template write<2>(tmem + ((uint32_t)quarter << 21), smem_addr(s_extra) + (warp - 2) * Extra::kStaged, a.out, t.n0, rows,
+                                        m - lane, a.M, half, lane);
         } else if (ok && warp >= 2) {
             for (int c = half * G; c < rows; c += 2 * G) {
                 float v[G];
@@ -1060,7 +1075,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 tc_fence_before();
                 fine = epilogue_all<256>(fine);
                 tc_fence_after();
-                if (fine) extra.template write<2>(tmem + ((uint32_t)quarter << 21), a.out, t.n0 + lo, hi - lo, m - lane, a.M, half, lane);
+                if (fine)
+                    extra.template write<2>(tmem + ((uint32_t)quarter << 21), smem_addr(s_extra) + (warp - 2) * Extra::kStaged, a.out,
+                                            t.n0 + lo, hi - lo, m - lane, a.M, half, lane);
             }
         } else if (ok && warp >= 2 && lo < hi) {
             for (int c = lo + half * G; c < hi; c += 2 * G) {
@@ -1154,7 +1171,8 @@ constexpr int kSplitSmemMax = 201 * 1024, kGemmSmemMax = 222 * 1024, kWgradSmemM
 template <class Kernel, class Extra>
 cudaError_t launch_gemm_as(Kernel kernel, int smem_most, unsigned blocks, unsigned threads, unsigned cluster, cudaStream_t stream,
                            const GemmMaps& maps, const GemmArgs& a, const Extra& extra) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most);
+    const int beside = 227 * 1024 - 512 - Extra::kFloats * 4;          // what the kernel's own arrays leave
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most < beside ? smem_most : beside);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
