@@ -406,12 +406,12 @@ void block_tiles(GemmArgs* a) {
     gemm_tiles(a, false, 0, 256, widest);
 }
 
-// The maps of the rows, in boxes of a.box and of twice that.
+// The maps of the rows, in boxes of a.box, and for gemm_kernel of twice that.
 ep_status encode_rows(GemmMaps* maps, const GemmArgs& a, const void* rows) {
     const uint64_t d[2] = {(uint64_t)a.C, (uint64_t)a.num_rows};
     uint32_t box[2] = {64, (uint32_t)a.box};
     const ep_status st = encode_map(&maps->b, rows, 2, d, box);
-    if (st != EP_OK) return st;
+    if (st != EP_OK || gemm_by_split(a)) return st;
     box[1] *= 2;
     return encode_map(&maps->b2, rows, 2, d, box);
 }

@@ -43,6 +43,13 @@ def _check(what: str, t: torch.Tensor, dtype: torch.dtype, *shape: Optional[int]
         raise ValueError(f"{what} has to be [{wants}], not {list(has)}")
 
 
+def _check_devices(*tensors: torch.Tensor) -> None:
+    """The library launches on the current device's current stream."""
+    at = tensors[0].device
+    if any(t.device != at for t in tensors) or (at.type == "cuda" and at.index != torch.cuda.current_device()):
+        raise ValueError(f"all tensors have to be on the current device, not on {[str(t.device) for t in tensors]}")
+
+
 def _one_of(what: str, value, names) -> None:
     if value not in names:
         raise ValueError(f"{what} has to be one of {', '.join(map(repr, names))}, not {value!r}")
@@ -297,6 +304,7 @@ def checkpoint_rows(x: torch.Tensor):
     """x [rows][features] bf16 -> (values, scales): the rows in 8 bits, uint8 [rows][features padded to
     16] of e4m3 and uint8 [rows][groups of 16], for a backward pass (see ep_checkpoint in ep.h)."""
     _check("x", x, torch.bfloat16, None, None)
+    _check_devices(x)
     (rows, features), width = x.shape, _kept_width(x.shape[1])
     values, scales = (torch.empty((rows, n), dtype=torch.uint8, device=x.device) for n in (width, width // EP_CHECKPOINT_GROUP))
     ep_checkpoint_rows(rows, features, x, make_checkpoint(values, scales), make_launch())
@@ -308,6 +316,7 @@ def restore_rows(values: torch.Tensor, scales: torch.Tensor, features: int) -> t
     width = _kept_width(features)
     _check("values", values, torch.uint8, None, width)
     _check("scales", scales, torch.uint8, values.shape[0], width // EP_CHECKPOINT_GROUP)
+    _check_devices(values, scales)
     x = torch.empty((values.shape[0], features), dtype=torch.bfloat16, device=values.device)
     ep_restore_rows(*x.shape, make_checkpoint(values, scales), x, make_launch())
     return x
@@ -360,6 +369,7 @@ def expert_feed_forward(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tens
     _one_of("activation", activation, tuple(_ACTIVATIONS))
     _one_of("checkpoint", checkpoint, ("bf16", "e4m3", "recompute"))
     _check_err(err)
+    _check_devices(x, gate_up, down, expert_prefix)
     return _FeedForward.apply(x, gate_up, down, expert_prefix, _ACTIVATIONS[activation], checkpoint,
                               _error_word(err, x.device))
 

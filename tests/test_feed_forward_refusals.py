@@ -33,6 +33,15 @@ def test_block_operands_fit():
     refuses("err", experts.expert_feed_forward, **good, err=t(F32, 1))
 
 
+def test_tensors_are_on_one_device():
+    x, gate_up, down, prefix = t(BF, 9, 64), t(BF, 3, 80, 64), t(BF, 3, 64, 40), t(I32, 4)
+    for f, args in ((experts.expert_feed_forward, (x.to("meta"), gate_up, down, prefix)),
+                    (experts.expert_feed_forward, (x, gate_up, down.to("meta"), prefix)),
+                    (experts.restore_rows, (t(U8, 4, 48), t(U8, 4, 3).to("meta"), 40))):
+        with pytest.raises(ValueError, match="^all tensors have to be on the current device"):
+            f(*args)
+
+
 def test_kept_rows_fit():
     refuses("x", experts.checkpoint_rows, t(F32, 4, 64))
     refuses("x", experts.checkpoint_rows, t(BF, 64))

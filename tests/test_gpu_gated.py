@@ -150,6 +150,27 @@ def test_kept_bytes_of_whole_numbers(name):
     b.outside(values, scales, halves)
 
 
+@pytest.mark.parametrize("E,expert,K,F", [(1, 0, 8, 8), (1, 0, 256, 128), (5, 3, 520, 1000), (300, 299, 64, 72), (2, 0, 4096, 264),
+                                          (3, 2, 4104, 136), (1, 0, 7168, 136), (1, 0, 16384, 64), (2, 1, 9000, 72), (4000, 2222, 264, 40)])
+@pytest.mark.parametrize("kind", ACTS)
+def test_one_row(kind, E, expert, K, F):
+    """A single token, which goes another way: sums of even and of odd values, of lanes and of warps."""
+    counts = [0] * E
+    counts[expert] = 1
+    b = Block(counts, K, F, seed=12, before=0, after=0)
+    h, _, _ = b.forward(kind)
+    (g, u), (g_off, u_off) = b.sums()
+    a, _, a_off, _ = act(g, kind)
+    assert_within(h, a * u, product_bound(a, a_off + STEEP * g_off, u, u_off) + (a * u).abs() * U32, U16)
+    assert int(b.err.item()) == 0
+    assert torch.equal(b.forward(kind)[0], h)
+    b.prefix[:] = 0                                  # a row of no expert
+    assert bool((b.forward(kind)[0] == 7).all()) and int(b.err.item()) == 0
+    b.prefix[1:] = 3                                 # beyond the rows: clipped, flagged
+    b.forward(kind)
+    assert int(b.err.item()) == ep.EP_DEVERR_RECV_OVERFLOW
+
+
 def backward(b, kind, keep, with_h=True, seed=9):
     g = torch.Generator(device="cuda").manual_seed(seed)
     values, scales, checkpoint = b.buffers(keep)
@@ -267,6 +288,36 @@ def test_prefix_beyond_the_rows_is_flagged():
     b.prefix[-1] = b.n + 9
     h, _, _ = b.forward("silu")
     assert int(b.err.item()) & ep.EP_DEVERR_RECV_OVERFLOW
+
+
+def test_calls_on_two_streams_and_replayed():
+    """The same buffers' shapes on two streams at once, and captured: nothing of the calls is shared."""
+    blocks = [Block([40, 0, 7, 90, 1], 264, 136, seed=s) for s in (20, 21)]
+    one = Block([1], 520, 72, seed=22, before=0, after=0)
+    want = [b.forward("silu", "e4m3") for b in blocks] + [one.forward("gelu")]
+    streams = [torch.cuda.Stream() for _ in blocks]
+    got = []
+    for s, b in zip(streams, blocks):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            b.launch = ep.make_launch(error_flags=b.err)
+            got.append([b.forward("silu", "e4m3") for _ in range(5)][-1])
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for a, w in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, w))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for b in (*blocks, one):
+            b.launch = ep.make_launch(error_flags=b.err)
+        out = [b.forward("silu", "e4m3") for b in blocks] + [one.forward("gelu")]
+    for _ in range(2):
+        for t in out:
+            t[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, w in zip(out, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, w) if x is not None)
 
 
 def test_no_rows():
