@@ -45,15 +45,13 @@ __device__ __forceinline__ Activated activate_both(float g) {
 // ------------------------------------------------------------------ what is kept
 
 // g and u of a row: bf16 [rows][2][F], or e4m3 [rows][2][F padded to 16] with a byte for each 16
-// features, [groups][rows][2]: what a warp writes of them lies side by side (by rows, single bytes of 32 lines
-// took 16 us of 53 for 4229 rows 560 -> 2616).
+// features, [rows][groups][2], so that a row's 64 or 128 features of a tile have theirs in 8 or 16 bytes.
 enum Keep { kNone, kBf16, kE4m3 };
 
 struct Kept {
     void* values;
     uint8_t* scales;
     int F, padded;
-    int64_t rows;
     __device__ __forceinline__ __nv_bfloat16* halves(int64_t row, int side) const {
         return reinterpret_cast<__nv_bfloat16*>(values) + (2 * row + side) * F;
     }
@@ -61,44 +59,51 @@ struct Kept {
         return reinterpret_cast<uint8_t*>(values) + (2 * row + side) * padded;
     }
     __device__ __forceinline__ uint8_t* exponent(int64_t row, int side, int feature) const {
-        return scales + ((feature / kKeptGroup) * rows + row) * 2 + side;
+        return scales + (row * (padded / kKeptGroup) + feature / kKeptGroup) * 2 + side;
     }
 };
 
 // ------------------------------------------------------------------ forward
+
+// Four warps, one for each quarter of the lanes, bring the same rows of a tile into the order of memory in
+// shared memory that they have together: a warp alone has 32 bytes of a row of h, which cost the way to L2
+// a request each, all four have its whole 128 bytes.
+__device__ __forceinline__ void quarters_barrier(int part) { asm volatile("bar.sync %0, 128;" ::"r"(2 + part) : "memory"); }
 
 // The M side has eight rows of Wg and eight of Wu in turn, so that a warp has both sums of a feature
 // in the same place of two sets of eight lanes, and a tile of 256 covers 128 features.
 template <Keep KEEP, int ACT>
 struct Gated : NoExtra {
     static constexpr bool kPairs = true, kWrites = true;
-    static constexpr int kStaged = 1024, kFloats = kWarps * kStaged / 4, kFewFloats = kFloats;
+    static constexpr int kStaged = 4096, kFloats = kWarps * kStaged / 16, kFewFloats = kFloats;          // of four warps
     Kept kept;
     __device__ __forceinline__ void tile(uint32_t tmem, float* shared, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows,
                                          int m0, int M, int half, int lane) const {
-        write<kWarps / 4>(tmem, smem_addr(shared) + ((threadIdx.x >> 5) - 4) * kStaged, out, row0, rows, m0, M, half, lane);
+        write<kWarps / 4>(tmem, smem_addr(shared), out, row0, rows, m0, M, half, lane);
     }
     __device__ __forceinline__ void prefetch(int64_t, int, int, int, int) const {}
 
-    // 16 features x 32 rows at a time, blocks b of 8 rows. Lane 4g + c has rows 2c, 2c+1 of features 8t + g of
-    // each block. By way of shared memory a lane gets eight features, chunk lane & 1, of rows lane / 2 and
-    // 16 + lane / 2: 16 bytes in bf16. (Chunks of row r lie r from the first, the second ones' rows swapped
-    // by fours, so that neither direction meets in a bank. Exchanging registers between lanes instead
-    // took twice the instructions, which bound short contractions.)
-    static __device__ __forceinline__ void by_rows(const uint32_t (&p)[2][4], uint32_t stage, int lane, uint4 (&q)[2]) {
-        __syncwarp();          // what was there has been read
+    // 64 features x 32 rows at a time, 16 features of blocks b of 8 rows a warp. Lane 4g + c has rows 2c, 2c+1 of
+    // features 8t + g of each block; afterwards it has chunk lane & 7 (eight features) of rows lane / 8 and 4 +
+    // lane / 8 of its quarter of the rows. Chunk n of row r is at r * 128 + (n ^ (r & 7)) * 16, where neither
+    // direction meets in a bank. (Exchanging registers between lanes instead took twice the instructions.)
+    static __device__ __forceinline__ void by_rows(const uint32_t (&p)[2][4], uint32_t stage, int part, int quarter, int lane, uint4 (&q)[2]) {
+        quarters_barrier(part);          // what was there has been read
 #pragma unroll
-        for (int t = 0; t < 2; ++t) store_blocks(stage + t * 512 + ((lane ^ (t * 4)) << 4), p[t]);
-        __syncwarp();
-        const int t = lane & 1, r = lane >> 1;
+        for (int t = 0; t < 2; ++t) store_blocks(stage + lane * 128 + (((quarter * 2 + t) ^ (lane & 7)) << 4), p[t]);
+        quarters_barrier(part);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) q[j] = ld_shared_v4(stage + t * 512 + (((r + j * 16) ^ (t * 4)) << 4));
+        for (int j = 0; j < 2; ++j) {
+            const int r = quarter * 8 + j * 4 + (lane >> 3);
+            q[j] = ld_shared_v4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        }
     }
-    template <int PARTS>          // how many warps share the rows
+    template <int PARTS>          // how many sets of four warps share the rows
     __device__ __forceinline__ void write(uint32_t tmem, uint32_t stage, __nv_bfloat16* out, int64_t row0, int rows, int m0, int M,
                                           int part, int lane) const {
-        const int F = M / 2, f0 = m0 / 2, f = f0 + (lane & 1) * 8;
+        const int F = M / 2, quarter = (threadIdx.x >> 5) & 3, f0 = m0 / 2 - quarter * 16, f = f0 + (lane & 7) * 8;
         if (f0 >= F) return;
+        stage += part * kStaged;
         for (int n = part * 32; n < rows; n += PARTS * 32) {
             float v[4][2][4];
 #pragma unroll
@@ -108,8 +113,8 @@ struct Gated : NoExtra {
             }
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_wait(v[b]);
-            const int64_t row = row0 + n + (lane >> 1);
-            const int left = rows - n - (lane >> 1);          // of the rows from that one on
+            const int64_t row = row0 + n + quarter * 8 + (lane >> 3);
+            const int left = rows - n - quarter * 8 - (lane >> 3);          // of the rows from that one on
             uint32_t p[2][4];
             uint4 q[2];
             if (out != nullptr) {
@@ -118,10 +123,10 @@ struct Gated : NoExtra {
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
                         p[t][b] = pack_bf16x2(activate<ACT>(v[b][t][0]) * v[b][t][2], activate<ACT>(v[b][t][1]) * v[b][t][3]);
-                by_rows(p, stage, lane, q);
+                by_rows(p, stage, part, quarter, lane, q);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    if (j * 16 < left && f < F) st_v4(out + (row + j * 16) * F + f, q[j]);
+                    if (j * 4 < left && f < F) st_v4(out + (row + j * 4) * F + f, q[j]);
             }
             uint32_t exponent[2][2];          // by side, row
 #pragma unroll
@@ -130,11 +135,11 @@ struct Gated : NoExtra {
                 for (int b = 0; b < 4; ++b)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) p[t][b] = pack_bf16x2(v[b][t][2 * h], v[b][t][2 * h + 1]);
-                by_rows(p, stage, lane, q);
+                by_rows(p, stage, part, quarter, lane, q);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     if (KEEP == kBf16) {
-                        if (j * 16 < left && f < F) st_v4(kept.halves(row + j * 16, h) + f, q[j]);
+                        if (j * 4 < left && f < F) st_v4(kept.halves(row + j * 4, h) + f, q[j]);
                         continue;
                     }
                     // The group is this lane's eight features and its neighbour's.
@@ -146,14 +151,14 @@ struct Gated : NoExtra {
                     const float inv = kept_inverse(e);
                     const uint2 eight = make_uint2(keep_pair(q[j].x, inv) | keep_pair(q[j].y, inv) << 16,
                                                    keep_pair(q[j].z, inv) | keep_pair(q[j].w, inv) << 16);
-                    if (j * 16 < left) *reinterpret_cast<uint2*>(kept.bytes(row + j * 16, h) + f) = eight;
+                    if (j * 4 < left && f < kept.padded) *reinterpret_cast<uint2*>(kept.bytes(row + j * 4, h) + f) = eight;
                 }
             }
-            if (KEEP == kE4m3 && (lane & 1) == 0)
+            if (KEEP == kE4m3 && (lane & 1) == 0 && f < kept.padded)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    if (j * 16 < left)
-                        *reinterpret_cast<uint16_t*>(kept.exponent(row + j * 16, 0, f0)) = (uint16_t)(exponent[0][j] | exponent[1][j] << 8);
+                    if (j * 4 < left)
+                        *reinterpret_cast<uint16_t*>(kept.exponent(row + j * 4, 0, f)) = (uint16_t)(exponent[0][j] | exponent[1][j] << 8);
         }
     }
 };
@@ -271,7 +276,7 @@ struct Back {
 template <Keep KEEP, int ACT>
 struct GatedBack : NoExtra {
     static constexpr bool kWrites = true;
-    static constexpr int kWarps = 16, kStaged = 512, kFloats = kWarps * kStaged / 4, kFewFloats = 8 * kStaged / 4;
+    static constexpr int kWarps = 16, kBlock = 2048, kStaged = 3 * kBlock, kFloats = kWarps * kStaged / 16, kFewFloats = kFloats / 2;
     Kept kept;
     Back to;
     // Eight features of one row's side as they are stored, and as four bf16 pairs.
@@ -303,38 +308,38 @@ struct GatedBack : NoExtra {
     }
     __device__ __forceinline__ void tile(uint32_t tmem, float* shared, unsigned char*, __nv_bfloat16* out, int64_t row0, int rows, int m0,
                                          int M, int half, int lane) const {
-        write<kWarps / 4>(tmem, smem_addr(shared) + ((threadIdx.x >> 5) - 4) * kStaged, out, row0, rows, m0, M, half, lane);
+        write<kWarps / 4>(tmem, smem_addr(shared), out, row0, rows, m0, M, half, lane);
     }
-    // 32 features x 8 rows at a time; the next rows' loads are under way meanwhile. In shared memory chunk t
-    // of eight features of row r is at 8t + (r ^ 2t), so that neither direction meets in a bank: `by_row` is
-    // where this lane's row lane / 4 and chunk lane & 3 are, `by_block` where row lane & 7 of block lane / 8 is.
+    // 128 features x 8 rows at a time, 32 features a warp; the next rows' loads are under way meanwhile. In shared
+    // memory chunk n (eight features) of row r is at r * 256 + (n ^ r) * 16, where neither direction meets in a
+    // bank; a lane reads and writes chunk lane & 15 of row lane / 16 of its quarter of the rows.
     template <int PARTS>
     __device__ __forceinline__ void write(uint32_t tmem, uint32_t stage, __nv_bfloat16*, int64_t row0, int rows, int m0, int M, int part,
                                           int lane) const {
-        if (m0 >= M) return;
-        const int g = lane >> 2, c = lane & 3, f = m0 + c * 8;
-        const uint32_t by_row = stage + ((c * 8 + (g ^ (2 * c))) << 4), by_block = stage + (((lane & ~7) + ((lane & 7) ^ (lane >> 3 << 1))) << 4);
+        const int quarter = (threadIdx.x >> 5) & 3, r = quarter * 2 + (lane >> 4), f = m0 - quarter * 32 + (lane & 15) * 8;
+        if (m0 - quarter * 32 >= M) return;
+        stage += part * kStaged;
+        const uint32_t by_row = stage + r * 256 + (((lane & 15) ^ r) << 4);
+        const uint32_t by_block = stage + (lane & 7) * 256 + (((quarter * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
         Raw next[2] = {};
-        if (part * 8 + g < rows && f < M)
+        if (part * 8 + r < rows && f < M)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) next[h] = load(row0 + part * 8 + g, h, f);
+            for (int h = 0; h < 2; ++h) next[h] = load(row0 + part * 8 + r, h, f);
         for (int n = part * 8; n < rows; n += 8 * PARTS) {
-            const bool there = n + g < rows && f < M;
-            const int64_t row = row0 + n + g;
-            uint32_t side[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                __syncwarp();
-                st_shared_v4(by_row, pairs(next[h]));
-                __syncwarp();
-                load_blocks(by_block, side[h]);
-            }
-            if (n + 8 * PARTS + g < rows && f < M)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) next[h] = load(row + 8 * PARTS, h, f);
+            const bool there = n + r < rows && f < M;
+            const int64_t row = row0 + n + r;
             float v[2][4];
             tmem_load_16x8(tmem + n, v[0]);
             tmem_load_16x8(tmem + n + (16u << 16), v[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) st_shared_v4(by_row + h * kBlock, pairs(next[h]));
+            quarters_barrier(part);
+            if (n + 8 * PARTS + r < rows && f < M)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) next[h] = load(row + 8 * PARTS, h, f);
+            uint32_t side[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) load_blocks(by_block + h * kBlock, side[h]);
             tmem_wait(v);
             uint32_t p[3][4];          // dg, du, h
 #pragma unroll
@@ -346,14 +351,17 @@ struct GatedBack : NoExtra {
                 p[1][i] = pack_bf16x2(d0 * a0.value, d1 * a1.value);
                 p[2][i] = pack_bf16x2(a0.value * u0, a1.value * u1);
             }
+            // A warp's blocks of what was kept are its own blocks of the results.
 #pragma unroll
-            for (int h = 0; h < 3; ++h) {
-                if (h == 2 && to.h == nullptr) break;
-                __syncwarp();
-                store_blocks(by_block, p[h]);
-                __syncwarp();
-                const uint4 q = ld_shared_v4(by_row);
-                if (there) st_v4(h == 2 ? to.h + row * M + f : to.dgu + (2 * row + h) * M + f, q);
+            for (int h = 0; h < 3; ++h) store_blocks(by_block + h * kBlock, p[h]);
+            quarters_barrier(part);
+            uint4 q[3];
+#pragma unroll
+            for (int h = 0; h < 3; ++h) q[h] = ld_shared_v4(by_row + h * kBlock);
+            if (there) {
+                st_v4(to.dgu + 2 * row * M + f, q[0]);
+                st_v4(to.dgu + (2 * row + 1) * M + f, q[1]);
+                if (to.h != nullptr) st_v4(to.h + row * M + f, q[2]);
             }
         }
     }
@@ -377,8 +385,8 @@ ep_status check_sides(const ep_checkpoint* c, bool rows) {
     return st == EP_OK && ((uintptr_t)c->scales & 1) != 0 ? EP_ERR_INVALID_ARG : st;
 }
 
-Kept kept_of(const ep_checkpoint* c, int F, int rows) {
-    Kept k{nullptr, nullptr, F, kept_features(F), rows};
+Kept kept_of(const ep_checkpoint* c, int F) {
+    Kept k{nullptr, nullptr, F, kept_features(F)};
     if (c != nullptr) k.values = c->values, k.scales = c->scales;
     return k;
 }
@@ -486,7 +494,7 @@ ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w,
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
-        const Kept kept = kept_of(keep, sh->out_features, sh->num_rows);
+        const Kept kept = kept_of(keep, sh->out_features);
         st = keep == nullptr              ? forward<kNone>(maps, a, activation, kept, launch->stream)
              : keep->dtype == EP_BF16 ? forward<kBf16>(maps, a, activation, kept, launch->stream)
                                           : forward<kE4m3>(maps, a, activation, kept, launch->stream);
@@ -520,7 +528,7 @@ ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const v
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows) {
-        const Kept k = kept_of(kept, sh->in_features, sh->num_rows);
+        const Kept k = kept_of(kept, sh->in_features);
         const Back to{reinterpret_cast<__nv_bfloat16*>(dgu), reinterpret_cast<__nv_bfloat16*>(h)};
         st = kept->dtype == EP_BF16 ? backward<kBf16>(maps, a, activation, k, to, launch->stream) : backward<kE4m3>(maps, a, activation, k, to, launch->stream);
         if (st != EP_OK) return st;

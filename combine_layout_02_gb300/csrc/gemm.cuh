@@ -517,7 +517,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
 //                       for each kGroup of them: v[j] belongs to row row0 + c + j. Two halves of 128
 //                       threads take groups in turn. kWrites: what is written is not the sums alone:
 //                       write does it from tensor memory, as tile, where joined sums have gone back to
-//                       (each warp with kStaged of the shared bytes),
 //                       and prefetch is called before for the rows, while the products run
 // kPairs (forward): the M side is two projections of out_features each, eight rows of one and eight of the
 // other in turn (maps.a has five dimensions: in_features, 8, 2, out_features / 8, experts).
@@ -1011,7 +1010,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     if (D != kWgrad && a.split == 1) {
         if constexpr (Extra::kWrites) {
             if (ok && warp >= 2)
-                extra.template write<2>(tmem + ((uint32_t)quarter << 21), smem_addr(s_extra) + (warp - 2) * Extra::kStaged, a.out, t.n0, rows,
+                extra.template write<2>(tmem + ((uint32_t)quarter << 21), smem_addr(s_extra), a.out, t.n0, rows,
                                         m - lane, a.M, half, lane);
         } else if (ok && warp >= 2) {
             for (int c = half * G; c < rows; c += 2 * G) {
@@ -1076,7 +1075,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 fine = epilogue_all<256>(fine);
                 tc_fence_after();
                 if (fine)
-                    extra.template write<2>(tmem + ((uint32_t)quarter << 21), smem_addr(s_extra) + (warp - 2) * Extra::kStaged, a.out,
+                    extra.template write<2>(tmem + ((uint32_t)quarter << 21), smem_addr(s_extra), a.out,
                                             t.n0 + lo, hi - lo, m - lane, a.M, half, lane);
             }
         } else if (ok && warp >= 2 && lo < hi) {

@@ -543,7 +543,7 @@ EP_API ep_status ep_expert_gemm_wgrad(const ep_gemm_shape* shape, const void* dy
  *           EP_CHECKPOINT_GROUP], bf16 [rows][features]
  *   scales  dev uint8 [rows][padded features / EP_CHECKPOINT_GROUP] (bytes 1 to 254)
  * Rows of two parts (ep_expert_gated's): values [rows][2][padded features], scales
- * [padded features / EP_CHECKPOINT_GROUP][rows][2], 2-byte aligned. */
+ * [rows][padded features / EP_CHECKPOINT_GROUP][2], 2-byte aligned. */
 #define EP_CHECKPOINT_GROUP 16
 
 typedef struct ep_checkpoint {

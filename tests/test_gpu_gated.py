@@ -39,8 +39,8 @@ def normal(g, *shape):
 
 
 def by_row(scales):
-    """[groups][rows][2] -> each side's [rows][groups]."""
-    return [scales[:, :, side].t().contiguous() for side in range(2)]
+    """[rows][groups][2] -> each side's [rows][groups]."""
+    return [scales[:, :, side].contiguous() for side in range(2)]
 
 
 class Block:
@@ -74,7 +74,7 @@ class Block:
         else:
             width = -(-self.F // GROUP) * GROUP
             values = torch.full((self.n, 2 * width), 0xA5, dtype=torch.uint8, device="cuda")
-            scales = torch.full((width // GROUP, self.n, 2), 0xA5, dtype=torch.uint8, device="cuda")
+            scales = torch.full((self.n, width // GROUP, 2), 0xA5, dtype=torch.uint8, device="cuda")
         return values, scales, ep.make_checkpoint(values, scales)
 
     def parts(self, values, scales):
@@ -103,7 +103,6 @@ class Block:
         """Rows of no expert are as they were."""
         for t in outputs:
             if t is not None:
-                t = t.transpose(0, 1) if t.dim() == 3 else t
                 rest = torch.cat([t[:self.mine.start], t[self.mine.stop:]])
                 assert bool((rest == (0xA5 if t.dtype == torch.uint8 else 7)).all())
 
@@ -181,8 +180,8 @@ def backward(b, kind, keep, with_h=True, seed=9):
         for side, part in enumerate(made.chunk(2, 1)):
             q, k, _ = quantised(part)
             wide = q.shape[1]
-            values[:, side * wide:(side + 1) * wide], scales[:, :, side] = q.cuda(), k.t().cuda()
-    for t in (values, None if scales is None else scales.transpose(0, 1)):          # rows of no expert: not read
+            values[:, side * wide:(side + 1) * wide], scales[:, :, side] = q.cuda(), k.cuda()
+    for t in (values, scales):          # rows of no expert: not read
         if t is not None:
             t[:b.mine.start], t[b.mine.stop:] = (math.nan, math.nan) if t.dtype == torch.bfloat16 else (0x7F, 0x7F)
     dgu = torch.full((b.n, 2 * b.F), 7.0, dtype=torch.bfloat16, device="cuda")
