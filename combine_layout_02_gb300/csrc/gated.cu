@@ -411,21 +411,31 @@ ep_status run_block(const GemmMaps& maps, const GemmArgs& a, const Wide& wide, c
     return e == cudaSuccess ? EP_OK : cuda_fail(e);
 }
 
-// Tiles and stages. Where the contraction is short and all tiles of 32 or 64 rows are on the GPU at once
-// (two an SM; of 64 rows over up to 8 steps of 64 also twice that), they are taken that narrow, not as
-// wide as gemm_tiles would: a pair's 256 x 256 costs 4 us more to set up, and its epilogue 4 (forward) to
-// 10 us (backward) that nothing hides. Forward keeping 8 bits / backward: 509 rows of 8 experts 256 -> 512
-// 9.0 / 11.7 us, with 32 rows 4.5 / 5.7; 1500 rows of 8, 1024 -> 512 14.7 / 19.8, with 64 and 32 rows
-// 9.2 / 9.3; 2048 rows of 16, 512 -> 512 14.3 / 19.3, 10.0 / 8.6. Longer contractions lose by it, as the
-// weights are read once for each tile (32 steps, 509 rows of 8 experts: 18.1 us, with 64 rows 24.2).
-void block_tiles(GemmArgs* a) {
+// Tiles and stages. A pair's tile of 256 x 256 costs 4 us more to set up than two CTAs of 128 x 64, and its epilogue 3
+// (forward) to 7 us (backward) that nothing hides in a short call. So tiles are taken that narrow where
+//   up to 8 steps of 64 are contracted and four of them are there for each SM (backward six), two being at work,
+//   up to 16 and two are there, or where two of 32 rows are, those,
+//   up to 32, one and a half are, and experts have 96 rows on average (else tiles of 64 rows read the weights
+//   twice where wider ones do so once).
+// Wide and so, forward keeping 8 bits / backward, us:
+//   509 rows of 8 experts 256 -> 512     9.0 / 10.4    4.5 / 4.8      200 rows of one 2048 -> 1024   13.3 / 14.5   10.0 / 8.1
+//   1500 rows of 8 1024 -> 512          14.4 / 17.6    8.5 / 8.8      1200 rows of 8 2048 -> 512     15.1 / 15.9   13.2 / 11.8
+//   8191 rows of 32 512 -> 512          29.3 / 31.8   (29.2)/ 20.8    509 rows of 8 2048 -> 1024     18.4 / 12.0  (16.7 / 12.7)
+//                                                                     150 rows of one 7168 -> 2048   20.5 / 16.0  (23.2 / 14.9)
+void block_tiles(GemmArgs* a, bool back) {
     const int steps = ceil_div(a->C, kBK), sms = sm_count();
-    int widest = 256;
-    for (int bn = 64; steps <= 16 && bn >= 32; bn /= 2) {
+    int widest = 256, parts = 8;
+    for (int bn = 64; bn >= 32; bn /= 2) {
         a->bn = bn;
-        if (gemm_most_tiles(*a, false, kBM) <= (bn == 64 && steps <= 8 ? 4 : 2) * sms) widest = bn;
+        const int64_t tiles = gemm_most_tiles(*a, false, kBM);
+        int halves = steps <= 16 ? 4 : 0;          // of the SMs
+        if (bn == 64 && steps <= 8) halves = back ? 12 : 8;
+        if (bn == 64 && steps > 16 && steps <= 32 && a->num_rows / 96 >= a->E) halves = 3;
+        if (2 * tiles > (int64_t)halves * sms) continue;
+        widest = bn;
+        parts = tiles > sms ? 1 : 8;          // (gemm_tiles' own count of the tiles is the least there can be)
     }
-    gemm_tiles(a, false, 0, 256, widest);
+    gemm_tiles(a, false, 0, 256, widest, 16, parts);
 }
 
 // The maps of the rows, in boxes of a.box, and for gemm_kernel of twice that.
@@ -502,7 +512,7 @@ ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w,
     a.M = 2 * sh->out_features;
     a.N = a.C = sh->in_features;
     a.err = launch->error_flags;
-    block_tiles(&a);
+    block_tiles(&a, false);
     GemmMaps maps{};
     if (rows) {
         const uint64_t d[5] = {K, 8, 2, F / 8, E}, strides[4] = {2 * K, 2 * F * K, 16 * K, 4 * F * K};
@@ -536,7 +546,7 @@ ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const v
     a.M = a.N = sh->in_features;
     a.C = sh->out_features;
     a.err = launch->error_flags;
-    block_tiles(&a);
+    block_tiles(&a, true);
     GemmMaps maps{};
     if (rows) {
         const uint64_t d[3] = {(uint64_t)sh->in_features, (uint64_t)sh->out_features, (uint64_t)sh->num_experts};

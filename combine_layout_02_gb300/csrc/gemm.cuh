@@ -1131,7 +1131,8 @@ inline bool gemm_by_split(const GemmArgs& a) { return a.bn <= 64 || a.split > 1;
 // Narrow tiles that are few take an SM each: 128 KB, so that two do not share one while others are
 // idle (128 rows 1024 -> 4096 with adapters of rank 64, 128 CTAs: 23 us, else 31). Not in clusters of
 // eight: an SM each, not all of them fit at once (70 rows 4096 -> 1024: 17 us, else 12).
-inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 256, int widest = 256, int least = 16) {
+inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 256, int widest = 256, int least = 16,
+                       int most_parts = 8) {
     int bn = 256;
     const int avg = (a->num_rows + a->E - 1) / a->E, wide = a->E > 1 ? 2 * (avg < 256 ? avg : 256) : avg;
     if (!wgrad)
@@ -1144,7 +1145,7 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 
         const int64_t tiles = (int64_t)ceil_div(a->M, kBM) * (a->E < a->num_rows ? a->E : a->num_rows) * ceil_div(avg, bn);
         const int64_t want = bn <= 64 ? 2 * sms : sms;
         const int steps = ceil_div(a->C, kBK);
-        while (a->split < 8 && tiles * a->split * 2 <= want &&
+        while (a->split < most_parts && tiles * a->split * 2 <= want &&
                steps >= a->split * (bn > 64 ? 32 : tiles * a->split * 2 <= sms / 2 ? least : 16))
             a->split *= 2;
         if (bn > 64 && (avg < bn ? avg : bn) > most_rows * a->split) a->split = 1;
