@@ -240,12 +240,15 @@ def lib():
 
 # ---------------------------------------------------------------- marshalling helpers
 
+class _Address(int):
+    """A part of an allocation that this package's own functions have made."""
+
+
 def _ptr(t) -> Optional[int]:
-    """Device pointer of a tensor (None -> NULL). Requires a contiguous CUDA tensor. (An address is
-    passed on: parts of one allocation.)"""
+    """Device pointer of a tensor (None -> NULL). Requires a contiguous CUDA tensor."""
     if t is None:
         return None
-    if isinstance(t, int):
+    if type(t) is _Address:
         return t or None
     if not t.is_cuda:
         raise ValueError("libep takes device tensors")

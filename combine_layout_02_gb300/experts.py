@@ -19,7 +19,7 @@ from typing import List, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (EP_ACT_GELU_TANH, EP_ACT_SILU, EP_BF16, EP_CHECKPOINT_GROUP, ep_adapter_gemm, ep_adapter_shape,
+from . import (_Address, EP_ACT_GELU_TANH, EP_ACT_SILU, EP_BF16, EP_CHECKPOINT_GROUP, ep_adapter_gemm, ep_adapter_shape,
                ep_adapter_workspace_size, ep_checkpoint_rows, ep_expert_gated, ep_expert_gated_dgrad, ep_expert_gemm,
                ep_expert_gemm_dgrad, ep_expert_gemm_wgrad, ep_expert_gemm_wgrad_checkpoint, ep_gemm_shape,
                ep_read_error_flags_sync, ep_restore_rows, ep_sort_layout, ep_sort_rows, ep_unsort_rows,
@@ -162,7 +162,7 @@ def _kept_bytes(rows: int, width: int) -> int:
 
 
 def _kept_at(address: int, rows: int, width: int):
-    return make_checkpoint(address, address + rows * width)
+    return make_checkpoint(_Address(address), _Address(address + rows * width))
 
 
 class _UnsortRowsKept(torch.autograd.Function):
@@ -263,8 +263,8 @@ class _FeedForward(torch.autograd.Function):
         room = max(16, ep_wgrad_checkpoint_workspace_size(up_shape)) if eight else 0
         scratch = new(rows * F * (6 if for_down else 4) + room, dtype=torch.uint8)          # the workspace, dgu, h
         workspace = scratch[:room] if eight else None
-        dgu = scratch.data_ptr() + room
-        h = dgu + rows * F * 4 if for_down else None
+        dgu = _Address(scratch.data_ptr() + room)
+        h = _Address(dgu + rows * F * 4) if for_down else None
         ep_expert_gated_dgrad(down_shape, grad, down, prefix, ctx.act, own, dgu, h, launch)
         dx = dgate_up = ddown = None
         if for_down:

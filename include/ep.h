@@ -591,7 +591,8 @@ EP_API ep_status ep_expert_gated(const ep_gemm_shape* shape, const void* x, cons
 
 /* Gradient of the block's down projection y[i] = Wd h[i] to g and u, with g and u as they were kept:
  *   dh = Wd^T dy[i]  (fp32),  dgu[i] = (dh * u * act'(g), dh * act(g)),  h[i] = act(g) * u
- * shape is the down projection's: in_features = F, out_features those of y.
+ * shape is the down projection's: in_features = F, out_features those of y; rules as for
+ * ep_expert_gemm (outputs overlap no inputs, what was kept included).
  *   dy dev [num_rows][out_features], w dev [E][out_features][F]
  *   dgu dev [num_rows][2][F]: dy of the gate and up projections as one product of 2F features
  *   h  dev [num_rows][F], what Wd's gradient wants; NULL to leave out */

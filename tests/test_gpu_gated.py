@@ -30,6 +30,8 @@ CASES = {
     "few_rows_split": ([3, 0, 2, 5, 1, 0, 4, 1], 4096, 256),
     "many_rows_few_features": ([3000, 0, 1111, 1], 136, 104),
     "one_long_expert": ([4099], 264, 392),
+    "one_deep": ([200], 4160, 264),
+    "wide_and_narrow": ([97, 0, 160, 31], 1096, 520),
     "decode": ([16, 30, 8, 15, 2, 40, 0, 9], 1024, 1024),
 }
 
