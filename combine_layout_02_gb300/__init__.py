@@ -40,6 +40,7 @@ __all__ = [
     "ep_checkpoint", "make_checkpoint", "ep_checkpoint_rows", "ep_restore_rows",
     "ep_wgrad_checkpoint_workspace_size", "ep_expert_gemm_wgrad_checkpoint",
     "EP_CHECKPOINT_GROUP", "EP_ACT_SILU", "EP_ACT_GELU_TANH", "ep_expert_gated", "ep_expert_gated_dgrad",
+    "ep_selftest_gated_timeout",
 ]
 
 EP_OK, EP_ERR_INVALID_ARG, EP_ERR_CUDA, EP_ERR_UNSUPPORTED = 0, 1, 2, 3
@@ -70,6 +71,7 @@ EXPORTED_SYMBOLS = (
     "ep_adapter_workspace_size", "ep_adapter_gemm",
     "ep_checkpoint_rows", "ep_restore_rows", "ep_wgrad_checkpoint_workspace_size",
     "ep_expert_gemm_wgrad_checkpoint", "ep_expert_gated", "ep_expert_gated_dgrad",
+    "ep_selftest_gated_timeout",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -224,10 +226,13 @@ def lib():
         L.ep_expert_gated.argtypes = [S(ep_gemm_shape), _P, _P, _P, _I32, _P, S(ep_checkpoint), S(ep_launch)]
         L.ep_expert_gated_dgrad.argtypes = [S(ep_gemm_shape), _P, _P, _P, _I32, S(ep_checkpoint), _P, _P,
                                             S(ep_launch)]
+        L.ep_selftest_gated_timeout.argtypes = [S(ep_gemm_shape), _I32, _P, _P, _P, S(ep_checkpoint), _P, _I32, _I32,
+                                                S(ep_launch)]
         for name in ("ep_sort_layout", "ep_sort_rows", "ep_unsort_rows", "ep_unsort_rows_backward",
                      "ep_expert_gemm", "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad",
                      "ep_adapter_gemm", "ep_checkpoint_rows", "ep_restore_rows",
-                     "ep_expert_gemm_wgrad_checkpoint", "ep_expert_gated", "ep_expert_gated_dgrad"):
+                     "ep_expert_gemm_wgrad_checkpoint", "ep_expert_gated", "ep_expert_gated_dgrad",
+                     "ep_selftest_gated_timeout"):
             getattr(L, name).restype = _I32
         for name in ("ep_get_layout", "ep_get_layout_static_scratch", "ep_dispatch", "ep_combine",
                      "ep_dispatch_expert_major", "ep_combine_expert_major", "ep_ll_dispatch",
@@ -543,6 +548,15 @@ def ep_selftest_gemm_timeout(shape: ep_gemm_shape, product: int, rows, other, ex
     _check("ep_selftest_gemm_timeout",
            lib().ep_selftest_gemm_timeout(ctypes.byref(shape), product, _ptr(rows), _ptr(other), _ptr(expert_prefix),
                                           _ptr(out), loads, timeout_ms, ctypes.byref(_launch(launch))))
+
+
+def ep_selftest_gated_timeout(shape: ep_gemm_shape, product: int, rows, w, expert_prefix,
+                              checkpoint: Optional[ep_checkpoint], out, loads: int, timeout_ms: int,
+                              launch: Optional[ep_launch] = None) -> None:
+    _check("ep_selftest_gated_timeout",
+           lib().ep_selftest_gated_timeout(ctypes.byref(shape), product, _ptr(rows), _ptr(w), _ptr(expert_prefix),
+                                           _checkpoint(checkpoint), _ptr(out), loads, timeout_ms,
+                                           ctypes.byref(_launch(launch))))
 
 
 def ep_read_error_flags_sync(error_flags, stream=None) -> int:

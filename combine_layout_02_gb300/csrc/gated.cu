@@ -478,20 +478,15 @@ ep_status backward(const GemmMaps& maps, const GemmArgs& a, int act, const Kept&
                               : backward<KEEP, EP_ACT_GELU_TANH>(maps, a, kept, to, stream);
 }
 
-}  // namespace
-}  // namespace ep
-
-extern "C" {
-
-ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w, const int32_t* expert_prefix, int32_t activation,
-                          void* h, const ep_checkpoint* keep, const ep_launch* launch) {
-    using namespace ep;
+// The calls; `loads` and `wait_ns` as in GemmArgs, for the self-test.
+ep_status run_forward(const ep_gemm_shape* sh, const void* x, const void* w, const int32_t* expert_prefix, int32_t activation, void* h,
+                      const ep_checkpoint* keep, const ep_launch* launch, int loads, uint64_t wait_ns) {
     ep_status st = check_block(sh, x, w, expert_prefix, activation, launch);
     if (st != EP_OK) return st;
     const bool rows = sh->num_rows > 0;
     if (keep != nullptr && (st = check_sides(keep, rows)) != EP_OK) return st;
     if ((rows && h == nullptr && keep == nullptr) || ((uintptr_t)h & 15) != 0) return EP_ERR_INVALID_ARG;
-    if (sh->num_rows == 1 && keep == nullptr) {
+    if (sh->num_rows == 1 && keep == nullptr && loads == GemmArgs{}.loads) {
         TokenArgs t{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(w), expert_prefix,
                     static_cast<__nv_bfloat16*>(h), launch->error_flags, sh->num_experts, sh->in_features, sh->out_features,
                     activation, kTokenWarps};
@@ -512,6 +507,8 @@ ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w,
     a.M = 2 * sh->out_features;
     a.N = a.C = sh->in_features;
     a.err = launch->error_flags;
+    a.loads = loads;
+    a.wait_ns = wait_ns;
     block_tiles(&a, false);
     GemmMaps maps{};
     if (rows) {
@@ -531,9 +528,8 @@ ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w,
     return end_call(launch);
 }
 
-ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const void* w, const int32_t* expert_prefix,
-                                int32_t activation, const ep_checkpoint* kept, void* dgu, void* h, const ep_launch* launch) {
-    using namespace ep;
+ep_status run_backward(const ep_gemm_shape* sh, const void* dy, const void* w, const int32_t* expert_prefix, int32_t activation,
+                       const ep_checkpoint* kept, void* dgu, void* h, const ep_launch* launch, int loads, uint64_t wait_ns) {
     ep_status st = check_block(sh, dy, w, expert_prefix, activation, launch);
     if (st != EP_OK) return st;
     const bool rows = sh->num_rows > 0;
@@ -546,6 +542,8 @@ ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const v
     a.M = a.N = sh->in_features;
     a.C = sh->out_features;
     a.err = launch->error_flags;
+    a.loads = loads;
+    a.wait_ns = wait_ns;
     block_tiles(&a, true);
     GemmMaps maps{};
     if (rows) {
@@ -558,10 +556,38 @@ ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const v
     if (rows) {
         const Kept k = kept_of(kept, sh->in_features);
         const Back to{reinterpret_cast<__nv_bfloat16*>(dgu), reinterpret_cast<__nv_bfloat16*>(h)};
-        st = kept->dtype == EP_BF16 ? backward<kBf16>(maps, a, activation, k, to, launch->stream) : backward<kE4m3>(maps, a, activation, k, to, launch->stream);
+        st = kept->dtype == EP_BF16 ? backward<kBf16>(maps, a, activation, k, to, launch->stream)
+                                    : backward<kE4m3>(maps, a, activation, k, to, launch->stream);
         if (st != EP_OK) return st;
     }
     return end_call(launch);
+}
+
+}  // namespace
+}  // namespace ep
+
+extern "C" {
+
+ep_status ep_expert_gated(const ep_gemm_shape* sh, const void* x, const void* w, const int32_t* expert_prefix, int32_t activation,
+                          void* h, const ep_checkpoint* keep, const ep_launch* launch) {
+    return ep::run_forward(sh, x, w, expert_prefix, activation, h, keep, launch, ep::GemmArgs{}.loads, ep::GemmArgs{}.wait_ns);
+}
+
+ep_status ep_expert_gated_dgrad(const ep_gemm_shape* sh, const void* dy, const void* w, const int32_t* expert_prefix,
+                                int32_t activation, const ep_checkpoint* kept, void* dgu, void* h, const ep_launch* launch) {
+    return ep::run_backward(sh, dy, w, expert_prefix, activation, kept, dgu, h, launch, ep::GemmArgs{}.loads, ep::GemmArgs{}.wait_ns);
+}
+
+ep_status ep_selftest_gated_timeout(const ep_gemm_shape* sh, int32_t product, const void* rows, const void* w,
+                                    const int32_t* expert_prefix, const ep_checkpoint* checkpoint, void* out, int32_t loads,
+                                    int32_t timeout_ms, const ep_launch* launch) {
+    using namespace ep;
+    if (launch == nullptr || launch->error_flags == nullptr || loads < 0 || loads % kBK != 0 || timeout_ms < 1 ||
+        timeout_ms > 10000 || product < 0 || product > 1)
+        return EP_ERR_INVALID_ARG;
+    const uint64_t ns = (uint64_t)timeout_ms * 1000000ull;
+    return product == 0 ? run_forward(sh, rows, w, expert_prefix, EP_ACT_SILU, out, checkpoint, launch, loads, ns)
+                        : run_backward(sh, rows, w, expert_prefix, EP_ACT_SILU, checkpoint, out, nullptr, launch, loads, ns);
 }
 
 }  // extern "C"

@@ -707,6 +707,14 @@ EP_API ep_status ep_selftest_gemm_timeout(const ep_gemm_shape* shape, int32_t pr
                                           const void* other, const int32_t* expert_prefix, void* out,
                                           int32_t loads, int32_t timeout_ms, const ep_launch* launch);
 
+/* And for those of the gated block: ep_expert_gated (product 0, out = h, checkpoint nullable) or
+ * ep_expert_gated_dgrad (1, out = dgu, without h) with EP_ACT_SILU. Nothing of a tile of a longer
+ * contraction is written, what is kept included. */
+EP_API ep_status ep_selftest_gated_timeout(const ep_gemm_shape* shape, int32_t product, const void* rows,
+                                           const void* w, const int32_t* expert_prefix,
+                                           const ep_checkpoint* checkpoint, void* out, int32_t loads,
+                                           int32_t timeout_ms, const ep_launch* launch);
+
 /* Static description of a status code. */
 EP_API const char* ep_status_string(ep_status status);
 

@@ -93,3 +93,15 @@ def test_gradient_from_kept_rows_refusals(ep):
     assert size >= 16 and ep.ep_wgrad_checkpoint_workspace_size(S(0, 1, 8, 8)) == 16
     for s, _ in shapes(S, go):
         assert ep.ep_wgrad_checkpoint_workspace_size(s) == 0
+
+
+def test_selftest_of_the_blocks_waits(ep):
+    launch, sh, q = ep.ep_launch(None, None, None, P), ep.ep_gemm_shape(10, 2, 64, 64), ep.ep_checkpoint(ep.EP_FP8_E4M3, P, P)
+
+    def go(shape=sh, product=0, rows=P, w=P, prefix=P, kept=q, out=P, loads=64, ms=20, launch=launch):
+        return call(ep, "ep_selftest_gated_timeout", shape, product, rows, w, prefix, kept, out, loads, ms, launch)
+
+    for bad in (dict(product=2), dict(product=-1), dict(loads=-64), dict(loads=32), dict(ms=0), dict(ms=10001), dict(launch=None),
+                dict(launch=ep.ep_launch(None, None, None, None)), dict(shape=ep.ep_gemm_shape(10, 2, 60, 64)), dict(rows=None),
+                dict(w=P + 8), dict(prefix=None), dict(product=1, out=None), dict(product=1, kept=None), dict(kept=None, out=None)):
+        assert go(**bad) == ep.EP_ERR_INVALID_ARG, bad
