@@ -3,6 +3,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "ep_internal.cuh"
 
 namespace ep {
@@ -1168,12 +1170,18 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 
 
 constexpr int kSplitSmemMax = 201 * 1024, kGemmSmemMax = 222 * 1024, kWgradSmemMax = 225 * 1024;
 
-template <class Kernel, class Extra>
+// WHICH: a number of its own for each kernel with this Extra. Its shared-memory limit is set once per device (0.6 us of
+// a call's 4 on the host), and once more where a launch is refused, as after a device reset.
+template <int WHICH, class Kernel, class Extra>
 cudaError_t launch_gemm_as(Kernel kernel, int smem_most, unsigned blocks, unsigned threads, unsigned cluster, cudaStream_t stream,
                            const GemmMaps& maps, const GemmArgs& a, const Extra& extra) {
+    static std::atomic<uint64_t> set[2];
     const int beside = 227 * 1024 - 512 - Extra::kFloats * 4;          // what the kernel's own arrays leave
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most < beside ? smem_most : beside);
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
+    if (device < 0 || device >= 128) return cudaErrorInvalidDevice;
+    const uint64_t bit = 1ull << (device & 63);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(threads);
@@ -1187,9 +1195,17 @@ cudaError_t launch_gemm_as(Kernel kernel, int smem_most, unsigned blocks, unsign
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, maps, a, extra);
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+    for (bool known = (set[device >> 6].load(std::memory_order_relaxed) & bit) != 0;; known = false) {
+        if (!known) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most < beside ? smem_most : beside);
+            if (e != cudaSuccess) return e;
+            set[device >> 6].fetch_or(bit, std::memory_order_relaxed);
+        }
+        e = cudaLaunchKernelEx(&cfg, kernel, maps, a, extra);
+        if (e == cudaSuccess) count_launches(1);
+        if (e != cudaErrorInvalidValue || !known) return e;
+        (void)cudaGetLastError();
+    }
 }
 
 // Launches the product (a.num_rows > 0) as gemm_tiles has laid it out.
@@ -1198,11 +1214,11 @@ cudaError_t launch_gemm(const GemmMaps& maps, const GemmArgs& a, const Wide& wid
     if (gemm_by_split(a)) {
         const int64_t tiles = gemm_most_tiles(a, D == kWgrad, kBM);
         if (tiles * a.split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-        return launch_gemm_as(gemm_split_kernel<D, Few>, kSplitSmemMax, (unsigned)(tiles * a.split), kSplitThreads,
+        return launch_gemm_as<2 * D + 1>(gemm_split_kernel<D, Few>, kSplitSmemMax, (unsigned)(tiles * a.split), kSplitThreads,
                               (unsigned)a.split, stream, maps, a, few);
     }
     const int64_t tiles = gemm_most_tiles(a, D == kWgrad, 2 * kBM), pairs = sm_count() / 2;
-    return launch_gemm_as(gemm_kernel<D, Wide>, D == kWgrad ? kWgradSmemMax : kGemmSmemMax, 2u * (unsigned)(tiles < pairs ? tiles : pairs),
+    return launch_gemm_as<2 * D>(gemm_kernel<D, Wide>, D == kWgrad ? kWgradSmemMax : kGemmSmemMax, 2u * (unsigned)(tiles < pairs ? tiles : pairs),
                           128 + 32 * Wide::kWarps, 2, stream,
                           maps, a, wide);
 }
