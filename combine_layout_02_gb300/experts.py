@@ -221,7 +221,7 @@ class _FeedForward(torch.autograd.Function):
         (rows, K), (E, H, F) = x.shape, down.shape
         launch, new = make_launch(error_flags=err), x.new_empty
         for_x, for_gate_up, for_down = ctx.needs_input_grad[:3]
-        wanted = for_x or for_gate_up or for_down
+        wanted = checkpoint is not None and (for_x or for_gate_up or for_down)
         h, y = new((rows, F)), new((rows, H))
         kept = rows_kept = keep = None
         if wanted and checkpoint == "bf16":
@@ -331,7 +331,7 @@ def unsort_rows(y: torch.Tensor, sort: ExpertSort, weights: Optional[torch.Tenso
     _check("y", y, torch.bfloat16, sort.rows, sort.H)
     if weights is not None:
         _check("weights", weights, torch.float32, sort.N, sort.k)
-        if checkpoint == "e4m3":
+        if checkpoint == "e4m3" and torch.is_grad_enabled():
             return _UnsortRowsKept.apply(y, weights, sort)
     return _UnsortRows.apply(y, weights, sort)
 
@@ -370,8 +370,9 @@ def expert_feed_forward(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tens
     _one_of("checkpoint", checkpoint, ("bf16", "e4m3", "recompute"))
     _check_err(err)
     _check_devices(x, gate_up, down, expert_prefix)
-    return _FeedForward.apply(x, gate_up, down, expert_prefix, _ACTIVATIONS[activation], checkpoint,
-                              _error_word(err, x.device))
+    # (Under torch.no_grad() a function still sees which inputs want gradients.)
+    return _FeedForward.apply(x, gate_up, down, expert_prefix, _ACTIVATIONS[activation],
+                              checkpoint if torch.is_grad_enabled() else None, _error_word(err, x.device))
 
 
 def adapter_projection(x: torch.Tensor, weight: torch.Tensor, a: Optional[torch.Tensor], b: Optional[torch.Tensor],

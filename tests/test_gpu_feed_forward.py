@@ -138,6 +138,32 @@ def test_what_is_kept_between_the_passes():
     assert held == {"bf16": rows * 4 * 512, "e4m3": rows * (1024 + 2 * 512) * 17 // 16, "recompute": 0}
 
 
+def test_serving_keeps_nothing():
+    """Under torch.no_grad() with parameters that want gradients: two kernels, memory for h and y alone, and a
+    single row takes the way of single rows."""
+    x, gate_up, down, prefix, _, _ = block([2048, 2048], 1024, 512, 1024, 9)
+    sort = ExpertSort(torch.arange(4096, device="cuda").remainder(2).view(-1, 1), 2, 1024)
+    weights = torch.rand(4096, 1, device="cuda").requires_grad_(True)
+    for mode in MODES:
+        with torch.no_grad():
+            torch.cuda.synchronize()
+            torch.cuda.reset_peak_memory_stats()
+            before, launched = torch.cuda.memory_allocated(), ep.ep_kernel_launch_count()
+            y = expert_feed_forward(x, gate_up, down, prefix, "silu", mode)
+            assert ep.ep_kernel_launch_count() - launched == 2
+            assert torch.cuda.max_memory_allocated() - before == 4096 * (512 + 1024) * 2
+            assert not y.requires_grad
+            launched = ep.ep_kernel_launch_count()
+            out = unsort_rows(y.requires_grad_(True), sort, weights, checkpoint="e4m3" if mode == "e4m3" else "bf16")
+            assert ep.ep_kernel_launch_count() - launched == 1 and not out.requires_grad
+    one = torch.tensor([0, 1, 1], dtype=torch.int32, device="cuda")
+    row = x.detach()[:1].contiguous()
+    h = torch.empty(1, 512, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_gated(ep.ep_gemm_shape(1, 2, 1024, 512), row, gate_up, one, ep.EP_ACT_SILU, h)
+    with torch.no_grad():
+        assert torch.equal(expert_feed_forward(row, gate_up, down, one), expert_product(h, down, one))
+
+
 def test_block_without_rows():
     x, gate_up, down, prefix, _, dy = block([0, 0], 64, 48, 72, 4)
     for mode in MODES:
