@@ -181,7 +181,7 @@ struct GatedShort : Gated<KEEP, ACT> {
 
 // One row, nothing kept: a stream of its expert's weights past it without tensor cores, whose set-up and
 // joining of parts are what such a call takes longest (1 row 4096 -> 4096: 15.4 us by gemm_split_kernel, so
-// 12.9; 1024 -> 1024 6.9, 2.8; two rows and more are as fast by tensor cores). Small blocks that ask
+// 12.5; 1024 -> 1024 6.9, 2.7; two rows and more are as fast by tensor cores). Small blocks that ask
 // for all of their weights at once and leave: with many of them an SM 64 MB come in 10.7 us, where blocks that
 // stay and load ahead take 12.5. `team` warps have a feature's two rows of weights, AHEAD pieces of 16
 // bytes a thread and row at a time. fp32 sums: a thread's, of even and of odd values, then over the lanes,
@@ -512,6 +512,8 @@ ep_status run_forward(const ep_gemm_shape* sh, const void* x, const void* w, con
     block_tiles(&a, false);
     GemmMaps maps{};
     if (rows) {
+        // Eight rows of Wg, the eight of Wu F rows on, the next eight of both, and so on. (The strides do not
+        // ascend: a box's address is a sum over its coordinates, whatever their order.)
         const uint64_t d[5] = {K, 8, 2, F / 8, E}, strides[4] = {2 * K, 2 * F * K, 16 * K, 4 * F * K};
         const uint32_t box[5] = {64, 8, 2, 8, 1};
         if ((st = encode_map(&maps.a, w, 5, d, box, strides)) != EP_OK) return st;
