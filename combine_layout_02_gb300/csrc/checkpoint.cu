@@ -4,7 +4,7 @@
 namespace ep {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kKeptThreads;
 
 // A thread has a group: 32 bytes of bf16, 16 of e4m3, one byte for the power of two, which 32 lanes write
 // side by side.
@@ -66,7 +66,7 @@ ep_status check_rows(int32_t rows, int32_t features, const void* x, const ep_che
     if (launch == nullptr || rows < 0 || features < 8 || features % 8 != 0) return EP_ERR_INVALID_ARG;
     if (rows > 1 << 30 || features > EP_GEMM_MAX_FEATURES) return EP_ERR_UNSUPPORTED;
     if ((rows > 0 && x == nullptr) || ((uintptr_t)x & 15) != 0) return EP_ERR_INVALID_ARG;
-    if ((int64_t)rows * (kept_features(features) / kKeptGroup) > (int64_t)0x7FFFFFFF * kThreads) return EP_ERR_UNSUPPORTED;
+    if (!kept_fits(rows, features)) return EP_ERR_UNSUPPORTED;
     return check_checkpoint(c, rows > 0, false);
 }
 

@@ -52,6 +52,12 @@ inline ep_status check_checkpoint(const ep_checkpoint* c, bool rows, bool any_ty
     return ((uintptr_t)c->values & 15) != 0 ? EP_ERR_INVALID_ARG : EP_OK;
 }
 
+// Whether a launch of blocks of kKeptThreads, a thread a group, reaches all of them.
+constexpr int kKeptThreads = 256;
+inline bool kept_fits(int rows, int features) {
+    return (int64_t)rows * (kept_features(features) / kKeptGroup) <= (int64_t)0x7FFFFFFF * kKeptThreads;
+}
+
 // Enqueues the values of a checkpoint's rows [rows][features] in bf16 (checkpoint.cu).
 cudaError_t launch_restore(int rows, int features, const void* values, const uint8_t* scales, void* x, cudaStream_t stream);
 

@@ -85,9 +85,15 @@ ep_status check_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* ot
     return EP_OK;
 }
 
-template <Direction D>
+struct NothingBefore {
+    cudaError_t operator()() const { return cudaSuccess; }
+};
+
+// `before` enqueues what the product reads.
+template <Direction D, class Before = NothingBefore>
 ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* other, const int32_t* prefix, void* out,
-                   const ep_launch* launch, int loads = GemmArgs{}.loads, uint64_t wait_ns = GemmArgs{}.wait_ns) {
+                   const ep_launch* launch, int loads = GemmArgs{}.loads, uint64_t wait_ns = GemmArgs{}.wait_ns,
+                   const Before& before = {}) {
     ep_status st = check_gemm(sh, rows_a, other, D == kWgrad, prefix, out, D != kWgrad, launch);
     if (st != EP_OK) return st;
     const uint64_t K = (uint64_t)sh->in_features, F = (uint64_t)sh->out_features, E = (uint64_t)sh->num_experts,
@@ -137,7 +143,8 @@ ep_status run_gemm(const ep_gemm_shape* sh, const void* rows_a, const void* othe
     }
     if ((st = begin_call(launch)) != EP_OK) return st;
     if (rows > 0) {
-        cudaError_t e = launch_gemm<D>(maps, a, NoExtra{}, NoExtra{}, launch->stream);
+        cudaError_t e = before();
+        if (e == cudaSuccess) e = launch_gemm<D>(maps, a, NoExtra{}, NoExtra{}, launch->stream);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return end_call(launch);
@@ -176,15 +183,11 @@ ep_status ep_expert_gemm_wgrad_checkpoint(const ep_gemm_shape* sh, const void* d
     ep_status st = check_gemm(sh, dy, workspace, true, expert_prefix, dw, false, launch);
     if (st != EP_OK) return st;
     if ((st = check_checkpoint(x, sh->num_rows > 0, false)) != EP_OK) return st;
+    if (!kept_fits(sh->num_rows, sh->in_features)) return EP_ERR_UNSUPPORTED;
     if (workspace == nullptr || workspace_bytes < ep_wgrad_checkpoint_workspace_size(sh)) return EP_ERR_INVALID_ARG;
-    ep_launch inner = *launch;          // the rows wait for the event, the product is recorded
-    inner.record_event = nullptr;
-    if ((st = begin_call(&inner)) != EP_OK) return st;
-    const cudaError_t e = launch_restore(sh->num_rows, sh->in_features, x->values, x->scales, workspace, launch->stream);
-    if (e != cudaSuccess) return cuda_fail(e);
-    inner = *launch;
-    inner.wait_event = nullptr;
-    return run_gemm<kWgrad>(sh, dy, workspace, expert_prefix, dw, &inner);
+    return run_gemm<kWgrad>(sh, dy, workspace, expert_prefix, dw, launch, GemmArgs{}.loads, GemmArgs{}.wait_ns, [&] {
+        return launch_restore(sh->num_rows, sh->in_features, x->values, x->scales, workspace, launch->stream);
+    });
 }
 
 ep_status ep_selftest_gemm_timeout(const ep_gemm_shape* sh, int32_t product, const void* rows, const void* other,

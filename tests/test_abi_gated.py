@@ -90,6 +90,7 @@ def test_gradient_from_kept_rows_refusals(ep):
     assert go(dy=P + 8) == bad and go(prefix=P + 2) == bad and go(dw=P + 2) == bad and go(ws=P + 8) == bad and go(n=size - 1) == bad
     for x in (C(ep.EP_BF16, P, None), C(ep.EP_FP8_E4M3, P, None), C(ep.EP_FP8_E4M3, None, P), C(ep.EP_FP8_E4M3, P + 8, P)):
         assert go(x=x) == bad
+    assert go(shape=S(1 << 30, 1, 1 << 20, 8), n=1 << 60) == unsup
     assert size >= 16 and ep.ep_wgrad_checkpoint_workspace_size(S(0, 1, 8, 8)) == 16
     for s, _ in shapes(S, go):
         assert ep.ep_wgrad_checkpoint_workspace_size(s) == 0

@@ -22,7 +22,7 @@ def wide_rows(rows, features, seed):
 
 
 @pytest.mark.parametrize("rows,features", [(1, 8), (1, 16), (2, 24), (7, 40), (3, 4104), (129, 200), (64, 512), (300, 136),
-                                           (1, 7168), (1000, 16)])
+                                           (1, 7168), (1000, 16), (3, 1 << 17)])
 def test_bytes_and_values(rows, features):
     x = wide_rows(rows, features, rows + features)
     x[0, :5] = torch.tensor([0.0, -0.0, 1.0, -1.0, 0.5], device="cuda")
@@ -73,6 +73,31 @@ def test_zeros_infinities_nan_and_extremes():
     assert torch.equal(torch.isnan(back), nans)
     # exact but where a value is below bf16's least one
     assert torch.equal(back[~nans], v.float().bfloat16().double()[~nans])
+
+
+def test_two_streams_and_a_replay():
+    x = [wide_rows(200, 136, s) for s in (1, 2)]
+    want = [quantised(t) for t in x]
+    streams = [torch.cuda.Stream() for _ in x]
+    got = []
+    for s, t in zip(streams, x):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            kept = checkpoint_rows(t)
+            got.append((*kept, restore_rows(*kept, 136)))
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for g, w in zip(got, want):
+        assert torch.equal(g[0].cpu(), w[0]) and torch.equal(g[1].cpu(), w[1]) and torch.equal(g[2].cpu().double(), w[2])
+    still = x[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = checkpoint_rows(still)
+        back = restore_rows(*kept, 136)
+    still.copy_(x[1])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(kept[0].cpu(), want[1][0]) and torch.equal(back.cpu().double(), want[1][2])
 
 
 def test_no_rows_and_refused_types():

@@ -321,6 +321,30 @@ def test_calls_on_two_streams_and_replayed():
             assert all(torch.equal(x, y) for x, y in zip(a, w) if x is not None)
 
 
+@pytest.mark.parametrize("counts,K,F", [([3], 1 << 20, 8), ([1, 2], 8, 1 << 20), ([1 if e % 80 == 3 else 0 for e in range(8192)], 64, 16),
+                                        ([70] * 3, 8, 1 << 16), ([5, 300], 1 << 16, 8)])
+def test_largest_sizes(counts, K, F):
+    """Features and experts at their limits, both ways, keeping 8 bits (the way back with as many features out)."""
+    b = Block(counts, K, F, seed=30)
+    h, values, scales = b.forward("silu", "e4m3")
+    (g, u), (g_off, u_off) = b.sums()
+    a, _, a_off, _ = act(g, "silu")
+    at = b.mine
+    assert_within(h[at], (a * u)[at], (product_bound(a, a_off + STEEP * g_off, u, u_off) + (a * u).abs() * U32)[at], U16)
+    dgu, _, (g, u) = backward(b, "silu", "e4m3", with_h=False)
+    dh, off = (torch.zeros(b.n, F, dtype=torch.float64, device="cuda") for _ in range(2))
+    for e in range(b.E):
+        rows = slice(b.edge[e], b.edge[e + 1])
+        if rows.start < rows.stop:
+            dh[rows] = b.dy[rows].double() @ b.down[e].double()
+            off[rows] = sum_bound(b.H, b.dy[rows].double().abs() @ b.down[e].double().abs(), 2 * U32)
+    a, da, a_off, da_off = act(g, "silu")
+    assert_within(dgu[at, :F], (dh * u * da)[at], (u.abs() * product_bound(dh, off, da, da_off) + (dh * u * da).abs() * 4 * U32)[at], U16)
+    assert_within(dgu[at, F:], (dh * a)[at], (product_bound(dh, off, a, a_off) + (dh * a).abs() * 4 * U32)[at], U16)
+    b.outside(h, values, scales, dgu)
+    assert int(b.err.item()) == 0
+
+
 def test_no_rows():
     sh = ep.ep_gemm_shape(0, 3, 64, 32)
     prefix = torch.zeros(4, dtype=torch.int32, device="cuda")
