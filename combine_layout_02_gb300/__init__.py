@@ -39,7 +39,7 @@ __all__ = [
     "ep_expert_gemm_dgrad", "ep_expert_gemm_wgrad", "ep_adapter_workspace_size", "ep_adapter_gemm",
     "ep_checkpoint", "make_checkpoint", "ep_checkpoint_rows", "ep_restore_rows",
     "ep_wgrad_checkpoint_workspace_size", "ep_expert_gemm_wgrad_checkpoint",
-    "EP_CHECKPOINT_GROUP", "EP_ACT_SILU", "EP_ACT_GELU_TANH", "ep_expert_gated", "ep_expert_gated_dgrad",
+    "EP_CHECKPOINT_GROUP", "EP_GEMM_MAX_FEATURES", "EP_ACT_SILU", "EP_ACT_GELU_TANH", "ep_expert_gated", "ep_expert_gated_dgrad",
     "ep_selftest_gated_timeout",
 ]
 
@@ -56,6 +56,7 @@ EP_MAX_TOPK = 32
 EP_EXPERT_MAJOR_MAX_EXPERTS = 4096
 EP_ADAPTER_MAX_RANK = 256
 EP_CHECKPOINT_GROUP = 16
+EP_GEMM_MAX_FEATURES = 1 << 20
 EP_ACT_SILU, EP_ACT_GELU_TANH = 0, 1
 
 # Every function include/ep.h declares (checked by the ABI test).

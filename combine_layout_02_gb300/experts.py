@@ -19,8 +19,8 @@ from typing import List, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (_Address, EP_ACT_GELU_TANH, EP_ACT_SILU, EP_BF16, EP_CHECKPOINT_GROUP, ep_adapter_gemm, ep_adapter_shape,
-               ep_adapter_workspace_size, ep_checkpoint_rows, ep_expert_gated, ep_expert_gated_dgrad, ep_expert_gemm,
+from . import (_Address, EP_ACT_GELU_TANH, EP_ACT_SILU, EP_BF16, EP_CHECKPOINT_GROUP, EP_GEMM_MAX_FEATURES,
+               ep_adapter_gemm, ep_adapter_shape, ep_adapter_workspace_size, ep_checkpoint_rows, ep_expert_gated, ep_expert_gated_dgrad, ep_expert_gemm,
                ep_expert_gemm_dgrad, ep_expert_gemm_wgrad, ep_expert_gemm_wgrad_checkpoint, ep_gemm_shape,
                ep_read_error_flags_sync, ep_restore_rows, ep_sort_layout, ep_sort_rows, ep_unsort_rows,
                ep_unsort_rows_backward, ep_wgrad_checkpoint_workspace_size, make_checkpoint, make_launch, make_shape)
@@ -219,9 +219,11 @@ class _FeedForward(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate_up, down, prefix, act, checkpoint, err):
         (rows, K), (E, H, F) = x.shape, down.shape
-        launch, new = make_launch(error_flags=err), x.new_empty
         for_x, for_gate_up, for_down = ctx.needs_input_grad[:3]
         wanted = checkpoint is not None and (for_x or for_gate_up or for_down)
+        if wanted and (for_x or for_gate_up) and 2 * F > EP_GEMM_MAX_FEATURES:          # one product of both, backward
+            raise ValueError(f"gate_up has to be of {EP_GEMM_MAX_FEATURES // 2} features or fewer for gradients, not {F}")
+        launch, new = make_launch(error_flags=err), x.new_empty
         h, y = new((rows, F)), new((rows, H))
         kept = rows_kept = keep = None
         if wanted and checkpoint == "bf16":
@@ -361,6 +363,7 @@ def expert_feed_forward(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tens
       "e4m3"       the same in 8 bits (1.0625 bytes); the matrices' gradients and act' then go by
                    those values, the result and the gradient's way through down do not
       "recompute"  x; both projections run again
+    For gradients to x or gate_up there are EP_GEMM_MAX_FEATURES / 2 features at most.
     Every row has to belong to an expert (expert_prefix runs from 0 to rows)."""
     _check("down", down, torch.bfloat16, None, None, None)
     _check("gate_up", gate_up, torch.bfloat16, down.shape[0], 2 * down.shape[2], None)

@@ -33,6 +33,19 @@ def test_block_operands_fit():
     refuses("err", experts.expert_feed_forward, **good, err=t(F32, 1))
 
 
+def test_widest_block_that_has_gradients():
+    F = 1 << 19
+    for features in (F, F + 8):
+        x, gate_up, down, prefix = t(BF, 1, 8), t(BF, 1, 2 * features, 8), t(BF, 1, 8, features), t(I32, 2)
+        for trained in (x, gate_up, down):
+            wide = features > F and trained is not down
+            trained.requires_grad_()
+            with pytest.raises((ValueError, RuntimeError)) as refusal:          # none of these is on a GPU
+                experts.expert_feed_forward(x, gate_up, down, prefix)
+            assert str(refusal.value).startswith("gate_up has to be of 524288") == wide
+            trained.requires_grad_(False)
+
+
 def test_tensors_are_on_one_device():
     x, gate_up, down, prefix = t(BF, 9, 64), t(BF, 3, 80, 64), t(BF, 3, 64, 40), t(I32, 4)
     for f, args in ((experts.expert_feed_forward, (x.to("meta"), gate_up, down, prefix)),
