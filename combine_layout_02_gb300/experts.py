@@ -372,7 +372,7 @@ def expert_feed_forward(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tens
     _one_of("activation", activation, tuple(_ACTIVATIONS))
     _one_of("checkpoint", checkpoint, ("bf16", "e4m3", "recompute"))
     _check_err(err)
-    _check_devices(x, gate_up, down, expert_prefix)
+    _check_devices(x, gate_up, down, expert_prefix, *(() if err is None else (err,)))
     # (Under torch.no_grad() a function still sees which inputs want gradients.)
     return _FeedForward.apply(x, gate_up, down, expert_prefix, _ACTIVATIONS[activation],
                               checkpoint if torch.is_grad_enabled() else None, _error_word(err, x.device))
