@@ -149,8 +149,9 @@ struct Gated : NoExtra {
                     m = larger_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                     const uint32_t e = exponent[h][j] = kept_exponent(m & 0xFFFFu);
                     const float inv = kept_inverse(e);
-                    const uint2 eight = make_uint2(keep_pair(q[j].x, inv) | keep_pair(q[j].y, inv) << 16,
-                                                   keep_pair(q[j].z, inv) | keep_pair(q[j].w, inv) << 16);
+                    uint2 eight = make_uint2(keep_pair(q[j].x, inv) | keep_pair(q[j].y, inv) << 16,
+                                             keep_pair(q[j].z, inv) | keep_pair(q[j].w, inv) << 16);
+                    if (f >= F) eight = make_uint2(0, 0);          // padding: an infinite row's sums are NaN there
                     if (j * 4 < left && f < kept.padded) *reinterpret_cast<uint2*>(kept.bytes(row + j * 4, h) + f) = eight;
                 }
             }

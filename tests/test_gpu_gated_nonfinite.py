@@ -1,0 +1,89 @@
+"""The gated feed-forward block with infinities and NaN in single rows: what is kept of them, and that the other
+rows come out as they would without them, bit for bit."""
+import math
+
+import pytest
+import torch
+
+import combine_layout_02_gb300 as ep
+from kept_util import GROUP, quantised
+
+pytestmark = pytest.mark.gpu
+
+ACTS = {"silu": ep.EP_ACT_SILU, "gelu": ep.EP_ACT_GELU_TANH}
+
+# rows per expert, in_features, out_features of h: pairs, narrow tiles, a contraction split over a cluster;
+# features that are odd multiples of 8 and multiples of 16
+CASES = {
+    "pairs": ([7000, 0, 5130], 1160, 264),
+    "pairs_short": ([3000, 1111], 136, 1032),
+    "narrow": ([40, 0, 200, 30], 64, 136),
+    "cluster": ([3, 7, 2], 4096, 264),
+    "cluster_whole_groups": ([9, 5], 4096, 128),
+}
+BEFORE, AFTER = 2, 3          # rows of no expert around them
+
+
+class Rows:
+    def __init__(self, counts, K, F, seed=1):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        new = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+        self.E, self.K, self.F, self.n = len(counts), K, F, BEFORE + sum(counts) + AFTER
+        self.prefix = (torch.tensor([0] + counts).cumsum(0) + BEFORE).int().cuda()
+        self.x, self.dy = new(self.n, K), new(self.n, K)
+        self.gate_up, self.down = (new(self.E, 2 * F, K) * 1.5 * K ** -0.5).bfloat16(), (new(self.E, K, F) * F ** -0.5).bfloat16()
+        for w in (self.gate_up, self.down):          # (0 times an infinity is a NaN all the same, but says less)
+            w[w == 0] = 2.0 ** -7
+        # a NaN, an infinity, both, a row of NaN: the first expert's second and third row, the last's two last
+        self.bad = [BEFORE + 1, BEFORE + 2, self.n - AFTER - 2, self.n - AFTER - 1]
+        self.good = torch.ones(self.n, dtype=torch.bool, device="cuda")
+        self.good[self.bad] = False
+        self.mine = slice(BEFORE, self.n - AFTER)
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.launch = ep.make_launch(error_flags=self.err)
+
+    def spoil(self, t):
+        """t with its bad rows."""
+        t = t.clone()
+        t[self.bad[0], t.shape[1] // 3] = math.nan
+        t[self.bad[1], 5] = math.inf
+        t[self.bad[2], 0], t[self.bad[2], -1] = -math.inf, math.nan
+        t[self.bad[3]] = math.nan
+        return t
+
+    def buffers(self, keep):
+        width = -(-self.F // GROUP) * GROUP
+        if keep == "bf16":
+            return torch.full((self.n, 2 * self.F), 7.0, dtype=torch.bfloat16, device="cuda"), None
+        return (torch.full((self.n, 2 * width), 0xA5, dtype=torch.uint8, device="cuda"),
+                torch.full((self.n, width // GROUP, 2), 0xA5, dtype=torch.uint8, device="cuda"))
+
+    def forward(self, x, kind, keep):
+        h = torch.full((self.n, self.F), 7.0, dtype=torch.bfloat16, device="cuda")
+        values, scales = self.buffers(keep)
+        ep.ep_expert_gated(ep.ep_gemm_shape(self.n, self.E, self.K, self.F), x, self.gate_up, self.prefix, ACTS[kind], h,
+                           ep.make_checkpoint(values, scales), self.launch)
+        return h, values, scales
+
+    def backward(self, dy, values, scales, kind):
+        dgu = torch.full((self.n, 2 * self.F), 7.0, dtype=torch.bfloat16, device="cuda")
+        h = torch.full((self.n, self.F), 7.0, dtype=torch.bfloat16, device="cuda")
+        ep.ep_expert_gated_dgrad(ep.ep_gemm_shape(self.n, self.E, self.F, self.K), dy, self.down, self.prefix, ACTS[kind],
+                                 ep.make_checkpoint(values, scales), dgu, h, self.launch)
+        return dgu, h
+
+    def outside(self, *outputs):
+        for t in outputs:
+            if t is not None:
+                rest = torch.cat([t[:self.mine.start], t[self.mine.stop:]])
+                assert bool((rest == (0xA5 if t.dtype == torch.uint8 else 7)).all())
+        assert int(self.err.item()) == 0
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_padding_is_zeros(name):
+    """Features beyond the last are zeros in a checkpoint whatever the row holds."""
+    b = Rows(*CASES[name])
+    _, values, _ = b.forward(b.spoil(b.x), "silu", "e4m3")
+    for part in values.chunk(2, 1):
+        assert not bool(part[b.mine, b.F:].any())
