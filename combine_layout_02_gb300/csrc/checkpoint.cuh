@@ -24,7 +24,7 @@ __device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// k + 127 from a group's largest magnitude (the bits of a bf16 without its sign): its exponent less 8, and one
+// k + 127 from a group's largest magnitude (the bits of a bf16 without its sign, not a NaN): its exponent less 8, and one
 // more where its mantissa is above 1.75, which then carries over. 1 for zeros (2^-126), 247 or less for
 // an infinity, whose e4m3 value 448 * 2^120 comes back as one.
 __device__ __forceinline__ uint32_t kept_exponent(uint32_t amax) { return max((amax + 0x1Fu) >> 7, 9u) - 8; }

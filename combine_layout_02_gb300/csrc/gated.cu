@@ -147,7 +147,7 @@ struct Gated : NoExtra {
                     m = larger_bf16x2(m, larger_bf16x2(magnitudes(q[j].z), magnitudes(q[j].w)));
                     m = larger_bf16x2(m, __byte_perm(m, 0, 0x1032));
                     m = larger_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                    const uint32_t e = exponent[h][j] = kept_exponent(m & 0xFFFFu);
+                    const uint32_t e = exponent[h][j] = kept_exponent(larger_bf16x2(m, 0) & 0xFFFFu);          // 0: nothing but NaN
                     const float inv = kept_inverse(e);
                     uint2 eight = make_uint2(keep_pair(q[j].x, inv) | keep_pair(q[j].y, inv) << 16,
                                              keep_pair(q[j].z, inv) | keep_pair(q[j].w, inv) << 16);

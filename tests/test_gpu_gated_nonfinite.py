@@ -87,3 +87,19 @@ def test_padding_is_zeros(name):
     _, values, _ = b.forward(b.spoil(b.x), "silu", "e4m3")
     for part in values.chunk(2, 1):
         assert not bool(part[b.mine, b.F:].any())
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_kept_bytes(name):
+    """What is kept in 8 bits is the checkpoint of the bf16 values, byte for byte: NaN is left out of its
+    group's scale, also where the group has nothing else."""
+    b = Rows(*CASES[name])
+    x = b.spoil(b.x)
+    _, values, scales = b.forward(x, "silu", "e4m3")
+    _, halves, _ = b.forward(x, "silu", "bf16")
+    nan = torch.isnan(halves[b.bad])
+    assert bool(nan[3].all()) and bool(torch.isinf(halves[b.bad[1]]).any())
+    for side in range(2):
+        q, k, _ = quantised(halves[b.mine].chunk(2, 1)[side])
+        assert torch.equal(scales[b.mine, :, side].cpu(), k)
+        assert torch.equal(values[b.mine].chunk(2, 1)[side][:, :b.F].cpu(), q[:, :b.F])
