@@ -103,3 +103,74 @@ def test_kept_bytes(name):
         q, k, _ = quantised(halves[b.mine].chunk(2, 1)[side])
         assert torch.equal(scales[b.mine, :, side].cpu(), k)
         assert torch.equal(values[b.mine].chunk(2, 1)[side][:, :b.F].cpu(), q[:, :b.F])
+
+
+def same(a, b):
+    """Bit for bit (NaN included)."""
+    as_bits = lambda t: t.view(torch.int16) if t.dtype == torch.bfloat16 else t  # noqa: E731
+    return torch.equal(as_bits(a), as_bits(b))
+
+
+@pytest.mark.parametrize("keep", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind", ACTS)
+@pytest.mark.parametrize("name", CASES)
+def test_bad_rows_stay_alone_forward(name, kind, keep):
+    """A row with a NaN or an infinity has no finite value of h (every weight is other than 0), and what is
+    kept of it is NaN or an infinity; all other rows are as they are without it."""
+    b = Rows(*CASES[name])
+    got, want = b.forward(b.spoil(b.x), kind, keep), b.forward(b.x, kind, keep)
+    for a, w in zip(got, want):
+        assert a is None or same(a[b.good], w[b.good])
+    assert not bool(torch.isfinite(got[0][b.bad]).any()) and bool(torch.isfinite(want[0][b.mine]).all())
+    if keep == "bf16":
+        assert not bool(torch.isfinite(got[1][b.bad]).any())
+    b.outside(*got)
+
+
+@pytest.mark.parametrize("keep", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind", ACTS)
+@pytest.mark.parametrize("name", CASES)
+def test_bad_rows_stay_alone_backward(name, kind, keep):
+    """Of dy: the row's dg and du have no finite value but where their factor is 0, h is as without. Of g
+    and u as they were kept: their own features of dg, du and h alone (bf16; in 8 bits an infinity
+    sets the scale of its group)."""
+    b = Rows(*CASES[name])
+    _, values, scales = b.forward(b.x, kind, keep)
+    want = b.backward(b.dy, values, scales, kind)
+    assert all(bool(torch.isfinite(t[b.mine]).all()) for t in want)
+    dgu, h = b.backward(b.spoil(b.dy), values, scales, kind)
+    assert same(dgu[b.good], want[0][b.good]) and same(h, want[1])
+    # dh is NaN or an infinity, and so is its product with any factor: 0 times an infinity is NaN
+    assert not bool(torch.isfinite(dgu[b.bad]).any())
+    b.outside(dgu, h)
+    # one feature of g in a row, one of u in another
+    for side, row in enumerate(b.bad[:2]):
+        for bad in (math.nan, math.inf, -math.inf):
+            f = b.F - 3
+            v, s = values.clone(), scales if scales is None else scales.clone()
+            if keep == "bf16":
+                v[row, side * b.F + f] = bad
+                group = [f]
+            else:
+                wide = v.shape[1] // 2
+                if math.isnan(bad):
+                    v[row, side * wide + f] = 0x7F
+                    group = [f]
+                else:          # 448 * 2^120
+                    v[row, side * wide + f] = 0x7E if bad > 0 else 0xFE
+                    s[row, f // GROUP, side] = 247
+                    group = list(range(f // GROUP * GROUP, min(b.F, (f // GROUP + 1) * GROUP)))
+            dgu, h = b.backward(b.dy, v, s, kind)
+            hit = torch.zeros(b.F, dtype=torch.bool, device="cuda")
+            hit[group] = True
+            rest = torch.ones(b.n, dtype=torch.bool, device="cuda")
+            rest[row] = False
+            assert same(dgu[rest], want[0][rest]) and same(h[rest], want[1][rest])
+            assert same(dgu[row].view(2, -1)[:, ~hit], want[0][row].view(2, -1)[:, ~hit]) and same(h[row, ~hit], want[1][row, ~hit])
+            if math.isnan(bad):          # act(g) u, dh u act'(g) and, of g, dh act(g) (of u: du does not have it)
+                assert bool(torch.isnan(h[row, f])) and bool(torch.isnan(dgu[row, f]))
+                assert bool(torch.isnan(dgu[row, b.F + f])) == (side == 0)
+            elif side == 1:          # u: h and dg are infinite (or NaN where act is 0), du has none of it
+                assert not bool(torch.isfinite(h[row, f]))
+                assert keep == "e4m3" or same(dgu[row, b.F + f], want[0][row, b.F + f])
+            b.outside(dgu, h)
