@@ -238,6 +238,9 @@ class _FeedForward(torch.autograd.Function):
                 ep_checkpoint_rows(rows, K, x, _kept_at(kept.data_ptr() + own, rows, width), launch)
         elif wanted:
             rows_kept = x
+            if rows == 1:          # keeping nothing it would go another way than the backward pass does again
+                spare = new((1, 2 * F))
+                keep = make_checkpoint(spare)
         ep_expert_gated(ep_gemm_shape(rows, E, K, F), x, gate_up, prefix, act, h, keep, launch)
         ep_expert_gemm(ep_gemm_shape(rows, E, F, H), h, down, prefix, y, launch)
         if wanted:
@@ -363,6 +366,8 @@ def expert_feed_forward(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tens
       "e4m3"       the same in 8 bits (1.0625 bytes); the matrices' gradients and act' then go by
                    those values, the result and the gradient's way through down do not
       "recompute"  x; both projections run again
+    The result is the same with all three. Where no gradient is wanted nothing is kept, and a single
+    row then goes another way (ep_expert_gated), with its sums in another order.
     For gradients to x or gate_up there are EP_GEMM_MAX_FEATURES / 2 features at most.
     Every row has to belong to an expert (expert_prefix runs from 0 to rows)."""
     _check("down", down, torch.bfloat16, None, None, None)

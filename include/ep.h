@@ -582,7 +582,9 @@ typedef enum ep_activation { EP_ACT_SILU = 0, EP_ACT_GELU_TANH = 1 } ep_activati
  *   EP_ACT_GELU_TANH  act(g) = g / 2 * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3)))
  *   x  dev [num_rows][in_features]
  *   w  dev [E][2][F][in_features]: Wg, then Wu
- *   h  dev [num_rows][F], from the fp32 sums, rounded once; NULL to leave out (with keep)
+ *   h  dev [num_rows][F], from the fp32 sums, rounded once; NULL to leave out (with keep). The same
+ *      with any keep and without, but for num_rows = 1: without keep that goes another way, which
+ *      adds up in another order
  *   keep  nullable: g and u, rounded to bf16, for ep_expert_gated_dgrad: a checkpoint of rows of two
  *         parts [num_rows][2][F], EP_BF16 or EP_FP8_E4M3 */
 EP_API ep_status ep_expert_gated(const ep_gemm_shape* shape, const void* x, const void* w,
