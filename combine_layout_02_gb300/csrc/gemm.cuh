@@ -1171,7 +1171,7 @@ inline void gemm_tiles(GemmArgs* a, bool wgrad, int beside = 0, int most_rows = 
 constexpr int kSplitSmemMax = 201 * 1024, kGemmSmemMax = 222 * 1024, kWgradSmemMax = 225 * 1024;
 
 // WHICH: a number of its own for each kernel with this Extra. Its shared-memory limit is set once per device (0.6 us of
-// a call's 4 on the host), and once more where a launch is refused, as after a device reset.
+// a call's 4 on the host): the runtime holds it for all of the device's contexts, and for one that was reset.
 template <int WHICH, class Kernel, class Extra>
 cudaError_t launch_gemm_as(Kernel kernel, int smem_most, unsigned blocks, unsigned threads, unsigned cluster, cudaStream_t stream,
                            const GemmMaps& maps, const GemmArgs& a, const Extra& extra) {
@@ -1195,17 +1195,14 @@ cudaError_t launch_gemm_as(Kernel kernel, int smem_most, unsigned blocks, unsign
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    for (bool known = (set[device >> 6].load(std::memory_order_relaxed) & bit) != 0;; known = false) {
-        if (!known) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most < beside ? smem_most : beside);
-            if (e != cudaSuccess) return e;
-            set[device >> 6].fetch_or(bit, std::memory_order_relaxed);
-        }
-        e = cudaLaunchKernelEx(&cfg, kernel, maps, a, extra);
-        if (e == cudaSuccess) count_launches(1);
-        if (e != cudaErrorInvalidValue || !known) return e;
-        (void)cudaGetLastError();
+    if ((set[device >> 6].load(std::memory_order_relaxed) & bit) == 0) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most < beside ? smem_most : beside);
+        if (e != cudaSuccess) return e;
+        set[device >> 6].fetch_or(bit, std::memory_order_relaxed);
     }
+    e = cudaLaunchKernelEx(&cfg, kernel, maps, a, extra);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 // Launches the product (a.num_rows > 0) as gemm_tiles has laid it out.
