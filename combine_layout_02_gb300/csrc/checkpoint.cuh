@@ -4,8 +4,8 @@
 // powers of two a value comes back exactly in bf16 (three bits after the first), and neither amax nor k
 // needs a division or a logarithm: 448 = 1.75 * 2^8, so k goes by amax's exponent and by whether its
 // mantissa is above 1.75.
-// 16 features, not more: that is what one warp of the gated product's epilogue holds of a row, and a byte in 16
-// makes 1.0625 bytes a value.
+// 16 features, not more: that is what two neighbouring lanes hold of a row in the gated product's epilogue, and a
+// byte in 16 makes 1.0625 bytes a value.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -24,8 +24,8 @@ __device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// k + 127 from a group's largest magnitude (the bits of a bf16 without its sign, not a NaN): its exponent less 8, and one
-// more where its mantissa is above 1.75, which then carries over. 1 for zeros (2^-126), 247 or less for
+// k + 127 from a group's largest magnitude (the bits of a bf16 without its sign, no NaN): its exponent less 8,
+// and one more where its mantissa is above 1.75, which then carries over. 1 for zeros (2^-126), 247 or less for
 // an infinity, whose e4m3 value 448 * 2^120 comes back as one.
 __device__ __forceinline__ uint32_t kept_exponent(uint32_t amax) { return max((amax + 0x1Fu) >> 7, 9u) - 8; }
 __device__ __forceinline__ float kept_scale(uint32_t exponent) { return __uint_as_float(exponent << 23); }

@@ -507,10 +507,10 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                  : "memory");
 }
 
-// What an epilogue adds to the sums before they are rounded; all 128 epilogue threads make the calls
-// together, each for output feature m. `shared`: kFloats floats of the block (gemm_split_kernel: kFewFloats). kFollows: the kernel
-// directly follows one of this library after which the call's inputs are complete; only the
-// epilogue waits for that kernel itself.
+// What an epilogue adds to the sums before they are rounded; all writing threads make the calls together,
+// each for output feature m. `shared`: kFloats floats of the block (gemm_split_kernel: kFewFloats).
+// kFollows: the kernel directly follows one of this library after which the call's inputs are
+// complete; only the epilogue waits for that kernel itself.
 //   gemm_kernel:        tile writes rows row0 .. row0 + rows - 1 of a tile, features m0 .. m0 + 31, out of
 //                       tensor memory; kWarps / 4 warps do, `half` 0, 1 and on. reordered: the rows are loaded
 //                       through other_b. prepare is called by all writing threads before, while
@@ -757,7 +757,8 @@ __global__ void __launch_bounds__(128 + 32 * Extra::kWarps, 1)
             const int rows = min(t.n, t.end - t.n0);
             if (D != kWgrad) extra.prepare(s_extra, smem + a.stages * stage_bytes, t.n0, rows, t.m0 + (int)rank * kBM);
             if (some) {
-                if (!epilogue_all<32 * Extra::kWarps>(mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a, D == kWgrad ? t.end - t.begin : a.C))) break;
+                const bool there = mbar_wait(&acc_full[acc], (used >> 1) & 1, &dead, a, D == kWgrad ? t.end - t.begin : a.C);
+                if (!epilogue_all<32 * Extra::kWarps>(there)) break;
                 tc_fence_after();
             }
             const int m = t.m0 + (int)rank * kBM + quarter * 32 + lane;

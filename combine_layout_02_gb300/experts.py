@@ -20,8 +20,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (_Address, EP_ACT_GELU_TANH, EP_ACT_SILU, EP_BF16, EP_CHECKPOINT_GROUP, EP_GEMM_MAX_FEATURES,
-               ep_adapter_gemm, ep_adapter_shape, ep_adapter_workspace_size, ep_checkpoint_rows, ep_expert_gated, ep_expert_gated_dgrad, ep_expert_gemm,
-               ep_expert_gemm_dgrad, ep_expert_gemm_wgrad, ep_expert_gemm_wgrad_checkpoint, ep_gemm_shape,
+               ep_adapter_gemm, ep_adapter_shape, ep_adapter_workspace_size, ep_checkpoint_rows, ep_expert_gated,
+               ep_expert_gated_dgrad, ep_expert_gemm, ep_expert_gemm_dgrad, ep_expert_gemm_wgrad, ep_expert_gemm_wgrad_checkpoint, ep_gemm_shape,
                ep_read_error_flags_sync, ep_restore_rows, ep_sort_layout, ep_sort_rows, ep_unsort_rows,
                ep_unsort_rows_backward, ep_wgrad_checkpoint_workspace_size, make_checkpoint, make_launch, make_shape)
 from .api import Buffer
@@ -457,8 +457,8 @@ class MoELayer(torch.nn.Module):
 
     checkpoint: None runs the experts product by product and keeps every step's result in bf16;
     "bf16", "e4m3" and "recompute" run them as expert_feed_forward does, the activation and the
-    product in the projections' kernel ("e4m3" keeps the experts' outputs in 8 bits too, for the
-    routing weights' gradient). activation: "silu", or with a checkpoint "gelu"."""
+    product in the projections' kernel, in serving too, where nothing is kept ("e4m3" keeps the
+    experts' outputs in 8 bits too, for the routing weights' gradient). activation: "silu", or with a checkpoint "gelu"."""
 
     def __init__(self, buf: Buffer, features: int, device="cuda", checkpoint: Optional[str] = None,
                  activation: str = "silu"):

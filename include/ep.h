@@ -536,8 +536,8 @@ EP_API ep_status ep_expert_gemm_wgrad(const ep_gemm_shape* shape, const void* dy
  * amax <= 448 * 2^k (amax: the group's largest magnitude, NaN left out); q = e4m3(x / 2^k), to
  * nearest even, and k + 127 in a byte. x comes back as q * 2^k: within 2^-4 of it relatively
  * (2^-10 * 2^k absolutely where that is more), exact in bf16 but for magnitudes below 2^-133.
- * NaN stays NaN; an infinity stays one, and what else its group has is held on that scale; above
- * 1.9375 * 2^127 a value comes back as an infinity.
+ * NaN stays NaN; an infinity stays one, and what else its group has is held on that scale; from
+ * 1.9375 * 2^127 on (a tie, to even) a value comes back as an infinity.
  *   dtype   EP_FP8_E4M3, or EP_BF16 where a call says so: bf16 values, scales NULL
  *   values  dev, 16-byte aligned: e4m3 [rows][features, padded with zeros to a multiple of
  *           EP_CHECKPOINT_GROUP], bf16 [rows][features]
